@@ -1,0 +1,76 @@
+// cap.cuh -- scores capped by a tanh: s -> cap * tanh(s / cap), the score
+// s = softmax scale * (q . k), applied before the mask.
+//
+// The kernels keep scores in the log2 domain, so the capped score of a dot
+// product x is c2 * tanh(x * k) with k = scale / cap and c2 = cap * log2(e)
+// (CapArgs).  The cap is increasing, so a row's largest capped score is the
+// capped largest dot product.
+//
+// tanh in two forms:
+//   * tanh_sfu: 1 - 2 / (1 + e^2y), two SFU operations, any y.  Absolute
+//     error a few 1e-7 (of 1), so a capped score is within cap * 1e-6.
+//   * cap_fma2: y * P(y^2) on the FMA pipe for |y| <= 1, where most scores of
+//     a trained model lie (|s| <= cap); P has five coefficients, fitted here
+//     to the smallest largest relative error on [-1, 1], 7.0e-6: at a cap
+//     of 50 at most 2.7e-4 of a weight, far below the 2^-8 of its rounding to
+//     bf16.
+//     The tensor-core kernels use it for a warp's part of a tile when every
+//     |y| there is at most 1, since their SFU share is already as large as
+//     the MMA's time.
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace duo {
+
+// 2^x and 1/x on the SFU (PTX approximations)
+__device__ __forceinline__ float sfu_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float sfu_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float tanh_sfu(float y) {
+    // e^2y overflows to inf for large y (1 / inf = 0: tanh = 1) and underflows
+    // to 0 for small y (tanh = -1)
+    const float e = sfu_exp2(y * (2.f * kLog2e));
+    return fmaf(-2.f, sfu_rcp(1.f + e), 1.f);
+}
+
+constexpr float kTanh0 = 0.999993085861206f, kTanh1 = -0.3329806625843048f, kTanh2 = 0.13036811351776123f,
+                kTanh3 = -0.04481755197048187f, kTanh4 = 0.00903642363846302f;
+
+// c2 * tanh(k x) of a pair of dot products with |k x| <= 1: the polynomial's
+// coefficients times c2 and the powers of k, so that it takes x itself.
+struct CapPoly {
+    float a0, a1, a2, a3, a4;
+};
+__device__ __forceinline__ CapPoly cap_poly(const CapArgs& cap) {
+    const float k = cap.k, k2 = k * k, s0 = cap.c2 * k;
+    return {kTanh0 * s0, kTanh1 * (s0 * k2), kTanh2 * (s0 * k2 * k2), kTanh3 * (s0 * k2 * k2 * k2),
+            kTanh4 * (s0 * k2 * k2 * k2 * k2)};
+}
+__device__ __forceinline__ float2 cap_fma2(float2 x, const CapPoly& c) {
+    const float2 u = fmul2(x, x);
+    float2 p = ffma2(u, make_float2(c.a4, c.a4), make_float2(c.a3, c.a3));
+    p = ffma2(p, u, make_float2(c.a2, c.a2));
+    p = ffma2(p, u, make_float2(c.a1, c.a1));
+    p = ffma2(p, u, make_float2(c.a0, c.a0));
+    return fmul2(p, x);
+}
+
+// The log2-domain score of a dot product: x * sl, or capped.  EXACT takes
+// CUDA's tanhf (the fp32 paths).
+template <bool CAP, bool EXACT = false>
+__device__ __forceinline__ float score_log2(float x, float sl, const CapArgs& cap) {
+    if constexpr (!CAP) return x * sl;
+    return cap.c2 * (EXACT ? tanhf(x * cap.k) : tanh_sfu(x * cap.k));
+}
+
+}  // namespace duo

@@ -35,6 +35,7 @@
 // advances seq_len, so one launch does duo_append_kv(T = 1) + decode.
 #include <utility>
 
+#include "cap.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "kvq4.cuh"
@@ -348,7 +349,7 @@ __device__ __forceinline__ void decode_finish(float* sM, uint64_t* comb_bar, int
     }
 }
 
-template <typename T, int D, int G, bool PAGED>
+template <typename T, int D, int G, bool PAGED, bool CAP>
 __global__ void __maxnreg__(decode_max_regs(G))
     decode_kernel(const LayerArgs a, const CacheArgs c, const DecodeArgs d) {
     using C = Cfg<T, D>;
@@ -554,7 +555,7 @@ __global__ void __maxnreg__(decode_max_regs(G))
     if (warp < NW) {
         float q[G][EPL];
         const T* qp = static_cast<const T*>(d.q) + ((size_t)b * a.Hq + a.q_head0[slot]) * D + dl * EPL;
-        const float qs = a.scale * kLog2e;
+        const float qs = CAP ? a.cap.k : a.scale * kLog2e;   // capped: the scores become tanh's argument
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             load_row_f32<T, EPL>(qp + (size_t)g * D, q[g]);
@@ -601,7 +602,9 @@ __global__ void __maxnreg__(decode_max_regs(G))
             float m_new[G], corr[G], p[G];
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                float sv = valid ? s[g] : kNegBig;
+                float sv = s[g];
+                if constexpr (CAP) sv = a.cap.c2 * tanhf(sv);
+                sv = valid ? sv : kNegBig;
                 float mt = sv;
                 if (DUP == 2) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
                 mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
@@ -782,7 +785,7 @@ __device__ __forceinline__ void warm_l2_split(const LayerArgs& a, const CacheArg
     }
 }
 
-template <int G, bool PAGED>
+template <int G, bool PAGED, bool CAP>
 __global__ void __maxnreg__(200)
     decode_mma_kernel(const __grid_constant__ CUtensorMap tmKf, const __grid_constant__ CUtensorMap tmVf,
                       const __grid_constant__ CUtensorMap tmKr, const __grid_constant__ CUtensorMap tmVr,
@@ -1055,7 +1058,8 @@ __global__ void __maxnreg__(200)
             }
             // this lane's keys: key_base + 2 quad + {0, 1} and + 8
             const int k0 = key_base + 2 * quad;
-            float sv[4] = {s0[0] * sl, s0[1] * sl, s1[0] * sl, s1[1] * sl};
+            float sv[4] = {score_log2<CAP>(s0[0], sl, a.cap), score_log2<CAP>(s0[1], sl, a.cap),
+                           score_log2<CAP>(s1[0], sl, a.cap), score_log2<CAP>(s1[1], sl, a.cap)};
             const bool vk[4] = {k0 < n, k0 + 1 < n, k0 + 8 < n, k0 + 9 < n};
             float mx = kNegBig;
 #pragma unroll
@@ -1122,7 +1126,7 @@ __global__ void __maxnreg__(200)
                                                                          split, retrieval, fused);
 }
 
-template <int G, bool PAGED>
+template <int G, bool PAGED, bool CAP>
 cudaError_t launch_mma_t(const LayerArgs& a, const CacheArgs& c, const DecodeArgs& d, int grid, cudaStream_t s) {
     const uint64_t row = 128 * 2;
     const uint32_t box3[3] = {64, (uint32_t)kTile, 1};
@@ -1153,17 +1157,17 @@ cudaError_t launch_mma_t(const LayerArgs& a, const CacheArgs& c, const DecodeArg
     if (!have_f) { mKf = mKr; mVf = mVr; }  // never read: there are no retrieval heads
     if (!have_r) { mKr = mKf; mVr = mVf; }  // never read: there are no streaming heads
     constexpr size_t smem = decode_mma_smem_bytes();
-    auto kern = decode_mma_kernel<G, PAGED>;
+    auto kern = decode_mma_kernel<G, PAGED, CAP>;
     static std::atomic<unsigned long long> configured{0};
     const cudaError_t e = smem_limit_once(kern, (int)smem, configured);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, grid, kMmaThreads, smem, s, mKf, mVf, mKr, mVr, a, c, d);
 }
 
-template <int G>
+template <int G, bool CAP>
 cudaError_t launch_mma_g(const LayerArgs& a, const CacheArgs& c, const DecodeArgs& d, int grid, cudaStream_t s) {
-    if (a.page_size) return launch_mma_t<G, true>(a, c, d, grid, s);
-    return launch_mma_t<G, false>(a, c, d, grid, s);
+    if (a.page_size) return launch_mma_t<G, true, CAP>(a, c, d, grid, s);
+    return launch_mma_t<G, false, CAP>(a, c, d, grid, s);
 }
 
 // Launch with programmatic stream serialization (PDL): the kernel may start
@@ -1184,10 +1188,10 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), int grid, int threads, size_t sme
     return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
-template <typename T, int D, int G, bool PAGED>
+template <typename T, int D, int G, bool PAGED, bool CAP>
 cudaError_t launch_t(const LayerArgs& a, const CacheArgs& c, const DecodeArgs& d, int grid, cudaStream_t s) {
     constexpr size_t smem = decode_smem_bytes<T, D, G>();
-    auto kern = decode_kernel<T, D, G, PAGED>;
+    auto kern = decode_kernel<T, D, G, PAGED, CAP>;
     constexpr int kThreads = (consumer_warps(G) + 1) * 32;
     static std::atomic<unsigned long long> configured{0};
     const cudaError_t e = smem_limit_once(kern, (int)smem, configured);
@@ -1195,19 +1199,19 @@ cudaError_t launch_t(const LayerArgs& a, const CacheArgs& c, const DecodeArgs& d
     return launch_pdl(kern, grid, kThreads, smem, s, a, c, d);
 }
 
-template <typename T, int D, int G>
+template <typename T, int D, int G, bool CAP>
 cudaError_t launch_g(const LayerArgs& a, const CacheArgs& c, const DecodeArgs& d, int grid, cudaStream_t s) {
-    if (a.page_size) return launch_t<T, D, G, true>(a, c, d, grid, s);
-    return launch_t<T, D, G, false>(a, c, d, grid, s);
+    if (a.page_size) return launch_t<T, D, G, true, CAP>(a, c, d, grid, s);
+    return launch_t<T, D, G, false, CAP>(a, c, d, grid, s);
 }
 
-template <typename T, int D>
+template <typename T, int D, bool CAP>
 cudaError_t launch_d(const LayerArgs& a, const CacheArgs& c, const DecodeArgs& d, int grid, cudaStream_t s) {
     switch (a.G) {
-        case 1: return launch_g<T, D, 1>(a, c, d, grid, s);
-        case 2: return launch_g<T, D, 2>(a, c, d, grid, s);
-        case 4: return launch_g<T, D, 4>(a, c, d, grid, s);
-        case 8: return launch_g<T, D, 8>(a, c, d, grid, s);
+        case 1: return launch_g<T, D, 1, CAP>(a, c, d, grid, s);
+        case 2: return launch_g<T, D, 2, CAP>(a, c, d, grid, s);
+        case 4: return launch_g<T, D, 4, CAP>(a, c, d, grid, s);
+        case 8: return launch_g<T, D, 8, CAP>(a, c, d, grid, s);
     }
     return cudaErrorInvalidValue;
 }
@@ -1265,7 +1269,7 @@ __device__ __forceinline__ void mma_f16_rows8_acc(float (&c)[4], uint32_t a0, ui
 constexpr int kRingRowBytes = 272;
 constexpr int kRingMax = 128;        // ring rows this path stages (sink + recent)
 
-template <int G>
+template <int G, bool CAP>
 __device__ __forceinline__ void decode_ring_simt(uint8_t* smem, const LayerArgs& a, const CacheArgs& c,
                                                  const DecodeArgs& d, int b, int slot, int L0, bool fused) {
     using T = __nv_bfloat16;
@@ -1306,7 +1310,8 @@ __device__ __forceinline__ void decode_ring_simt(uint8_t* smem, const LayerArgs&
     const float sl = a.scale * kLog2e;
     for (int i = tid; i < G * D; i += nthr) {
         const int g = i / D, e = i % D;
-        sQ[i] = __bfloat162float(static_cast<const T*>(d.q)[((size_t)b * a.Hq + a.q_head0[slot] + g) * D + e]) * sl;
+        sQ[i] = __bfloat162float(static_cast<const T*>(d.q)[((size_t)b * a.Hq + a.q_head0[slot] + g) * D + e]) *
+                (CAP ? a.cap.k : sl);
     }
     __syncthreads();
     // scores
@@ -1321,7 +1326,7 @@ __device__ __forceinline__ void decode_ring_simt(uint8_t* smem, const LayerArgs&
 #pragma unroll
             for (int e = 0; e < 8; ++e) acc = fmaf(q[piece * 8 + e], kf[e], acc);
         }
-        sS[g * kRingMax + j] = acc;
+        sS[g * kRingMax + j] = CAP ? a.cap.c2 * tanh_sfu(acc) : acc;
     }
     __syncthreads();
     // softmax of each head's scores: p in place, 1 / sum aside
@@ -1372,17 +1377,18 @@ static_assert(ring_simt_smem_bytes(8) <= 2 * (size_t)kQ8Stages * kQ8Bytes + kQ8S
 // there keys at or past n get a score of -inf and a V scale of 0, so that
 // neither a stale score nor a stale scale (whatever the cache holds past the
 // length) reaches the sums.
+template <bool CAP>
 __device__ __forceinline__ void quant_scores(float s0, float s1, float s2, float s3, const float* ksc,
-                                             const float* vsc, int k0, int n, float sl, float (&sv)[4],
-                                             float (&vs)[4]) {
+                                             const float* vsc, int k0, int n, float sl, const CapArgs& cap,
+                                             float (&sv)[4], float (&vs)[4]) {
     const float2 ks0 = *reinterpret_cast<const float2*>(ksc + k0);
     const float2 ks1 = *reinterpret_cast<const float2*>(ksc + k0 + 8);
     const float2 vs0 = *reinterpret_cast<const float2*>(vsc + k0);
     const float2 vs1 = *reinterpret_cast<const float2*>(vsc + k0 + 8);
-    sv[0] = s0 * ks0.x * sl;
-    sv[1] = s1 * ks0.y * sl;
-    sv[2] = s2 * ks1.x * sl;
-    sv[3] = s3 * ks1.y * sl;
+    sv[0] = score_log2<CAP>(s0 * ks0.x, sl, cap);
+    sv[1] = score_log2<CAP>(s1 * ks0.y, sl, cap);
+    sv[2] = score_log2<CAP>(s2 * ks1.x, sl, cap);
+    sv[3] = score_log2<CAP>(s3 * ks1.y, sl, cap);
     vs[0] = vs0.x;
     vs[1] = vs0.y;
     vs[2] = vs1.x;
@@ -1457,7 +1463,7 @@ __device__ __forceinline__ void softmax_exp(const float (&sv)[4], float m_run, f
     l_run += (pr[0] + pr[1]) + (pr[2] + pr[3]);
 }
 
-template <int G>
+template <int G, bool CAP>
 __global__ void __maxnreg__(200)
     decode_q8_kernel(const __grid_constant__ CUtensorMap tmK8, const __grid_constant__ CUtensorMap tmV8,
                      const LayerArgs a, const CacheArgs c, const DecodeArgs d) {
@@ -1519,7 +1525,7 @@ __global__ void __maxnreg__(200)
     const int L0 = *s_flag;
     if (fused && d.grid_ticket && threadIdx.x == 0) length_ticket(a, c, d);
     if (!retrieval) {
-        decode_ring_simt<G>(smem, a, c, d, b, slot, L0, fused);
+        decode_ring_simt<G, CAP>(smem, a, c, d, b, slot, L0, fused);
         return;
     }
     int len = L0;
@@ -1658,8 +1664,8 @@ __global__ void __maxnreg__(200)
                     }
                 }
                 const float* ksc = sSc + st[i] * 2 * kTile;
-                quant_scores(s[0][0] - q_corr, s[0][1] - q_corr, s[1][0] - q_corr, s[1][1] - q_corr, ksc,
-                             ksc + kTile, k0, s_tile_n[st[i]], sl, sv[i], vs[i]);
+                quant_scores<CAP>(s[0][0] - q_corr, s[0][1] - q_corr, s[1][0] - q_corr, s[1][1] - q_corr, ksc,
+                             ksc + kTile, k0, s_tile_n[st[i]], sl, a.cap, sv[i], vs[i]);
             }
             float mx = kNegBig;
 #pragma unroll
@@ -1725,7 +1731,7 @@ __global__ void __maxnreg__(200)
                                                                       true, fused);
 }
 
-template <int G>
+template <int G, bool CAP>
 cudaError_t launch_q8_g(const LayerArgs& a, const CacheArgs& c, const DecodeArgs& d, int grid, cudaStream_t s) {
     CUtensorMap mK{}, mV{};
     {
@@ -1743,7 +1749,7 @@ cudaError_t launch_q8_g(const LayerArgs& a, const CacheArgs& c, const DecodeArgs
             return cudaErrorInvalidValue;
     }
     constexpr size_t smem = decode_q8_smem_bytes();
-    auto kern = decode_q8_kernel<G>;
+    auto kern = decode_q8_kernel<G, CAP>;
     static std::atomic<unsigned long long> configured{0};
     const cudaError_t e = smem_limit_once(kern, (int)smem, configured);
     if (e != cudaSuccess) return e;
@@ -1784,7 +1790,7 @@ constexpr size_t decode_q4_smem_bytes() {
 // slower at 128K, the register cap costing spills.
 static_assert(2 * (decode_q4_smem_bytes<8>() + 1024) <= 232448, "two 4-bit CTAs per SM");
 
-template <int G>
+template <int G, bool CAP>
 __global__ void __maxnreg__(200)
     decode_q4_kernel(const LayerArgs a, const CacheArgs c, const DecodeArgs d) {
     using T = __nv_bfloat16;
@@ -1836,7 +1842,7 @@ __global__ void __maxnreg__(200)
     const int L0 = *s_flag;
     if (fused && d.grid_ticket && threadIdx.x == 0) length_ticket(a, c, d);
     if (!retrieval) {
-        decode_ring_simt<G>(smem, a, c, d, b, slot, L0, fused);
+        decode_ring_simt<G, CAP>(smem, a, c, d, b, slot, L0, fused);
         return;
     }
     int len = L0;
@@ -1997,9 +2003,9 @@ __global__ void __maxnreg__(200)
                     }
                 }
                 const float* ksc = sSc + st[i] * 2 * kTile;
-                quant_scores(s[0][0][0] + s[0][1][0] - q_corr, s[0][0][1] + s[0][1][1] - q_corr,
+                quant_scores<CAP>(s[0][0][0] + s[0][1][0] - q_corr, s[0][0][1] + s[0][1][1] - q_corr,
                              s[1][0][0] + s[1][1][0] - q_corr, s[1][0][1] + s[1][1][1] - q_corr, ksc, ksc + kTile,
-                             k0, s_tile_n[st[i]], sl, sv[i], vs[i]);
+                             k0, s_tile_n[st[i]], sl, a.cap, sv[i], vs[i]);
             }
             float mx = kNegBig;
 #pragma unroll
@@ -2073,20 +2079,22 @@ __global__ void __maxnreg__(200)
                                                                           split, true, fused);
 }
 
-template <int G>
+template <int G, bool CAP>
 cudaError_t launch_q4_g(const LayerArgs& a, const CacheArgs& c, const DecodeArgs& d, int grid, cudaStream_t s) {
     constexpr size_t smem = decode_q4_smem_bytes<G>();
-    auto kern = decode_q4_kernel<G>;
+    auto kern = decode_q4_kernel<G, CAP>;
     static std::atomic<unsigned long long> configured{0};
     const cudaError_t e = smem_limit_once(kern, (int)smem, configured);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, grid, kMmaThreads, smem, s, a, c, d);
 }
 
-}  // namespace
-
-cudaError_t launch_decode(const LayerArgs& a, const CacheArgs& c, const DecodePlan& plan, const void* q, void* out,
-                          void* workspace, cudaStream_t s, const void* k_new, const void* v_new) {
+// CAP: the layer's scores are capped (cap.cuh).  The cap is a few operations
+// per score of kernels that wait for HBM, but the uncapped kernels are
+// instantiations of their own and carry none of it.
+template <bool CAP>
+cudaError_t launch_decode_t(const LayerArgs& a, const CacheArgs& c, const DecodePlan& plan, const void* q, void* out,
+                            void* workspace, cudaStream_t s, const void* k_new, const void* v_new) {
     DecodeArgs d;
     d.k_new = k_new;
     d.v_new = v_new;
@@ -2109,10 +2117,10 @@ cudaError_t launch_decode(const LayerArgs& a, const CacheArgs& c, const DecodePl
     if (a.kv_bits == 4 && a.R > 0) {
         // 4-bit full cache: as the 8-bit path, over nibble codes
         switch (a.G) {
-            case 1: return launch_q4_g<1>(a, c, d, (int)grid, s);
-            case 2: return launch_q4_g<2>(a, c, d, (int)grid, s);
-            case 4: return launch_q4_g<4>(a, c, d, (int)grid, s);
-            case 8: return launch_q4_g<8>(a, c, d, (int)grid, s);
+            case 1: return launch_q4_g<1, CAP>(a, c, d, (int)grid, s);
+            case 2: return launch_q4_g<2, CAP>(a, c, d, (int)grid, s);
+            case 4: return launch_q4_g<4, CAP>(a, c, d, (int)grid, s);
+            case 8: return launch_q4_g<8, CAP>(a, c, d, (int)grid, s);
         }
         return cudaErrorInvalidValue;
     }
@@ -2120,10 +2128,10 @@ cudaError_t launch_decode(const LayerArgs& a, const CacheArgs& c, const DecodePl
         // 8-bit full cache: retrieval CTAs on the int8 tiles, streaming CTAs
         // over the bf16 ring on the CUDA cores, one launch
         switch (a.G) {
-            case 1: return launch_q8_g<1>(a, c, d, (int)grid, s);
-            case 2: return launch_q8_g<2>(a, c, d, (int)grid, s);
-            case 4: return launch_q8_g<4>(a, c, d, (int)grid, s);
-            case 8: return launch_q8_g<8>(a, c, d, (int)grid, s);
+            case 1: return launch_q8_g<1, CAP>(a, c, d, (int)grid, s);
+            case 2: return launch_q8_g<2, CAP>(a, c, d, (int)grid, s);
+            case 4: return launch_q8_g<4, CAP>(a, c, d, (int)grid, s);
+            case 8: return launch_q8_g<8, CAP>(a, c, d, (int)grid, s);
         }
         return cudaErrorInvalidValue;
     }
@@ -2131,17 +2139,25 @@ cudaError_t launch_decode(const LayerArgs& a, const CacheArgs& c, const DecodePl
         if (a.D == 128) {
             // bf16, head_dim 128: the tensor-core consumer
             switch (a.G) {
-                case 1: return launch_mma_g<1>(a, c, d, (int)grid, s);
-                case 2: return launch_mma_g<2>(a, c, d, (int)grid, s);
-                case 4: return launch_mma_g<4>(a, c, d, (int)grid, s);
-                case 8: return launch_mma_g<8>(a, c, d, (int)grid, s);
+                case 1: return launch_mma_g<1, CAP>(a, c, d, (int)grid, s);
+                case 2: return launch_mma_g<2, CAP>(a, c, d, (int)grid, s);
+                case 4: return launch_mma_g<4, CAP>(a, c, d, (int)grid, s);
+                case 8: return launch_mma_g<8, CAP>(a, c, d, (int)grid, s);
             }
             return cudaErrorInvalidValue;
         }
-        return launch_d<__nv_bfloat16, 64>(a, c, d, (int)grid, s);
+        return launch_d<__nv_bfloat16, 64, CAP>(a, c, d, (int)grid, s);
     }
-    if (a.D == 128) return launch_d<float, 128>(a, c, d, (int)grid, s);
-    return launch_d<float, 64>(a, c, d, (int)grid, s);
+    if (a.D == 128) return launch_d<float, 128, CAP>(a, c, d, (int)grid, s);
+    return launch_d<float, 64, CAP>(a, c, d, (int)grid, s);
+}
+
+}  // namespace
+
+cudaError_t launch_decode(const LayerArgs& a, const CacheArgs& c, const DecodePlan& plan, const void* q, void* out,
+                          void* workspace, cudaStream_t s, const void* k_new, const void* v_new) {
+    return a.cap.on ? launch_decode_t<true>(a, c, plan, q, out, workspace, s, k_new, v_new)
+                    : launch_decode_t<false>(a, c, plan, q, out, workspace, s, k_new, v_new);
 }
 
 }  // namespace duo

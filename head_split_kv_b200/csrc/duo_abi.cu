@@ -97,6 +97,7 @@ void fill_args(const duo_layer_desc* d, duo::LayerArgs& a) {
     a.kv_bits = d->kv_quant == DUO_KV_INT8 ? 8 : d->kv_quant == DUO_KV_INT4 ? 4 : 0;
     a.page_size = d->page_size;
     a.capacity = a.max_pages = a.n_pages = 0;
+    a.cap = duo::CapArgs{0, 0.f, 0.f};
     a.scale = d->scale > 0.f ? d->scale : 1.0f / std::sqrt(static_cast<float>(d->head_dim));
     for (int i = 0; i < DUO_MAX_KV_HEADS; ++i) {
         a.q_head0[i] = 0;
@@ -191,6 +192,162 @@ DecodePlan decode_plan(const LayerArgs& a) {
     return p;
 }
 }  // namespace duo
+
+// ===========================================================================
+// The attention calls, with and without a score cap (cap 0: none).
+// ===========================================================================
+namespace {
+
+duo_status set_cap(duo::LayerArgs& a, float cap) {
+    if (!std::isfinite(cap) || cap < 0.f)
+        return fail(DUO_ERR_INVALID_ARG, "cap must be finite and >= 0 (0: scores are not capped), got %g", (double)cap);
+    if (cap > 0.f) {
+        a.cap.on = 1;
+        a.cap.k = a.scale / cap;
+        a.cap.c2 = cap * 1.4426950408889634f;
+        // the kernels raise scale / cap to the 8th power and cap * log2(e) stays fp32
+        if (!(a.cap.k <= 1e4f) || !std::isfinite(a.cap.c2))
+            return fail(DUO_ERR_INVALID_ARG, "cap %g is out of range (from softmax scale / 1e4 to 2e38)", (double)cap);
+    }
+    return DUO_OK;
+}
+
+duo_status decode_attn_call(const duo_layer_desc* desc, const duo_kv_state* st, float cap, const void* q, void* out,
+                            void* workspace, size_t ws_bytes, duo_stream_t stream, const char* name) {
+    duo_status s = check_desc(desc);
+    if (s != DUO_OK) return s;
+    duo::LayerArgs a;
+    duo::CacheArgs c;
+    fill_args(desc, a);
+    if ((s = set_cap(a, cap)) != DUO_OK) return s;
+    if ((s = check_state(desc, st, a, c)) != DUO_OK) return s;
+    if (!q || !out) return fail(DUO_ERR_INVALID_ARG, "q / out is NULL");
+    if (!aligned16(q) || !aligned16(out)) return fail(DUO_ERR_INVALID_ARG, "q / out not 16-byte aligned");
+    const duo::DecodePlan plan = duo::decode_plan(a);
+    if (!workspace) return fail(DUO_ERR_INVALID_ARG, "workspace is NULL");
+    if (!aligned16(workspace)) return fail(DUO_ERR_INVALID_ARG, "workspace not 16-byte aligned");
+    if (ws_bytes < plan.bytes)
+        return fail(DUO_ERR_CAPACITY, "workspace holds %zu bytes, decode needs %zu", ws_bytes, plan.bytes);
+    const cudaError_t e = duo::launch_decode(a, c, plan, q, out, workspace, (cudaStream_t)stream);
+    return e == cudaSuccess ? ok() : cuda_fail(e, name);
+}
+
+duo_status decode_step_call(const duo_layer_desc* desc, const duo_kv_state* st, float cap, const void* q,
+                            const void* k_new, const void* v_new, void* out, void* workspace, size_t ws_bytes,
+                            duo_stream_t stream, const char* name) {
+    duo_status s = check_desc(desc);
+    if (s != DUO_OK) return s;
+    duo::LayerArgs a;
+    duo::CacheArgs c;
+    fill_args(desc, a);
+    if ((s = set_cap(a, cap)) != DUO_OK) return s;
+    if ((s = check_state(desc, st, a, c)) != DUO_OK) return s;
+    if (!q || !out || !k_new || !v_new) return fail(DUO_ERR_INVALID_ARG, "q / k_new / v_new / out is NULL");
+    if (!aligned16(q) || !aligned16(out) || !aligned16(k_new) || !aligned16(v_new))
+        return fail(DUO_ERR_INVALID_ARG, "q / k_new / v_new / out not 16-byte aligned");
+    const duo::DecodePlan plan = duo::decode_plan(a);
+    if (!workspace) return fail(DUO_ERR_INVALID_ARG, "workspace is NULL");
+    if (!aligned16(workspace)) return fail(DUO_ERR_INVALID_ARG, "workspace not 16-byte aligned");
+    if (ws_bytes < plan.bytes)
+        return fail(DUO_ERR_CAPACITY, "workspace holds %zu bytes, decode needs %zu", ws_bytes, plan.bytes);
+    const cudaError_t e = duo::launch_decode(a, c, plan, q, out, workspace, (cudaStream_t)stream, k_new, v_new);
+    return e == cudaSuccess ? ok() : cuda_fail(e, name);
+}
+
+duo_status prefill_chunk_call(const duo_layer_desc* desc, const duo_kv_state* st, float cap, const void* q,
+                              const void* k_chunk, const void* v_chunk, int32_t C, void* out, void* workspace,
+                              size_t ws_bytes, duo_stream_t stream, const char* name) {
+    duo_status s = check_desc(desc);
+    if (s != DUO_OK) return s;
+    duo::LayerArgs a;
+    duo::CacheArgs c;
+    fill_args(desc, a);
+    if ((s = set_cap(a, cap)) != DUO_OK) return s;
+    if ((s = check_state(desc, st, a, c)) != DUO_OK) return s;
+    if (C < 1) return fail(DUO_ERR_SHAPE, "chunk length must be >= 1 (got %d)", C);
+    if (!q || !k_chunk || !v_chunk || !out) return fail(DUO_ERR_INVALID_ARG, "q / k_chunk / v_chunk / out is NULL");
+    if (!aligned16(q) || !aligned16(k_chunk) || !aligned16(v_chunk) || !aligned16(out))
+        return fail(DUO_ERR_INVALID_ARG, "pre-fill tensors must be 16-byte aligned");
+    if (desc->page_size != 0)
+        return fail(DUO_ERR_UNSUPPORTED, "%s takes a contiguous full cache (page_size 0)", name);
+    cudaError_t e;
+    if (a.kv_bits && a.R > 0) {
+        // an 8- or 4-bit full cache: its rows below seq_len are staged in
+        // the workspace -- K codes as bf16, V codes x16 as fp16, each row's scales --
+        // and the tensor-core pre-fill reads the codes as its cache and
+        // applies the scales to the scores and to p; the rest of the
+        // workspace serves the key-range splits
+        const size_t staging = (duo::dequant_staging_bytes(a) + 255) / 256 * 256;
+        if (!workspace || ws_bytes < staging)
+            return fail(DUO_ERR_CAPACITY,
+                        "an 8- or 4-bit layer's pre-fill needs a workspace of duo_prefill_workspace_bytes (at least "
+                        "%zu bytes; given %zu)", staging, workspace ? ws_bytes : (size_t)0);
+        if (!aligned16(workspace)) return fail(DUO_ERR_INVALID_ARG, "workspace not 16-byte aligned");
+        duo::LayerArgs ap = a;
+        ap.kv_bits = 0;
+        if (!duo::prefill_tc_supported(ap))
+            return fail(DUO_ERR_UNSUPPORTED, "tensor-core pre-fill cannot take this layer");
+        e = duo::launch_dequant(a, c, workspace, (cudaStream_t)stream);
+        if (e == cudaSuccess) {
+            const size_t code_bytes = (size_t)a.B * a.R * a.capacity * 128 * 2;   // one of K, V
+            duo::CacheArgs cp = c;
+            cp.k_full = workspace;
+            cp.v_full = static_cast<uint8_t*>(workspace) + code_bytes;
+            cp.k_scale = cp.v_scale = nullptr;
+            const float* qscale = reinterpret_cast<const float*>(static_cast<uint8_t*>(workspace) + 2 * code_bytes);
+            e = duo::launch_prefill_tc(ap, cp, q, k_chunk, v_chunk, C, out, static_cast<uint8_t*>(workspace) + staging,
+                                       ws_bytes - staging, (cudaStream_t)stream, nullptr, qscale);
+        }
+    } else if (a.dtype == DUO_BF16 && a.D == 128) {
+        if (!duo::prefill_tc_supported(a))
+            return fail(DUO_ERR_UNSUPPORTED, "tensor-core pre-fill cannot take this layer");
+        e = duo::launch_prefill_tc(a, c, q, k_chunk, v_chunk, C, out, workspace, ws_bytes, (cudaStream_t)stream);
+    } else {
+        e = duo::launch_simt_attention(a, &c, nullptr, q, k_chunk, v_chunk, C, out, 0, (cudaStream_t)stream);
+    }
+    return e == cudaSuccess ? ok() : cuda_fail(e, name);
+}
+
+duo_status rope_args(const duo_layer_desc* desc, const duo_rope* rope, int inverse, duo::RopeArgs& r) {
+    if (!rope) return fail(DUO_ERR_INVALID_ARG, "rope is NULL");
+    if (!rope->inv_freq) return fail(DUO_ERR_INVALID_ARG, "rope.inv_freq is NULL");
+    if (((uintptr_t)rope->inv_freq & 3u) || ((uintptr_t)rope->pos & 3u))
+        return fail(DUO_ERR_INVALID_ARG, "rope.inv_freq / rope.pos not 4-byte aligned");
+    if (rope->rot_dim < 2 || rope->rot_dim % 2 || rope->rot_dim > desc->head_dim)
+        return fail(DUO_ERR_SHAPE, "rope.rot_dim must be even and in 2..head_dim (got %d, head_dim %d)", rope->rot_dim,
+                    desc->head_dim);
+    if (rope->layout != DUO_ROPE_HALVES && rope->layout != DUO_ROPE_PAIRS)
+        return fail(DUO_ERR_INVALID_ARG, "unknown rope.layout %d", rope->layout);
+    if (rope->n_axes < 1 || rope->n_axes > DUO_ROPE_MAX_AXES)
+        return fail(DUO_ERR_SHAPE, "rope.n_axes must be in 1..%d (got %d)", DUO_ROPE_MAX_AXES, rope->n_axes);
+    if (rope->n_axes > 1 && !rope->pos)
+        return fail(DUO_ERR_INVALID_ARG, "rope.pos is required with several axes");
+    int64_t pairs = 0;
+    r.section_end[0] = r.section_end[1] = 0x7fffffff;
+    for (int i = 0; i < rope->n_axes; ++i) {
+        if (rope->sections[i] < 0) return fail(DUO_ERR_SHAPE, "rope.sections[%d] is negative", i);
+        pairs += rope->sections[i];
+        if (i + 1 < rope->n_axes) r.section_end[i] = (int)(pairs < 0x7fffffff ? pairs : 0x7fffffff);
+    }
+    if (pairs != rope->rot_dim / 2)
+        return fail(DUO_ERR_SHAPE, "rope.sections must add up to rot_dim / 2 = %d pairs (got %lld)", rope->rot_dim / 2,
+                    (long long)pairs);
+    if (!std::isfinite(rope->factor)) return fail(DUO_ERR_INVALID_ARG, "rope.factor is not finite");
+    r.rot_dim = rope->rot_dim;
+    r.layout = rope->layout;
+    r.inverse = inverse;
+    r.factor = rope->factor;
+    r.inv_freq = rope->inv_freq;
+    r.pos = rope->pos;
+    return DUO_OK;
+}
+
+bool overlap(const void* x, size_t nx, const void* y, size_t ny) {
+    const uintptr_t a = (uintptr_t)x, b = (uintptr_t)y;
+    return a < b + ny && b < a + nx;
+}
+
+}  // namespace
 
 // ===========================================================================
 // extern "C"
@@ -343,96 +500,91 @@ duo_status duo_append_kv(const duo_layer_desc* desc, const duo_kv_state* st, con
     return e == cudaSuccess ? ok() : cuda_fail(e, "duo_append_kv");
 }
 
-duo_status duo_decode_attn(const duo_layer_desc* desc, const duo_kv_state* st, const void* q, void* out,
-                           void* workspace, size_t ws_bytes, duo_stream_t stream) {
+duo_status duo_rope_qk(const duo_layer_desc* desc, const duo_rope* rope, const int32_t* seq_len, const void* q,
+                       const void* k, void* q_out, void* k_out, int32_t T, int32_t inverse, duo_stream_t stream) {
+    duo_status s = check_desc(desc);
+    if (s != DUO_OK) return s;
+    duo::RopeArgs r;
+    if ((s = rope_args(desc, rope, inverse != 0, r)) != DUO_OK) return s;
+    if (T < 0) return fail(DUO_ERR_SHAPE, "T must be >= 0 (got %d)", T);
+    if ((q == nullptr) != (q_out == nullptr) || (k == nullptr) != (k_out == nullptr))
+        return fail(DUO_ERR_INVALID_ARG, "duo_rope_qk: q and q_out (k and k_out) are given together");
+    if (!q && !k) return fail(DUO_ERR_INVALID_ARG, "duo_rope_qk: neither q nor k is given");
+    if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out))
+        return fail(DUO_ERR_INVALID_ARG, "duo_rope_qk tensors must be 16-byte aligned");
+    if (T == 0) return ok();
+    const size_t row = (size_t)desc->head_dim * (desc->dtype == DUO_BF16 ? 2 : 4);
+    const size_t nq = q ? (size_t)desc->batch * T * desc->n_q_heads * row : 0;
+    const size_t nk = k ? (size_t)desc->batch * T * desc->n_kv_heads * row : 0;
+    if ((q != q_out && overlap(q, nq, q_out, nq)) || (k != k_out && overlap(k, nk, k_out, nk)) ||
+        overlap(q_out, nq, k, nk) || overlap(k_out, nk, q, nq) || overlap(q_out, nq, k_out, nk))
+        return fail(DUO_ERR_INVALID_ARG, "duo_rope_qk: an output overlaps another tensor (it may only be its input itself)");
+    duo::LayerArgs a;
+    fill_args(desc, a);
+    const cudaError_t e = duo::launch_rope(a, seq_len, r, q, k, q_out, k_out, T, (cudaStream_t)stream);
+    return e == cudaSuccess ? ok() : cuda_fail(e, "duo_rope_qk");
+}
+
+duo_status duo_append_kv_rope(const duo_layer_desc* desc, const duo_kv_state* st, const duo_rope* rope, const void* q,
+                              const void* k_new, const void* v_new, void* q_out, int32_t T, duo_stream_t stream) {
     duo_status s = check_desc(desc);
     if (s != DUO_OK) return s;
     duo::LayerArgs a;
     duo::CacheArgs c;
     fill_args(desc, a);
     if ((s = check_state(desc, st, a, c)) != DUO_OK) return s;
-    if (!q || !out) return fail(DUO_ERR_INVALID_ARG, "q / out is NULL");
-    if (!aligned16(q) || !aligned16(out)) return fail(DUO_ERR_INVALID_ARG, "q / out not 16-byte aligned");
-    const duo::DecodePlan plan = duo::decode_plan(a);
-    if (!workspace) return fail(DUO_ERR_INVALID_ARG, "workspace is NULL");
-    if (!aligned16(workspace)) return fail(DUO_ERR_INVALID_ARG, "workspace not 16-byte aligned");
-    if (ws_bytes < plan.bytes)
-        return fail(DUO_ERR_CAPACITY, "workspace holds %zu bytes, decode needs %zu", ws_bytes, plan.bytes);
-    const cudaError_t e = duo::launch_decode(a, c, plan, q, out, workspace, (cudaStream_t)stream);
-    return e == cudaSuccess ? ok() : cuda_fail(e, "duo_decode_attn");
+    duo::RopeArgs r;
+    if ((s = rope_args(desc, rope, 0, r)) != DUO_OK) return s;
+    if (T < 0) return fail(DUO_ERR_SHAPE, "T must be >= 0 (got %d)", T);
+    if (T == 0) return ok();
+    if (!k_new || !v_new) return fail(DUO_ERR_INVALID_ARG, "k_new / v_new is NULL");
+    if ((q == nullptr) != (q_out == nullptr))
+        return fail(DUO_ERR_INVALID_ARG, "duo_append_kv_rope: q and q_out are given together");
+    if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(q) || !aligned16(q_out))
+        return fail(DUO_ERR_INVALID_ARG, "duo_append_kv_rope tensors must be 16-byte aligned");
+    const size_t row = (size_t)desc->head_dim * (desc->dtype == DUO_BF16 ? 2 : 4);
+    const size_t nq = q ? (size_t)desc->batch * T * desc->n_q_heads * row : 0;
+    const size_t nk = (size_t)desc->batch * T * desc->n_kv_heads * row;
+    if ((q != q_out && overlap(q, nq, q_out, nq)) || overlap(q_out, nq, k_new, nk) || overlap(q_out, nq, v_new, nk))
+        return fail(DUO_ERR_INVALID_ARG, "duo_append_kv_rope: q_out overlaps another tensor (it may only be q itself)");
+    const cudaError_t e = duo::launch_append_rope(a, c, r, q, k_new, v_new, q_out, T, (cudaStream_t)stream);
+    return e == cudaSuccess ? ok() : cuda_fail(e, "duo_append_kv_rope");
+}
+
+duo_status duo_decode_attn(const duo_layer_desc* desc, const duo_kv_state* st, const void* q, void* out,
+                           void* workspace, size_t ws_bytes, duo_stream_t stream) {
+    return decode_attn_call(desc, st, 0.f, q, out, workspace, ws_bytes, stream, "duo_decode_attn");
+}
+
+duo_status duo_decode_attn_capped(const duo_layer_desc* desc, const duo_kv_state* st, float cap, const void* q,
+                                  void* out, void* workspace, size_t ws_bytes, duo_stream_t stream) {
+    return decode_attn_call(desc, st, cap, q, out, workspace, ws_bytes, stream, "duo_decode_attn_capped");
 }
 
 duo_status duo_decode_step(const duo_layer_desc* desc, const duo_kv_state* st, const void* q, const void* k_new,
                            const void* v_new, void* out, void* workspace, size_t ws_bytes, duo_stream_t stream) {
-    duo_status s = check_desc(desc);
-    if (s != DUO_OK) return s;
-    duo::LayerArgs a;
-    duo::CacheArgs c;
-    fill_args(desc, a);
-    if ((s = check_state(desc, st, a, c)) != DUO_OK) return s;
-    if (!q || !out || !k_new || !v_new) return fail(DUO_ERR_INVALID_ARG, "q / k_new / v_new / out is NULL");
-    if (!aligned16(q) || !aligned16(out) || !aligned16(k_new) || !aligned16(v_new))
-        return fail(DUO_ERR_INVALID_ARG, "q / k_new / v_new / out not 16-byte aligned");
-    const duo::DecodePlan plan = duo::decode_plan(a);
-    if (!workspace) return fail(DUO_ERR_INVALID_ARG, "workspace is NULL");
-    if (!aligned16(workspace)) return fail(DUO_ERR_INVALID_ARG, "workspace not 16-byte aligned");
-    if (ws_bytes < plan.bytes)
-        return fail(DUO_ERR_CAPACITY, "workspace holds %zu bytes, decode needs %zu", ws_bytes, plan.bytes);
-    const cudaError_t e = duo::launch_decode(a, c, plan, q, out, workspace, (cudaStream_t)stream, k_new, v_new);
-    return e == cudaSuccess ? ok() : cuda_fail(e, "duo_decode_step");
+    return decode_step_call(desc, st, 0.f, q, k_new, v_new, out, workspace, ws_bytes, stream, "duo_decode_step");
+}
+
+duo_status duo_decode_step_capped(const duo_layer_desc* desc, const duo_kv_state* st, float cap, const void* q,
+                                  const void* k_new, const void* v_new, void* out, void* workspace, size_t ws_bytes,
+                                  duo_stream_t stream) {
+    return decode_step_call(desc, st, cap, q, k_new, v_new, out, workspace, ws_bytes, stream,
+                            "duo_decode_step_capped");
 }
 
 duo_status duo_prefill_chunk(const duo_layer_desc* desc, const duo_kv_state* st, const void* q, const void* k_chunk,
                              const void* v_chunk, int32_t C, void* out, void* workspace, size_t ws_bytes,
                              duo_stream_t stream) {
-    duo_status s = check_desc(desc);
-    if (s != DUO_OK) return s;
-    duo::LayerArgs a;
-    duo::CacheArgs c;
-    fill_args(desc, a);
-    if ((s = check_state(desc, st, a, c)) != DUO_OK) return s;
-    if (C < 1) return fail(DUO_ERR_SHAPE, "chunk length must be >= 1 (got %d)", C);
-    if (!q || !k_chunk || !v_chunk || !out) return fail(DUO_ERR_INVALID_ARG, "q / k_chunk / v_chunk / out is NULL");
-    if (!aligned16(q) || !aligned16(k_chunk) || !aligned16(v_chunk) || !aligned16(out))
-        return fail(DUO_ERR_INVALID_ARG, "pre-fill tensors must be 16-byte aligned");
-    if (desc->page_size != 0)
-        return fail(DUO_ERR_UNSUPPORTED, "duo_prefill_chunk takes a contiguous full cache (page_size 0)");
-    cudaError_t e;
-    if (a.kv_bits && a.R > 0) {
-        // an 8- or 4-bit full cache: its rows below seq_len are staged in
-        // the workspace -- K codes as bf16, V codes x16 as fp16, each row's scales --
-        // and the tensor-core pre-fill reads the codes as its cache and
-        // applies the scales to the scores and to p; the rest of the
-        // workspace serves the key-range splits
-        const size_t staging = (duo::dequant_staging_bytes(a) + 255) / 256 * 256;
-        if (!workspace || ws_bytes < staging)
-            return fail(DUO_ERR_CAPACITY,
-                        "an 8- or 4-bit layer's pre-fill needs a workspace of duo_prefill_workspace_bytes (at least "
-                        "%zu bytes; given %zu)", staging, workspace ? ws_bytes : (size_t)0);
-        if (!aligned16(workspace)) return fail(DUO_ERR_INVALID_ARG, "workspace not 16-byte aligned");
-        duo::LayerArgs ap = a;
-        ap.kv_bits = 0;
-        if (!duo::prefill_tc_supported(ap))
-            return fail(DUO_ERR_UNSUPPORTED, "tensor-core pre-fill cannot take this layer");
-        e = duo::launch_dequant(a, c, workspace, (cudaStream_t)stream);
-        if (e == cudaSuccess) {
-            const size_t code_bytes = (size_t)a.B * a.R * a.capacity * 128 * 2;   // one of K, V
-            duo::CacheArgs cp = c;
-            cp.k_full = workspace;
-            cp.v_full = static_cast<uint8_t*>(workspace) + code_bytes;
-            cp.k_scale = cp.v_scale = nullptr;
-            const float* qscale = reinterpret_cast<const float*>(static_cast<uint8_t*>(workspace) + 2 * code_bytes);
-            e = duo::launch_prefill_tc(ap, cp, q, k_chunk, v_chunk, C, out, static_cast<uint8_t*>(workspace) + staging,
-                                       ws_bytes - staging, (cudaStream_t)stream, nullptr, qscale);
-        }
-    } else if (a.dtype == DUO_BF16 && a.D == 128) {
-        if (!duo::prefill_tc_supported(a))
-            return fail(DUO_ERR_UNSUPPORTED, "tensor-core pre-fill cannot take this layer");
-        e = duo::launch_prefill_tc(a, c, q, k_chunk, v_chunk, C, out, workspace, ws_bytes, (cudaStream_t)stream);
-    } else {
-        e = duo::launch_simt_attention(a, &c, nullptr, q, k_chunk, v_chunk, C, out, 0, (cudaStream_t)stream);
-    }
-    return e == cudaSuccess ? ok() : cuda_fail(e, "duo_prefill_chunk");
+    return prefill_chunk_call(desc, st, 0.f, q, k_chunk, v_chunk, C, out, workspace, ws_bytes, stream,
+                              "duo_prefill_chunk");
+}
+
+duo_status duo_prefill_chunk_capped(const duo_layer_desc* desc, const duo_kv_state* st, float cap, const void* q,
+                                    const void* k_chunk, const void* v_chunk, int32_t C, void* out, void* workspace,
+                                    size_t ws_bytes, duo_stream_t stream) {
+    return prefill_chunk_call(desc, st, cap, q, k_chunk, v_chunk, C, out, workspace, ws_bytes, stream,
+                              "duo_prefill_chunk_capped");
 }
 
 duo_status duo_gated_mix(const duo_layer_desc* desc, const float* alpha, const void* q, const void* k, const void* v,
@@ -482,7 +634,9 @@ duo_status duo_gated_mix(const duo_layer_desc* desc, const float* alpha, const v
     if (duo::prefill_tc_supported(as) && duo::prefill_tc_supported(ac)) {
         duo::CacheArgs none{};   // no lengths, no caches: every sequence starts at position 0
         none.status = status;    // device conditions (a wait that ran out) are reported here
-        const duo::EpiArgs mix{duo::EPI_MIX, alpha, nullptr, nullptr, 0.f};
+        duo::EpiArgs mix;
+        mix.mode = duo::EPI_MIX;
+        mix.alpha = alpha;
         cudaError_t e = duo::launch_prefill_tc(as, none, q, k, v, N, out, nullptr, 0, (cudaStream_t)stream);
         if (e == cudaSuccess)
             e = duo::launch_prefill_tc(ac, none, q, k, v, N, out, nullptr, 0, (cudaStream_t)stream, &mix);
@@ -530,8 +684,13 @@ duo_status duo_gated_mix_grad_alpha(const duo_layer_desc* desc, const void* q, c
     if (duo::prefill_tc_supported(as) && duo::prefill_tc_supported(ac)) {
         duo::CacheArgs none{};
         none.status = status;
-        const duo::EpiArgs minus{duo::EPI_DOT, nullptr, dout, dalpha, -1.f};
-        const duo::EpiArgs plus{duo::EPI_DOT, nullptr, dout, dalpha, 1.f};
+        duo::EpiArgs minus;
+        minus.mode = duo::EPI_DOT;
+        minus.dout = dout;
+        minus.dalpha = dalpha;
+        minus.sign = -1.f;
+        duo::EpiArgs plus = minus;
+        plus.sign = 1.f;
         e = duo::launch_prefill_tc(as, none, q, k, v, N, nullptr, nullptr, 0, (cudaStream_t)stream, &minus);
         if (e == cudaSuccess)
             e = duo::launch_prefill_tc(ac, none, q, k, v, N, nullptr, nullptr, 0, (cudaStream_t)stream, &plus);

@@ -28,6 +28,14 @@ inline cudaError_t smem_limit_once(K* kernel, int bytes, std::atomic<unsigned lo
     return e;
 }
 
+// Capped scores (cap.cuh): the log2-domain score of a dot product x is
+// c2 * tanh(x * k); on is 0 where the layer's scores are not capped.
+struct CapArgs {
+    int on;
+    float k;    // softmax scale / cap
+    float c2;   // cap * log2(e)
+};
+
 // Flattened, validated view of a layer descriptor plus state, passed by
 // value to every kernel.
 struct LayerArgs {
@@ -36,6 +44,7 @@ struct LayerArgs {
     int stream_chunk;  // pre-fill: streaming heads see the whole chunk (DUO_STREAM_CHUNK)
     int kv_bits;       // the full cache holds 8- or 4-bit codes + scales (DUO_KV_INT8 / DUO_KV_INT4); 0: plain
     float scale;       // softmax scale
+    CapArgs cap;       // score cap of this call
     // For block slot i (0..Hkv-1): index of its first query head and of its
     // KV head in the caller's q / k / v / out tensors (model or block order).
     int q_head0[DUO_MAX_KV_HEADS];
@@ -93,18 +102,24 @@ int sm_count();
 PrefillPlan prefill_plan(const LayerArgs& a, int C, int n_sms);
 size_t prefill_workspace_bytes(const LayerArgs& a, int max_chunk);
 // Epilogues of the tensor-core attention kernel: the pre-fill's store, and
-// the gated mix's two (no key-range splits):
+// the gated mix's (no key-range splits):
 //   EPI_MIX: out is read back as the streaming attention and overwritten
 //            with alpha[kv] * result + (1 - alpha[kv]) * out;
 //   EPI_DOT: nothing is stored; sign * <dout row, result row> summed over
-//            the rows is added into dalpha[kv] (atomics).
-enum { EPI_STORE = 0, EPI_MIX = 1, EPI_DOT = 2 };
+//            the rows is added into dalpha[kv] (atomics);
+//   EPI_KEEP: the result is stored to out and each row's lse kept;
+//   EPI_MIX_KEEP: as EPI_MIX, with the streaming attention read from
+//            `streaming`, and the result itself and its lse kept too.
+enum { EPI_STORE = 0, EPI_MIX = 1, EPI_DOT = 2, EPI_KEEP = 3, EPI_MIX_KEEP = 4 };
 struct EpiArgs {
-    int mode;
-    const float* alpha;   // EPI_MIX: [Hkv] gates
-    const void* dout;     // EPI_DOT: [B][C][Hq][d] bf16
-    float* dalpha;        // EPI_DOT: [Hkv] accumulated
-    float sign;           // EPI_DOT: +1 or -1
+    int mode = EPI_STORE;
+    const float* alpha = nullptr;      // EPI_MIX, EPI_MIX_KEEP: [Hkv] gates
+    const void* dout = nullptr;        // EPI_DOT: [B][C][Hq][d] bf16
+    float* dalpha = nullptr;           // EPI_DOT: [Hkv] accumulated
+    float sign = 0.f;                  // EPI_DOT: +1 or -1
+    const void* streaming = nullptr;   // EPI_MIX_KEEP: [B][C][Hq][d]
+    void* causal = nullptr;            // EPI_MIX_KEEP: [B][C][Hq][d], the result before the mix
+    float* lse = nullptr;              // EPI_KEEP, EPI_MIX_KEEP: [B][Hq][C], log2 of the sum of 2^score
 };
 // qscale non-NULL: the full cache holds 8- or 4-bit codes (as bf16 values)
 // and qscale [B][R][capacity][4] fp32 the (k scale, v scale, -, -) of each
@@ -131,6 +146,21 @@ bool encode_tmap_bf16(CUtensorMap* map, const void* base, int rank, const uint64
 // Any element type (a CUtensorMapDataType) and a 32/64/128-byte swizzle (0: none).
 bool encode_tmap(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes,
                  const uint32_t* box, int dtype, int swizzle_bytes);
+
+// A validated duo_rope (rope.cu).
+struct RopeArgs {
+    int rot_dim, layout;
+    int section_end[2];     // pair index at which the second and third axes begin
+    int inverse;            // rotate by the negative angle (the gradient)
+    float factor;
+    const float* inv_freq;  // [rot_dim / 2]
+    const int32_t* pos;     // [axes][B][T], or NULL: seq_len[b] + t
+};
+// q or k may be NULL (not rotated); seq_len may be NULL (0).
+cudaError_t launch_rope(const LayerArgs& a, const int32_t* seq_len, const RopeArgs& r, const void* q, const void* k,
+                        void* q_out, void* k_out, int T, cudaStream_t s);
+cudaError_t launch_append_rope(const LayerArgs& a, const CacheArgs& c, const RopeArgs& r, const void* q,
+                               const void* k_new, const void* v_new, void* q_out, int T, cudaStream_t s);
 
 cudaError_t launch_permute(const void* x, void* y, int64_t rows, int hkv, const int* perm, int heads_per_kv,
                            int64_t head_elems, int elem_bytes, int direction, cudaStream_t s);

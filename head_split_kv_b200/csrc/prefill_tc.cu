@@ -51,6 +51,7 @@
 // behind them.
 #include <cuda.h>
 
+#include "cap.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "tcgen05.cuh"
@@ -307,8 +308,14 @@ __device__ __forceinline__ float2 exp2_fma2(float2 x) {
 // 2^-11 of the value.  p <= 2^8 (the lazy rescale) keeps p v_scale / 16
 // within fp16 for v scales up to 4095.  Other tiles: P in bf16, the row sum
 // of the rounded P.
-__device__ __forceinline__ float softmax_tile(uint32_t s_addr, float sl, bool masked, const uint32_t (&vis)[4],
-                                              float& m_ref, float& l_sum, bool& need, const float* qsc) {
+//
+// CAP (cap.cuh): the scores become c2 * tanh(k * s) in place, in the log2
+// domain already, before the mask: on the FMA pipe when every |k * s| of the
+// warp's part of the tile is at most 1 (a vote), else on the SFU.
+template <bool CAP>
+__device__ __forceinline__ float softmax_tile(uint32_t s_addr, float sl, const CapArgs& cap, bool masked,
+                                              const uint32_t (&vis)[4], float& m_ref, float& l_sum, bool& need,
+                                              const float* qsc) {
     float s[128];
     tmem_ld128(s_addr, s);
     if (qsc) {
@@ -322,6 +329,33 @@ __device__ __forceinline__ float softmax_tile(uint32_t s_addr, float sl, bool ma
             s[4 * i + 1] = a.y;
             s[4 * i + 2] = b.x;
             s[4 * i + 3] = b.y;
+        }
+    }
+    if constexpr (CAP) {
+        float lo[4] = {s[0], s[1], s[2], s[3]}, hi[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int c = 4; c < 124; c += 8) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                hi[i] = fmax3(hi[i], s[c + i], s[c + 4 + i]);
+                lo[i] = fmin3(lo[i], s[c + i], s[c + 4 + i]);
+            }
+        }
+        float big = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            big = fmax3(big, fmaxf(hi[i], s[124 + i]), -fminf(lo[i], s[124 + i]));
+        if (__all_sync(0xffffffffu, big * cap.k <= 1.f)) {
+            const CapPoly cp = cap_poly(cap);
+#pragma unroll
+            for (int c = 0; c < 128; c += 2) {
+                const float2 t = cap_fma2(make_float2(s[c], s[c + 1]), cp);
+                s[c] = t.x;
+                s[c + 1] = t.y;
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < 128; ++c) s[c] = cap.c2 * tanh_sfu(s[c] * cap.k);
         }
     }
     if (masked) {
@@ -339,7 +373,7 @@ __device__ __forceinline__ float softmax_tile(uint32_t s_addr, float sl, bool ma
 #pragma unroll
     for (int i = 0; i < 4; ++i) m4[i] = fmaxf(m4[i], s[124 + i]);
     // into the log2 domain: the scale is positive, so it commutes with max
-    const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl;
+    const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * (CAP ? 1.f : sl);
     const float m_new = fmaxf(m_ref, mx);
     need = m_new > m_ref + 8.f;                           // lazy rescale threshold: 2^8
     const float m_use = need ? m_new : m_ref;
@@ -352,7 +386,8 @@ __device__ __forceinline__ float softmax_tile(uint32_t s_addr, float sl, bool ma
         uint32_t pk[32];
 #pragma unroll
         for (int c2 = 0; c2 < 32; ++c2) {
-            const float2 x = ffma2(make_float2(s[64 * h + 2 * c2], s[64 * h + 2 * c2 + 1]), sl2, nm2);
+            const float2 sv = make_float2(s[64 * h + 2 * c2], s[64 * h + 2 * c2 + 1]);
+            const float2 x = CAP ? fadd2(sv, nm2) : ffma2(sv, sl2, nm2);
             const float2 e = (c2 % kFmaExpEvery == kFmaExpEvery - 1) ? exp2_fma2(x)
                                                                   : make_float2(exp2_approx(x.x), exp2_approx(x.y));
             if (qsc) {
@@ -461,8 +496,8 @@ __device__ __noinline__ void merge_split_records(const float* base, int ns_use, 
 
 // ------------------------------------------------------------------ kernel
 
-// EPI: EPI_STORE (pre-fill: store, or key-range split records), EPI_MIX or
-// EPI_DOT (the gated mix's epilogues; no key-range splits).  Ten warps leave
+// EPI: EPI_STORE (pre-fill: store, or key-range split records) or one of the
+// gated mix's epilogues (internal.h; no key-range splits).  Ten warps leave
 // 168 registers a thread (three of them share an SM sub-partition's 16K);
 // the split epilogue keeps its indices in shared memory and its record
 // write and merge out of line, so that the softmax loop fits without spills.
@@ -470,7 +505,7 @@ __device__ __noinline__ void merge_split_records(const float* base, int ns_use, 
 // V codes times 16 in fp16, both exact -- and tmS its per-row (k scale,
 // v scale / 16) pairs, applied in the softmax; the PV MMAs of those tiles
 // run in fp16.
-template <int EPI, bool QS>
+template <int EPI, bool QS, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmKc,
                       const __grid_constant__ CUtensorMap tmVc, const __grid_constant__ CUtensorMap tmKx,
@@ -698,7 +733,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float* qsc = QS && t.src == SRC_CACHE
                                    ? reinterpret_cast<const float*>(smem + kOffScale + (j & 3) * kScaleTileBytes)
                                    : nullptr;
-            const float corr = softmax_tile(lane_base + col_s(qi), sl, masked, vis, m_ref, l_sum, need, qsc);
+            const float corr = softmax_tile<CAP>(lane_base + col_s(qi), sl, a.cap, masked, vis, m_ref, l_sum, need,
+                                                 qsc);
             // O_qi holds every PV up to tile j - 1 (the commit behind s_full
             // covered them); rescale it before PV_qi(j) is issued
             if (j >= 1 && __any_sync(0xffffffffu, need)) {
@@ -720,10 +756,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const size_t row_off = (((size_t)b * p.C + crow) * a.Hq + q_idx) * HD;
         // the output row (and the record of a split) exist: CTA-uniform
         const bool out_ok = bounds_ok(b < a.B && q_idx >= 0 && q_idx < a.Hq, p.status);
-        uint4 pre[16];   // EPI_MIX / EPI_DOT: this row of out / dout, loaded before the wait below
-        if constexpr (EPI != EPI_STORE) {
+        constexpr bool kMixes = EPI == EPI_MIX || EPI == EPI_MIX_KEEP;
+        constexpr bool kKeeps = EPI == EPI_KEEP || EPI == EPI_MIX_KEEP;
+        uint4 pre[16];   // kMixes / EPI_DOT: this row of the streaming attention / dout, loaded before the wait below
+        if constexpr (kMixes || EPI == EPI_DOT) {
             const uint4* src = reinterpret_cast<const uint4*>(
-                static_cast<const __nv_bfloat16*>(EPI == EPI_MIX ? p.out : p.epi.dout) + row_off);
+                static_cast<const __nv_bfloat16*>(EPI == EPI_MIX ? p.out : EPI == EPI_DOT ? p.epi.dout : p.epi.streaming) +
+                row_off);
 #pragma unroll
             for (int i = 0; i < 16; ++i) pre[i] = crow < p.C && out_ok ? src[i] : make_uint4(0u, 0u, 0u, 0u);
         }
@@ -735,8 +774,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok && n_me >= 1) {
                 tc_fence_after();
                 const float inv = l_sum > 0.f ? 1.f / l_sum : 0.f;
-                const float al = EPI == EPI_MIX ? p.epi.alpha[kv_idx] : 0.f;
+                const float al = kMixes ? p.epi.alpha[kv_idx] : 0.f;
                 float dot = 0.f;
+                if constexpr (kKeeps) {   // the row's log2 of the sum of 2^score, for the backward pass
+                    if (crow < p.C) p.epi.lse[((size_t)b * a.Hq + q_idx) * p.C + crow] = m_ref + log2f(l_sum);
+                }
 #pragma unroll
                 for (int ch = 0; ch < 4; ++ch) {
                     float o[32];
@@ -746,13 +788,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float v8[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) v8[e] = o[8 * q4 + e] * inv;
-                        if constexpr (EPI == EPI_STORE) {
+                        if constexpr (EPI == EPI_STORE || EPI == EPI_KEEP) {
                             if (crow < p.C) store_row<__nv_bfloat16, 8>(op + 32 * ch + 8 * q4, v8);
                         } else {
                             const uint4 u = pre[4 * ch + q4];
                             const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-                            if constexpr (EPI == EPI_MIX) {
-                                // out held the streaming attention: mix it in
+                            if constexpr (EPI == EPI_MIX_KEEP) {
+                                if (crow < p.C)
+                                    store_row<__nv_bfloat16, 8>(static_cast<__nv_bfloat16*>(p.epi.causal) + row_off +
+                                                                    32 * ch + 8 * q4, v8);
+                            }
+                            if constexpr (kMixes) {
+                                // mix the streaming attention in
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
                                     v8[2 * e] = al * v8[2 * e] + (1.f - al) * bf16_lo(w[e]);
@@ -801,6 +848,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
+}
+
+struct TcMaps {
+    CUtensorMap q, kc, vc, kx, vx, kr, vr, sc;
+};
+
+template <int EPI, bool QS, bool CAP>
+cudaError_t launch_variant(const TcMaps& m, const TcArgs& p, unsigned grid, cudaStream_t s) {
+    constexpr size_t smem = kSmemBytes + 1024;
+    static std::atomic<unsigned long long> configured{0};
+    const cudaError_t e = smem_limit_once(prefill_tc_kernel<EPI, QS, CAP>, (int)smem, configured);
+    if (e != cudaSuccess) return e;
+    prefill_tc_kernel<EPI, QS, CAP><<<grid, kThreads, smem, s>>>(m.q, m.kc, m.vc, m.kx, m.vx, m.kr, m.vr, m.sc, p);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -928,22 +989,12 @@ cudaError_t launch_prefill_tc(const LayerArgs& a, const CacheArgs& c, const void
     p.seq_len = c.seq_len;
     p.status = c.status;
     p.out = out;
-    p.epi = epi ? *epi : EpiArgs{EPI_STORE, nullptr, nullptr, nullptr, 0.f};
+    p.epi = epi ? *epi : EpiArgs{};
     const long grid = (long)p.n_ret_ctas + (long)a.B * a.S * a.G * p.n_mpairs;
     if (grid == 0) return cudaSuccess;
     if (grid > 0x7fffffffL) return cudaErrorInvalidConfiguration;
-    static std::atomic<unsigned long long> configured[4] = {{0}, {0}, {0}, {0}};
     const bool qs = qscale != nullptr;
     if (qs && mode != EPI_STORE) return cudaErrorInvalidValue;
-    {
-        cudaError_t e = cudaErrorInvalidValue;
-        constexpr int kS = (int)(kSmemBytes + 1024);
-        if (mode == EPI_STORE && !qs) e = smem_limit_once(prefill_tc_kernel<EPI_STORE, false>, kS, configured[0]);
-        if (mode == EPI_STORE && qs) e = smem_limit_once(prefill_tc_kernel<EPI_STORE, true>, kS, configured[3]);
-        if (mode == EPI_MIX) e = smem_limit_once(prefill_tc_kernel<EPI_MIX, false>, kS, configured[1]);
-        if (mode == EPI_DOT) e = smem_limit_once(prefill_tc_kernel<EPI_DOT, false>, kS, configured[2]);
-        if (e != cudaSuccess) return e;
-    }
     if (split) {
         // the ticket words sit after this chunk length's partial records, so
         // a call with another chunk length may find there what an earlier
@@ -952,16 +1003,25 @@ cudaError_t launch_prefill_tc(const LayerArgs& a, const CacheArgs& c, const void
         if (e != cudaSuccess) return e;
     }
     const unsigned g = (unsigned)grid;
-    constexpr size_t kS = kSmemBytes + 1024;
-    if (mode == EPI_MIX)
-        prefill_tc_kernel<EPI_MIX, false><<<g, kThreads, kS, s>>>(mQ, mKc, mVc, mKx, mVx, mKr, mVr, mS, p);
-    else if (mode == EPI_DOT)
-        prefill_tc_kernel<EPI_DOT, false><<<g, kThreads, kS, s>>>(mQ, mKc, mVc, mKx, mVx, mKr, mVr, mS, p);
-    else if (qs)
-        prefill_tc_kernel<EPI_STORE, true><<<g, kThreads, kS, s>>>(mQ, mKc, mVc, mKx, mVx, mKr, mVr, mS, p);
-    else
-        prefill_tc_kernel<EPI_STORE, false><<<g, kThreads, kS, s>>>(mQ, mKc, mVc, mKx, mVx, mKr, mVr, mS, p);
-    return cudaGetLastError();
+    const TcMaps mp{mQ, mKc, mVc, mKx, mVx, mKr, mVr, mS};
+    if (a.cap.on) {
+        switch (mode) {
+            case EPI_STORE: return qs ? launch_variant<EPI_STORE, true, true>(mp, p, g, s)
+                                      : launch_variant<EPI_STORE, false, true>(mp, p, g, s);
+            case EPI_KEEP: return launch_variant<EPI_KEEP, false, true>(mp, p, g, s);
+            case EPI_MIX_KEEP: return launch_variant<EPI_MIX_KEEP, false, true>(mp, p, g, s);
+        }
+        return cudaErrorInvalidValue;
+    }
+    switch (mode) {
+        case EPI_STORE: return qs ? launch_variant<EPI_STORE, true, false>(mp, p, g, s)
+                                  : launch_variant<EPI_STORE, false, false>(mp, p, g, s);
+        case EPI_MIX: return launch_variant<EPI_MIX, false, false>(mp, p, g, s);
+        case EPI_DOT: return launch_variant<EPI_DOT, false, false>(mp, p, g, s);
+        case EPI_KEEP: return launch_variant<EPI_KEEP, false, false>(mp, p, g, s);
+        case EPI_MIX_KEEP: return launch_variant<EPI_MIX_KEEP, false, false>(mp, p, g, s);
+    }
+    return cudaErrorInvalidValue;
 }
 
 namespace {

@@ -36,9 +36,11 @@ STREAM_LAMBDA, STREAM_CHUNK = 0, 1
 KV_PLAIN, KV_INT8, KV_INT4 = 0, 1, 2
 MODEL_TO_BLOCK, BLOCK_TO_MODEL = 0, 1
 OP_DECODE, OP_PREFILL = 0, 1
+ROPE_HALVES, ROPE_PAIRS = 0, 1
 DEV_FULL_CACHE_OVERFLOW, DEV_BAD_PAGE, DEV_WAIT_TIMEOUT, DEV_BAD_LENGTH, DEV_BOUNDS = 1, 2, 4, 8, 16
 MAX_KV_HEADS = 64
 STATE_COUNTER_WORDS = 4
+ROPE_MAX_AXES = 3
 
 
 class LayerDesc(ctypes.Structure):
@@ -62,10 +64,19 @@ class KVState(ctypes.Structure):
     ]
 
 
+class Rope(ctypes.Structure):
+    _fields_ = [
+        ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("n_axes", ctypes.c_int32),
+        ("sections", ctypes.c_int32 * ROPE_MAX_AXES), ("factor", ctypes.c_float), ("reserved0", ctypes.c_int32),
+        ("inv_freq", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+    ]
+
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _DESC = ctypes.POINTER(LayerDesc)
 _STATE = ctypes.POINTER(KVState)
+_ROPE = ctypes.POINTER(Rope)
 
 
 def _fn(name, restype, *argtypes):
@@ -100,6 +111,14 @@ _lib_check = _fn("duo_check_status", ctypes.c_int, _STATE, ctypes.POINTER(_I32),
 _lib_decode_step = _fn("duo_decode_step", ctypes.c_int, _DESC, _STATE, _P, _P, _P, _P, _P, ctypes.c_size_t, _P)
 _lib_decode_noalloc = _fn("duo_decode_attn_noalloc", ctypes.c_int, _DESC, _STATE, _P, _P, _P)
 _lib_exp2_probe = _fn("duo_exp2_fma_probe", ctypes.c_int, _P, _P, ctypes.c_int64, _P)
+_lib_rope = _fn("duo_rope_qk", ctypes.c_int, _DESC, _ROPE, _P, _P, _P, _P, _P, _I32, _I32, _P)
+_lib_append_rope = _fn("duo_append_kv_rope", ctypes.c_int, _DESC, _STATE, _ROPE, _P, _P, _P, _P, _I32, _P)
+_lib_decode_capped = _fn("duo_decode_attn_capped", ctypes.c_int, _DESC, _STATE, ctypes.c_float, _P, _P, _P,
+                         ctypes.c_size_t, _P)
+_lib_decode_step_capped = _fn("duo_decode_step_capped", ctypes.c_int, _DESC, _STATE, ctypes.c_float, _P, _P, _P, _P,
+                              _P, ctypes.c_size_t, _P)
+_lib_prefill_capped = _fn("duo_prefill_chunk_capped", ctypes.c_int, _DESC, _STATE, ctypes.c_float, _P, _P, _P, _I32,
+                          _P, _P, ctypes.c_size_t, _P)
 NOALLOC_SCRATCH_BYTES = 2 << 20
 
 
@@ -184,6 +203,20 @@ def desc_validate(desc: LayerDesc) -> int:
     return int(_lib_desc_validate(ctypes.byref(desc)))
 
 
+def rope_init(rot_dim, inv_freq, *, layout=ROPE_HALVES, sections=None, factor=1.0, pos=None) -> Rope:
+    """A rotary embedding: inv_freq fp32 [rot_dim / 2] and pos (int32
+    [axes, B, T] or None) are device tensors or pointers that the caller
+    keeps alive; sections: pairs per axis (None: one axis)."""
+    sections = [rot_dim // 2] if sections is None else [int(x) for x in sections]
+    if not 1 <= len(sections) <= ROPE_MAX_AXES:
+        raise ValueError(f"1 to {ROPE_MAX_AXES} sections, got {len(sections)}")
+    r = Rope(rot_dim=rot_dim, layout=layout, n_axes=len(sections), factor=factor, inv_freq=_ptr(inv_freq),
+             pos=_ptr(pos))
+    for i, n in enumerate(sections):
+        r.sections[i] = n
+    return r
+
+
 def workspace_bytes(desc: LayerDesc, op: int, max_tokens: int) -> int:
     return int(_lib_ws_bytes(ctypes.byref(desc), op, max_tokens))
 
@@ -228,6 +261,40 @@ def prefill_chunk(desc, state: KVState, q, k_chunk, v_chunk, C: int, out, worksp
                   stream=None) -> None:
     _check(_lib_prefill(ctypes.byref(desc), ctypes.byref(state), _ptr(q), _ptr(k_chunk), _ptr(v_chunk), C,
                         _ptr(out), _ptr(workspace), ws_bytes, _stream(stream)), "duo_prefill_chunk")
+
+
+def rope_qk(desc, rope: Rope, q, k, q_out, k_out, T: int, seq_len=None, inverse: bool = False, stream=None) -> None:
+    """Rotary embedding of q and k (either may be None, with its output), or
+    with inverse its gradient.  Outputs may be the inputs themselves."""
+    _check(_lib_rope(ctypes.byref(desc), ctypes.byref(rope), _ptr(seq_len), _ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out),
+                     T, int(inverse), _stream(stream)), "duo_rope_qk")
+
+
+def append_kv_rope(desc, state: KVState, rope: Rope, q, k_new, v_new, q_out, T: int, stream=None) -> None:
+    """append_kv with the rotary embedding of k_new on the way in, and of q
+    into q_out (both None: no queries), in one launch."""
+    _check(_lib_append_rope(ctypes.byref(desc), ctypes.byref(state), ctypes.byref(rope), _ptr(q), _ptr(k_new),
+                            _ptr(v_new), _ptr(q_out), T, _stream(stream)), "duo_append_kv_rope")
+
+
+def decode_attn_capped(desc, state: KVState, cap: float, q, out, workspace, ws_bytes: int, stream=None) -> None:
+    """decode_attn with every score s replaced by cap * tanh(s / cap) (0: not capped)."""
+    _check(_lib_decode_capped(ctypes.byref(desc), ctypes.byref(state), cap, _ptr(q), _ptr(out), _ptr(workspace),
+                              ws_bytes, _stream(stream)), "duo_decode_attn_capped")
+
+
+def decode_step_capped(desc, state: KVState, cap: float, q, k_new, v_new, out, workspace, ws_bytes: int,
+                       stream=None) -> None:
+    """decode_step with capped scores: append one token per sequence and attend, in one launch."""
+    _check(_lib_decode_step_capped(ctypes.byref(desc), ctypes.byref(state), cap, _ptr(q), _ptr(k_new), _ptr(v_new),
+                                   _ptr(out), _ptr(workspace), ws_bytes, _stream(stream)), "duo_decode_step_capped")
+
+
+def prefill_chunk_capped(desc, state: KVState, cap: float, q, k_chunk, v_chunk, C: int, out, workspace=None,
+                         ws_bytes: int = 0, stream=None) -> None:
+    """prefill_chunk with capped scores."""
+    _check(_lib_prefill_capped(ctypes.byref(desc), ctypes.byref(state), cap, _ptr(q), _ptr(k_chunk), _ptr(v_chunk), C,
+                               _ptr(out), _ptr(workspace), ws_bytes, _stream(stream)), "duo_prefill_chunk_capped")
 
 
 def gated_mix(desc, alpha, q, k, v, N: int, out, status, stream=None) -> None:

@@ -81,6 +81,11 @@ enum {
 };
 /* duo_permute_heads directions */
 enum { DUO_MODEL_TO_BLOCK = 0, DUO_BLOCK_TO_MODEL = 1 };
+/* which channels a rotary embedding pairs */
+enum {
+    DUO_ROPE_HALVES = 0, /* (i, i + rot_dim / 2)                             */
+    DUO_ROPE_PAIRS = 1   /* (2 i, 2 i + 1)                                   */
+};
 /* workspace queries */
 enum { DUO_OP_DECODE = 0, DUO_OP_PREFILL = 1 };
 /* device status bits (OR-ed into duo_kv_state.status) */
@@ -96,6 +101,7 @@ enum {
 
 #define DUO_MAX_KV_HEADS 64
 #define DUO_STATE_COUNTER_WORDS 4
+#define DUO_ROPE_MAX_AXES 3
 
 /* One attention layer.  Fill it with duo_desc_init(). */
 typedef struct {
@@ -181,6 +187,30 @@ typedef struct {
     float* k_scale;      /* 8-bit full cache only, else NULL         */
     float* v_scale;
 } duo_kv_state;
+
+/*
+ * A rotary position embedding.  (No counterpart on the pages: it is a step of
+ * the models they deploy on, between the projections and the caches.)
+ * Channel pair i (i < rot_dim / 2) of a row (a, b) at position p becomes
+ *   factor * (a cos t - b sin t, b cos t + a sin t),  t = p * inv_freq[i];
+ * channels rot_dim .. head_dim - 1 pass through.  With several axes (time,
+ * height, width of image or video tokens) pairs 0 .. sections[0] - 1 take the
+ * positions of the first axis, the next sections[1] those of the second, and
+ * so on.  Angles are reduced in fp64, so far positions keep fp32 accuracy;
+ * the rotation is fp32, rounded once to the layer's dtype.
+ */
+typedef struct {
+    int32_t rot_dim;      /* rotated channels: even, 2..head_dim               */
+    int32_t layout;       /* DUO_ROPE_HALVES or DUO_ROPE_PAIRS                 */
+    int32_t n_axes;       /* position axes: 1..DUO_ROPE_MAX_AXES               */
+    int32_t sections[DUO_ROPE_MAX_AXES]; /* pairs of each axis; sum rot_dim / 2 */
+    float factor;         /* multiplies the rotated channels (1: a rotation)   */
+    int32_t reserved0;
+    const float* inv_freq;  /* device fp32 [rot_dim / 2]: radians per position */
+    const int32_t* pos;     /* device int32 [n_axes][B][T], any values; NULL
+                               (one axis only): token t of sequence b has
+                               position seq_len[b] + t                         */
+} duo_rope;
 
 /* ------------------------------------------------------------------------ */
 /* Library information                                                      */
@@ -395,6 +425,64 @@ duo_status duo_decode_step(const duo_layer_desc* desc, const duo_kv_state* st, c
 duo_status duo_prefill_chunk(const duo_layer_desc* desc, const duo_kv_state* st, const void* q,
                              const void* k_chunk, const void* v_chunk, int32_t C, void* out,
                              void* workspace, size_t ws_bytes, duo_stream_t stream);
+
+/*
+ * duo_rope_qk -- the rotary embedding of queries and keys, or its gradient.
+ *
+ * q [B][T][Hq][d], k [B][T][Hkv][d] -> q_out, k_out of the same shapes (the
+ * head order does not matter: every head of a token turns alike).  Either of
+ * q and k may be NULL, with its output.  An output may be its input itself (in
+ * place); other overlaps are refused.  seq_len: device int32 [B] or NULL (0),
+ * the position of each sequence's first token where rope->pos is NULL (the
+ * state's seq_len before a chunk's pre-fill).
+ * inverse != 0: the gradient -- given the gradients of q_out and k_out, those
+ * of q and k: the same map by the negative angles.
+ * T == 0 is a no-op.
+ * Errors: DUO_ERR_INVALID_ARG, DUO_ERR_SHAPE, DUO_ERR_CUDA.
+ */
+duo_status duo_rope_qk(const duo_layer_desc* desc, const duo_rope* rope, const int32_t* seq_len, const void* q,
+                       const void* k, void* q_out, void* k_out, int32_t T, int32_t inverse, duo_stream_t stream);
+
+/*
+ * duo_append_kv_rope -- duo_append_kv with the rotary embedding applied to the
+ * keys on the way into the caches, and to the tokens' queries, in one launch.
+ *
+ * k_new, v_new [B][T][Hkv][d]: as for duo_append_kv, k_new before its
+ * rotation.  q [B][T][Hq][d] -> q_out, rotated (both NULL: no queries; q_out
+ * may be q itself).  The caches, ring positions, seq_len and status bits end
+ * as after duo_rope_qk and duo_append_kv, bit for bit: the rotated keys are
+ * rounded to the layer's dtype before they are stored or quantized.  A cache
+ * position is always seq_len[b] + t; rope->pos only gives the angles.
+ * Uses state counter word 0, as duo_append_kv.  T == 0 is a no-op.
+ * A decode step of a rotary model is this call with T = 1, then
+ * duo_decode_attn (or _capped) on q_out.
+ * Errors: DUO_ERR_INVALID_ARG, DUO_ERR_SHAPE, DUO_ERR_CUDA.
+ */
+duo_status duo_append_kv_rope(const duo_layer_desc* desc, const duo_kv_state* st, const duo_rope* rope, const void* q,
+                              const void* k_new, const void* v_new, void* q_out, int32_t T, duo_stream_t stream);
+
+/*
+ * duo_decode_attn_capped, duo_decode_step_capped, duo_prefill_chunk_capped --
+ * duo_decode_attn, duo_decode_step and duo_prefill_chunk for models that cap
+ * their attention scores: with s = scale * (q . k), every score becomes
+ *   cap * tanh(s / cap)
+ * before the mask and the softmax.  cap = 0: not capped (the plain call).
+ * Everything else -- tensors, caches of every kind, workspaces (those of the
+ * plain calls), status bits, refusals -- is as for the plain calls.
+ * The capped score is within cap * 1e-6 of the formula in decode and, on the
+ * tensor-core pre-fill, within 8e-6 of its own size (7e-6 of it from the
+ * polynomial that stands for tanh where |s| <= cap).
+ * Errors: as the plain calls, and DUO_ERR_INVALID_ARG for a cap that is
+ * negative, not finite, or below scale / 1e4.
+ */
+duo_status duo_decode_attn_capped(const duo_layer_desc* desc, const duo_kv_state* st, float cap, const void* q,
+                                  void* out, void* workspace, size_t ws_bytes, duo_stream_t stream);
+duo_status duo_decode_step_capped(const duo_layer_desc* desc, const duo_kv_state* st, float cap, const void* q,
+                                  const void* k_new, const void* v_new, void* out, void* workspace, size_t ws_bytes,
+                                  duo_stream_t stream);
+duo_status duo_prefill_chunk_capped(const duo_layer_desc* desc, const duo_kv_state* st, float cap, const void* q,
+                                    const void* k_chunk, const void* v_chunk, int32_t C, void* out, void* workspace,
+                                    size_t ws_bytes, duo_stream_t stream);
 
 /*
  * duo_gated_mix -- the head-identification forward over whole sequences, no

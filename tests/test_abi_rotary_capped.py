@@ -1,0 +1,121 @@
+"""Refusals and no-ops of the rotary and capped entry points: every call here
+returns on the host before anything is queued."""
+
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def _desc(duo, **kw):
+    args = dict(batch=2, n_q_heads=8, n_kv_heads=4, head_dim=128, dtype=duo.BF16, kv_perm=[0, 1, 2, 3], n_retrieval=2)
+    args.update(kw)
+    return duo.desc_init(**args)
+
+
+def _state(duo, **kw):
+    st = duo.KVState()
+    for k, v in dict(k_full=16, v_full=32, capacity=1024, k_ring=48, v_ring=64, ring_pos=80, seq_len=96, counters=112,
+                     status=128, **kw).items():
+        setattr(st, k, v)
+    return st
+
+
+Q, K, V, QO, KO = (i << 24 for i in range(1, 6))
+
+
+def _refused(duo, status, call, *args, **kw):
+    with pytest.raises(duo.DuoError) as e:
+        call(*args, **kw, stream=0)
+    assert e.value.status == getattr(duo, status), str(e.value)
+    assert duo.last_error()
+
+
+def test_rope_struct_matches_the_c_compiler(duo, tmp_path):
+    src = tmp_path / "rope.c"
+    src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "duo.h"\n'
+                   'int main(void) { printf("%zu %zu %zu %zu %zu\\n", sizeof(duo_rope), offsetof(duo_rope, sections), '
+                   'offsetof(duo_rope, factor), offsetof(duo_rope, inv_freq), offsetof(duo_rope, pos)); return 0; }\n')
+    exe = tmp_path / "rope"
+    subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    got = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
+    R = duo.Rope
+    assert got == [ctypes.sizeof(R), R.sections.offset, R.factor.offset, R.inv_freq.offset, R.pos.offset]
+
+
+BAD_ROPES = [
+    (dict(rot_dim=127), "ERR_SHAPE"), (dict(rot_dim=0), "ERR_SHAPE"), (dict(rot_dim=130), "ERR_SHAPE"),
+    (dict(layout=2), "ERR_INVALID_ARG"), (dict(inv_freq=0), "ERR_INVALID_ARG"), (dict(inv_freq=6), "ERR_INVALID_ARG"),
+    (dict(factor=float("nan")), "ERR_INVALID_ARG"), (dict(factor=float("inf")), "ERR_INVALID_ARG"),
+    (dict(n_axes=0), "ERR_SHAPE"), (dict(n_axes=4), "ERR_SHAPE"), (dict(sections=[63]), "ERR_SHAPE"),
+    (dict(sections=[-1, 65], pos=4096), "ERR_SHAPE"), (dict(sections=[32, 32]), "ERR_INVALID_ARG"),   # no positions
+    (dict(sections=[2 ** 31 - 1, 2 ** 31 - 1, 64], pos=4096), "ERR_SHAPE"), (dict(pos=4098), "ERR_INVALID_ARG"),
+]
+
+
+@pytest.mark.parametrize("kw,status", BAD_ROPES)
+def test_bad_rope_descriptors(duo, kw, status):
+    kw = dict(kw)
+    n_axes = kw.pop("n_axes", None)
+    rope = duo.rope_init(kw.pop("rot_dim", 128), kw.pop("inv_freq", 256), **{**dict(layout=0), **kw}) if \
+        "sections" in kw or "rot_dim" not in kw else duo.rope_init(kw["rot_dim"], 256)
+    if n_axes is not None:
+        rope.n_axes = n_axes
+    _refused(duo, status, duo.rope_qk, _desc(duo), rope, Q, K, QO, KO, 3)
+    _refused(duo, status, duo.append_kv_rope, _desc(duo), _state(duo), rope, Q, K, V, QO, 3)
+
+
+def test_rope_takes_one_to_three_sections(duo):
+    for sections in ([], [16] * 4):
+        with pytest.raises(ValueError):
+            duo.rope_init(128, 256, sections=sections)
+
+
+def test_rope_tensors(duo):
+    rope, d = duo.rope_init(128, 256), _desc(duo)
+    nq, nk = 2 * 3 * 8 * 256, 2 * 3 * 4 * 256
+    _refused(duo, "ERR_SHAPE", duo.rope_qk, d, rope, Q, K, QO, KO, -1)
+    for args in ((None, None, None, None), (Q, K, None, KO), (Q, None, QO, KO), (Q + 8, K, QO, KO), (Q, K, QO, KO + 2),
+                 (Q, K, Q + 16, KO), (Q, K, Q + nq - 16, KO), (Q, K, K, KO), (Q, K, K + nk - 16, KO), (Q, K, QO, Q),
+                 (Q, K, QO, QO)):
+        _refused(duo, "ERR_INVALID_ARG", duo.rope_qk, d, rope, *args, 3)
+    duo.rope_qk(d, rope, Q, K, QO, KO, 0, stream=0)                     # no tokens: nothing to do
+    with pytest.raises(duo.DuoError):
+        duo.rope_qk(_desc(duo, head_dim=96), rope, Q, K, QO, KO, 0, stream=0)
+
+
+def test_append_rope_tensors(duo):
+    rope, d, st = duo.rope_init(128, 256), _desc(duo), _state(duo)
+    nq, nk = 2 * 3 * 8 * 256, 2 * 3 * 4 * 256
+    _refused(duo, "ERR_SHAPE", duo.append_kv_rope, d, st, rope, Q, K, V, QO, -1)
+    for q, k, v, qo in ((Q, None, V, QO), (Q, K, None, QO), (Q, K, V, None), (None, K, V, QO), (Q, K + 8, V, QO),
+                        (Q, K, V, Q + 16), (Q, K, V, K), (Q, K, V, V + nk - 16), (Q, K, V, Q - nq + 16)):
+        _refused(duo, "ERR_INVALID_ARG", duo.append_kv_rope, d, st, rope, q, k, v, qo, 3)
+    st.seq_len = None
+    _refused(duo, "ERR_INVALID_ARG", duo.append_kv_rope, d, st, rope, Q, K, V, QO, 3)
+    duo.append_kv_rope(d, _state(duo), rope, Q, K, V, QO, 0, stream=0)
+
+
+@pytest.mark.parametrize("cap", [-1.0, float("nan"), float("inf"), -float("inf"), 1e-7, 3e38])
+def test_bad_caps(duo, cap):
+    d, st = _desc(duo), _state(duo)
+    need = duo.workspace_bytes(d, duo.OP_DECODE, 1024)
+    _refused(duo, "ERR_INVALID_ARG", duo.decode_attn_capped, d, st, cap, Q, QO, V, need)
+    _refused(duo, "ERR_INVALID_ARG", duo.decode_step_capped, d, st, cap, Q, K, V, QO, KO, need)
+    _refused(duo, "ERR_INVALID_ARG", duo.prefill_chunk_capped, d, st, cap, Q, K, V, 3, QO)
+
+
+def test_capped_calls_refuse_what_the_plain_calls_refuse(duo):
+    d, st = _desc(duo), _state(duo)
+    need = duo.workspace_bytes(d, duo.OP_DECODE, 1024)
+    _refused(duo, "ERR_CAPACITY", duo.decode_attn_capped, d, st, 30.0, Q, QO, V, need - 16)
+    _refused(duo, "ERR_INVALID_ARG", duo.decode_attn_capped, d, st, 30.0, None, QO, V, need)
+    _refused(duo, "ERR_INVALID_ARG", duo.decode_step_capped, d, st, 30.0, Q, K, V + 8, QO, KO, need)
+    _refused(duo, "ERR_SHAPE", duo.prefill_chunk_capped, d, st, 30.0, Q, K, V, 0, QO)
+    paged = duo.desc_init(2, 8, 4, 128, duo.BF16, [0, 1, 2, 3], 2, page_size=64)
+    _refused(duo, "ERR_UNSUPPORTED", duo.prefill_chunk_capped, paged,
+             _state(duo, page_table=144, max_pages=16, n_pages=16), 30.0, Q, K, V, 3, QO)
+    assert "duo_prefill_chunk_capped" in duo.last_error()
