@@ -302,6 +302,8 @@ duo_status prefill_chunk_call(const duo_layer_desc* desc, const duo_kv_state* st
         if (!duo::prefill_tc_supported(a))
             return fail(DUO_ERR_UNSUPPORTED, "tensor-core pre-fill cannot take this layer");
         e = duo::launch_prefill_tc(a, c, q, k_chunk, v_chunk, C, out, workspace, ws_bytes, (cudaStream_t)stream);
+    } else if (a.cap.on) {
+        e = duo::launch_tiled_prefill(a, c, q, k_chunk, v_chunk, C, out, (cudaStream_t)stream);
     } else {
         e = duo::launch_simt_attention(a, &c, nullptr, q, k_chunk, v_chunk, C, out, 0, (cudaStream_t)stream);
     }
@@ -340,6 +342,37 @@ duo_status rope_args(const duo_layer_desc* desc, const duo_rope* rope, int inver
     r.inv_freq = rope->inv_freq;
     r.pos = rope->pos;
     return DUO_OK;
+}
+
+// What duo_gated_mix_train keeps: A_c and A_s in the layer's dtype, then both
+// lse rows; every part starts on a multiple of 256 bytes.
+struct MixSaved {
+    size_t streaming, lse, bytes;
+};
+MixSaved mix_saved(const duo_layer_desc* d, int32_t N) {
+    const size_t heads = (size_t)d->batch * N * d->n_q_heads;
+    const size_t attn = (heads * d->head_dim * (d->dtype == DUO_BF16 ? 2 : 4) + 255) / 256 * 256;
+    return {attn, 2 * attn, 2 * attn + (2 * heads * sizeof(float) + 255) / 256 * 256};
+}
+
+// The two single-mask layers of a gated mix (every KV head in the streaming /
+// the retrieval block, model head order, no cache).
+void mix_layers(duo::LayerArgs& a, duo::LayerArgs& as, duo::LayerArgs& ac) {
+    for (int i = 0; i < a.Hkv; ++i) {
+        a.kv_head[i] = i;
+        a.q_head0[i] = i * a.G;
+        a.slot_of[i] = i;
+    }
+    a.page_size = 0;
+    a.capacity = 0;
+    a.stream_chunk = 0;
+    a.kv_bits = 0;
+    as = a;
+    as.R = 0;
+    as.S = a.Hkv;
+    ac = a;
+    ac.R = a.Hkv;
+    ac.S = 0;
 }
 
 bool overlap(const void* x, size_t nx, const void* y, size_t ny) {
@@ -698,6 +731,133 @@ duo_status duo_gated_mix_grad_alpha(const duo_layer_desc* desc, const void* q, c
     }
     e = duo::launch_simt_attention(a, nullptr, nullptr, q, k, v, N, nullptr, 2, (cudaStream_t)stream, dout, dalpha);
     return e == cudaSuccess ? ok() : cuda_fail(e, "duo_gated_mix_grad_alpha");
+}
+
+size_t duo_gated_mix_saved_bytes(const duo_layer_desc* desc, int32_t N) {
+    if (check_desc(desc) != DUO_OK || N < 0) return 0;
+    return mix_saved(desc, N).bytes;
+}
+
+size_t duo_gated_mix_grad_workspace_bytes(const duo_layer_desc* desc, int32_t N) {
+    if (check_desc(desc) != DUO_OK || N < 0) return 0;
+    duo::LayerArgs a;
+    fill_args(desc, a);
+    return duo::mix_grad_plan(a, N).bytes;
+}
+
+duo_status duo_gated_mix_train(const duo_layer_desc* desc, const float* alpha, float cap, const void* q, const void* k,
+                               const void* v, int32_t N, void* out, void* saved, size_t saved_bytes, int32_t* status,
+                               duo_stream_t stream) {
+    duo_status s = check_desc(desc);
+    if (s != DUO_OK) return s;
+    duo::LayerArgs a, as, ac;
+    fill_args(desc, a);
+    if ((s = set_cap(a, cap)) != DUO_OK) return s;
+    if (N < 0) return fail(DUO_ERR_SHAPE, "N must be >= 0 (got %d)", N);
+    if (!alpha || !q || !k || !v || !out || !saved || !status)
+        return fail(DUO_ERR_INVALID_ARG, "duo_gated_mix_train: NULL argument");
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(saved))
+        return fail(DUO_ERR_INVALID_ARG, "duo_gated_mix_train tensors must be 16-byte aligned");
+    if (N == 0) return ok();
+    const MixSaved sv = mix_saved(desc, N);
+    if (saved_bytes < sv.bytes)
+        return fail(DUO_ERR_CAPACITY, "saved holds %zu bytes, duo_gated_mix_train needs %zu", saved_bytes, sv.bytes);
+    const size_t es = desc->dtype == DUO_BF16 ? 2 : 4, rows = (size_t)desc->batch * N;
+    const size_t nq = rows * desc->n_q_heads * desc->head_dim * es, nkv = rows * desc->n_kv_heads * desc->head_dim * es;
+    for (const void* x : {q, k, v})
+        if (overlap(out, nq, x, x == q ? nq : nkv) || overlap(saved, sv.bytes, x, x == q ? nq : nkv))
+            return fail(DUO_ERR_INVALID_ARG, "duo_gated_mix_train: out or saved overlaps q, k or v");
+    if (overlap(out, nq, saved, sv.bytes)) return fail(DUO_ERR_INVALID_ARG, "duo_gated_mix_train: out overlaps saved");
+    void* causal = saved;
+    void* streaming = static_cast<uint8_t*>(saved) + sv.streaming;
+    float* lse = reinterpret_cast<float*>(static_cast<uint8_t*>(saved) + sv.lse);
+    mix_layers(a, as, ac);
+    cudaError_t e;
+    if (duo::prefill_tc_supported(as) && duo::prefill_tc_supported(ac)) {
+        duo::CacheArgs none{};
+        none.status = status;
+        duo::EpiArgs keep;
+        keep.mode = duo::EPI_KEEP;
+        keep.lse = lse + (size_t)a.B * a.Hq * N;
+        e = duo::launch_prefill_tc(as, none, q, k, v, N, streaming, nullptr, 0, (cudaStream_t)stream, &keep);
+        duo::EpiArgs mix;
+        mix.mode = duo::EPI_MIX_KEEP;
+        mix.alpha = alpha;
+        mix.streaming = streaming;
+        mix.causal = causal;
+        mix.lse = lse;
+        if (e == cudaSuccess)
+            e = duo::launch_prefill_tc(ac, none, q, k, v, N, out, nullptr, 0, (cudaStream_t)stream, &mix);
+    } else {
+        e = duo::launch_tiled_mix(ac, alpha, q, k, v, N, out, causal, streaming, lse, status, (cudaStream_t)stream);
+    }
+    return e == cudaSuccess ? ok() : cuda_fail(e, "duo_gated_mix_train");
+}
+
+duo_status duo_gated_mix_grad(const duo_layer_desc* desc, const float* alpha, float cap, const void* q, const void* k,
+                              const void* v, int32_t N, const void* saved, size_t saved_bytes, const void* dout, void* dq,
+                              void* dk, void* dv, float* dalpha, void* workspace, size_t ws_bytes, int32_t* status,
+                              duo_stream_t stream) {
+    duo_status s = check_desc(desc);
+    if (s != DUO_OK) return s;
+    duo::LayerArgs a, as, ac;
+    fill_args(desc, a);
+    if ((s = set_cap(a, cap)) != DUO_OK) return s;
+    if (N < 0) return fail(DUO_ERR_SHAPE, "N must be >= 0 (got %d)", N);
+    if (!alpha || !q || !k || !v || !saved || !dout || !dq || !dk || !dv || !dalpha || !workspace || !status)
+        return fail(DUO_ERR_INVALID_ARG, "duo_gated_mix_grad: NULL argument");
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(saved) || !aligned16(dout) || !aligned16(dq) ||
+        !aligned16(dk) || !aligned16(dv) || !aligned16(workspace))
+        return fail(DUO_ERR_INVALID_ARG, "duo_gated_mix_grad tensors must be 16-byte aligned");
+    if (N == 0) {
+        const cudaError_t e = cudaMemsetAsync(dalpha, 0, sizeof(float) * desc->n_kv_heads, (cudaStream_t)stream);
+        return e == cudaSuccess ? ok() : cuda_fail(e, "duo_gated_mix_grad");
+    }
+    const MixSaved sv = mix_saved(desc, N);
+    if (saved_bytes < sv.bytes)
+        return fail(DUO_ERR_CAPACITY, "saved holds %zu bytes, duo_gated_mix_train writes %zu", saved_bytes, sv.bytes);
+    const duo::MixGradPlan plan = duo::mix_grad_plan(a, N);
+    if (ws_bytes < plan.bytes)
+        return fail(DUO_ERR_CAPACITY, "workspace holds %zu bytes, duo_gated_mix_grad needs %zu", ws_bytes, plan.bytes);
+    const size_t es = desc->dtype == DUO_BF16 ? 2 : 4, rows = (size_t)desc->batch * N;
+    const size_t nq = rows * desc->n_q_heads * desc->head_dim * es, nkv = rows * desc->n_kv_heads * desc->head_dim * es;
+    {
+        // every output is written while inputs are still being read
+        const struct { const void* p; size_t n; } in[] = {{q, nq}, {dout, nq}, {k, nkv}, {v, nkv}, {saved, sv.bytes}},
+                                                  out[] = {{dq, nq}, {dk, nkv}, {dv, nkv}, {workspace, plan.bytes}};
+        for (int i = 0; i < 4; ++i) {
+            for (const auto& x : in)
+                if (overlap(out[i].p, out[i].n, x.p, x.n))
+                    return fail(DUO_ERR_INVALID_ARG, "duo_gated_mix_grad: an output or the workspace overlaps an input");
+            for (int j = 0; j < i; ++j)
+                if (overlap(out[i].p, out[i].n, out[j].p, out[j].n))
+                    return fail(DUO_ERR_INVALID_ARG, "duo_gated_mix_grad: two outputs (or the workspace) overlap");
+        }
+    }
+    const uint8_t* sb = static_cast<const uint8_t*>(saved);
+    duo::MixGradArgs g{};
+    g.q = q;
+    g.k = k;
+    g.v = v;
+    g.dout = dout;
+    g.causal = sb;
+    g.streaming = sb + sv.streaming;
+    g.lse = reinterpret_cast<const float*>(sb + sv.lse);
+    g.alpha = alpha;
+    g.stats = static_cast<float*>(workspace);
+    g.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.part_offset);
+    g.dq = dq;
+    g.dk = dk;
+    g.dv = dv;
+    g.dalpha = dalpha;
+    g.status = status;
+    mix_layers(a, as, ac);
+    cudaError_t e = duo::launch_mix_stats(ac, g, N, (cudaStream_t)stream);
+    if (e == cudaSuccess)
+        e = duo::prefill_tc_supported(as) && duo::prefill_tc_supported(ac)
+                ? duo::launch_mix_grad_tc(ac, g, N, (cudaStream_t)stream)
+                : duo::launch_tiled_mix_grad(ac, g, N, (cudaStream_t)stream);
+    return e == cudaSuccess ? ok() : cuda_fail(e, "duo_gated_mix_grad");
 }
 
 duo_status duo_exp2_fma_probe(const float* x, float* y, int64_t n, duo_stream_t stream) {

@@ -127,6 +127,36 @@ struct EpiArgs {
 cudaError_t launch_prefill_tc(const LayerArgs& a, const CacheArgs& c, const void* q, const void* k_chunk,
                               const void* v_chunk, int C, void* out, void* workspace, size_t ws_bytes,
                               cudaStream_t s, const EpiArgs* epi = nullptr, const float* qscale = nullptr);
+// CUDA-core attention in 64 x 64 tiles (tiled_attn.cu): the capped pre-fill,
+// and the gated mix's training passes, where the tensor-core kernels do not
+// take the call.
+cudaError_t launch_tiled_prefill(const LayerArgs& a, const CacheArgs& c, const void* q, const void* k, const void* v,
+                                 int C, void* out, cudaStream_t st);
+cudaError_t launch_tiled_mix(const LayerArgs& a, const float* alpha, const void* q, const void* k, const void* v, int N,
+                             void* out, void* causal, void* streaming, float* lse, int32_t* status, cudaStream_t st);
+// Backward pass of the gated mix: the rows' statistics (both paths), then dK /
+// dV / dalpha and dQ on the tensor cores (mix_grad.cu) or in 64 x 64 tiles.
+struct MixGradPlan {
+    int n_pad;             // rows of a head's statistics: N rounded up to 128
+    int chunks;            // shares of dalpha per sequence and KV head
+    size_t part_offset;    // bytes from workspace start to the shares
+    size_t bytes;
+};
+struct MixGradArgs {
+    const void *q, *k, *v, *dout;
+    const void *causal, *streaming;    // A_c, A_s of the forward pass
+    const float* lse;                  // [2][B][Hq][N]
+    const float* alpha;
+    float* stats;                      // workspace: [B][Hq][4][n_pad]
+    float* part;                       // workspace: [Hkv][B * chunks]
+    void *dq, *dk, *dv;
+    float* dalpha;
+    int32_t* status;
+};
+MixGradPlan mix_grad_plan(const LayerArgs& a, int N);
+cudaError_t launch_mix_stats(const LayerArgs& a, const MixGradArgs& g, int N, cudaStream_t s);
+cudaError_t launch_mix_grad_tc(const LayerArgs& a, const MixGradArgs& g, int N, cudaStream_t s);
+cudaError_t launch_tiled_mix_grad(const LayerArgs& a, const MixGradArgs& g, int N, cudaStream_t st);
 cudaError_t launch_exp2_fma_probe(const float* x, float* y, int64_t n, cudaStream_t s);
 // An 8- or 4-bit layer's cached rows (below seq_len) staged for the
 // tensor-core pre-fill: the codes as bf16 values (exact) in a contiguous

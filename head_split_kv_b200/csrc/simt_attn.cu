@@ -18,7 +18,6 @@
 // A CTA holds 32 query rows of one query head; four threads share a row, each
 // with a quarter of the head dimension, and reduce the dot product with two
 // shuffles.  Keys stream through shared memory 32 at a time, widened to fp32.
-#include "cap.cuh"
 #include "common.cuh"
 #include "internal.h"
 
@@ -41,7 +40,7 @@ struct SimtArgs {
     float* dalpha;        // mode 2: [Hkv], accumulated
 };
 
-template <typename T, int D, bool CAP>
+template <typename T, int D>
 __global__ void __launch_bounds__(kThreadsSimt) simt_attention_kernel(const LayerArgs a, const CacheArgs c,
                                                                       const SimtArgs s) {
     constexpr int QD = D / 4;  // elements per thread
@@ -76,8 +75,7 @@ __global__ void __launch_bounds__(kThreadsSimt) simt_attention_kernel(const Laye
     {
         const T* qp = static_cast<const T*>(s.q) + (((size_t)b * N + (row_ok ? row : 0)) * a.Hq + q_idx) * D + quarter * QD;
 #pragma unroll
-        for (int e = 0; e < QD; ++e)
-            q[e] = CAP ? Elem<T>::to_f32(qp[e]) * a.cap.k : Elem<T>::to_f32(qp[e]) * a.scale * kLog2e;
+        for (int e = 0; e < QD; ++e) q[e] = Elem<T>::to_f32(qp[e]) * a.scale * kLog2e;
     }
     // two online-softmax states: 0 = the head's mask (mode 0) or causal
     // (mode 1); 1 = Lambda (mode 1 only)
@@ -154,7 +152,6 @@ __global__ void __launch_bounds__(kThreadsSimt) simt_attention_kernel(const Laye
                 for (int e = 0; e < QD; ++e) part = fmaf(q[e], sK[j][quarter * QD + e], part);
                 part += __shfl_xor_sync(0xffffffffu, part, 1);
                 part += __shfl_xor_sync(0xffffffffu, part, 2);
-                if constexpr (CAP) part = a.cap.c2 * tanhf(part);
                 const int kp = sPos[j];
                 const bool causal = kp >= 0 && kp <= qpos;
                 const bool lam = causal && (kp < a.sink || (a.stream_chunk && !mix ? kp >= c0 - a.recent
@@ -220,10 +217,7 @@ __global__ void __launch_bounds__(kThreadsSimt) simt_attention_kernel(const Laye
 template <typename T, int D>
 cudaError_t launch_simt_t(const LayerArgs& a, const CacheArgs& c, const SimtArgs& s, cudaStream_t st) {
     dim3 grid((s.n_tokens + kRows - 1) / kRows, a.Hq, a.B);
-    if (a.cap.on)
-        simt_attention_kernel<T, D, true><<<grid, kThreadsSimt, 0, st>>>(a, c, s);
-    else
-        simt_attention_kernel<T, D, false><<<grid, kThreadsSimt, 0, st>>>(a, c, s);
+    simt_attention_kernel<T, D><<<grid, kThreadsSimt, 0, st>>>(a, c, s);
     return cudaGetLastError();
 }
 

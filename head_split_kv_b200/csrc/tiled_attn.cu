@@ -1,0 +1,519 @@
+// tiled_attn.cu -- attention on the CUDA cores in 64 x 64 tiles, for what the
+// tensor-core kernels do not take (fp32, head_dim 64, wide windows): the
+// capped pre-fill, and the gated mix's training forward and backward passes.
+// All arithmetic is fp32 (CUDA's exp2f and tanhf).
+//
+// 256 threads as 16 x 16; every product is a register tile of 4 x 4 scores
+// (or 4 rows x D / 16 columns) per thread, operands in shared memory as fp32
+// rows padded by four floats, so that 16 threads reading 16 rows use all
+// banks.  A thread's rows are 4 ty .. 4 ty + 3, the same for scores and
+// accumulators, so a row's softmax state stays in the 16 threads of one
+// half-warp (shuffles, no shared memory); its score columns are tx + 16 j.
+// Probabilities pass between the products through shared memory, transposed.
+// Bound by the fp32 FMA pipe and, for short sequences, by latency.
+#include "cap.cuh"
+#include "common.cuh"
+#include "internal.h"
+#include "mix_grad.cuh"
+
+namespace duo {
+namespace {
+
+constexpr int TT = 64;              // rows of a tile
+constexpr int kTiledThreads = 256;
+constexpr int PS = TT + 4;          // row stride of the transposed probabilities
+
+template <int D>
+__host__ __device__ constexpr int row_stride() { return D + 4; }
+template <int D>
+__host__ __device__ constexpr size_t tile_floats() { return (size_t)TT * row_stride<D>(); }
+
+// 64 rows of D elements into shared memory as fp32; rows where src(r) is NULL are zero.
+template <typename T, int D, typename F>
+__device__ __forceinline__ void load_tile(float* dst, F src) {
+    constexpr int N = 16 / (int)sizeof(T), PPR = D / N;   // elements of a 16-byte piece, pieces per row
+#pragma unroll
+    for (int k = 0; k < TT * PPR / kTiledThreads; ++k) {
+        const int i = threadIdx.x + k * kTiledThreads, r = i / PPR, c = i % PPR * N;
+        const T* p = src(r);
+        float v[N];
+        if (p) load_row_f32<T, N>(p + c, v);
+        else
+#pragma unroll
+            for (int e = 0; e < N; ++e) v[e] = 0.f;
+#pragma unroll
+        for (int e = 0; e < N; e += 4)
+            *reinterpret_cast<float4*>(dst + r * row_stride<D>() + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+    }
+}
+
+// s[i][j] = X row (4 ty + i) . Y row (tx + 16 j)
+template <int D>
+__device__ __forceinline__ void tile_dot(const float* x, const float* y, int tx, int ty, float (&s)[4][4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+    for (int e = 0; e < D; e += 4) {
+        float4 a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(x + (4 * ty + i) * row_stride<D>() + e);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(y + (tx + 16 * j) * row_stride<D>() + e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                s[i][j] = fmaf(a[i].x, b[j].x, fmaf(a[i].y, b[j].y, fmaf(a[i].z, b[j].z, fmaf(a[i].w, b[j].w, s[i][j]))));
+    }
+}
+
+// acc[i][:] += sum over the tile's 64 inner rows k of pt[k][4 ty + i] * y[k][columns 4 tx + 64 j ..]
+template <int D>
+__device__ __forceinline__ void tile_acc(const float* pt, const float* y, int tx, int ty, float (&acc)[4][D / 16]) {
+#pragma unroll 4
+    for (int k = 0; k < TT; ++k) {
+        const float4 p = *reinterpret_cast<const float4*>(pt + k * PS + 4 * ty);
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+            const float4 v = *reinterpret_cast<const float4*>(y + k * row_stride<D>() + 4 * tx + 64 * j);
+            const float pr[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                acc[i][4 * j] = fmaf(pr[i], v.x, acc[i][4 * j]);
+                acc[i][4 * j + 1] = fmaf(pr[i], v.y, acc[i][4 * j + 1]);
+                acc[i][4 * j + 2] = fmaf(pr[i], v.z, acc[i][4 * j + 2]);
+                acc[i][4 * j + 3] = fmaf(pr[i], v.w, acc[i][4 * j + 3]);
+            }
+        }
+    }
+}
+
+// pt[tx + 16 j][4 ty .. + 3] = p[..][j]
+__device__ __forceinline__ void put_transposed(float* pt, const float (&p)[4][4], int tx, int ty) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<float4*>(pt + (tx + 16 * j) * PS + 4 * ty) = make_float4(p[0][j], p[1][j], p[2][j], p[3][j]);
+}
+
+// Over the 16 threads that hold a row's columns.
+__device__ __forceinline__ float row_max(float v) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// One online-softmax step of a row group: x (log2-domain scores, -inf where
+// unseen) becomes p; m, l and acc are brought to the new maximum.
+template <int W>
+__device__ __forceinline__ void softmax_step(float (&x)[4][4], float (&m)[4], float (&l)[4], float (&acc)[4][W]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float mn = fmaxf(m[i], row_max(fmaxf(fmaxf(x[i][0], x[i][1]), fmaxf(x[i][2], x[i][3]))));
+        const float corr = exp2f(m[i] - mn);
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[i][j] = exp2f(x[i][j] - mn);           // mn is at least kNegBig, so -inf gives 0
+            sum += x[i][j];
+        }
+        l[i] = l[i] * corr + sum;                     // this thread's columns; summed over the row at the end
+        m[i] = mn;
+#pragma unroll
+        for (int e = 0; e < W; ++e) acc[i][e] *= corr;
+    }
+}
+
+// ------------------------------------------------------------------ forward
+
+struct TiledArgs {
+    const void* q;         // [B][N][Hq][D]
+    const void* k;         // [B][N][Hkv][D]: the chunk (pre-fill) or the sequence (mix)
+    const void* v;
+    int N;
+    void* out;
+    const float* alpha;    // mix: [Hkv]
+    void* causal;          // mix: A_c and A_s, [B][N][Hq][D]
+    void* streaming;
+    float* lse;            // mix: [2][B][Hq][N]
+};
+
+template <int D, bool MIX>
+constexpr size_t forward_smem() {
+    return (3 * tile_floats<D>() + (MIX ? 2 : 1) * (size_t)TT * PS) * sizeof(float) + TT * sizeof(int);
+}
+
+template <typename T, int D, bool MIX, bool CAP>
+__global__ void __launch_bounds__(kTiledThreads) tiled_forward_kernel(const LayerArgs a, const CacheArgs c,
+                                                                      const TiledArgs s) {
+    extern __shared__ __align__(16) float sm[];
+    float* sQ = sm;
+    float* sK = sQ + tile_floats<D>();
+    float* sV = sK + tile_floats<D>();
+    float* sP = sV + tile_floats<D>();
+    float* sP2 = sP + TT * PS;                        // mix only
+    int* sPos = reinterpret_cast<int*>(sP + (MIX ? 2 : 1) * TT * PS);
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int b = blockIdx.z, slot = blockIdx.y / a.G, g = blockIdx.y % a.G;
+    const int q_idx = a.q_head0[slot] + g, kv_idx = a.kv_head[slot];
+    if (!bounds_ok(b < a.B && q_idx >= 0 && q_idx < a.Hq && kv_idx >= 0 && kv_idx < a.Hkv, c.status)) return;
+    const int r0 = (gridDim.x - 1 - blockIdx.x) * TT;  // the longest rows first
+    const int N = s.N;
+    const bool retrieval = MIX || slot < a.R;
+    int c0 = 0;
+    if constexpr (!MIX) {
+        c0 = c.seq_len[b];
+        if (c0 < 0 || (retrieval && c0 > a.capacity)) {
+            if (threadIdx.x == 0) atomicOr(c.status, DUO_DEV_BAD_LENGTH);
+            c0 = c0 < 0 ? 0 : a.capacity;
+        }
+    }
+    load_tile<T, D>(sQ, [&](int r) {
+        return r0 + r < N ? static_cast<const T*>(s.q) + (((size_t)b * N + r0 + r) * a.Hq + q_idx) * D : nullptr;
+    });
+    constexpr int W = D / 16;
+    float o[4][W], o2[MIX ? 4 : 1][W], m[4], l[4], m2[4], l2[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m[i] = m2[i] = kNegBig;
+        l[i] = l2[i] = 0.f;
+#pragma unroll
+        for (int e = 0; e < W; ++e) o[i][e] = 0.f;
+    }
+    if constexpr (MIX) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < W; ++e) o2[i][e] = 0.f;
+    }
+    const float sl = a.scale * kLog2e;
+    const int last = min(N, r0 + TT);                 // chunk rows some query of this tile sees
+    // key segments: 0 = prior keys from the caches, 1 and 2 = chunk rows
+    int begin[3] = {0, 0, 0}, end[3] = {0, last, 0};
+    if constexpr (!MIX) {
+        end[0] = retrieval ? c0 : a.W;
+        if (!retrieval && !a.stream_chunk) {
+            end[1] = max(0, min(last, a.sink - c0));  // the chunk's own sink tokens, then the recent band
+            begin[2] = max(end[1], r0 - a.recent + 1);
+            end[2] = last;
+        }
+    }
+    for (int seg = 0; seg < 3; ++seg) {
+        for (int k0 = begin[seg]; k0 < end[seg]; k0 += TT) {
+            const int nk = min(TT, end[seg] - k0);
+            __syncthreads();
+            auto row = [&](int r, const void* full, const void* ring, const void* chunk) -> const T* {
+                if (r >= nk) return nullptr;
+                const int kr = k0 + r;
+                if (MIX || seg > 0) return static_cast<const T*>(chunk) + (((size_t)b * N + kr) * a.Hkv + kv_idx) * D;
+                if (retrieval) return static_cast<const T*>(full) + (((size_t)b * a.R + slot) * a.capacity + kr) * D;
+                const int pos = c.ring_pos[(size_t)b * a.W + kr];
+                if (pos < 0 || pos >= c0) return nullptr;
+                return static_cast<const T*>(ring) + (((size_t)b * a.S + (slot - a.R)) * a.W + kr) * D;
+            };
+            load_tile<T, D>(sK, [&](int r) { return row(r, c.k_full, c.k_ring, s.k); });
+            load_tile<T, D>(sV, [&](int r) { return row(r, c.v_full, c.v_ring, s.v); });
+            if (threadIdx.x < TT) {
+                const int r = threadIdx.x;
+                int pos = -1;
+                if (r < nk) {
+                    pos = MIX || seg > 0 ? c0 + k0 + r : retrieval ? k0 + r : c.ring_pos[(size_t)b * a.W + k0 + r];
+                    if (!MIX && seg == 0 && pos >= c0) pos = -1;   // only tokens before the chunk come from the caches
+                }
+                sPos[r] = pos;
+            }
+            __syncthreads();
+            float x[4][4], x2[4][4];
+            tile_dot<D>(sQ, sK, tx, ty, x);
+            // the tile's keys are before the band of every row: no Lambda state (mix)
+            const bool lam_tile = MIX && (k0 < a.sink || r0 - (k0 + TT - 1) < a.recent);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int pos = sPos[tx + 16 * j];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int P = c0 + r0 + 4 * ty + i;
+                    const bool causal = pos >= 0 && pos <= P;
+                    const bool lam = causal && (pos < a.sink || (!MIX && a.stream_chunk ? pos >= c0 - a.recent
+                                                                                       : P - pos < a.recent));
+                    const float sc = score_log2<CAP, true>(x[i][j], sl, a.cap);
+                    x[i][j] = (MIX || retrieval ? causal : lam) ? sc : -INFINITY;
+                    x2[i][j] = lam ? sc : -INFINITY;
+                }
+            }
+            softmax_step<W>(x, m, l, o);
+            put_transposed(sP, x, tx, ty);
+            if constexpr (MIX) {
+                if (lam_tile) {
+                    softmax_step<W>(x2, m2, l2, o2);
+                    put_transposed(sP2, x2, tx, ty);
+                }
+            }
+            __syncthreads();
+            tile_acc<D>(sP, sV, tx, ty, o);
+            if constexpr (MIX) {
+                if (lam_tile) tile_acc<D>(sP2, sV, tx, ty, o2);
+            }
+        }
+    }
+    const float al = MIX ? s.alpha[kv_idx] : 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float ls = row_sum(l[i]), inv = ls > 0.f ? 1.f / ls : 0.f;
+        const float ls2 = MIX ? row_sum(l2[i]) : 0.f, inv2 = ls2 > 0.f ? 1.f / ls2 : 0.f;
+        const int r = r0 + 4 * ty + i;
+        if (r >= N) continue;
+        const size_t off = (((size_t)b * N + r) * a.Hq + q_idx) * D + 4 * tx;
+        if (MIX && tx == 0) {
+            const size_t at = ((size_t)b * a.Hq + q_idx) * N + r;
+            s.lse[at] = m[i] + log2f(ls);
+            s.lse[(size_t)a.B * a.Hq * N + at] = m2[i] + log2f(ls2);
+        }
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+            float v[4], v2[4], mix[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[e] = o[i][4 * j + e] * inv;
+                if constexpr (MIX) {
+                    v2[e] = o2[i][4 * j + e] * inv2;
+                    mix[e] = al * v[e] + (1.f - al) * v2[e];
+                }
+            }
+            T* out = static_cast<T*>(s.out) + off + 64 * j;
+            if constexpr (MIX) {
+                store_row<T, 4>(out, mix);
+                store_row<T, 4>(static_cast<T*>(s.causal) + off + 64 * j, v);
+                store_row<T, 4>(static_cast<T*>(s.streaming) + off + 64 * j, v2);
+            } else {
+                store_row<T, 4>(out, v);
+            }
+        }
+    }
+}
+
+// ----------------------------------------------------------------- backward
+//
+// The scheme of mix_grad.cu: keys outer for dK and dV, queries outer for dQ.
+
+struct TiledGradArgs {
+    const void* q;
+    const void* dout;
+    const void* k;
+    const void* v;
+    const float* stats;    // [B][Hq][4][n_pad]
+    const float* alpha;
+    void* d0;              // dK or dQ
+    void* d1;              // dV
+    const float* part;
+    int n_part;
+    float* dalpha;
+    int32_t* status;
+    int N, n_pad;
+};
+
+template <int D, bool KEYS>
+constexpr size_t grad_smem() {
+    return (4 * tile_floats<D>() + (KEYS ? 2 : 1) * (size_t)TT * PS + 4 * TT) * sizeof(float);
+}
+
+template <typename T, int D, bool KEYS, bool CAP>
+__global__ void __launch_bounds__(kTiledThreads) tiled_grad_kernel(const LayerArgs a, const TiledGradArgs p) {
+    extern __shared__ __align__(16) float sm[];
+    float* sX0 = sm;
+    float* sX1 = sX0 + tile_floats<D>();
+    float* sY0 = sX1 + tile_floats<D>();
+    float* sY1 = sY0 + tile_floats<D>();
+    float* sStat = sY1 + tile_floats<D>();            // [4][TT] of the tile's queries
+    float* sG = sStat + 4 * TT;                       // dS, transposed
+    float* sW = sG + TT * PS;                         // W, transposed (keys outer)
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int b = blockIdx.z, head = blockIdx.y, N = p.N;
+    const int heads = KEYS ? a.Hkv : a.Hq, kv = KEYS ? head : head / a.G;
+    const int nt = (N + TT - 1) / TT;
+    const int ot = KEYS ? blockIdx.x : nt - 1 - blockIdx.x;   // the longest first
+    auto rows = [&](const void* base, int H, int h, int tile) {
+        return [=](int r) -> const T* {
+            const int i = tile * TT + r;
+            return i < N ? static_cast<const T*>(base) + (((size_t)b * N + i) * H + h) * D : nullptr;
+        };
+    };
+    auto load_stats = [&](int qh, int tile) {
+        if (threadIdx.x < TT) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                sStat[r * TT + threadIdx.x] =
+                    p.stats[(((size_t)b * a.Hq + qh) * 4 + r) * p.n_pad + tile * TT + threadIdx.x];
+        }
+    };
+    if constexpr (KEYS) {
+        load_tile<T, D>(sX0, rows(p.k, a.Hkv, kv, ot));
+        load_tile<T, D>(sX1, rows(p.v, a.Hkv, kv, ot));
+    } else {
+        load_tile<T, D>(sX0, rows(p.q, a.Hq, head, ot));
+        load_tile<T, D>(sX1, rows(p.dout, a.Hq, head, ot));
+        load_stats(head, ot);
+    }
+    constexpr int W = D / 16;
+    float a0[4][W], a1[KEYS ? 4 : 1][W];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            a0[i][e] = 0.f;
+            if constexpr (KEYS) a1[i][e] = 0.f;
+        }
+    const float al = p.alpha[kv], sl = a.scale * kLog2e;
+    const float sgn_c = al < 0.f ? -1.f : 1.f, sgn_s = 1.f - al < 0.f ? -1.f : 1.f;
+    const int per_head = nt - ot, n_in = KEYS ? a.G * per_head : ot + 1;
+    for (int j0 = 0; j0 < n_in; ++j0) {
+        const int it = KEYS ? ot + j0 % per_head : j0, qh = KEYS ? kv * a.G + j0 / per_head : head;
+        __syncthreads();
+        if constexpr (KEYS) {
+            load_tile<T, D>(sY0, rows(p.q, a.Hq, qh, it));
+            load_tile<T, D>(sY1, rows(p.dout, a.Hq, qh, it));
+            load_stats(qh, it);
+        } else {
+            load_tile<T, D>(sY0, rows(p.k, a.Hkv, kv, it));
+            load_tile<T, D>(sY1, rows(p.v, a.Hkv, kv, it));
+        }
+        __syncthreads();
+        float x[4][4], d[4][4];
+        tile_dot<D>(sX0, sY0, tx, ty, x);
+        tile_dot<D>(sX1, sY1, tx, ty, d);
+        const int qt = KEYS ? it : ot, kt = KEYS ? ot : it;
+        const bool lam_tile = kt * TT < a.sink || (qt - kt) * TT - (TT - 1) < a.recent;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int orow = 4 * ty + i, icol = tx + 16 * j;
+                const int qr = KEYS ? icol : orow;                    // the query's row in its tile
+                const int query = qt * TT + qr, key = kt * TT + (KEYS ? orow : icol);
+                float slope = 1.f, s;
+                if constexpr (CAP) {
+                    const float t = tanhf(x[i][j] * a.cap.k);
+                    slope = fmaf(-t, t, 1.f);
+                    s = t * a.cap.c2;
+                } else {
+                    s = x[i][j] * sl;
+                }
+                const bool causal = key <= query;
+                const float wc = causal ? sgn_c * exp2f(s - sStat[qr]) : 0.f;
+                float ws = 0.f;
+                if (lam_tile && causal && (key < a.sink || query - key < a.recent))
+                    ws = sgn_s * exp2f(s - sStat[2 * TT + qr]);
+                x[i][j] = wc + ws;
+                d[i][j] = slope * (wc * (d[i][j] - sStat[TT + qr]) + ws * (d[i][j] - sStat[3 * TT + qr]));
+            }
+        }
+        put_transposed(sG, d, tx, ty);
+        if constexpr (KEYS) put_transposed(sW, x, tx, ty);
+        __syncthreads();
+        tile_acc<D>(sG, sY0, tx, ty, a0);
+        if constexpr (KEYS) tile_acc<D>(sW, sY1, tx, ty, a1);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = ot * TT + 4 * ty + i;
+        if (r >= N || !bounds_ok(b < a.B && head < heads, p.status)) continue;
+        const size_t off = (((size_t)b * N + r) * heads + head) * D + 4 * tx;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = a0[i][4 * j + e] * a.scale;
+            store_row<T, 4>(static_cast<T*>(p.d0) + off + 64 * j, v);
+            if constexpr (KEYS) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = a1[i][4 * j + e];
+                store_row<T, 4>(static_cast<T*>(p.d1) + off + 64 * j, v);
+            }
+        }
+    }
+    if (KEYS && ot == 0 && b == 0 && threadIdx.x < 32)
+        sum_shares(p.part + (size_t)kv * p.n_part, p.n_part, &p.dalpha[kv], threadIdx.x);
+}
+
+template <typename T, int D, bool MIX, bool CAP>
+cudaError_t launch_forward(const LayerArgs& a, const CacheArgs& c, const TiledArgs& s, cudaStream_t st) {
+    constexpr size_t smem = forward_smem<D, MIX>();
+    static std::atomic<unsigned long long> configured{0};
+    const cudaError_t e = smem_limit_once(tiled_forward_kernel<T, D, MIX, CAP>, (int)smem, configured);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)((s.N + TT - 1) / TT), (unsigned)a.Hq, (unsigned)a.B);
+    tiled_forward_kernel<T, D, MIX, CAP><<<grid, kTiledThreads, smem, st>>>(a, c, s);
+    return cudaGetLastError();
+}
+
+template <typename T, int D, bool KEYS, bool CAP>
+cudaError_t launch_grad(const LayerArgs& a, const TiledGradArgs& p, cudaStream_t st) {
+    constexpr size_t smem = grad_smem<D, KEYS>();
+    static std::atomic<unsigned long long> configured{0};
+    const cudaError_t e = smem_limit_once(tiled_grad_kernel<T, D, KEYS, CAP>, (int)smem, configured);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)((p.N + TT - 1) / TT), (unsigned)(KEYS ? a.Hkv : a.Hq), (unsigned)a.B);
+    tiled_grad_kernel<T, D, KEYS, CAP><<<grid, kTiledThreads, smem, st>>>(a, p);
+    return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_grads(const LayerArgs& a, TiledGradArgs p, void* dq, cudaStream_t st) {
+    const cudaError_t e = a.cap.on ? launch_grad<T, D, true, true>(a, p, st) : launch_grad<T, D, true, false>(a, p, st);
+    if (e != cudaSuccess) return e;
+    p.d0 = dq;
+    p.d1 = nullptr;
+    return a.cap.on ? launch_grad<T, D, false, true>(a, p, st) : launch_grad<T, D, false, false>(a, p, st);
+}
+
+}  // namespace
+
+cudaError_t launch_tiled_prefill(const LayerArgs& a, const CacheArgs& c, const void* q, const void* k, const void* v,
+                                 int C, void* out, cudaStream_t st) {
+    if (a.B > 65535 || !a.cap.on) return cudaErrorInvalidConfiguration;
+    const TiledArgs s{q, k, v, C, out, nullptr, nullptr, nullptr, nullptr};
+    if (a.dtype == DUO_BF16) {
+        if (a.D == 128) return launch_forward<__nv_bfloat16, 128, false, true>(a, c, s, st);
+        return launch_forward<__nv_bfloat16, 64, false, true>(a, c, s, st);
+    }
+    if (a.D == 128) return launch_forward<float, 128, false, true>(a, c, s, st);
+    return launch_forward<float, 64, false, true>(a, c, s, st);
+}
+
+cudaError_t launch_tiled_mix(const LayerArgs& a, const float* alpha, const void* q, const void* k, const void* v, int N,
+                             void* out, void* causal, void* streaming, float* lse, int32_t* status, cudaStream_t st) {
+    if (a.B > 65535) return cudaErrorInvalidConfiguration;
+    const TiledArgs s{q, k, v, N, out, alpha, causal, streaming, lse};
+    CacheArgs c{};
+    c.status = status;
+    auto run = [&](auto t, auto d) {
+        using T = decltype(t);
+        constexpr int D = decltype(d)::value;
+        return a.cap.on ? launch_forward<T, D, true, true>(a, c, s, st) : launch_forward<T, D, true, false>(a, c, s, st);
+    };
+    using D64 = std::integral_constant<int, 64>;
+    using D128 = std::integral_constant<int, 128>;
+    if (a.dtype == DUO_BF16) return a.D == 128 ? run(__nv_bfloat16{}, D128{}) : run(__nv_bfloat16{}, D64{});
+    return a.D == 128 ? run(float{}, D128{}) : run(float{}, D64{});
+}
+
+cudaError_t launch_tiled_mix_grad(const LayerArgs& a, const MixGradArgs& g, int N, cudaStream_t st) {
+    if (a.B > 65535) return cudaErrorInvalidConfiguration;
+    const MixGradPlan pl = mix_grad_plan(a, N);
+    const TiledGradArgs p{g.q, g.dout, g.k, g.v, g.stats, g.alpha, g.dk, g.dv, g.part, a.B * pl.chunks, g.dalpha,
+                          g.status, N, pl.n_pad};
+    if (a.dtype == DUO_BF16) {
+        if (a.D == 128) return launch_grads<__nv_bfloat16, 128>(a, p, g.dq, st);
+        return launch_grads<__nv_bfloat16, 64>(a, p, g.dq, st);
+    }
+    if (a.D == 128) return launch_grads<float, 128>(a, p, g.dq, st);
+    return launch_grads<float, 64>(a, p, g.dq, st);
+}
+
+}  // namespace duo

@@ -119,6 +119,12 @@ _lib_decode_step_capped = _fn("duo_decode_step_capped", ctypes.c_int, _DESC, _ST
                               _P, ctypes.c_size_t, _P)
 _lib_prefill_capped = _fn("duo_prefill_chunk_capped", ctypes.c_int, _DESC, _STATE, ctypes.c_float, _P, _P, _P, _I32,
                           _P, _P, ctypes.c_size_t, _P)
+_lib_mix_saved = _fn("duo_gated_mix_saved_bytes", ctypes.c_size_t, _DESC, _I32)
+_lib_mix_grad_ws = _fn("duo_gated_mix_grad_workspace_bytes", ctypes.c_size_t, _DESC, _I32)
+_lib_mix_train = _fn("duo_gated_mix_train", ctypes.c_int, _DESC, _P, ctypes.c_float, _P, _P, _P, _I32, _P, _P,
+                     ctypes.c_size_t, _P, _P)
+_lib_mix_full_grad = _fn("duo_gated_mix_grad", ctypes.c_int, _DESC, _P, ctypes.c_float, _P, _P, _P, _I32, _P,
+                         ctypes.c_size_t, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P, _P)
 NOALLOC_SCRATCH_BYTES = 2 << 20
 
 
@@ -306,6 +312,29 @@ def gated_mix(desc, alpha, q, k, v, N: int, out, status, stream=None) -> None:
 def gated_mix_grad_alpha(desc, q, k, v, N: int, dout, dalpha, status, stream=None) -> None:
     _check(_lib_mix_grad(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), N, _ptr(dout), _ptr(dalpha), _ptr(status),
                          _stream(stream)), "duo_gated_mix_grad_alpha")
+
+
+def gated_mix_saved_bytes(desc: LayerDesc, N: int) -> int:
+    return int(_lib_mix_saved(ctypes.byref(desc), N))
+
+
+def gated_mix_grad_workspace_bytes(desc: LayerDesc, N: int) -> int:
+    return int(_lib_mix_grad_ws(ctypes.byref(desc), N))
+
+
+def gated_mix_train(desc, alpha, cap: float, q, k, v, N: int, out, saved, saved_bytes: int, status,
+                    stream=None) -> None:
+    """gated_mix (scores capped when cap > 0) that keeps in `saved` what gated_mix_grad needs."""
+    _check(_lib_mix_train(ctypes.byref(desc), _ptr(alpha), cap, _ptr(q), _ptr(k), _ptr(v), N, _ptr(out), _ptr(saved),
+                          saved_bytes, _ptr(status), _stream(stream)), "duo_gated_mix_train")
+
+
+def gated_mix_grad(desc, alpha, cap: float, q, k, v, N: int, saved, saved_bytes: int, dout, dq, dk, dv, dalpha,
+                   workspace, ws_bytes: int, status, stream=None) -> None:
+    """Gradients of q, k, v and the gates from that of gated_mix_train's output."""
+    _check(_lib_mix_full_grad(ctypes.byref(desc), _ptr(alpha), cap, _ptr(q), _ptr(k), _ptr(v), N, _ptr(saved),
+                              saved_bytes, _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dalpha), _ptr(workspace),
+                              ws_bytes, _ptr(status), _stream(stream)), "duo_gated_mix_grad")
 
 
 def wait_probe(status, limit_us: int, stream=None) -> None:

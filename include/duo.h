@@ -571,6 +571,45 @@ duo_status duo_gated_mix_grad_alpha(const duo_layer_desc* desc, const void* q, c
                                     duo_stream_t stream);
 
 /*
+ * duo_gated_mix_train, duo_gated_mix_grad -- a training step through the gated
+ * mix: the forward pass that keeps what the backward pass needs, and the
+ * gradients of q, k, v and the gates.  Head identification trains the gates
+ * only [Review S3 "Retrieval-head identification"], but the loss sits behind
+ * the last layer, so the gates of a layer get their gradient through the
+ * queries, keys and values of the layers above it.
+ *
+ * Forward: out as duo_gated_mix (alpha, q, k, v, out, status as there, model
+ * head order); with cap > 0 the scores are capped before both masks, as
+ * duo_prefill_chunk_capped caps them (0: not capped).
+ *   saved: duo_gated_mix_saved_bytes(desc, N) bytes, 16-byte aligned: both
+ *   attentions in the layer's dtype and the rows' log-sums, for
+ *   duo_gated_mix_grad with the same desc, alpha, cap, q, k, v and N.
+ * Backward: dout [B][N][Hq][d] -> dq [B][N][Hq][d], dk, dv [B][N][Hkv][d] in
+ *   the layer's dtype (the heads of a group summed in fp32 and rounded once)
+ *   and dalpha [Hkv] fp32; all overwritten.  Gates may have any finite value.
+ *   workspace: duo_gated_mix_grad_workspace_bytes(desc, N) bytes, 16-byte
+ *   aligned, no initialisation; calls that can overlap on the GPU need one each.
+ *   No atomics: results do not depend on the order in which CTAs run.
+ * Outputs, saved and workspace must not overlap each other or an input.
+ * bf16 with d = 128 and sink + recent <= 128 runs on the tcgen05 tensor cores
+ * (the weights and their gradients rounded to bf16 as MMA operands, sums in
+ * fp32); the rest on the CUDA cores in fp32.
+ * N == 0: nothing is done but that dalpha is zeroed.
+ * status: as for duo_gated_mix.
+ * Errors: DUO_ERR_INVALID_ARG, DUO_ERR_SHAPE, DUO_ERR_CAPACITY (saved,
+ * workspace), DUO_ERR_UNSUPPORTED, DUO_ERR_CUDA.
+ */
+size_t duo_gated_mix_saved_bytes(const duo_layer_desc* desc, int32_t N);
+size_t duo_gated_mix_grad_workspace_bytes(const duo_layer_desc* desc, int32_t N);
+duo_status duo_gated_mix_train(const duo_layer_desc* desc, const float* alpha, float cap, const void* q, const void* k,
+                               const void* v, int32_t N, void* out, void* saved, size_t saved_bytes, int32_t* status,
+                               duo_stream_t stream);
+duo_status duo_gated_mix_grad(const duo_layer_desc* desc, const float* alpha, float cap, const void* q, const void* k,
+                              const void* v, int32_t N, const void* saved, size_t saved_bytes, const void* dout, void* dq,
+                              void* dk, void* dv, float* dalpha, void* workspace, size_t ws_bytes, int32_t* status,
+                              duo_stream_t stream);
+
+/*
  * duo_exp2_fma_probe -- y[i] = the pre-fill softmax's FMA-pipe 2^x of x[i]
  * (Cody-Waite range reduction to x = n + f, f in [-0.5, 0.5], a fitted cubic
  * for 2^f and n added to the exponent field; inputs below -125, -inf

@@ -119,3 +119,69 @@ def test_capped_calls_refuse_what_the_plain_calls_refuse(duo):
     _refused(duo, "ERR_UNSUPPORTED", duo.prefill_chunk_capped, paged,
              _state(duo, page_table=144, max_pages=16, n_pages=16), 30.0, Q, K, V, 3, QO)
     assert "duo_prefill_chunk_capped" in duo.last_error()
+
+
+# ---------------------------------------------------------------------------
+# The gated mix's training step
+# ---------------------------------------------------------------------------
+
+ALPHA, OUT, SAVED, DO, DQ, DK, DV, DA, WS, STATUS = (i << 28 for i in range(1, 11))
+
+
+def _mix_sizes(duo, d, N):
+    return duo.gated_mix_saved_bytes(d, N), duo.gated_mix_grad_workspace_bytes(d, N)
+
+
+def test_mix_buffer_sizes(duo):
+    up = lambda x: -(-x // 256) * 256  # noqa: E731
+    for dtype, es in ((duo.BF16, 2), (duo.FP32, 4)):
+        d = duo.desc_init(3, 8, 4, 64, dtype, [0, 1, 2, 3], 4)
+        saved, ws = _mix_sizes(duo, d, 130)
+        assert saved == 2 * up(3 * 130 * 8 * 64 * es) + up(2 * 3 * 130 * 8 * 4)
+        assert ws == up(3 * 8 * 4 * 256 * 4) + up(4 * 3 * 8 * 4)       # rows padded to 256, a share per 32 of them
+    assert _mix_sizes(duo, d, -1) == (0, 0)
+    d.head_dim = 96
+    assert _mix_sizes(duo, d, 130) == (0, 0)
+
+
+def test_mix_train_rejects(duo):
+    d, N = _desc(duo), 10
+    saved, _ = _mix_sizes(duo, d, N)
+    good = dict(alpha=ALPHA, cap=30.0, q=Q, k=K, v=V, N=N, out=OUT, saved=SAVED, saved_bytes=saved, status=STATUS)
+
+    def refused(status, **kw):
+        _refused(duo, status, duo.gated_mix_train, d, *{**good, **kw}.values())
+
+    for name in ("alpha", "q", "k", "v", "out", "saved", "status"):
+        refused("ERR_INVALID_ARG", **{name: None})
+    for name in ("q", "k", "v", "out", "saved"):
+        refused("ERR_INVALID_ARG", **{name: good[name] + 8})
+    for cap in (-1.0, float("nan"), float("inf"), 1e-7):
+        refused("ERR_INVALID_ARG", cap=cap)
+    refused("ERR_SHAPE", N=-1)
+    refused("ERR_CAPACITY", saved_bytes=saved - 1)
+    for kw in (dict(out=Q), dict(out=K - 16), dict(saved=V - 16), dict(saved=Q + 16), dict(out=SAVED), dict(out=SAVED + saved - 16)):
+        refused("ERR_INVALID_ARG", **kw)
+    duo.gated_mix_train(d, *{**good, "N": 0, "saved_bytes": 0}.values(), stream=0)
+
+
+def test_mix_grad_rejects(duo):
+    d, N = _desc(duo), 10
+    saved, ws = _mix_sizes(duo, d, N)
+    good = dict(alpha=ALPHA, cap=0.0, q=Q, k=K, v=V, N=N, saved=SAVED, saved_bytes=saved, dout=DO, dq=DQ, dk=DK, dv=DV, dalpha=DA,
+                workspace=WS, ws_bytes=ws, status=STATUS)
+
+    def refused(status, **kw):
+        _refused(duo, status, duo.gated_mix_grad, d, *{**good, **kw}.values())
+
+    for name in ("alpha", "q", "k", "v", "saved", "dout", "dq", "dk", "dv", "dalpha", "workspace", "status"):
+        refused("ERR_INVALID_ARG", **{name: None})
+    for name in ("q", "k", "v", "saved", "dout", "dq", "dk", "dv", "workspace"):
+        refused("ERR_INVALID_ARG", **{name: good[name] + 8})
+    refused("ERR_SHAPE", N=-3)
+    refused("ERR_CAPACITY", saved_bytes=saved - 1)
+    refused("ERR_CAPACITY", ws_bytes=ws - 1)
+    refused("ERR_INVALID_ARG", cap=-2.0)
+    for kw in (dict(dq=Q), dict(dq=DO), dict(dk=K), dict(dv=V - 16), dict(dk=SAVED + 256), dict(workspace=SAVED), dict(dk=DQ),
+               dict(dv=DK), dict(workspace=DV + 16), dict(workspace=DO - 16)):
+        refused("ERR_INVALID_ARG", **kw)
