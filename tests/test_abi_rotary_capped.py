@@ -149,8 +149,8 @@ def test_mix_train_rejects(duo):
     saved, _ = _mix_sizes(duo, d, N)
     good = dict(alpha=ALPHA, cap=30.0, q=Q, k=K, v=V, N=N, out=OUT, saved=SAVED, saved_bytes=saved, status=STATUS)
 
-    def refused(status, **kw):
-        _refused(duo, status, duo.gated_mix_train, d, *{**good, **kw}.values())
+    def refused(expected, **kw):
+        _refused(duo, expected, duo.gated_mix_train, d, *{**good, **kw}.values())
 
     for name in ("alpha", "q", "k", "v", "out", "saved", "status"):
         refused("ERR_INVALID_ARG", **{name: None})
@@ -171,8 +171,8 @@ def test_mix_grad_rejects(duo):
     good = dict(alpha=ALPHA, cap=0.0, q=Q, k=K, v=V, N=N, saved=SAVED, saved_bytes=saved, dout=DO, dq=DQ, dk=DK, dv=DV, dalpha=DA,
                 workspace=WS, ws_bytes=ws, status=STATUS)
 
-    def refused(status, **kw):
-        _refused(duo, status, duo.gated_mix_grad, d, *{**good, **kw}.values())
+    def refused(expected, **kw):
+        _refused(duo, expected, duo.gated_mix_grad, d, *{**good, **kw}.values())
 
     for name in ("alpha", "q", "k", "v", "saved", "dout", "dq", "dk", "dv", "dalpha", "workspace", "status"):
         refused("ERR_INVALID_ARG", **{name: None})
