@@ -344,17 +344,6 @@ duo_status rope_args(const duo_layer_desc* desc, const duo_rope* rope, int inver
     return DUO_OK;
 }
 
-// What duo_gated_mix_train keeps: A_c and A_s in the layer's dtype, then both
-// lse rows; every part starts on a multiple of 256 bytes.
-struct MixSaved {
-    size_t streaming, lse, bytes;
-};
-MixSaved mix_saved(const duo_layer_desc* d, int32_t N) {
-    const size_t heads = (size_t)d->batch * N * d->n_q_heads;
-    const size_t attn = (heads * d->head_dim * (d->dtype == DUO_BF16 ? 2 : 4) + 255) / 256 * 256;
-    return {attn, 2 * attn, 2 * attn + (2 * heads * sizeof(float) + 255) / 256 * 256};
-}
-
 // The two single-mask layers of a gated mix (every KV head in the streaming /
 // the retrieval block, model head order, no cache).
 void mix_layers(duo::LayerArgs& a, duo::LayerArgs& as, duo::LayerArgs& ac) {
@@ -373,6 +362,21 @@ void mix_layers(duo::LayerArgs& a, duo::LayerArgs& as, duo::LayerArgs& ac) {
     ac = a;
     ac.R = a.Hkv;
     ac.S = 0;
+}
+
+// What duo_gated_mix_train keeps, every part on a multiple of 256 bytes: both
+// log-sums of every row; then, for the tensor-core passes, A_s in bf16 (used
+// within the forward pass only), else A_c and A_s in fp32.
+struct MixSaved {
+    bool tc;
+    size_t streaming, causal, bytes;   // the log-sums are at 0
+};
+MixSaved mix_saved(const duo::LayerArgs& as, const duo::LayerArgs& ac, int32_t N) {
+    const size_t rows = (size_t)as.B * N * as.Hq;
+    const size_t lse = (2 * rows * sizeof(float) + 255) / 256 * 256;
+    const bool tc = duo::prefill_tc_supported(as) && duo::prefill_tc_supported(ac);
+    const size_t attn = (rows * as.D * (tc ? 2 : 4) + 255) / 256 * 256;
+    return {tc, lse, lse + attn, lse + (tc ? 1 : 2) * attn};
 }
 
 bool overlap(const void* x, size_t nx, const void* y, size_t ny) {
@@ -735,7 +739,10 @@ duo_status duo_gated_mix_grad_alpha(const duo_layer_desc* desc, const void* q, c
 
 size_t duo_gated_mix_saved_bytes(const duo_layer_desc* desc, int32_t N) {
     if (check_desc(desc) != DUO_OK || N < 0) return 0;
-    return mix_saved(desc, N).bytes;
+    duo::LayerArgs a, as, ac;
+    fill_args(desc, a);
+    mix_layers(a, as, ac);
+    return mix_saved(as, ac, N).bytes;
 }
 
 size_t duo_gated_mix_grad_workspace_bytes(const duo_layer_desc* desc, int32_t N) {
@@ -759,7 +766,8 @@ duo_status duo_gated_mix_train(const duo_layer_desc* desc, const float* alpha, f
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(saved))
         return fail(DUO_ERR_INVALID_ARG, "duo_gated_mix_train tensors must be 16-byte aligned");
     if (N == 0) return ok();
-    const MixSaved sv = mix_saved(desc, N);
+    mix_layers(a, as, ac);
+    const MixSaved sv = mix_saved(as, ac, N);
     if (saved_bytes < sv.bytes)
         return fail(DUO_ERR_CAPACITY, "saved holds %zu bytes, duo_gated_mix_train needs %zu", saved_bytes, sv.bytes);
     const size_t es = desc->dtype == DUO_BF16 ? 2 : 4, rows = (size_t)desc->batch * N;
@@ -768,12 +776,10 @@ duo_status duo_gated_mix_train(const duo_layer_desc* desc, const float* alpha, f
         if (overlap(out, nq, x, x == q ? nq : nkv) || overlap(saved, sv.bytes, x, x == q ? nq : nkv))
             return fail(DUO_ERR_INVALID_ARG, "duo_gated_mix_train: out or saved overlaps q, k or v");
     if (overlap(out, nq, saved, sv.bytes)) return fail(DUO_ERR_INVALID_ARG, "duo_gated_mix_train: out overlaps saved");
-    void* causal = saved;
     void* streaming = static_cast<uint8_t*>(saved) + sv.streaming;
-    float* lse = reinterpret_cast<float*>(static_cast<uint8_t*>(saved) + sv.lse);
-    mix_layers(a, as, ac);
+    float* lse = static_cast<float*>(saved);
     cudaError_t e;
-    if (duo::prefill_tc_supported(as) && duo::prefill_tc_supported(ac)) {
+    if (sv.tc) {
         duo::CacheArgs none{};
         none.status = status;
         duo::EpiArgs keep;
@@ -784,12 +790,13 @@ duo_status duo_gated_mix_train(const duo_layer_desc* desc, const float* alpha, f
         mix.mode = duo::EPI_MIX_KEEP;
         mix.alpha = alpha;
         mix.streaming = streaming;
-        mix.causal = causal;
         mix.lse = lse;
         if (e == cudaSuccess)
             e = duo::launch_prefill_tc(ac, none, q, k, v, N, out, nullptr, 0, (cudaStream_t)stream, &mix);
     } else {
-        e = duo::launch_tiled_mix(ac, alpha, q, k, v, N, out, causal, streaming, lse, status, (cudaStream_t)stream);
+        e = duo::launch_tiled_mix(ac, alpha, q, k, v, N, out,
+                                  reinterpret_cast<float*>(static_cast<uint8_t*>(saved) + sv.causal),
+                                  static_cast<float*>(streaming), lse, status, (cudaStream_t)stream);
     }
     return e == cudaSuccess ? ok() : cuda_fail(e, "duo_gated_mix_train");
 }
@@ -813,7 +820,8 @@ duo_status duo_gated_mix_grad(const duo_layer_desc* desc, const float* alpha, fl
         const cudaError_t e = cudaMemsetAsync(dalpha, 0, sizeof(float) * desc->n_kv_heads, (cudaStream_t)stream);
         return e == cudaSuccess ? ok() : cuda_fail(e, "duo_gated_mix_grad");
     }
-    const MixSaved sv = mix_saved(desc, N);
+    mix_layers(a, as, ac);
+    const MixSaved sv = mix_saved(as, ac, N);
     if (saved_bytes < sv.bytes)
         return fail(DUO_ERR_CAPACITY, "saved holds %zu bytes, duo_gated_mix_train writes %zu", saved_bytes, sv.bytes);
     const duo::MixGradPlan plan = duo::mix_grad_plan(a, N);
@@ -840,9 +848,9 @@ duo_status duo_gated_mix_grad(const duo_layer_desc* desc, const float* alpha, fl
     g.k = k;
     g.v = v;
     g.dout = dout;
-    g.causal = sb;
-    g.streaming = sb + sv.streaming;
-    g.lse = reinterpret_cast<const float*>(sb + sv.lse);
+    g.lse = static_cast<const float*>(saved);
+    g.streaming = reinterpret_cast<const float*>(sb + sv.streaming);
+    g.causal = reinterpret_cast<const float*>(sb + sv.causal);
     g.alpha = alpha;
     g.stats = static_cast<float*>(workspace);
     g.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.part_offset);
@@ -851,12 +859,8 @@ duo_status duo_gated_mix_grad(const duo_layer_desc* desc, const float* alpha, fl
     g.dv = dv;
     g.dalpha = dalpha;
     g.status = status;
-    mix_layers(a, as, ac);
-    cudaError_t e = duo::launch_mix_stats(ac, g, N, (cudaStream_t)stream);
-    if (e == cudaSuccess)
-        e = duo::prefill_tc_supported(as) && duo::prefill_tc_supported(ac)
-                ? duo::launch_mix_grad_tc(ac, g, N, (cudaStream_t)stream)
-                : duo::launch_tiled_mix_grad(ac, g, N, (cudaStream_t)stream);
+    const cudaError_t e = sv.tc ? duo::launch_mix_grad_tc(ac, g, N, (cudaStream_t)stream)
+                                : duo::launch_tiled_mix_grad(ac, g, N, (cudaStream_t)stream);
     return e == cudaSuccess ? ok() : cuda_fail(e, "duo_gated_mix_grad");
 }
 

@@ -109,7 +109,7 @@ size_t prefill_workspace_bytes(const LayerArgs& a, int max_chunk);
 //            the rows is added into dalpha[kv] (atomics);
 //   EPI_KEEP: the result is stored to out and each row's lse kept;
 //   EPI_MIX_KEEP: as EPI_MIX, with the streaming attention read from
-//            `streaming`, and the result itself and its lse kept too.
+//            `streaming`, and the result's lse kept too.
 enum { EPI_STORE = 0, EPI_MIX = 1, EPI_DOT = 2, EPI_KEEP = 3, EPI_MIX_KEEP = 4 };
 struct EpiArgs {
     int mode = EPI_STORE;
@@ -118,7 +118,6 @@ struct EpiArgs {
     float* dalpha = nullptr;           // EPI_DOT: [Hkv] accumulated
     float sign = 0.f;                  // EPI_DOT: +1 or -1
     const void* streaming = nullptr;   // EPI_MIX_KEEP: [B][C][Hq][d]
-    void* causal = nullptr;            // EPI_MIX_KEEP: [B][C][Hq][d], the result before the mix
     float* lse = nullptr;              // EPI_KEEP, EPI_MIX_KEEP: [B][Hq][C], log2 of the sum of 2^score
 };
 // qscale non-NULL: the full cache holds 8- or 4-bit codes (as bf16 values)
@@ -133,28 +132,26 @@ cudaError_t launch_prefill_tc(const LayerArgs& a, const CacheArgs& c, const void
 cudaError_t launch_tiled_prefill(const LayerArgs& a, const CacheArgs& c, const void* q, const void* k, const void* v,
                                  int C, void* out, cudaStream_t st);
 cudaError_t launch_tiled_mix(const LayerArgs& a, const float* alpha, const void* q, const void* k, const void* v, int N,
-                             void* out, void* causal, void* streaming, float* lse, int32_t* status, cudaStream_t st);
-// Backward pass of the gated mix: the rows' statistics (both paths), then dK /
-// dV / dalpha and dQ on the tensor cores (mix_grad.cu) or in 64 x 64 tiles.
+                             void* out, float* causal, float* streaming, float* lse, int32_t* status, cudaStream_t st);
+// Backward pass of the gated mix, on the tensor cores (mix_grad.cu) or in
+// 64 x 64 tiles: the rows' statistics, then dK, dV and dalpha, then dQ.
 struct MixGradPlan {
-    int n_pad;             // rows of a head's statistics: N rounded up to 128
-    int chunks;            // shares of dalpha per sequence and KV head
+    int n_tiles, n_pad;    // 128-row tiles of a head's statistics, and their rows
     size_t part_offset;    // bytes from workspace start to the shares
     size_t bytes;
 };
 struct MixGradArgs {
     const void *q, *k, *v, *dout;
-    const void *causal, *streaming;    // A_c, A_s of the forward pass
-    const float* lse;                  // [2][B][Hq][N]
+    const float* lse;                  // [2][B][Hq][N] of the forward pass: causal, Lambda
     const float* alpha;
     float* stats;                      // workspace: [B][Hq][4][n_pad]
-    float* part;                       // workspace: [Hkv][B * chunks]
+    const float *causal, *streaming;   // 64 x 64 tiles: A_c, A_s of the forward pass, [B][N][Hq][d]
+    float* part;                       // workspace: shares of dalpha, by KV head
     void *dq, *dk, *dv;
     float* dalpha;
     int32_t* status;
 };
 MixGradPlan mix_grad_plan(const LayerArgs& a, int N);
-cudaError_t launch_mix_stats(const LayerArgs& a, const MixGradArgs& g, int N, cudaStream_t s);
 cudaError_t launch_mix_grad_tc(const LayerArgs& a, const MixGradArgs& g, int N, cudaStream_t s);
 cudaError_t launch_tiled_mix_grad(const LayerArgs& a, const MixGradArgs& g, int N, cudaStream_t st);
 cudaError_t launch_exp2_fma_probe(const float* x, float* y, int64_t n, cudaStream_t s);

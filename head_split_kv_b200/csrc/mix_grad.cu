@@ -17,9 +17,21 @@
 // lse that the forward pass kept; a and 1 - a ride in the exponent:
 // |a| P_c = 2^(s - (lse_c - log2 |a|)).
 //
-// mix_stats_kernel writes each row's {lse_c - log2|a|, D_c, lse_s - log2|1-a|,
-// D_s} and its share of da; rows past the sequence get lse = +inf, so that
-// their weights are 0 everywhere below.
+// One row of statistics serves both attentions.  P_c and P_s of a row are the
+// same exponentials over different sums, so for a key that both see
+//   W = 2^(s - lse*)  with  2^-lse* = a 2^-lse_c + (1 - a) 2^-lse_s,
+//   dS ~ W (dP - D*)  with  D* the mean of D_c and D_s under those two shares,
+// and a tile with sink or recent keys costs a choice between two (lse, D)
+// pairs, not a second exponential.  (A gate outside [0, 1] makes the shares
+// differ in sign; those heads take both exponentials there.)
+//
+// mix_stats_kernel computes D_c and D_s as sums of P dP in fp32 over the same
+// tiles, and corrects the log-sums by the sum of P: dout . A from the stored
+// bf16 attention would carry the roundings of P and of A, which where a row's
+// softmax is peaked are as large as dP - D itself (dq and dk were 3.4 times as
+// far from fp64 as their rounding).  It writes each row's {lse_c - log2 a, D_c,
+// lse*, D*} and its share of da; rows past the sequence get lse = +inf, so that
+// their weights are 0 below.
 //
 // mix_grad_kernel, twice: with keys outer (dK, dV: a CTA owns 128 keys of one
 // KV head and walks the 128-query tiles at or below the diagonal of every
@@ -50,75 +62,6 @@
 namespace duo {
 namespace {
 
-// ------------------------------------------------------------ row statistics
-
-constexpr int kStatRows = 32;      // rows of a CTA, each with the G heads of one KV head
-constexpr int kStatWarps = 8;
-
-struct StatArgs {
-    const void* dout;      // [B][N][Hq][d]
-    const void* causal;    // A_c, [B][N][Hq][d]
-    const void* streaming; // A_s
-    const float* lse;      // [2][B][Hq][N]: causal, streaming
-    const float* alpha;    // [Hkv]
-    float* stats;          // [B][Hq][4][n_pad]
-    float* part;           // [Hkv][B * chunks] shares of dalpha
-    int N, n_pad, chunks;
-};
-
-template <typename T, int D>
-__global__ void __launch_bounds__(kStatWarps * 32) mix_stats_kernel(const LayerArgs a, const StatArgs x) {
-    constexpr int E = D / 32;      // elements a lane
-    const int chunk = blockIdx.x, kv = blockIdx.y, b = blockIdx.z;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const float al = x.alpha[kv];
-    const float shift_c = -log2f(fabsf(al)), shift_s = -log2f(fabsf(1.f - al));   // +inf for a closed gate
-    const size_t plane = (size_t)a.B * a.Hq * x.N;
-    float share = 0.f;
-    for (int it = warp; it < kStatRows * a.G; it += kStatWarps) {
-        const int i = chunk * kStatRows + it / a.G, h = kv * a.G + it % a.G;
-        if (i >= x.n_pad) break;
-        float* st = x.stats + ((size_t)b * a.Hq + h) * 4 * x.n_pad + i;
-        if (i >= x.N) {
-            if (lane == 0) {
-                st[0] = st[2 * (size_t)x.n_pad] = INFINITY;
-                st[x.n_pad] = st[3 * (size_t)x.n_pad] = 0.f;
-            }
-            continue;
-        }
-        const size_t o = (((size_t)b * x.N + i) * a.Hq + h) * D + lane * E;
-        float dc = 0.f, ds = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float g = Elem<T>::to_f32(static_cast<const T*>(x.dout)[o + e]);
-            dc = fmaf(g, Elem<T>::to_f32(static_cast<const T*>(x.causal)[o + e]), dc);
-            ds = fmaf(g, Elem<T>::to_f32(static_cast<const T*>(x.streaming)[o + e]), ds);
-        }
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) {
-            dc += __shfl_xor_sync(0xffffffffu, dc, s);
-            ds += __shfl_xor_sync(0xffffffffu, ds, s);
-        }
-        if (lane == 0) {
-            const size_t r = ((size_t)b * a.Hq + h) * x.N + i;
-            st[0] = x.lse[r] + shift_c;
-            st[x.n_pad] = dc;
-            st[2 * (size_t)x.n_pad] = x.lse[plane + r] + shift_s;
-            st[3 * (size_t)x.n_pad] = ds;
-            share += dc - ds;
-        }
-    }
-    __shared__ float s_share[kStatWarps];
-    if (lane == 0) s_share[warp] = share;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        float sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < kStatWarps; ++w) sum += s_share[w];
-        x.part[(size_t)kv * a.B * x.chunks + (size_t)b * x.chunks + chunk] = sum;
-    }
-}
-
 // --------------------------------------------------------------- the kernel
 
 constexpr int BM = 128;            // rows of an outer or inner tile
@@ -140,49 +83,103 @@ static_assert(kGradSmem + 1024 <= 232448, "one CTA per SM");
 struct GradArgs {
     LayerArgs a;
     int N, n_tiles, n_pad;
-    const float* stats;    // [B][Hq][4][n_pad]
+    float* stats;          // [B][Hq][4][n_pad]
+    const float* lse;      // [2][B][Hq][N] of the forward pass
     const float* alpha;
     void* d0;              // keys outer: dK; queries outer: dQ
     void* d1;              // keys outer: dV
-    const float* part;     // [Hkv][n_part], keys outer: the shares of dalpha
-    int n_part;
+    float* part;           // [Hkv][B][n_tiles][G], the shares of dalpha
     float* dalpha;
     int32_t* status;
 };
 
-// A tile pair holds keys some query sees in the Lambda attention: sink tokens,
-// or the recent band (the diagonal tile always does, so every tile that
-// needs a mask is one of these).
-__device__ __forceinline__ bool lambda_tile(const LayerArgs& a, int qt, int kt) {
-    return kt * BM < a.sink || (qt - kt) * BM - (BM - 1) < a.recent;
-}
+// What a launch computes: the rows' statistics, dK and dV (keys outer), or dQ.
+enum { STATS = 0, KEYS = 1, QUERIES = 2 };
 
 __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
     __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
     return *reinterpret_cast<uint32_t*>(&h);
 }
 
-// A warp's 64 columns of a tile without Lambda keys.  First half: x[] dot
-// products -> |a| P_c (packed bf16 to TMEM when `store`), x[] = |a| P_c times
-// the cap's slope.
-template <bool CAP, bool KEYS>
-__device__ __forceinline__ void causal_weights(float (&x)[64], const LayerArgs& a, float sl, const float* s_lse, float lse,
-                                               bool neg, uint32_t w_addr) {
-    float big = 0.f;
-    bool poly = false;
-    if constexpr (CAP) {
-#pragma unroll
-        for (int c = 0; c < 64; c += 2) big = fmax3(big, fabsf(x[c]), fabsf(x[c + 1]));
-        poly = __all_sync(0xffffffffu, big * a.cap.k <= 1.f);
-        if (!poly) {
-#pragma unroll
-            for (int c = 0; c < 64; ++c) x[c] = tanh_sfu(x[c] * a.cap.k);
-        }
+// Bits lo .. hi (inclusive, clipped to 0 .. 63).
+__device__ __forceinline__ uint64_t bit_range(int lo, int hi) {
+    lo = max(lo, 0);
+    hi = min(hi, 63);
+    return lo > hi ? 0ull : (~0ull >> (63 - hi)) & (~0ull << lo);
+}
+
+// Which of a thread's 64 columns its row sees under the two masks.  Rows are
+// keys and columns queries, or the other way round.
+struct Seen {
+    uint32_t causal[2], lam[2];
+};
+__device__ __forceinline__ Seen seen_columns(const LayerArgs& a, bool keys_outer, int row, int col0) {
+    uint64_t c, l;
+    if (keys_outer) {
+        c = bit_range(row - col0, 63);
+        l = row < a.sink ? c : bit_range(row - col0, row + a.recent - 1 - col0);
+    } else {
+        c = bit_range(0, row - col0);
+        l = c & (bit_range(0, a.sink - 1 - col0) | bit_range(row - a.recent + 1 - col0, 63));
     }
+    return {{(uint32_t)c, (uint32_t)(c >> 32)}, {(uint32_t)l, (uint32_t)(l >> 32)}};
+}
+
+// Where a thread finds the (lse, D) pairs of its columns: one pair of pairs in
+// registers when its row is the query, four rows of shared memory (one entry
+// per column) when its columns are.
+struct RowStats {
+    float lse_c, dc, lse_l, dl;
+    const float* cols;
+};
+template <bool COLS>
+__device__ __forceinline__ float4 stat4(const RowStats& r, int which, int c4) {
+    if constexpr (COLS) return reinterpret_cast<const float4*>(r.cols + which * BM)[c4];
+    const float v = which == 0 ? r.lse_c : which == 1 ? r.dc : which == 2 ? r.lse_l : r.dl;
+    return make_float4(v, v, v, v);
+}
+
+__device__ __forceinline__ float4 choose4(uint32_t bits, int shift, const float4& yes, const float4& no) {
+    return make_float4((bits >> shift) & 1u ? yes.x : no.x, (bits >> (shift + 1)) & 1u ? yes.y : no.y,
+                       (bits >> (shift + 2)) & 1u ? yes.z : no.z, (bits >> (shift + 3)) & 1u ? yes.w : no.w);
+}
+
+// Dot products to tanh, in place (CAP): on the FMA pipe when every |k x| of the
+// warp's part is at most 1, else on the SFU.
+template <int W>
+__device__ __forceinline__ void tanh_columns(float (&x)[W], const CapArgs& cap) {
+    float big = 0.f;
+#pragma unroll
+    for (int c = 0; c < W; c += 2) big = fmax3(big, fabsf(x[c]), fabsf(x[c + 1]));
+    if (__all_sync(0xffffffffu, big * cap.k <= 1.f)) {
+#pragma unroll
+        for (int c = 0; c < W; c += 2) {
+            const float2 t = tanh_fma2(fmul2(make_float2(x[c], x[c + 1]), make_float2(cap.k, cap.k)));
+            x[c] = t.x;
+            x[c + 1] = t.y;
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < W; ++c) x[c] = tanh_sfu(x[c] * cap.k);
+    }
+}
+
+// A warp's 64 columns: x[] dot products -> W times the cap's slope, W packed
+// as bf16 to TMEM on the way when COLS (keys outer).  MASKED: some column is
+// not seen, or is seen by both attentions.
+template <bool CAP, bool COLS, bool MASKED>
+__device__ __forceinline__ void weights(float (&x)[64], const LayerArgs& a, float sl, const RowStats& r, const Seen& seen,
+                                        bool neg, uint32_t w_addr) {
+    if constexpr (CAP) tanh_columns<64>(x, a.cap);
     uint32_t pk[32];
 #pragma unroll
     for (int c4 = 0; c4 < 16; ++c4) {
-        float4 l4 = KEYS ? reinterpret_cast<const float4*>(s_lse)[c4] : make_float4(lse, lse, lse, lse);
+        float4 l4 = stat4<COLS>(r, 0, c4);
+        if constexpr (MASKED) {
+            const int w = c4 >> 3, sh = 4 * (c4 & 7);
+            l4 = choose4(seen.lam[w], sh, stat4<COLS>(r, 2, c4), l4);
+            l4 = choose4(seen.causal[w], sh, l4, make_float4(INFINITY, INFINITY, INFINITY, INFINITY));
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int c = 4 * c4 + 2 * h;
@@ -190,7 +187,6 @@ __device__ __forceinline__ void causal_weights(float (&x)[64], const LayerArgs& 
             const float2 nl = h ? make_float2(-l4.z, -l4.w) : make_float2(-l4.x, -l4.y);
             float2 slope;
             if constexpr (CAP) {
-                if (poly) v = tanh_fma2(fmul2(v, make_float2(a.cap.k, a.cap.k)));
                 slope = ffma2(make_float2(-v.x, -v.y), v, make_float2(1.f, 1.f));
                 v = ffma2(v, make_float2(a.cap.c2, a.cap.c2), nl);
             } else {
@@ -198,20 +194,130 @@ __device__ __forceinline__ void causal_weights(float (&x)[64], const LayerArgs& 
             }
             v = make_float2(sfu_exp2(v.x), sfu_exp2(v.y));
             if (neg) v = make_float2(-v.x, -v.y);
-            if constexpr (KEYS) pk[c / 2] = pack_bf16(v.x, v.y);
+            if constexpr (COLS) pk[c / 2] = pack_bf16(v.x, v.y);
             if constexpr (CAP) v = fmul2(v, slope);
             x[c] = v.x;
             x[c + 1] = v.y;
         }
     }
-    if constexpr (KEYS) tmem_st32(w_addr, pk);
+    if constexpr (COLS) tmem_st32(w_addr, pk);
 }
 
-template <bool KEYS, bool CAP>
+// x[] = W (times slope), TMEM dP -> dS packed as bf16 over dP's columns.
+template <bool COLS, bool MASKED>
+__device__ __forceinline__ void score_grads(const float (&x)[64], const RowStats& r, const Seen& seen, uint32_t d_addr) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float d[32];
+        tmem_ld32(d_addr + 32 * h, d);
+        uint32_t pk[16];
+#pragma unroll
+        for (int c4 = 0; c4 < 8; ++c4) {
+            float4 q = stat4<COLS>(r, 1, 8 * h + c4);
+            if constexpr (MASKED) q = choose4(seen.lam[h], 4 * c4, stat4<COLS>(r, 3, 8 * h + c4), q);
+            const int c = 4 * c4;
+            const float2 u = fmul2(make_float2(x[32 * h + c], x[32 * h + c + 1]),
+                                   fadd2(make_float2(d[c], d[c + 1]), make_float2(-q.x, -q.y)));
+            const float2 v = fmul2(make_float2(x[32 * h + c + 2], x[32 * h + c + 3]),
+                                   fadd2(make_float2(d[c + 2], d[c + 3]), make_float2(-q.z, -q.w)));
+            pk[2 * c4] = pack_bf16(u.x, u.y);
+            pk[2 * c4 + 1] = pack_bf16(v.x, v.y);
+        }
+        tmem_st16(d_addr + 16 * h, pk);
+    }
+}
+
+// A tile with keys that both attentions see, for a gate outside [0, 1]: the
+// shares a P_c and (1 - a) P_s differ in sign and are formed one by one (the
+// statistics hold lse_s - log2 |1 - a| and D_s), 16 columns at a time.
+template <bool CAP, bool COLS>
+__device__ __forceinline__ void signed_shares(const LayerArgs& a, float sl, const RowStats& r, const Seen& seen, bool neg_c,
+                                              bool neg_s, uint32_t s_addr, uint32_t d_addr) {
+#pragma unroll 1
+    for (int ch = 0; ch < 4; ++ch) {
+        float x[16], d[16];
+        tmem_ld16(s_addr + 16 * ch, x);
+        tmem_ld16(d_addr + 16 * ch, d);
+        const uint32_t causal = seen.causal[ch >> 1] >> (16 * (ch & 1)), lam = seen.lam[ch >> 1] >> (16 * (ch & 1));
+        uint32_t pw[8], pg[8];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+            const float* st = r.cols + 16 * ch + c;
+            const float lc = COLS ? st[0] : r.lse_c, qc = COLS ? st[BM] : r.dc;
+            const float ls = COLS ? st[2 * BM] : r.lse_l, qs = COLS ? st[3 * BM] : r.dl;
+            float slope = 1.f, s;
+            if constexpr (CAP) {
+                const float t = tanh_sfu(x[c] * a.cap.k);
+                slope = fmaf(-t, t, 1.f);
+                s = t * a.cap.c2;
+            } else {
+                s = x[c] * sl;
+            }
+            float wc = (causal >> c) & 1u ? sfu_exp2(s - lc) : 0.f;
+            float ws = (lam >> c) & 1u ? sfu_exp2(s - ls) : 0.f;
+            wc = neg_c ? -wc : wc;
+            ws = neg_s ? -ws : ws;
+            x[c] = wc + ws;
+            d[c] = slope * fmaf(x[c], d[c], -fmaf(wc, qc, ws * qs));
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            pw[c] = pack_bf16(x[2 * c], x[2 * c + 1]);
+            pg[c] = pack_bf16(d[2 * c], d[2 * c + 1]);
+        }
+        if constexpr (COLS) tmem_st8(s_addr + 8 * ch, pw);
+        tmem_st8(d_addr + 8 * ch, pg);
+    }
+}
+
+// The sums of P and P dP of a thread's 64 columns under each mask.
+struct RowSums {
+    float lc, dc, ls, ds;
+};
+template <bool CAP, bool MASKED>
+__device__ __forceinline__ void add_sums(RowSums& sum, const LayerArgs& a, float sl, float lse_c, float lse_s,
+                                         const Seen& seen, uint32_t s_addr, uint32_t d_addr) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float x[32], d[32];
+        tmem_ld32(s_addr + 32 * h, x);
+        tmem_ld32(d_addr + 32 * h, d);
+        if constexpr (CAP) tanh_columns<32>(x, a.cap);
+        const float f = CAP ? a.cap.c2 : sl;
+        float2 lc = make_float2(0.f, 0.f), dc = lc;
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+            float2 v = ffma2(make_float2(x[c], x[c + 1]), make_float2(f, f), make_float2(-lse_c, -lse_c));
+            if constexpr (MASKED) {
+                // both attentions: the score once more, relative to lse_s
+                if ((seen.lam[h] >> c) & 1u) {
+                    const float p = sfu_exp2(fmaf(x[c], f, -lse_s));
+                    sum.ls += p;
+                    sum.ds = fmaf(p, d[c], sum.ds);
+                }
+                if ((seen.lam[h] >> (c + 1)) & 1u) {
+                    const float p = sfu_exp2(fmaf(x[c + 1], f, -lse_s));
+                    sum.ls += p;
+                    sum.ds = fmaf(p, d[c + 1], sum.ds);
+                }
+                v.x = (seen.causal[h] >> c) & 1u ? v.x : -INFINITY;
+                v.y = (seen.causal[h] >> (c + 1)) & 1u ? v.y : -INFINITY;
+            }
+            v = make_float2(sfu_exp2(v.x), sfu_exp2(v.y));
+            lc = fadd2(lc, v);
+            dc = ffma2(v, make_float2(d[c], d[c + 1]), dc);
+        }
+        sum.lc += lc.x + lc.y;
+        sum.dc += dc.x + dc.y;
+    }
+}
+
+template <int MODE, bool CAP>
 __global__ void __launch_bounds__(kGradThreads, 1)
     mix_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDo,
                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const GradArgs p) {
     extern __shared__ __align__(1024) uint8_t smem[];
+    constexpr bool kKeys = MODE == KEYS, kStats = MODE == STATS;
     const LayerArgs& a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if ((smem_u32(smem) & 1023u) != 0) {   // the swizzled layouts need 1024-byte alignment
@@ -226,29 +332,29 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     uint64_t* s_full = bars + 5;
     uint64_t* d_full = bars + 6;
     uint64_t* w_ready = bars + 7;   // W written (keys outer), S read
-    uint64_t* g_ready = bars + 8;   // dS written
+    uint64_t* g_ready = bars + 8;   // dS written, dP read
     uint64_t* done = bars + 9;
     uint32_t* holder = reinterpret_cast<uint32_t*>(smem + kOffHolder);
 
     // Work item, the longest first.  Keys outer: key tile ot of KV head `head`,
     // whose inner tiles are (query head of the group, query tile >= ot);
     // queries outer: query tile ot of query head `head`, key tiles 0 .. ot.
-    const int heads = KEYS ? a.Hkv : a.Hq;
+    const int heads = kKeys ? a.Hkv : a.Hq;
     const int ord = blockIdx.x / (a.B * heads), rest = blockIdx.x % (a.B * heads);
     const int head = rest % heads, b = rest / heads;
-    const int ot = KEYS ? ord : p.n_tiles - 1 - ord;
-    const int kv = KEYS ? head : head / a.G;
+    const int ot = kKeys ? ord : p.n_tiles - 1 - ord;
+    const int kv = kKeys ? head : head / a.G;
     const int per_head = p.n_tiles - ot;                   // keys outer: query tiles per query head
-    const int n_in = KEYS ? a.G * per_head : ot + 1;
-    auto inner_tile = [&](int j) { return KEYS ? ot + j % per_head : j; };
-    auto inner_qhead = [&](int j) { return KEYS ? kv * a.G + j / per_head : head; };
+    const int n_in = kKeys ? a.G * per_head : ot + 1;
+    auto inner_tile = [&](int j) { return kKeys ? ot + j % per_head : j; };
+    auto inner_qhead = [&](int j) { return kKeys ? kv * a.G + j / per_head : head; };
 
     if (warp == kMmaWarp) tmem_alloc(holder, kTmemCols);
     if (tid == 0) {
         mbar_init(x_full, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&y_full[i], 1);
-            mbar_init(&y_empty[i], KEYS ? 9 : 1);   // the MMAs' commit, and the warps that read the stage's statistics
+            mbar_init(&y_empty[i], kKeys ? 9 : 1);   // the MMAs' commit, and the warps that read the stage's statistics
         }
         mbar_init(s_full, 1);
         mbar_init(d_full, 1);
@@ -264,25 +370,25 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 
     if (warp == kTmaWarp) {
         if (lane == 0) {
-            const CUtensorMap* mx0 = KEYS ? &tmK : &tmQ;
-            const CUtensorMap* mx1 = KEYS ? &tmV : &tmDo;
-            const CUtensorMap* my0 = KEYS ? &tmQ : &tmK;
-            const CUtensorMap* my1 = KEYS ? &tmDo : &tmV;
+            const CUtensorMap* mx0 = kKeys ? &tmK : &tmQ;
+            const CUtensorMap* mx1 = kKeys ? &tmV : &tmDo;
+            const CUtensorMap* my0 = kKeys ? &tmQ : &tmK;
+            const CUtensorMap* my1 = kKeys ? &tmDo : &tmV;
             mbar_arrive_expect_tx(x_full, 2 * kTileBytes);
             for (int half = 0; half < 2; ++half) {
                 tma_load_4d(sX + half * kHalfBytes, mx0, 64 * half, head, BM * ot, b, x_full);
                 tma_load_4d(sX + kTileBytes + half * kHalfBytes, mx1, 64 * half, head, BM * ot, b, x_full);
             }
             for (int j = 0; j < n_in; ++j) {
-                const int st = j & 1, it = inner_tile(j), ih = KEYS ? inner_qhead(j) : kv;
+                const int st = j & 1, it = inner_tile(j), ih = kKeys ? inner_qhead(j) : kv;
                 if (j >= 2 && !mbar_wait(&y_empty[st], ((j >> 1) - 1) & 1, p.status)) break;
-                mbar_arrive_expect_tx(&y_full[st], 2 * kTileBytes + (KEYS ? kStatBytes : 0u));
+                mbar_arrive_expect_tx(&y_full[st], 2 * kTileBytes + (kKeys ? kStatBytes : 0u));
                 const uint32_t y = sY + st * 2 * kTileBytes;
                 for (int half = 0; half < 2; ++half) {
                     tma_load_4d(y + half * kHalfBytes, my0, 64 * half, ih, BM * it, b, &y_full[st]);
                     tma_load_4d(y + kTileBytes + half * kHalfBytes, my1, 64 * half, ih, BM * it, b, &y_full[st]);
                 }
-                if constexpr (KEYS) {
+                if constexpr (kKeys) {
                     const float* src = p.stats + ((size_t)b * a.Hq + ih) * 4 * p.n_pad + BM * it;
                     for (int r = 0; r < 4; ++r)
                         bulk_g2s(smem + kOffStat + st * kStatBytes + r * BM * 4, src + (size_t)r * p.n_pad, BM * 4,
@@ -318,6 +424,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 tc_commit(s_full);
                 issue_xy(kColP, 1, 0);
                 tc_commit(d_full);
+                if (kStats) tc_commit(&y_empty[0]);
             }
             for (int j = 0; j < n_in && ok; ++j) {
                 const bool next = j + 1 < n_in;
@@ -325,7 +432,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 ok = ok && mbar_wait(w_ready, j & 1, p.status);
                 if (!ok) break;
                 tc_fence_after();
-                if constexpr (KEYS) issue_acc(kColA1, kColS, 1, j);
+                if constexpr (kKeys) issue_acc(kColA1, kColS, 1, j);
                 if (next) {
                     issue_xy(kColS, 0, j + 1);
                     tc_commit(s_full);
@@ -333,11 +440,14 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 ok = mbar_wait(g_ready, j & 1, p.status);
                 if (!ok) break;
                 tc_fence_after();
-                issue_acc(kColA2, kColP, 0, j);
-                tc_commit(&y_empty[j & 1]);
+                if constexpr (!kStats) {
+                    issue_acc(kColA2, kColP, 0, j);
+                    tc_commit(&y_empty[j & 1]);
+                }
                 if (next) {
                     issue_xy(kColP, 1, j + 1);
                     tc_commit(d_full);
+                    if (kStats) tc_commit(&y_empty[(j + 1) & 1]);
                 } else {
                     tc_commit(done);
                 }
@@ -353,117 +463,126 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         const float al = p.alpha[kv];
         const bool neg_c = al < 0.f, neg_s = 1.f - al < 0.f;
         const int orow = BM * ot + row;                       // key (keys outer) or query
-        float lse_c = 0.f, dc = 0.f, lse_s = 0.f, ds = 0.f;
-        if constexpr (!KEYS) {
+        RowStats rs{0.f, 0.f, 0.f, 0.f, nullptr};
+        RowSums sum{0.f, 0.f, 0.f, 0.f};
+        if constexpr (kStats) {
+            const bool live = orow < p.N;
+            const size_t r = ((size_t)b * a.Hq + head) * p.N + (live ? orow : 0);
+            rs.lse_c = live ? p.lse[r] : INFINITY;
+            rs.lse_l = live ? p.lse[(size_t)a.B * a.Hq * p.N + r] : INFINITY;
+        } else if constexpr (!kKeys) {
             const float* st = p.stats + ((size_t)b * a.Hq + head) * 4 * p.n_pad + orow;
-            lse_c = st[0];
-            dc = st[p.n_pad];
-            lse_s = st[2 * (size_t)p.n_pad];
-            ds = st[3 * (size_t)p.n_pad];
+            rs = {st[0], st[p.n_pad], st[2 * (size_t)p.n_pad], st[3 * (size_t)p.n_pad], nullptr};
         }
         bool ok = true;
         for (int j = 0; j < n_in; ++j) {
             const int it = inner_tile(j);
-            const float* stat = reinterpret_cast<const float*>(smem + kOffStat + (j & 1) * kStatBytes) + 64 * wg;
-            // the statistics arrived with the tile that S(j) was computed from;
-            // this wait makes the copy visible to this thread too
-            if constexpr (KEYS) ok = ok && mbar_wait(&y_full[j & 1], (j >> 1) & 1, p.status);
+            if constexpr (kKeys) {
+                rs.cols = reinterpret_cast<const float*>(smem + kOffStat + (j & 1) * kStatBytes) + 64 * wg;
+                // the statistics arrived with the tile that S(j) was computed from;
+                // this wait makes the copy visible to this thread too
+                ok = ok && mbar_wait(&y_full[j & 1], (j >> 1) & 1, p.status);
+            }
             ok = __all_sync(0xffffffffu, ok && mbar_wait(s_full, j & 1, p.status));
             if (!ok) break;
             tc_fence_after();
-            if (!lambda_tile(a, KEYS ? it : ot, KEYS ? ot : it)) {
+            // every pair of the warp's part is seen by the causal attention only?
+            const int r0 = BM * ot + 32 * (warp & 3), c0 = BM * it + 64 * wg;
+            const int key0 = kKeys ? r0 : c0, key1 = kKeys ? r0 + 31 : c0 + 63, query0 = kKeys ? c0 : r0;
+            const bool plain = key0 >= a.sink && query0 - key1 >= a.recent;   // recent >= 1: below the diagonal too
+            Seen seen{};
+            if (!plain) seen = seen_columns(a, kKeys, orow, c0);
+            if constexpr (kStats) {
+                ok = __all_sync(0xffffffffu, mbar_wait(d_full, j & 1, p.status));
+                if (!ok) break;
+                tc_fence_after();
+                if (plain)
+                    add_sums<CAP, false>(sum, a, sl, rs.lse_c, rs.lse_l, seen, s_addr, d_addr);
+                else
+                    add_sums<CAP, true>(sum, a, sl, rs.lse_c, rs.lse_l, seen, s_addr, d_addr);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(w_ready);
+            } else if (plain || !(neg_c || neg_s)) {
                 float x[64];
                 tmem_ld64(s_addr, x);
-                causal_weights<CAP, KEYS>(x, a, sl, stat, lse_c, neg_c, s_addr);
-                if constexpr (KEYS) tmem_wait_st();
+                if (plain)
+                    weights<CAP, kKeys, false>(x, a, sl, rs, seen, neg_c, s_addr);
+                else
+                    weights<CAP, kKeys, true>(x, a, sl, rs, seen, false, s_addr);
+                if constexpr (kKeys) tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(w_ready);
                 ok = __all_sync(0xffffffffu, mbar_wait(d_full, j & 1, p.status));
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float d[32];
-                    tmem_ld32(d_addr + 32 * h, d);
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int c4 = 0; c4 < 8; ++c4) {
-                        const float4 q = KEYS ? reinterpret_cast<const float4*>(stat + BM)[8 * h + c4] : make_float4(dc, dc, dc, dc);
-                        const int c = 4 * c4;
-                        const float2 u = fmul2(make_float2(x[32 * h + c], x[32 * h + c + 1]),
-                                               fadd2(make_float2(d[c], d[c + 1]), make_float2(-q.x, -q.y)));
-                        const float2 v = fmul2(make_float2(x[32 * h + c + 2], x[32 * h + c + 3]),
-                                               fadd2(make_float2(d[c + 2], d[c + 3]), make_float2(-q.z, -q.w)));
-                        pk[2 * c4] = pack_bf16(u.x, u.y);
-                        pk[2 * c4 + 1] = pack_bf16(v.x, v.y);
-                    }
-                    tmem_st16(d_addr + 16 * h, pk);
-                }
+                if (plain)
+                    score_grads<kKeys, false>(x, rs, seen, d_addr);
+                else
+                    score_grads<kKeys, true>(x, rs, seen, d_addr);
             } else {
-                // both attentions, and the masks: 16 columns at a time
                 ok = __all_sync(0xffffffffu, mbar_wait(d_full, j & 1, p.status));
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll 1
-                for (int ch = 0; ch < 4; ++ch) {
-                    float x[16], d[16];
-                    tmem_ld16(s_addr + 16 * ch, x);
-                    tmem_ld16(d_addr + 16 * ch, d);
-                    uint32_t pw[8], pg[8];
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        const int icol = BM * it + 64 * wg + 16 * ch + c;
-                        const int query = KEYS ? icol : orow, key = KEYS ? orow : icol;
-                        const float lc = KEYS ? stat[16 * ch + c] : lse_c, qc = KEYS ? stat[BM + 16 * ch + c] : dc;
-                        const float ls = KEYS ? stat[2 * BM + 16 * ch + c] : lse_s, qs = KEYS ? stat[3 * BM + 16 * ch + c] : ds;
-                        float slope = 1.f, s;
-                        if constexpr (CAP) {
-                            const float t = tanh_sfu(x[c] * a.cap.k);
-                            slope = fmaf(-t, t, 1.f);
-                            s = t * a.cap.c2;
-                        } else {
-                            s = x[c] * sl;
-                        }
-                        const bool causal = key <= query;
-                        const bool lam = causal && (key < a.sink || query - key < a.recent);
-                        float wc = causal ? sfu_exp2(s - lc) : 0.f;
-                        float ws = lam ? sfu_exp2(s - ls) : 0.f;
-                        wc = neg_c ? -wc : wc;
-                        ws = neg_s ? -ws : ws;
-                        const float w = wc + ws;
-                        x[c] = w;
-                        d[c] = slope * fmaf(w, d[c], -fmaf(wc, qc, ws * qs));
-                    }
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        pw[c] = pack_bf16(x[2 * c], x[2 * c + 1]);
-                        pg[c] = pack_bf16(d[2 * c], d[2 * c + 1]);
-                    }
-                    if constexpr (KEYS) tmem_st8(s_addr + 8 * ch, pw);
-                    tmem_st8(d_addr + 8 * ch, pg);
-                }
+                signed_shares<CAP, kKeys>(a, sl, rs, seen, neg_c, neg_s, s_addr, d_addr);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(w_ready);
             }
-            tmem_wait_st();
+            if constexpr (!kStats) tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(g_ready);
-                if constexpr (KEYS) mbar_arrive(&y_empty[j & 1]);   // done with the stage's statistics
+                if constexpr (kKeys) mbar_arrive(&y_empty[j & 1]);   // done with the stage's statistics
             }
         }
         ok = ok && __all_sync(0xffffffffu, mbar_wait(done, 0, p.status));
-        if (ok) {
-            tc_fence_after();
-            const int H = KEYS ? a.Hkv : a.Hq;
-            const size_t off = (((size_t)b * p.N + orow) * H + head) * HD + 64 * wg;
-            const bool live = orow < p.N && bounds_ok(b < a.B && head < H, p.status);
+        if constexpr (kStats) {
+            // join the two halves of each row, then the row's statistics
+            float4* half = reinterpret_cast<float4*>(smem + kOffStat);   // [128] sums of columns 64 ..
+            float* share = reinterpret_cast<float*>(half + BM);          // [4] of the warps
+            if (wg == 1) half[row] = make_float4(sum.lc, sum.dc, sum.ls, sum.ds);
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (wg == 0) {
+                const float4 o = half[row];
+                const float lc = sum.lc + o.x, ls = sum.ls + o.z;
+                const bool live = ok && orow < p.N && lc > 0.f && ls > 0.f;
+                const float dc = live ? (sum.dc + o.y) / lc : 0.f, ds = live ? (sum.ds + o.w) / ls : 0.f;
+                const float lse_c = live ? rs.lse_c + log2f(lc) - log2f(fabsf(al)) : INFINITY;       // +inf: a closed gate
+                const float lse_s = live ? rs.lse_l + log2f(ls) - log2f(fabsf(1.f - al)) : INFINITY;
+                float lse_l = lse_s, dl = ds;
+                if (!(neg_c || neg_s) && live) {
+                    // 2^-lse* = 2^-lse_c + 2^-lse_s, the two shares' weights
+                    const float lo = fminf(lse_c, lse_s);
+                    const float wc = exp2f(lo - lse_c), ws = exp2f(lo - lse_s);
+                    lse_l = lo - log2f(wc + ws);
+                    dl = (wc * dc + ws * ds) / (wc + ws);
+                }
+                float* st = p.stats + ((size_t)b * a.Hq + head) * 4 * p.n_pad + orow;
+                if (bounds_ok(orow < p.n_pad, p.status)) {
+                    st[0] = lse_c;
+                    st[p.n_pad] = dc;
+                    st[2 * (size_t)p.n_pad] = lse_l;
+                    st[3 * (size_t)p.n_pad] = dl;
+                }
+                float d = dc - ds;
 #pragma unroll
-            for (int t = 0; t < (KEYS ? 2 : 1); ++t) {
+                for (int s = 16; s > 0; s >>= 1) d += __shfl_xor_sync(0xffffffffu, d, s);
+                if (lane == 0) share[warp] = d;
+                asm volatile("bar.sync 2, 128;" ::: "memory");
+                if (tid == 0)
+                    p.part[(((size_t)kv * a.B + b) * p.n_tiles + ot) * a.G + head % a.G] =
+                        (share[0] + share[1]) + (share[2] + share[3]);
+            }
+        } else if (ok) {
+            tc_fence_after();
+            const size_t off = (((size_t)b * p.N + orow) * heads + head) * HD + 64 * wg;
+            const bool live = orow < p.N && bounds_ok(b < a.B && head < heads, p.status);
+#pragma unroll
+            for (int t = 0; t < (kKeys ? 2 : 1); ++t) {
                 __nv_bfloat16* o = static_cast<__nv_bfloat16*>(t ? p.d1 : p.d0) + off;
                 const float f = t ? 1.f : a.scale;            // dS held back the softmax scale
 #pragma unroll
@@ -481,7 +600,10 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             }
         }
         // one warp per KV head adds up the shares of dalpha, in their order
-        if (KEYS && ot == 0 && b == 0 && warp == 0) sum_shares(p.part + (size_t)kv * p.n_part, p.n_part, &p.dalpha[kv], lane);
+        if (kKeys && ot == 0 && b == 0 && warp == 0) {
+            const int n = a.B * p.n_tiles * a.G;
+            sum_shares(p.part + (size_t)kv * n, n, &p.dalpha[kv], lane);
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -491,14 +613,14 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
 }
 
-template <bool KEYS, bool CAP>
+template <int MODE, bool CAP>
 cudaError_t launch_grad(const CUtensorMap (&m)[4], const GradArgs& p, cudaStream_t s) {
     static std::atomic<unsigned long long> configured{0};
-    const cudaError_t e = smem_limit_once(mix_grad_kernel<KEYS, CAP>, (int)kGradSmem, configured);
+    const cudaError_t e = smem_limit_once(mix_grad_kernel<MODE, CAP>, (int)kGradSmem, configured);
     if (e != cudaSuccess) return e;
-    const long grid = (long)p.a.B * (KEYS ? p.a.Hkv : p.a.Hq) * p.n_tiles;
+    const long grid = (long)p.a.B * (MODE == KEYS ? p.a.Hkv : p.a.Hq) * p.n_tiles;
     if (grid > 0x7fffffffL) return cudaErrorInvalidConfiguration;
-    mix_grad_kernel<KEYS, CAP><<<(unsigned)grid, kGradThreads, kGradSmem, s>>>(m[0], m[1], m[2], m[3], p);
+    mix_grad_kernel<MODE, CAP><<<(unsigned)grid, kGradThreads, kGradSmem, s>>>(m[0], m[1], m[2], m[3], p);
     return cudaGetLastError();
 }
 
@@ -506,28 +628,14 @@ cudaError_t launch_grad(const CUtensorMap (&m)[4], const GradArgs& p, cudaStream
 
 MixGradPlan mix_grad_plan(const LayerArgs& a, int N) {
     MixGradPlan pl{};
-    pl.n_pad = (N + BM - 1) / BM * BM;
-    pl.chunks = (pl.n_pad + kStatRows - 1) / kStatRows;
+    pl.n_tiles = (N + BM - 1) / BM;
+    pl.n_pad = pl.n_tiles * BM;
     const size_t stats = (size_t)a.B * a.Hq * 4 * pl.n_pad * sizeof(float);
     pl.part_offset = (stats + 255) / 256 * 256;
-    pl.bytes = pl.part_offset + ((size_t)a.Hkv * a.B * pl.chunks * sizeof(float) + 255) / 256 * 256;
+    // a share per query head and 128 rows (here), or per KV head and 32 rows (tiled_attn.cu)
+    const size_t shares = (size_t)a.B * pl.n_tiles * (a.Hq > 4 * a.Hkv ? a.Hq : 4 * a.Hkv);
+    pl.bytes = pl.part_offset + (shares * sizeof(float) + 255) / 256 * 256;
     return pl;
-}
-
-cudaError_t launch_mix_stats(const LayerArgs& a, const MixGradArgs& g, int N, cudaStream_t s) {
-    const MixGradPlan pl = mix_grad_plan(a, N);
-    if (a.B > 65535) return cudaErrorInvalidConfiguration;
-    const StatArgs x{g.dout, g.causal, g.streaming, g.lse, g.alpha, g.stats, g.part, N, pl.n_pad, pl.chunks};
-    const dim3 grid((unsigned)pl.chunks, (unsigned)a.Hkv, (unsigned)a.B);
-    constexpr int th = kStatWarps * 32;
-    if (a.dtype == DUO_BF16) {
-        if (a.D == 128) mix_stats_kernel<__nv_bfloat16, 128><<<grid, th, 0, s>>>(a, x);
-        else mix_stats_kernel<__nv_bfloat16, 64><<<grid, th, 0, s>>>(a, x);
-    } else {
-        if (a.D == 128) mix_stats_kernel<float, 128><<<grid, th, 0, s>>>(a, x);
-        else mix_stats_kernel<float, 64><<<grid, th, 0, s>>>(a, x);
-    }
-    return cudaGetLastError();
 }
 
 cudaError_t launch_mix_grad_tc(const LayerArgs& a, const MixGradArgs& g, int N, cudaStream_t s) {
@@ -541,12 +649,16 @@ cudaError_t launch_mix_grad_tc(const LayerArgs& a, const MixGradArgs& g, int N, 
         const uint32_t bx[4] = {64, 1, BM, 1};
         if (!encode_tmap_bf16(&m[i], base[i], 4, d, st, bx)) return cudaErrorInvalidValue;
     }
-    GradArgs p{a, N, pl.n_pad / BM, pl.n_pad, g.stats, g.alpha, g.dk, g.dv, g.part, a.B * pl.chunks, g.dalpha, g.status};
-    cudaError_t e = a.cap.on ? launch_grad<true, true>(m, p, s) : launch_grad<true, false>(m, p, s);
+    GradArgs p{a, N, pl.n_tiles, pl.n_pad, g.stats, g.lse, g.alpha, nullptr, nullptr, g.part, g.dalpha, g.status};
+    cudaError_t e = a.cap.on ? launch_grad<STATS, true>(m, p, s) : launch_grad<STATS, false>(m, p, s);
+    if (e != cudaSuccess) return e;
+    p.d0 = g.dk;
+    p.d1 = g.dv;
+    e = a.cap.on ? launch_grad<KEYS, true>(m, p, s) : launch_grad<KEYS, false>(m, p, s);
     if (e != cudaSuccess) return e;
     p.d0 = g.dq;
     p.d1 = nullptr;
-    return a.cap.on ? launch_grad<false, true>(m, p, s) : launch_grad<false, false>(m, p, s);
+    return a.cap.on ? launch_grad<QUERIES, true>(m, p, s) : launch_grad<QUERIES, false>(m, p, s);
 }
 
 }  // namespace duo

@@ -793,11 +793,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else {
                             const uint4 u = pre[4 * ch + q4];
                             const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-                            if constexpr (EPI == EPI_MIX_KEEP) {
-                                if (crow < p.C)
-                                    store_row<__nv_bfloat16, 8>(static_cast<__nv_bfloat16*>(p.epi.causal) + row_off +
-                                                                    32 * ch + 8 * q4, v8);
-                            }
                             if constexpr (kMixes) {
                                 // mix the streaming attention in
 #pragma unroll

@@ -139,8 +139,8 @@ struct TiledArgs {
     int N;
     void* out;
     const float* alpha;    // mix: [Hkv]
-    void* causal;          // mix: A_c and A_s, [B][N][Hq][D]
-    void* streaming;
+    float* causal;         // mix: A_c and A_s, [B][N][Hq][D]
+    float* streaming;
     float* lse;            // mix: [2][B][Hq][N]
 };
 
@@ -289,8 +289,8 @@ __global__ void __launch_bounds__(kTiledThreads) tiled_forward_kernel(const Laye
             T* out = static_cast<T*>(s.out) + off + 64 * j;
             if constexpr (MIX) {
                 store_row<T, 4>(out, mix);
-                store_row<T, 4>(static_cast<T*>(s.causal) + off + 64 * j, v);
-                store_row<T, 4>(static_cast<T*>(s.streaming) + off + 64 * j, v2);
+                store_row<float, 4>(s.causal + off + 64 * j, v);
+                store_row<float, 4>(s.streaming + off + 64 * j, v2);
             } else {
                 store_row<T, 4>(out, v);
             }
@@ -301,6 +301,75 @@ __global__ void __launch_bounds__(kTiledThreads) tiled_forward_kernel(const Laye
 // ----------------------------------------------------------------- backward
 //
 // The scheme of mix_grad.cu: keys outer for dK and dV, queries outer for dQ.
+// The forward pass kept both attentions in fp32, so D_c and D_s are plain dot
+// products here, and both shares of a key are formed one by one (the
+// statistics are {lse_c - log2 |a|, D_c, lse_s - log2 |1 - a|, D_s}).
+
+constexpr int kStatRows = 32;      // rows of a CTA, each with the G heads of one KV head
+constexpr int kStatWarps = 8;
+
+struct StatArgs {
+    const void* dout;      // [B][N][Hq][D]
+    const float* causal;   // A_c, [B][N][Hq][D]
+    const float* streaming;
+    const float* lse;      // [2][B][Hq][N]: causal, Lambda
+    const float* alpha;    // [Hkv]
+    float* stats;          // [B][Hq][4][n_pad]
+    float* part;           // [Hkv][B][chunks] shares of dalpha
+    int N, n_pad;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kStatWarps * 32) tiled_stats_kernel(const LayerArgs a, const StatArgs x) {
+    constexpr int E = D / 32;      // elements a lane
+    const int chunk = blockIdx.x, kv = blockIdx.y, b = blockIdx.z;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const float al = x.alpha[kv];
+    const float shift_c = -log2f(fabsf(al)), shift_s = -log2f(fabsf(1.f - al));   // +inf for a closed gate
+    const size_t plane = (size_t)a.B * a.Hq * x.N;
+    float share = 0.f;
+    for (int it = warp; it < kStatRows * a.G; it += kStatWarps) {
+        const int i = chunk * kStatRows + it / a.G, h = kv * a.G + it % a.G;
+        float* st = x.stats + ((size_t)b * a.Hq + h) * 4 * x.n_pad + i;   // n_pad is whole chunks
+        if (i >= x.N) {
+            if (lane == 0) {
+                st[0] = st[2 * (size_t)x.n_pad] = INFINITY;
+                st[x.n_pad] = st[3 * (size_t)x.n_pad] = 0.f;
+            }
+            continue;
+        }
+        const size_t o = (((size_t)b * x.N + i) * a.Hq + h) * D + lane * E;
+        float dc = 0.f, ds = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float g = Elem<T>::to_f32(static_cast<const T*>(x.dout)[o + e]);
+            dc = fmaf(g, x.causal[o + e], dc);
+            ds = fmaf(g, x.streaming[o + e], ds);
+        }
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) {
+            dc += __shfl_xor_sync(0xffffffffu, dc, s);
+            ds += __shfl_xor_sync(0xffffffffu, ds, s);
+        }
+        if (lane == 0) {
+            const size_t r = ((size_t)b * a.Hq + h) * x.N + i;
+            st[0] = x.lse[r] + shift_c;
+            st[x.n_pad] = dc;
+            st[2 * (size_t)x.n_pad] = x.lse[plane + r] + shift_s;
+            st[3 * (size_t)x.n_pad] = ds;
+            share += dc - ds;
+        }
+    }
+    __shared__ float s_share[kStatWarps];
+    if (lane == 0) s_share[warp] = share;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kStatWarps; ++w) sum += s_share[w];
+        x.part[((size_t)kv * a.B + b) * gridDim.x + chunk] = sum;
+    }
+}
 
 struct TiledGradArgs {
     const void* q;
@@ -464,8 +533,12 @@ cudaError_t launch_grad(const LayerArgs& a, const TiledGradArgs& p, cudaStream_t
 }
 
 template <typename T, int D>
-cudaError_t launch_grads(const LayerArgs& a, TiledGradArgs p, void* dq, cudaStream_t st) {
-    const cudaError_t e = a.cap.on ? launch_grad<T, D, true, true>(a, p, st) : launch_grad<T, D, true, false>(a, p, st);
+cudaError_t launch_grads(const LayerArgs& a, TiledGradArgs p, const StatArgs& x, void* dq, cudaStream_t st) {
+    const dim3 grid((unsigned)(x.n_pad / kStatRows), (unsigned)a.Hkv, (unsigned)a.B);
+    tiled_stats_kernel<T, D><<<grid, kStatWarps * 32, 0, st>>>(a, x);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    e = a.cap.on ? launch_grad<T, D, true, true>(a, p, st) : launch_grad<T, D, true, false>(a, p, st);
     if (e != cudaSuccess) return e;
     p.d0 = dq;
     p.d1 = nullptr;
@@ -487,7 +560,7 @@ cudaError_t launch_tiled_prefill(const LayerArgs& a, const CacheArgs& c, const v
 }
 
 cudaError_t launch_tiled_mix(const LayerArgs& a, const float* alpha, const void* q, const void* k, const void* v, int N,
-                             void* out, void* causal, void* streaming, float* lse, int32_t* status, cudaStream_t st) {
+                             void* out, float* causal, float* streaming, float* lse, int32_t* status, cudaStream_t st) {
     if (a.B > 65535) return cudaErrorInvalidConfiguration;
     const TiledArgs s{q, k, v, N, out, alpha, causal, streaming, lse};
     CacheArgs c{};
@@ -506,14 +579,15 @@ cudaError_t launch_tiled_mix(const LayerArgs& a, const float* alpha, const void*
 cudaError_t launch_tiled_mix_grad(const LayerArgs& a, const MixGradArgs& g, int N, cudaStream_t st) {
     if (a.B > 65535) return cudaErrorInvalidConfiguration;
     const MixGradPlan pl = mix_grad_plan(a, N);
-    const TiledGradArgs p{g.q, g.dout, g.k, g.v, g.stats, g.alpha, g.dk, g.dv, g.part, a.B * pl.chunks, g.dalpha,
-                          g.status, N, pl.n_pad};
+    const StatArgs x{g.dout, g.causal, g.streaming, g.lse, g.alpha, g.stats, g.part, N, pl.n_pad};
+    const TiledGradArgs p{g.q, g.dout, g.k, g.v, g.stats, g.alpha, g.dk, g.dv, g.part, a.B * (pl.n_pad / kStatRows),
+                          g.dalpha, g.status, N, pl.n_pad};
     if (a.dtype == DUO_BF16) {
-        if (a.D == 128) return launch_grads<__nv_bfloat16, 128>(a, p, g.dq, st);
-        return launch_grads<__nv_bfloat16, 64>(a, p, g.dq, st);
+        if (a.D == 128) return launch_grads<__nv_bfloat16, 128>(a, p, x, g.dq, st);
+        return launch_grads<__nv_bfloat16, 64>(a, p, x, g.dq, st);
     }
-    if (a.D == 128) return launch_grads<float, 128>(a, p, g.dq, st);
-    return launch_grads<float, 64>(a, p, g.dq, st);
+    if (a.D == 128) return launch_grads<float, 128>(a, p, x, g.dq, st);
+    return launch_grads<float, 64>(a, p, x, g.dq, st);
 }
 
 }  // namespace duo

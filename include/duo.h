@@ -581,9 +581,9 @@ duo_status duo_gated_mix_grad_alpha(const duo_layer_desc* desc, const void* q, c
  * Forward: out as duo_gated_mix (alpha, q, k, v, out, status as there, model
  * head order); with cap > 0 the scores are capped before both masks, as
  * duo_prefill_chunk_capped caps them (0: not capped).
- *   saved: duo_gated_mix_saved_bytes(desc, N) bytes, 16-byte aligned: both
- *   attentions in the layer's dtype and the rows' log-sums, for
- *   duo_gated_mix_grad with the same desc, alpha, cap, q, k, v and N.
+ *   saved: duo_gated_mix_saved_bytes(desc, N) bytes, 16-byte aligned: what
+ *   duo_gated_mix_grad needs (both log-sums of every row, and on the CUDA cores
+ *   both attentions) with the same desc, alpha, cap, q, k, v and N.
  * Backward: dout [B][N][Hq][d] -> dq [B][N][Hq][d], dk, dv [B][N][Hkv][d] in
  *   the layer's dtype (the heads of a group summed in fp32 and rounded once)
  *   and dalpha [Hkv] fp32; all overwritten.  Gates may have any finite value.

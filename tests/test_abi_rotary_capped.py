@@ -134,11 +134,13 @@ def _mix_sizes(duo, d, N):
 
 def test_mix_buffer_sizes(duo):
     up = lambda x: -(-x // 256) * 256  # noqa: E731
-    for dtype, es in ((duo.BF16, 2), (duo.FP32, 4)):
-        d = duo.desc_init(3, 8, 4, 64, dtype, [0, 1, 2, 3], 4)
+    for dtype, hd in ((duo.BF16, 64), (duo.FP32, 64), (duo.BF16, 128)):
+        d = duo.desc_init(3, 8, 4, hd, dtype, [0, 1, 2, 3], 4)
         saved, ws = _mix_sizes(duo, d, 130)
-        assert saved == 2 * up(3 * 130 * 8 * 64 * es) + up(2 * 3 * 130 * 8 * 4)
-        assert ws == up(3 * 8 * 4 * 256 * 4) + up(4 * 3 * 8 * 4)       # rows padded to 256, a share per 32 of them
+        # both log-sums; one attention in bf16 beside them (tensor cores) or both in fp32
+        rows = 3 * 130 * 8
+        assert saved == up(2 * rows * 4) + (up(rows * 128 * 2) if hd == 128 else 2 * up(rows * 64 * 4))
+        assert ws == up(3 * 8 * 4 * 256 * 4) + up(3 * 2 * 16 * 4)      # rows padded to 256; a share per KV head and 32 rows
     assert _mix_sizes(duo, d, -1) == (0, 0)
     d.head_dim = 96
     assert _mix_sizes(duo, d, 130) == (0, 0)
