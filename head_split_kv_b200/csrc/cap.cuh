@@ -9,7 +9,7 @@
 // tanh in two forms:
 //   * tanh_sfu: 1 - 2 / (1 + e^2y), two SFU operations, any y.  Absolute
 //     error a few 1e-7 (of 1), so a capped score is within cap * 1e-6.
-//   * tanh_fma2, cap_fma2: y * P(y^2) on the FMA pipe for |y| <= 1, where most scores of
+//   * poly_fma2: y * P(y^2) on the FMA pipe for |y| <= 1, where most scores of
 //     a trained model lie (|s| <= cap); P has five coefficients, fitted here
 //     to the smallest largest relative error on [-1, 1], 7.0e-6: at a cap
 //     of 50 at most 2.7e-4 of a weight, far below the 2^-8 of its rounding to
@@ -46,27 +46,16 @@ __device__ __forceinline__ float tanh_sfu(float y) {
 constexpr float kTanh0 = 0.999993085861206f, kTanh1 = -0.3329806625843048f, kTanh2 = 0.13036811351776123f,
                 kTanh3 = -0.04481755197048187f, kTanh4 = 0.00903642363846302f;
 
-// tanh of a pair, |y| <= 1
-__device__ __forceinline__ float2 tanh_fma2(float2 y) {
-    const float2 u = fmul2(y, y);
-    float2 p = ffma2(u, make_float2(kTanh4, kTanh4), make_float2(kTanh3, kTanh3));
-    p = ffma2(p, u, make_float2(kTanh2, kTanh2));
-    p = ffma2(p, u, make_float2(kTanh1, kTanh1));
-    p = ffma2(p, u, make_float2(kTanh0, kTanh0));
-    return fmul2(p, y);
-}
-
-// c2 * tanh(k x) of a pair of dot products with |k x| <= 1: the polynomial's
-// coefficients times c2 and the powers of k, so that it takes x itself.
-struct CapPoly {
+// f * tanh(k x) of a pair of dot products with |k x| <= 1: the polynomial's
+// coefficients times f and the powers of k, so that it takes x itself.
+struct TanhPoly {
     float a0, a1, a2, a3, a4;
 };
-__device__ __forceinline__ CapPoly cap_poly(const CapArgs& cap) {
-    const float k = cap.k, k2 = k * k, s0 = cap.c2 * k;
-    return {kTanh0 * s0, kTanh1 * (s0 * k2), kTanh2 * (s0 * k2 * k2), kTanh3 * (s0 * k2 * k2 * k2),
-            kTanh4 * (s0 * k2 * k2 * k2 * k2)};
+__device__ __forceinline__ TanhPoly tanh_poly(float k, float f = 1.f) {
+    const float k2 = k * k, s0 = f * k, s1 = s0 * k2, s2 = s1 * k2, s3 = s2 * k2;
+    return {kTanh0 * s0, kTanh1 * s1, kTanh2 * s2, kTanh3 * s3, kTanh4 * (s3 * k2)};
 }
-__device__ __forceinline__ float2 cap_fma2(float2 x, const CapPoly& c) {
+__device__ __forceinline__ float2 poly_fma2(float2 x, const TanhPoly& c) {
     const float2 u = fmul2(x, x);
     float2 p = ffma2(u, make_float2(c.a4, c.a4), make_float2(c.a3, c.a3));
     p = ffma2(p, u, make_float2(c.a2, c.a2));

@@ -45,12 +45,18 @@
 //   S = X0 Y0^T, dP = X1 Y1^T (lane = outer row), then W and dS rounded to
 //   bf16 over the columns of S and dP they came from, and
 //   ACC1 += W Y1 (dV), ACC2 += dS Y0 (dK or dQ) with A read from TMEM.
-// TMEM: S | dP | ACC1 | ACC2, 128 columns each.  The MMA thread's order is
+// TMEM: S | dP | ACC1 | ACC2, 128 columns each; without ACC1 (statistics, dQ) a
+// second S takes its place, and for the statistics a second dP that of ACC2.
+// Keys outer, the MMA thread's order is
 //   ACC1(j) S(j+1) | ACC2(j) dP(j+1) | ...
 // so the element-wise warps turn dP(j) into dS(j) while the tensor core runs
 // ACC1(j) and S(j+1), and S(j+1) into W(j+1) while it runs ACC2(j) and
-// dP(j+1).  Roles (320 threads): warps 0-7 element-wise (warp w: lanes
-// 32 (w % 4) .., columns 64 (w / 4) ..), warp 8 TMA, warp 9 MMA.
+// dP(j+1); with two S it is always one S ahead.
+// Roles (576 threads): warps 0-15 element-wise (warp w: lanes 32 (w % 4) ..,
+// columns 32 (w / 4) ..), warp 16 TMA, warp 17 MMA.  Sixteen warps at 96
+// registers (an SM sub-partition holds five warps) against eight at 168: the
+// element-wise work is a chain of dependent operations, and with two warps
+// to a sub-partition it issued on 29-39 % of cycles.
 #include <cuda.h>
 
 #include "cap.cuh"
@@ -66,9 +72,11 @@ namespace {
 
 constexpr int BM = 128;            // rows of an outer or inner tile
 constexpr int HD = 128;
-constexpr int kTmaWarp = 8, kMmaWarp = 9, kGradThreads = 320;
+constexpr int kElemWarps = 16, kCols = 32;          // columns of an element-wise warp
+constexpr int kTmaWarp = 16, kMmaWarp = 17, kGradThreads = 576;
+constexpr int kRegThreads = 640;                   // five warps to a sub-partition: 96 registers
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0, kColP = 128, kColA1 = 256, kColA2 = 384;
+constexpr uint32_t kColS = 0, kColP = 128, kColA1 = 256, kColA2 = 384;   // second S at kColA1, second dP at kColA2
 constexpr uint32_t kTileBytes = BM * HD * 2;       // 32 KB: two 16 KB halves of d
 constexpr uint32_t kHalfBytes = kTileBytes / 2;
 constexpr uint32_t kStatBytes = 4 * BM * 4;        // a query tile's four rows of statistics
@@ -83,7 +91,7 @@ static_assert(kGradSmem + 1024 <= 232448, "one CTA per SM");
 struct GradArgs {
     LayerArgs a;
     int N, n_tiles, n_pad;
-    float* stats;          // [B][Hq][4][n_pad]
+    float* stats;          // [B][Hq][4][n_pad]: -(lse_c - log2 a), -D_c, -lse*, -D*
     const float* lse;      // [2][B][Hq][N] of the forward pass
     const float* alpha;
     void* d0;              // keys outer: dK; queries outer: dQ
@@ -101,33 +109,30 @@ __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
     return *reinterpret_cast<uint32_t*>(&h);
 }
 
-// Bits lo .. hi (inclusive, clipped to 0 .. 63).
-__device__ __forceinline__ uint64_t bit_range(int lo, int hi) {
+// Bits lo .. hi (inclusive, clipped to 0 .. 31).
+__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
     lo = max(lo, 0);
-    hi = min(hi, 63);
-    return lo > hi ? 0ull : (~0ull >> (63 - hi)) & (~0ull << lo);
+    hi = min(hi, 31);
+    return lo > hi ? 0u : (~0u >> (31 - hi)) & (~0u << lo);
 }
 
-// Which of a thread's 64 columns its row sees under the two masks.  Rows are
+// Which of a thread's 32 columns its row sees under the two masks.  Rows are
 // keys and columns queries, or the other way round.
 struct Seen {
-    uint32_t causal[2], lam[2];
+    uint32_t causal, lam;
 };
 __device__ __forceinline__ Seen seen_columns(const LayerArgs& a, bool keys_outer, int row, int col0) {
-    uint64_t c, l;
     if (keys_outer) {
-        c = bit_range(row - col0, 63);
-        l = row < a.sink ? c : bit_range(row - col0, row + a.recent - 1 - col0);
-    } else {
-        c = bit_range(0, row - col0);
-        l = c & (bit_range(0, a.sink - 1 - col0) | bit_range(row - a.recent + 1 - col0, 63));
+        const uint32_t c = bit_range(row - col0, 31);
+        return {c, row < a.sink ? c : bit_range(row - col0, row + a.recent - 1 - col0)};
     }
-    return {{(uint32_t)c, (uint32_t)(c >> 32)}, {(uint32_t)l, (uint32_t)(l >> 32)}};
+    const uint32_t c = bit_range(0, row - col0);
+    return {c, c & (bit_range(0, a.sink - 1 - col0) | bit_range(row - a.recent + 1 - col0, 31))};
 }
 
-// Where a thread finds the (lse, D) pairs of its columns: one pair of pairs in
-// registers when its row is the query, four rows of shared memory (one entry
-// per column) when its columns are.
+// Where a thread finds the (-lse, -D) pairs of its columns: one pair of pairs
+// in registers when its row is the query, four rows of shared memory (one
+// entry per column) when its columns are.
 struct RowStats {
     float lse_c, dc, lse_l, dl;
     const float* cols;
@@ -152,9 +157,10 @@ __device__ __forceinline__ void tanh_columns(float (&x)[W], const CapArgs& cap) 
 #pragma unroll
     for (int c = 0; c < W; c += 2) big = fmax3(big, fabsf(x[c]), fabsf(x[c + 1]));
     if (__all_sync(0xffffffffu, big * cap.k <= 1.f)) {
+        const TanhPoly tp = tanh_poly(cap.k);
 #pragma unroll
         for (int c = 0; c < W; c += 2) {
-            const float2 t = tanh_fma2(fmul2(make_float2(x[c], x[c + 1]), make_float2(cap.k, cap.k)));
+            const float2 t = poly_fma2(make_float2(x[c], x[c + 1]), tp);
             x[c] = t.x;
             x[c + 1] = t.y;
         }
@@ -164,30 +170,30 @@ __device__ __forceinline__ void tanh_columns(float (&x)[W], const CapArgs& cap) 
     }
 }
 
-// A warp's 64 columns: x[] dot products -> W times the cap's slope, W packed
+// A warp's 32 columns: x[] dot products -> W, or with a cap -W times its slope
+// (t^2 - 1 is one instruction; the sign goes into the last multiply); W packed
 // as bf16 to TMEM on the way when COLS (keys outer).  MASKED: some column is
 // not seen, or is seen by both attentions.
 template <bool CAP, bool COLS, bool MASKED>
-__device__ __forceinline__ void weights(float (&x)[64], const LayerArgs& a, float sl, const RowStats& r, const Seen& seen,
-                                        bool neg, uint32_t w_addr) {
-    if constexpr (CAP) tanh_columns<64>(x, a.cap);
-    uint32_t pk[32];
+__device__ __forceinline__ void weights(float (&x)[kCols], const LayerArgs& a, float sl, const RowStats& r,
+                                        const Seen& seen, bool neg, uint32_t w_addr) {
+    if constexpr (CAP) tanh_columns<kCols>(x, a.cap);
+    uint32_t pk[kCols / 2];
 #pragma unroll
-    for (int c4 = 0; c4 < 16; ++c4) {
+    for (int c4 = 0; c4 < kCols / 4; ++c4) {
         float4 l4 = stat4<COLS>(r, 0, c4);
         if constexpr (MASKED) {
-            const int w = c4 >> 3, sh = 4 * (c4 & 7);
-            l4 = choose4(seen.lam[w], sh, stat4<COLS>(r, 2, c4), l4);
-            l4 = choose4(seen.causal[w], sh, l4, make_float4(INFINITY, INFINITY, INFINITY, INFINITY));
+            l4 = choose4(seen.lam, 4 * c4, stat4<COLS>(r, 2, c4), l4);
+            l4 = choose4(seen.causal, 4 * c4, l4, make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY));
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int c = 4 * c4 + 2 * h;
             float2 v = make_float2(x[c], x[c + 1]);
-            const float2 nl = h ? make_float2(-l4.z, -l4.w) : make_float2(-l4.x, -l4.y);
+            const float2 nl = h ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y);
             float2 slope;
             if constexpr (CAP) {
-                slope = ffma2(make_float2(-v.x, -v.y), v, make_float2(1.f, 1.f));
+                slope = ffma2(v, v, make_float2(-1.f, -1.f));
                 v = ffma2(v, make_float2(a.cap.c2, a.cap.c2), nl);
             } else {
                 v = ffma2(v, make_float2(sl, sl), nl);
@@ -200,45 +206,42 @@ __device__ __forceinline__ void weights(float (&x)[64], const LayerArgs& a, floa
             x[c + 1] = v.y;
         }
     }
-    if constexpr (COLS) tmem_st32(w_addr, pk);
+    if constexpr (COLS) tmem_st16(w_addr, pk);
 }
 
-// x[] = W (times slope), TMEM dP -> dS packed as bf16 over dP's columns.
+// x[] as weights left it, TMEM dP -> dS (with a cap: -dS) packed as bf16 over
+// dP's columns.
 template <bool COLS, bool MASKED>
-__device__ __forceinline__ void score_grads(const float (&x)[64], const RowStats& r, const Seen& seen, uint32_t d_addr) {
+__device__ __forceinline__ void score_grads(const float (&x)[kCols], const RowStats& r, const Seen& seen,
+                                            uint32_t d_addr) {
+    float d[kCols];
+    tmem_ld32(d_addr, d);
+    uint32_t pk[kCols / 2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        float d[32];
-        tmem_ld32(d_addr + 32 * h, d);
-        uint32_t pk[16];
-#pragma unroll
-        for (int c4 = 0; c4 < 8; ++c4) {
-            float4 q = stat4<COLS>(r, 1, 8 * h + c4);
-            if constexpr (MASKED) q = choose4(seen.lam[h], 4 * c4, stat4<COLS>(r, 3, 8 * h + c4), q);
-            const int c = 4 * c4;
-            const float2 u = fmul2(make_float2(x[32 * h + c], x[32 * h + c + 1]),
-                                   fadd2(make_float2(d[c], d[c + 1]), make_float2(-q.x, -q.y)));
-            const float2 v = fmul2(make_float2(x[32 * h + c + 2], x[32 * h + c + 3]),
-                                   fadd2(make_float2(d[c + 2], d[c + 3]), make_float2(-q.z, -q.w)));
-            pk[2 * c4] = pack_bf16(u.x, u.y);
-            pk[2 * c4 + 1] = pack_bf16(v.x, v.y);
-        }
-        tmem_st16(d_addr + 16 * h, pk);
+    for (int c4 = 0; c4 < kCols / 4; ++c4) {
+        float4 q = stat4<COLS>(r, 1, c4);
+        if constexpr (MASKED) q = choose4(seen.lam, 4 * c4, stat4<COLS>(r, 3, c4), q);
+        const int c = 4 * c4;
+        const float2 u = fmul2(make_float2(x[c], x[c + 1]), fadd2(make_float2(d[c], d[c + 1]), make_float2(q.x, q.y)));
+        const float2 v = fmul2(make_float2(x[c + 2], x[c + 3]), fadd2(make_float2(d[c + 2], d[c + 3]), make_float2(q.z, q.w)));
+        pk[2 * c4] = pack_bf16(u.x, u.y);
+        pk[2 * c4 + 1] = pack_bf16(v.x, v.y);
     }
+    tmem_st16(d_addr, pk);
 }
 
 // A tile with keys that both attentions see, for a gate outside [0, 1]: the
 // shares a P_c and (1 - a) P_s differ in sign and are formed one by one (the
-// statistics hold lse_s - log2 |1 - a| and D_s), 16 columns at a time.
+// statistics hold lse_s - log2 |1 - a| and D_s), 16 columns at a time.  Signs
+// as in weights.
 template <bool CAP, bool COLS>
-__device__ __forceinline__ void signed_shares(const LayerArgs& a, float sl, const RowStats& r, const Seen& seen, bool neg_c,
+__device__ __forceinline__ void signed_shares(const LayerArgs& a, float sl, const RowStats& r, Seen seen, bool neg_c,
                                               bool neg_s, uint32_t s_addr, uint32_t d_addr) {
 #pragma unroll 1
-    for (int ch = 0; ch < 4; ++ch) {
+    for (int ch = 0; ch < kCols / 16; ++ch) {
         float x[16], d[16];
         tmem_ld16(s_addr + 16 * ch, x);
         tmem_ld16(d_addr + 16 * ch, d);
-        const uint32_t causal = seen.causal[ch >> 1] >> (16 * (ch & 1)), lam = seen.lam[ch >> 1] >> (16 * (ch & 1));
         uint32_t pw[8], pg[8];
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
@@ -248,18 +251,20 @@ __device__ __forceinline__ void signed_shares(const LayerArgs& a, float sl, cons
             float slope = 1.f, s;
             if constexpr (CAP) {
                 const float t = tanh_sfu(x[c] * a.cap.k);
-                slope = fmaf(-t, t, 1.f);
+                slope = fmaf(t, t, -1.f);
                 s = t * a.cap.c2;
             } else {
                 s = x[c] * sl;
             }
-            float wc = (causal >> c) & 1u ? sfu_exp2(s - lc) : 0.f;
-            float ws = (lam >> c) & 1u ? sfu_exp2(s - ls) : 0.f;
+            float wc = (seen.causal >> c) & 1u ? sfu_exp2(s + lc) : 0.f;
+            float ws = (seen.lam >> c) & 1u ? sfu_exp2(s + ls) : 0.f;
             wc = neg_c ? -wc : wc;
             ws = neg_s ? -ws : ws;
             x[c] = wc + ws;
-            d[c] = slope * fmaf(x[c], d[c], -fmaf(wc, qc, ws * qs));
+            d[c] = slope * fmaf(x[c], d[c], fmaf(wc, qc, ws * qs));
         }
+        seen.causal >>= 16;
+        seen.lam >>= 16;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
             pw[c] = pack_bf16(x[2 * c], x[2 * c + 1]);
@@ -270,50 +275,52 @@ __device__ __forceinline__ void signed_shares(const LayerArgs& a, float sl, cons
     }
 }
 
-// The sums of P and P dP of a thread's 64 columns under each mask.
+// The sums of P and P dP of a thread's 32 columns under each mask.
 struct RowSums {
     float lc, dc, ls, ds;
 };
 template <bool CAP, bool MASKED>
-__device__ __forceinline__ void add_sums(RowSums& sum, const LayerArgs& a, float sl, float lse_c, float lse_s,
+__device__ __forceinline__ void add_sums(RowSums& sum, const LayerArgs& a, float sl, float nlse_c, float nlse_s,
                                          const Seen& seen, uint32_t s_addr, uint32_t d_addr) {
+    float x[kCols];
+    tmem_ld32(s_addr, x);
+    if constexpr (CAP) tanh_columns<kCols>(x, a.cap);
+    const float f = CAP ? a.cap.c2 : sl;
+    float2 lc = make_float2(0.f, 0.f), dc = lc;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        float x[32], d[32];
-        tmem_ld32(s_addr + 32 * h, x);
-        tmem_ld32(d_addr + 32 * h, d);
-        if constexpr (CAP) tanh_columns<32>(x, a.cap);
-        const float f = CAP ? a.cap.c2 : sl;
-        float2 lc = make_float2(0.f, 0.f), dc = lc;
+        float d[16];
+        tmem_ld16(d_addr + 16 * h, d);
 #pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-            float2 v = ffma2(make_float2(x[c], x[c + 1]), make_float2(f, f), make_float2(-lse_c, -lse_c));
+        for (int i = 0; i < 16; i += 2) {
+            const int c = 16 * h + i;
+            float2 v = ffma2(make_float2(x[c], x[c + 1]), make_float2(f, f), make_float2(nlse_c, nlse_c));
             if constexpr (MASKED) {
                 // both attentions: the score once more, relative to lse_s
-                if ((seen.lam[h] >> c) & 1u) {
-                    const float p = sfu_exp2(fmaf(x[c], f, -lse_s));
-                    sum.ls += p;
-                    sum.ds = fmaf(p, d[c], sum.ds);
-                }
-                if ((seen.lam[h] >> (c + 1)) & 1u) {
-                    const float p = sfu_exp2(fmaf(x[c + 1], f, -lse_s));
-                    sum.ls += p;
-                    sum.ds = fmaf(p, d[c + 1], sum.ds);
-                }
-                v.x = (seen.causal[h] >> c) & 1u ? v.x : -INFINITY;
-                v.y = (seen.causal[h] >> (c + 1)) & 1u ? v.y : -INFINITY;
+                const float p0 = (seen.lam >> c) & 1u ? sfu_exp2(fmaf(x[c], f, nlse_s)) : 0.f;
+                const float p1 = (seen.lam >> (c + 1)) & 1u ? sfu_exp2(fmaf(x[c + 1], f, nlse_s)) : 0.f;
+                sum.ls += p0 + p1;
+                sum.ds = fmaf(p0, d[i], fmaf(p1, d[i + 1], sum.ds));
+                v.x = (seen.causal >> c) & 1u ? v.x : -INFINITY;
+                v.y = (seen.causal >> (c + 1)) & 1u ? v.y : -INFINITY;
             }
             v = make_float2(sfu_exp2(v.x), sfu_exp2(v.y));
             lc = fadd2(lc, v);
-            dc = ffma2(v, make_float2(d[c], d[c + 1]), dc);
+            dc = ffma2(v, make_float2(d[i], d[i + 1]), dc);
         }
-        sum.lc += lc.x + lc.y;
-        sum.dc += dc.x + dc.y;
     }
+    sum.lc += lc.x + lc.y;
+    sum.dc += dc.x + dc.y;
 }
 
+// TMEM columns of S(j) and dP(j).
+template <int MODE>
+__device__ __forceinline__ uint32_t s_col(int j) { return MODE != KEYS && (j & 1) ? kColA1 : kColS; }
+template <int MODE>
+__device__ __forceinline__ uint32_t d_col(int j) { return MODE == STATS && (j & 1) ? kColA2 : kColP; }
+
 template <int MODE, bool CAP>
-__global__ void __launch_bounds__(kGradThreads, 1)
+__global__ void __launch_bounds__(kRegThreads, 1)
     mix_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDo,
                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const GradArgs p) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -329,11 +336,11 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     uint64_t* x_full = bars + 0;
     uint64_t* y_full = bars + 1;    // [2]
     uint64_t* y_empty = bars + 3;   // [2]
-    uint64_t* s_full = bars + 5;
-    uint64_t* d_full = bars + 6;
-    uint64_t* w_ready = bars + 7;   // W written (keys outer), S read
-    uint64_t* g_ready = bars + 8;   // dS written, dP read
-    uint64_t* done = bars + 9;
+    uint64_t* s_full = bars + 5;    // [2], by the tile's parity, as the next three
+    uint64_t* d_full = bars + 7;
+    uint64_t* w_ready = bars + 9;   // W written (keys outer), S read (statistics: dP too)
+    uint64_t* g_ready = bars + 11;  // dS written
+    uint64_t* done = bars + 13;
     uint32_t* holder = reinterpret_cast<uint32_t*>(smem + kOffHolder);
 
     // Work item, the longest first.  Keys outer: key tile ot of KV head `head`,
@@ -354,12 +361,13 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         mbar_init(x_full, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&y_full[i], 1);
-            mbar_init(&y_empty[i], kKeys ? 9 : 1);   // the MMAs' commit, and the warps that read the stage's statistics
+            // the MMAs' commit, and the warps that read the stage's statistics
+            mbar_init(&y_empty[i], kKeys ? 1 + kElemWarps : 1);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&d_full[i], 1);
+            mbar_init(&w_ready[i], kElemWarps);
+            mbar_init(&g_ready[i], kElemWarps);
         }
-        mbar_init(s_full, 1);
-        mbar_init(d_full, 1);
-        mbar_init(w_ready, 8);
-        mbar_init(g_ready, 8);
         mbar_init(done, 1);
         fence_barrier_init();
     }
@@ -414,51 +422,81 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 const uint32_t y = sY + ((j & 1) * 2 + w) * kTileBytes;
 #pragma unroll
                 for (int kk = 0; kk < BM / 16; ++kk)
-                    tc_mma_ta(tmem + col, tmem + a_col + 64 * (kk >> 2) + 8 * (kk & 3),
+                    tc_mma_ta(tmem + col, tmem + a_col + kCols * (kk >> 1) + 8 * (kk & 1),
                               sw128_desc(y + kk * 2048, kHalfBytes, 1024), idesc_mn, (j > 0 || kk > 0) ? 1u : 0u);
             };
-            bool ok = mbar_wait(x_full, 0, p.status) && mbar_wait(&y_full[0], 0, p.status);
+            auto wait_tile = [&](int j) { return mbar_wait(&y_full[j & 1], (j >> 1) & 1, p.status); };
+            auto issue_s = [&](int j) {
+                issue_xy(s_col<MODE>(j), 0, j);
+                tc_commit(&s_full[j & 1]);
+            };
+            auto issue_d = [&](int j) {
+                issue_xy(d_col<MODE>(j), 1, j);
+                tc_commit(&d_full[j & 1]);
+            };
+            bool ok = mbar_wait(x_full, 0, p.status) && wait_tile(0);
             if (ok) {
                 tc_fence_after();
-                issue_xy(kColS, 0, 0);
-                tc_commit(s_full);
-                issue_xy(kColP, 1, 0);
-                tc_commit(d_full);
+                issue_s(0);
+                issue_d(0);
                 if (kStats) tc_commit(&y_empty[0]);
             }
-            for (int j = 0; j < n_in && ok; ++j) {
-                const bool next = j + 1 < n_in;
-                if (next) ok = mbar_wait(&y_full[(j + 1) & 1], ((j + 1) >> 1) & 1, p.status);
-                ok = ok && mbar_wait(w_ready, j & 1, p.status);
-                if (!ok) break;
-                tc_fence_after();
-                if constexpr (kKeys) issue_acc(kColA1, kColS, 1, j);
-                if (next) {
-                    issue_xy(kColS, 0, j + 1);
-                    tc_commit(s_full);
-                }
-                ok = mbar_wait(g_ready, j & 1, p.status);
-                if (!ok) break;
-                tc_fence_after();
-                if constexpr (!kStats) {
-                    issue_acc(kColA2, kColP, 0, j);
-                    tc_commit(&y_empty[j & 1]);
-                }
-                if (next) {
-                    issue_xy(kColP, 1, j + 1);
-                    tc_commit(d_full);
-                    if (kStats) tc_commit(&y_empty[(j + 1) & 1]);
-                } else {
-                    tc_commit(done);
+            if (!kKeys && n_in > 1 && ok) {
+                ok = wait_tile(1);
+                if (ok) {
+                    tc_fence_after();
+                    issue_s(1);
+                    if (kStats) {
+                        issue_d(1);
+                        tc_commit(&y_empty[1]);
+                    }
                 }
             }
+            for (int j = 0; j < n_in && ok; ++j) {
+                const int ph = (j >> 1) & 1;
+                if constexpr (kStats) {
+                    // both slots run ahead: tile j + 2 once tile j is read
+                    ok = mbar_wait(&w_ready[j & 1], ph, p.status);
+                    if (ok && j + 2 < n_in) {
+                        ok = wait_tile(j + 2);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_s(j + 2);
+                        issue_d(j + 2);
+                        tc_commit(&y_empty[j & 1]);
+                    }
+                } else {
+                    const bool next = j + 1 < n_in;
+                    if constexpr (kKeys) {
+                        if (next) ok = wait_tile(j + 1);
+                        ok = ok && mbar_wait(&w_ready[j & 1], ph, p.status);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_acc(kColA1, kColS, 1, j);
+                        if (next) issue_s(j + 1);
+                    }
+                    ok = mbar_wait(&g_ready[j & 1], ph, p.status);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_acc(kColA2, kColP, 0, j);
+                    tc_commit(&y_empty[j & 1]);
+                    if (next) issue_d(j + 1);
+                    if (!kKeys && j + 2 < n_in) {
+                        // one S ahead: its slot was read before dS(j) was written
+                        ok = mbar_wait(&w_ready[j & 1], ph, p.status) && wait_tile(j + 2);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_s(j + 2);
+                    }
+                }
+            }
+            if (ok) tc_commit(done);
         }
-    } else {
+    } else if (warp < kElemWarps) {
         // ------------------------------------------------ element-wise warps
-        const int wg = warp >> 2;                             // columns 64 wg ..
+        const int wg = warp >> 2;                             // columns 32 wg ..
         const int row = 32 * (warp & 3) + lane;               // TMEM lane: outer row
         const uint32_t lane_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        const uint32_t s_addr = lane_addr + kColS + 64 * wg, d_addr = lane_addr + kColP + 64 * wg;
         const float sl = a.scale * kLog2e;
         const float al = p.alpha[kv];
         const bool neg_c = al < 0.f, neg_s = 1.f - al < 0.f;
@@ -468,32 +506,33 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         if constexpr (kStats) {
             const bool live = orow < p.N;
             const size_t r = ((size_t)b * a.Hq + head) * p.N + (live ? orow : 0);
-            rs.lse_c = live ? p.lse[r] : INFINITY;
-            rs.lse_l = live ? p.lse[(size_t)a.B * a.Hq * p.N + r] : INFINITY;
+            rs.lse_c = live ? -p.lse[r] : -INFINITY;
+            rs.lse_l = live ? -p.lse[(size_t)a.B * a.Hq * p.N + r] : -INFINITY;
         } else if constexpr (!kKeys) {
             const float* st = p.stats + ((size_t)b * a.Hq + head) * 4 * p.n_pad + orow;
             rs = {st[0], st[p.n_pad], st[2 * (size_t)p.n_pad], st[3 * (size_t)p.n_pad], nullptr};
         }
         bool ok = true;
         for (int j = 0; j < n_in; ++j) {
-            const int it = inner_tile(j);
+            const int it = inner_tile(j), ph = (j >> 1) & 1;
+            const uint32_t s_addr = lane_addr + s_col<MODE>(j) + kCols * wg, d_addr = lane_addr + d_col<MODE>(j) + kCols * wg;
             if constexpr (kKeys) {
-                rs.cols = reinterpret_cast<const float*>(smem + kOffStat + (j & 1) * kStatBytes) + 64 * wg;
+                rs.cols = reinterpret_cast<const float*>(smem + kOffStat + (j & 1) * kStatBytes) + kCols * wg;
                 // the statistics arrived with the tile that S(j) was computed from;
                 // this wait makes the copy visible to this thread too
-                ok = ok && mbar_wait(&y_full[j & 1], (j >> 1) & 1, p.status);
+                ok = ok && mbar_wait(&y_full[j & 1], ph, p.status);
             }
-            ok = __all_sync(0xffffffffu, ok && mbar_wait(s_full, j & 1, p.status));
+            ok = __all_sync(0xffffffffu, ok && mbar_wait(&s_full[j & 1], ph, p.status));
             if (!ok) break;
             tc_fence_after();
             // every pair of the warp's part is seen by the causal attention only?
-            const int r0 = BM * ot + 32 * (warp & 3), c0 = BM * it + 64 * wg;
-            const int key0 = kKeys ? r0 : c0, key1 = kKeys ? r0 + 31 : c0 + 63, query0 = kKeys ? c0 : r0;
+            const int r0 = BM * ot + 32 * (warp & 3), c0 = BM * it + kCols * wg;
+            const int key0 = kKeys ? r0 : c0, key1 = kKeys ? r0 + 31 : c0 + kCols - 1, query0 = kKeys ? c0 : r0;
             const bool plain = key0 >= a.sink && query0 - key1 >= a.recent;   // recent >= 1: below the diagonal too
             Seen seen{};
             if (!plain) seen = seen_columns(a, kKeys, orow, c0);
             if constexpr (kStats) {
-                ok = __all_sync(0xffffffffu, mbar_wait(d_full, j & 1, p.status));
+                ok = __all_sync(0xffffffffu, mbar_wait(&d_full[j & 1], ph, p.status));
                 if (!ok) break;
                 tc_fence_after();
                 if (plain)
@@ -502,10 +541,11 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                     add_sums<CAP, true>(sum, a, sl, rs.lse_c, rs.lse_l, seen, s_addr, d_addr);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(w_ready);
+                if (lane == 0) mbar_arrive(&w_ready[j & 1]);
+                continue;
             } else if (plain || !(neg_c || neg_s)) {
-                float x[64];
-                tmem_ld64(s_addr, x);
+                float x[kCols];
+                tmem_ld32(s_addr, x);
                 if (plain)
                     weights<CAP, kKeys, false>(x, a, sl, rs, seen, neg_c, s_addr);
                 else
@@ -513,8 +553,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 if constexpr (kKeys) tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(w_ready);
-                ok = __all_sync(0xffffffffu, mbar_wait(d_full, j & 1, p.status));
+                if (lane == 0) mbar_arrive(&w_ready[j & 1]);
+                ok = __all_sync(0xffffffffu, mbar_wait(&d_full[j & 1], ph, p.status));
                 if (!ok) break;
                 tc_fence_after();
                 if (plain)
@@ -522,37 +562,42 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 else
                     score_grads<kKeys, true>(x, rs, seen, d_addr);
             } else {
-                ok = __all_sync(0xffffffffu, mbar_wait(d_full, j & 1, p.status));
+                ok = __all_sync(0xffffffffu, mbar_wait(&d_full[j & 1], ph, p.status));
                 if (!ok) break;
                 tc_fence_after();
                 signed_shares<CAP, kKeys>(a, sl, rs, seen, neg_c, neg_s, s_addr, d_addr);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(w_ready);
+                if (lane == 0) mbar_arrive(&w_ready[j & 1]);
             }
-            if constexpr (!kStats) tmem_wait_st();
+            tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(g_ready);
+                mbar_arrive(&g_ready[j & 1]);
                 if constexpr (kKeys) mbar_arrive(&y_empty[j & 1]);   // done with the stage's statistics
             }
         }
         ok = ok && __all_sync(0xffffffffu, mbar_wait(done, 0, p.status));
         if constexpr (kStats) {
-            // join the two halves of each row, then the row's statistics
-            float4* half = reinterpret_cast<float4*>(smem + kOffStat);   // [128] sums of columns 64 ..
-            float* share = reinterpret_cast<float*>(half + BM);          // [4] of the warps
-            if (wg == 1) half[row] = make_float4(sum.lc, sum.dc, sum.ls, sum.ds);
-            asm volatile("bar.sync 1, 256;" ::: "memory");
+            // join the four quarters of each row, then the row's statistics
+            float4* quarter = reinterpret_cast<float4*>(smem + kOffY);   // [3][128]; every tile has been read
+            float* share = reinterpret_cast<float*>(quarter + 3 * BM);   // [4] of the warps
+            if (wg > 0) quarter[(wg - 1) * BM + row] = make_float4(sum.lc, sum.dc, sum.ls, sum.ds);
+            asm volatile("bar.sync 1, 512;" ::: "memory");
             if (wg == 0) {
-                const float4 o = half[row];
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    const float4 t = quarter[k * BM + row];
+                    o = make_float4(o.x + t.x, o.y + t.y, o.z + t.z, o.w + t.w);
+                }
                 const float lc = sum.lc + o.x, ls = sum.ls + o.z;
                 const bool live = ok && orow < p.N && lc > 0.f && ls > 0.f;
                 const float dc = live ? (sum.dc + o.y) / lc : 0.f, ds = live ? (sum.ds + o.w) / ls : 0.f;
-                const float lse_c = live ? rs.lse_c + log2f(lc) - log2f(fabsf(al)) : INFINITY;       // +inf: a closed gate
-                const float lse_s = live ? rs.lse_l + log2f(ls) - log2f(fabsf(1.f - al)) : INFINITY;
+                const float lse_c = live ? log2f(lc) - rs.lse_c - log2f(fabsf(al)) : INFINITY;       // +inf: a closed gate
+                const float lse_s = live ? log2f(ls) - rs.lse_l - log2f(fabsf(1.f - al)) : INFINITY;
                 float lse_l = lse_s, dl = ds;
                 if (!(neg_c || neg_s) && live) {
                     // 2^-lse* = 2^-lse_c + 2^-lse_s, the two shares' weights
@@ -563,10 +608,10 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 }
                 float* st = p.stats + ((size_t)b * a.Hq + head) * 4 * p.n_pad + orow;
                 if (bounds_ok(orow < p.n_pad, p.status)) {
-                    st[0] = lse_c;
-                    st[p.n_pad] = dc;
-                    st[2 * (size_t)p.n_pad] = lse_l;
-                    st[3 * (size_t)p.n_pad] = dl;
+                    st[0] = -lse_c;
+                    st[p.n_pad] = -dc;
+                    st[2 * (size_t)p.n_pad] = -lse_l;
+                    st[3 * (size_t)p.n_pad] = -dl;
                 }
                 float d = dc - ds;
 #pragma unroll
@@ -579,23 +624,20 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             }
         } else if (ok) {
             tc_fence_after();
-            const size_t off = (((size_t)b * p.N + orow) * heads + head) * HD + 64 * wg;
+            const size_t off = (((size_t)b * p.N + orow) * heads + head) * HD + kCols * wg;
             const bool live = orow < p.N && bounds_ok(b < a.B && head < heads, p.status);
 #pragma unroll
             for (int t = 0; t < (kKeys ? 2 : 1); ++t) {
                 __nv_bfloat16* o = static_cast<__nv_bfloat16*>(t ? p.d1 : p.d0) + off;
-                const float f = t ? 1.f : a.scale;            // dS held back the softmax scale
+                const float f = t ? 1.f : CAP ? -a.scale : a.scale;   // dS held back the softmax scale
+                float v[kCols];
+                tmem_ld32(lane_addr + (t ? kColA1 : kColA2) + kCols * wg, v);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float v[32];
-                    tmem_ld32(lane_addr + (t ? kColA1 : kColA2) + 64 * wg + 32 * h, v);
+                for (int e = 0; e < kCols / 8; ++e) {
+                    float v8[8];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float v8[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v8[i] = v[8 * e + i] * f;
-                        if (live) store_row<__nv_bfloat16, 8>(o + 32 * h + 8 * e, v8);
-                    }
+                    for (int i = 0; i < 8; ++i) v8[i] = v[8 * e + i] * f;
+                    if (live) store_row<__nv_bfloat16, 8>(o + 8 * e, v8);
                 }
             }
         }

@@ -346,10 +346,10 @@ __device__ __forceinline__ float softmax_tile(uint32_t s_addr, float sl, const C
         for (int i = 0; i < 4; ++i)
             big = fmax3(big, fmaxf(hi[i], s[124 + i]), -fminf(lo[i], s[124 + i]));
         if (__all_sync(0xffffffffu, big * cap.k <= 1.f)) {
-            const CapPoly cp = cap_poly(cap);
+            const TanhPoly cp = tanh_poly(cap.k, cap.c2);
 #pragma unroll
             for (int c = 0; c < 128; c += 2) {
-                const float2 t = cap_fma2(make_float2(s[c], s[c + 1]), cp);
+                const float2 t = poly_fma2(make_float2(s[c], s[c + 1]), cp);
                 s[c] = t.x;
                 s[c + 1] = t.y;
             }
