@@ -43,6 +43,7 @@ __device__ __forceinline__ float tanh_sfu(float y) {
     return fmaf(-2.f, sfu_rcp(1.f + e), 1.f);
 }
 
+constexpr float kTanhRange = 1.f;   // of |y|
 constexpr float kTanh0 = 0.999993085861206f, kTanh1 = -0.3329806625843048f, kTanh2 = 0.13036811351776123f,
                 kTanh3 = -0.04481755197048187f, kTanh4 = 0.00903642363846302f;
 

@@ -156,7 +156,7 @@ __device__ __forceinline__ void tanh_columns(float (&x)[W], const CapArgs& cap) 
     float big = 0.f;
 #pragma unroll
     for (int c = 0; c < W; c += 2) big = fmax3(big, fabsf(x[c]), fabsf(x[c + 1]));
-    if (__all_sync(0xffffffffu, big * cap.k <= 1.f)) {
+    if (__all_sync(0xffffffffu, big * cap.k <= kTanhRange)) {
         const TanhPoly tp = tanh_poly(cap.k);
 #pragma unroll
         for (int c = 0; c < W; c += 2) {
