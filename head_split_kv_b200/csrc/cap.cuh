@@ -65,6 +65,19 @@ __device__ __forceinline__ float2 poly_fma2(float2 x, const TanhPoly& c) {
     return fmul2(p, x);
 }
 
+// The largest |x|, in four chains.
+template <int W>
+__device__ __forceinline__ float largest(const float (&x)[W]) {
+    static_assert(W % 8 == 0, "pairs for four chains");
+    float m[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < W; c += 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m[i] = fmax3(m[i], fabsf(x[c + 2 * i]), fabsf(x[c + 2 * i + 1]));
+    }
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
 // The log2-domain score of a dot product: x * sl, or capped.  EXACT takes
 // CUDA's tanhf (the fp32 paths).
 template <bool CAP, bool EXACT = false>

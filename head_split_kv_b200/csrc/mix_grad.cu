@@ -149,36 +149,24 @@ __device__ __forceinline__ float4 choose4(uint32_t bits, int shift, const float4
                        (bits >> (shift + 2)) & 1u ? yes.z : no.z, (bits >> (shift + 3)) & 1u ? yes.w : no.w);
 }
 
-// Dot products to tanh, in place (CAP): on the FMA pipe when every |k x| of the
-// warp's part is at most 1, else on the SFU.
-template <int W>
-__device__ __forceinline__ void tanh_columns(float (&x)[W], const CapArgs& cap) {
-    float big = 0.f;
-#pragma unroll
-    for (int c = 0; c < W; c += 2) big = fmax3(big, fabsf(x[c]), fabsf(x[c + 1]));
-    if (__all_sync(0xffffffffu, big * cap.k <= kTanhRange)) {
-        const TanhPoly tp = tanh_poly(cap.k);
-#pragma unroll
-        for (int c = 0; c < W; c += 2) {
-            const float2 t = poly_fma2(make_float2(x[c], x[c + 1]), tp);
-            x[c] = t.x;
-            x[c + 1] = t.y;
-        }
-    } else {
-#pragma unroll
-        for (int c = 0; c < W; ++c) x[c] = tanh_sfu(x[c] * cap.k);
-    }
+// tanh(k x) of a pair (CAP); POLY: |k x| is within the polynomial's range.
+template <bool POLY>
+__device__ __forceinline__ float2 tanh2(float2 x, const CapArgs& cap, const TanhPoly& tp) {
+    return POLY ? poly_fma2(x, tp) : make_float2(tanh_sfu(x.x * cap.k), tanh_sfu(x.y * cap.k));
 }
 
 // A warp's 32 columns: x[] dot products -> W, or with a cap -W times its slope
 // (t^2 - 1 is one instruction; the sign goes into the last multiply); W packed
 // as bf16 to TMEM on the way when COLS (keys outer).  MASKED: some column is
-// not seen, or is seen by both attentions.
-template <bool CAP, bool COLS, bool MASKED>
-__device__ __forceinline__ void weights(float (&x)[kCols], const LayerArgs& a, float sl, const RowStats& r,
-                                        const Seen& seen, bool neg, uint32_t w_addr) {
-    if constexpr (CAP) tanh_columns<kCols>(x, a.cap);
+// not seen, or is seen by both attentions.  One loop from the dot product to
+// the packed W, so that the FMA, SFU and ALU work of neighbouring pairs
+// interleaves (in separate loops the pipes took turns: their shares of the
+// time added up to 96 %).
+template <bool CAP, bool COLS, bool MASKED, bool POLY>
+__device__ __forceinline__ void weights_loop(float (&x)[kCols], const LayerArgs& a, float sl, const RowStats& r,
+                                             const Seen& seen, uint32_t sign, uint32_t w_addr) {
     uint32_t pk[kCols / 2];
+    const TanhPoly tp = tanh_poly(a.cap.k);
 #pragma unroll
     for (int c4 = 0; c4 < kCols / 4; ++c4) {
         float4 l4 = stat4<COLS>(r, 0, c4);
@@ -193,14 +181,14 @@ __device__ __forceinline__ void weights(float (&x)[kCols], const LayerArgs& a, f
             const float2 nl = h ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y);
             float2 slope;
             if constexpr (CAP) {
+                v = tanh2<POLY>(v, a.cap, tp);
                 slope = ffma2(v, v, make_float2(-1.f, -1.f));
                 v = ffma2(v, make_float2(a.cap.c2, a.cap.c2), nl);
             } else {
                 v = ffma2(v, make_float2(sl, sl), nl);
             }
             v = make_float2(sfu_exp2(v.x), sfu_exp2(v.y));
-            if (neg) v = make_float2(-v.x, -v.y);
-            if constexpr (COLS) pk[c / 2] = pack_bf16(v.x, v.y);
+            if constexpr (COLS) pk[c / 2] = pack_bf16(v.x, v.y) ^ sign;
             if constexpr (CAP) v = fmul2(v, slope);
             x[c] = v.x;
             x[c + 1] = v.y;
@@ -208,12 +196,20 @@ __device__ __forceinline__ void weights(float (&x)[kCols], const LayerArgs& a, f
     }
     if constexpr (COLS) tmem_st16(w_addr, pk);
 }
+template <bool CAP, bool COLS, bool MASKED>
+__device__ __forceinline__ void weights(float (&x)[kCols], const LayerArgs& a, float sl, const RowStats& r,
+                                        const Seen& seen, uint32_t sign, uint32_t w_addr) {
+    if (!CAP || __all_sync(0xffffffffu, largest(x) * a.cap.k <= kTanhRange))
+        weights_loop<CAP, COLS, MASKED, true>(x, a, sl, r, seen, sign, w_addr);
+    else
+        weights_loop<CAP, COLS, MASKED, false>(x, a, sl, r, seen, sign, w_addr);
+}
 
 // x[] as weights left it, TMEM dP -> dS (with a cap: -dS) packed as bf16 over
 // dP's columns.
 template <bool COLS, bool MASKED>
 __device__ __forceinline__ void score_grads(const float (&x)[kCols], const RowStats& r, const Seen& seen,
-                                            uint32_t d_addr) {
+                                            uint32_t sign, uint32_t d_addr) {
     float d[kCols];
     tmem_ld32(d_addr, d);
     uint32_t pk[kCols / 2];
@@ -224,8 +220,8 @@ __device__ __forceinline__ void score_grads(const float (&x)[kCols], const RowSt
         const int c = 4 * c4;
         const float2 u = fmul2(make_float2(x[c], x[c + 1]), fadd2(make_float2(d[c], d[c + 1]), make_float2(q.x, q.y)));
         const float2 v = fmul2(make_float2(x[c + 2], x[c + 3]), fadd2(make_float2(d[c + 2], d[c + 3]), make_float2(q.z, q.w)));
-        pk[2 * c4] = pack_bf16(u.x, u.y);
-        pk[2 * c4 + 1] = pack_bf16(v.x, v.y);
+        pk[2 * c4] = pack_bf16(u.x, u.y) ^ sign;
+        pk[2 * c4 + 1] = pack_bf16(v.x, v.y) ^ sign;
     }
     tmem_st16(d_addr, pk);
 }
@@ -279,13 +275,11 @@ __device__ __forceinline__ void signed_shares(const LayerArgs& a, float sl, cons
 struct RowSums {
     float lc, dc, ls, ds;
 };
-template <bool CAP, bool MASKED>
-__device__ __forceinline__ void add_sums(RowSums& sum, const LayerArgs& a, float sl, float nlse_c, float nlse_s,
-                                         const Seen& seen, uint32_t s_addr, uint32_t d_addr) {
-    float x[kCols];
-    tmem_ld32(s_addr, x);
-    if constexpr (CAP) tanh_columns<kCols>(x, a.cap);
+template <bool CAP, bool MASKED, bool POLY>
+__device__ __forceinline__ void sums_loop(RowSums& sum, const float (&x)[kCols], const LayerArgs& a, float sl, float nlse_c,
+                                          float nlse_s, const Seen& seen, uint32_t d_addr) {
     const float f = CAP ? a.cap.c2 : sl;
+    const TanhPoly tp = tanh_poly(a.cap.k);
     float2 lc = make_float2(0.f, 0.f), dc = lc;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -294,11 +288,13 @@ __device__ __forceinline__ void add_sums(RowSums& sum, const LayerArgs& a, float
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
             const int c = 16 * h + i;
-            float2 v = ffma2(make_float2(x[c], x[c + 1]), make_float2(f, f), make_float2(nlse_c, nlse_c));
+            float2 t = make_float2(x[c], x[c + 1]);
+            if constexpr (CAP) t = tanh2<POLY>(t, a.cap, tp);
+            float2 v = ffma2(t, make_float2(f, f), make_float2(nlse_c, nlse_c));
             if constexpr (MASKED) {
                 // both attentions: the score once more, relative to lse_s
-                const float p0 = (seen.lam >> c) & 1u ? sfu_exp2(fmaf(x[c], f, nlse_s)) : 0.f;
-                const float p1 = (seen.lam >> (c + 1)) & 1u ? sfu_exp2(fmaf(x[c + 1], f, nlse_s)) : 0.f;
+                const float p0 = (seen.lam >> c) & 1u ? sfu_exp2(fmaf(t.x, f, nlse_s)) : 0.f;
+                const float p1 = (seen.lam >> (c + 1)) & 1u ? sfu_exp2(fmaf(t.y, f, nlse_s)) : 0.f;
                 sum.ls += p0 + p1;
                 sum.ds = fmaf(p0, d[i], fmaf(p1, d[i + 1], sum.ds));
                 v.x = (seen.causal >> c) & 1u ? v.x : -INFINITY;
@@ -311,6 +307,16 @@ __device__ __forceinline__ void add_sums(RowSums& sum, const LayerArgs& a, float
     }
     sum.lc += lc.x + lc.y;
     sum.dc += dc.x + dc.y;
+}
+template <bool CAP, bool MASKED>
+__device__ __forceinline__ void add_sums(RowSums& sum, const LayerArgs& a, float sl, float nlse_c, float nlse_s,
+                                         const Seen& seen, uint32_t s_addr, uint32_t d_addr) {
+    float x[kCols];
+    tmem_ld32(s_addr, x);
+    if (!CAP || __all_sync(0xffffffffu, largest(x) * a.cap.k <= kTanhRange))
+        sums_loop<CAP, MASKED, true>(sum, x, a, sl, nlse_c, nlse_s, seen, d_addr);
+    else
+        sums_loop<CAP, MASKED, false>(sum, x, a, sl, nlse_c, nlse_s, seen, d_addr);
 }
 
 // TMEM columns of S(j) and dP(j).
@@ -500,6 +506,7 @@ __global__ void __launch_bounds__(kRegThreads, 1)
         const float sl = a.scale * kLog2e;
         const float al = p.alpha[kv];
         const bool neg_c = al < 0.f, neg_s = 1.f - al < 0.f;
+        const uint32_t sign = neg_c ? 0x80008000u : 0u;        // of a packed pair of W or dS, where only a P_c counts
         const int orow = BM * ot + row;                       // key (keys outer) or query
         RowStats rs{0.f, 0.f, 0.f, 0.f, nullptr};
         RowSums sum{0.f, 0.f, 0.f, 0.f};
@@ -547,9 +554,9 @@ __global__ void __launch_bounds__(kRegThreads, 1)
                 float x[kCols];
                 tmem_ld32(s_addr, x);
                 if (plain)
-                    weights<CAP, kKeys, false>(x, a, sl, rs, seen, neg_c, s_addr);
+                    weights<CAP, kKeys, false>(x, a, sl, rs, seen, sign, s_addr);
                 else
-                    weights<CAP, kKeys, true>(x, a, sl, rs, seen, false, s_addr);
+                    weights<CAP, kKeys, true>(x, a, sl, rs, seen, 0u, s_addr);
                 if constexpr (kKeys) tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -558,9 +565,9 @@ __global__ void __launch_bounds__(kRegThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 if (plain)
-                    score_grads<kKeys, false>(x, rs, seen, d_addr);
+                    score_grads<kKeys, false>(x, rs, seen, sign, d_addr);
                 else
-                    score_grads<kKeys, true>(x, rs, seen, d_addr);
+                    score_grads<kKeys, true>(x, rs, seen, 0u, d_addr);
             } else {
                 ok = __all_sync(0xffffffffu, mbar_wait(&d_full[j & 1], ph, p.status));
                 if (!ok) break;

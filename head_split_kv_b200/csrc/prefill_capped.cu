@@ -71,31 +71,18 @@ __device__ __forceinline__ float2 exp2_fma_bounded2(float2 x) {
                        __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(t.y) << 23)));
 }
 
-// 32 columns of a row: dot products at s_addr -> p, packed as bf16 over the
-// first 16 of them; returns the sum of the rounded p.
-template <bool MASKED>
-__device__ __forceinline__ float exp_columns(uint32_t s_addr, const CapArgs& cap, const TanhPoly& tp, uint32_t vis) {
-    float x[32];
-    tmem_ld32(s_addr, x);
-    float big = 0.f;
-#pragma unroll
-    for (int c = 0; c < 32; c += 2) big = fmax3(big, fabsf(x[c]), fabsf(x[c + 1]));
-    if (__all_sync(0xffffffffu, big * cap.k <= kTanhRange)) {
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-            const float2 t = poly_fma2(make_float2(x[c], x[c + 1]), tp);
-            x[c] = t.x;
-            x[c + 1] = t.y;
-        }
-    } else {
-#pragma unroll
-        for (int c = 0; c < 32; ++c) x[c] = cap.c2 * tanh_sfu(x[c] * cap.k);
-    }
-    uint32_t pk[16];
+// 32 columns of a row: dot products x -> p, packed as bf16 in pk; returns the
+// sum of the rounded p.  POLY: every |k x| is within the polynomial's range.
+// One loop from the dot product to the packed p, so that the FMA, SFU and ALU
+// work of neighbouring pairs interleaves.
+template <bool MASKED, bool POLY>
+__device__ __forceinline__ float exp_loop(const float (&x)[32], uint32_t (&pk)[16], const CapArgs& cap, const TanhPoly& tp,
+                                          uint32_t vis) {
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
     for (int c2 = 0; c2 < 16; ++c2) {
-        const float2 v = make_float2(x[2 * c2], x[2 * c2 + 1]);
+        float2 v = make_float2(x[2 * c2], x[2 * c2 + 1]);
+        v = POLY ? poly_fma2(v, tp) : make_float2(cap.c2 * tanh_sfu(v.x * cap.k), cap.c2 * tanh_sfu(v.y * cap.k));
         float2 e = c2 % kFmaExpEvery == kFmaExpEvery - 1 ? exp2_fma_bounded2(v) : make_float2(sfu_exp2(v.x), sfu_exp2(v.y));
         if constexpr (MASKED) {
             e.x = (vis >> (2 * c2)) & 1u ? e.x : 0.f;
@@ -105,8 +92,19 @@ __device__ __forceinline__ float exp_columns(uint32_t s_addr, const CapArgs& cap
         pk[c2] = *reinterpret_cast<uint32_t*>(&h);
         sum[c2 & 1] = fadd2(sum[c2 & 1], make_float2(bf16_lo(pk[c2]), bf16_hi(pk[c2])));
     }
-    tmem_st16(s_addr, pk);
     return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+}
+
+// 32 columns of a row: dot products at s_addr -> p over the first 16 of them.
+template <bool MASKED>
+__device__ __forceinline__ float exp_columns(uint32_t s_addr, const CapArgs& cap, const TanhPoly& tp, uint32_t vis) {
+    float x[32];
+    tmem_ld32(s_addr, x);
+    uint32_t pk[16];
+    const float l = __all_sync(0xffffffffu, largest(x) * cap.k <= kTanhRange) ? exp_loop<MASKED, true>(x, pk, cap, tp, vis)
+                                                                             : exp_loop<MASKED, false>(x, pk, cap, tp, vis);
+    tmem_st16(s_addr, pk);
+    return l;
 }
 
 // EPI: EPI_STORE (store, or key-range split records), EPI_KEEP, EPI_MIX_KEEP
