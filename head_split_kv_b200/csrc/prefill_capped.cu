@@ -229,58 +229,59 @@ __global__ void __launch_bounds__(kRegThreads, 1)
             }
         }
     } else if (warp == kMmaWarp) {
-        if (lane == 0) {
-            constexpr uint32_t idesc_qk = idesc_bf16(BM, BN, 0, 0);
-            constexpr uint32_t idesc_pv = idesc_bf16(BM, HD, 0, 1);
-            auto issue_qk = [&](int qi, int j) {
-                const uint32_t q = sQ + qi * kQBytes, k = sK + (j & 1) * kTileBytes;
+        // the whole warp, one lane issuing
+        const uint32_t lead = lane == 0 ? 1u : 0u;
+        constexpr uint32_t idesc_qk = idesc_bf16(BM, BN, 0, 0);
+        constexpr uint32_t idesc_pv = idesc_bf16(BM, HD, 0, 1);
+        const uint32_t q_lo = sw128_lo(sQ, 16), k_lo = sw128_lo(sK, 16), v_lo = sw128_lo(sV, kHalfBytes);
+        auto issue_qk = [&](int qi, int j) {
+            const uint32_t q = q_lo + qi * (kQBytes >> 4), k = k_lo + (j & 1) * (kTileBytes >> 4);
 #pragma unroll
-                for (int kk = 0; kk < HD / 16; ++kk) {
-                    const uint32_t o = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
-                    tc_mma(tmem + col_s(qi), sw128_desc(q + o, 16, 1024), sw128_desc(k + o, 16, 1024), idesc_qk,
-                           kk > 0 ? 1u : 0u);
-                }
-                tc_commit(&s_full[qi]);
-            };
-            // P from TMEM: 16 packed columns at the start of every 32 of S
-            auto issue_pv = [&](int qi, int j) {
-                const uint32_t v = sV + (j & 1) * kTileBytes;
-#pragma unroll
-                for (int kk = 0; kk < BN / 16; ++kk)
-                    tc_mma_ta(tmem + col_o(qi), tmem + col_s(qi) + 32 * (kk >> 1) + 8 * (kk & 1),
-                              sw128_desc(v + kk * 2048, kHalfBytes, 1024), idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
-            };
-            bool ok = mbar_wait(q_full, 0, p.status) && mbar_wait(&k_full[0], 0, p.status);
-            if (ok) {
-                tc_fence_after();
-                if (nl0 > 0) issue_qk(0, 0);
-                issue_qk(1, 0);
-                tc_commit(&k_empty[0]);
+            for (int kk = 0; kk < HD / 16; ++kk) {
+                const uint32_t o = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
+                tc_mma_lead(lead, tmem + col_s(qi), q + o, k + o, idesc_qk, kk > 0 ? 1u : 0u);
             }
-            for (int j = 0; j < nl && ok; ++j) {
-                const bool next = j + 1 < nl;
-                if (next) ok = mbar_wait(&k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, p.status);
-                ok = ok && mbar_wait(&v_full[j & 1], (j >> 1) & 1, p.status);
-                if (j < nl0) {
-                    ok = ok && mbar_wait(&p_full[0], j & 1, p.status);
-                    if (!ok) break;
-                    tc_fence_after();
-                    issue_pv(0, j);
-                    if (j == nl0 - 1) tc_commit(&o_done[0]);
-                    if (j + 1 < nl0) issue_qk(0, j + 1);
-                }
-                ok = ok && mbar_wait(&p_full[1], j & 1, p.status);
+            tc_commit_lead(lead, &s_full[qi]);
+        };
+        // P from TMEM: 16 packed columns at the start of every 32 of S
+        auto issue_pv = [&](int qi, int j) {
+            const uint32_t v = v_lo + (j & 1) * (kTileBytes >> 4);
+#pragma unroll
+            for (int kk = 0; kk < BN / 16; ++kk)
+                tc_mma_ta_lead(lead, tmem + col_o(qi), tmem + col_s(qi) + 32 * (kk >> 1) + 8 * (kk & 1),
+                               v + kk * (2048 >> 4), idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
+        };
+        bool ok = mbar_wait(q_full, 0, p.status) && mbar_wait(&k_full[0], 0, p.status);
+        if (ok) {
+            tc_fence_after();
+            if (nl0 > 0) issue_qk(0, 0);
+            issue_qk(1, 0);
+            tc_commit_lead(lead, &k_empty[0]);
+        }
+        for (int j = 0; j < nl && ok; ++j) {
+            const bool next = j + 1 < nl;
+            if (next) ok = mbar_wait(&k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, p.status);
+            ok = ok && mbar_wait(&v_full[j & 1], (j >> 1) & 1, p.status);
+            if (j < nl0) {
+                ok = ok && mbar_wait(&p_full[0], j & 1, p.status);
                 if (!ok) break;
                 tc_fence_after();
-                issue_pv(1, j);
-                tc_commit(&v_empty[j & 1]);
-                if (!next) tc_commit(&o_done[1]);
-                if (next) {
-                    issue_qk(1, j + 1);
-                    tc_commit(&k_empty[(j + 1) & 1]);
-                }
+                issue_pv(0, j);
+                if (j == nl0 - 1) tc_commit_lead(lead, &o_done[0]);
+                if (j + 1 < nl0) issue_qk(0, j + 1);
+            }
+            ok = ok && mbar_wait(&p_full[1], j & 1, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(1, j);
+            tc_commit_lead(lead, &v_empty[j & 1]);
+            if (!next) tc_commit_lead(lead, &o_done[1]);
+            if (next) {
+                issue_qk(1, j + 1);
+                tc_commit_lead(lead, &k_empty[(j + 1) & 1]);
             }
         }
+        __syncwarp();
     } else if (warp < kExpWarps) {
         const int qi = warp >> 3, half = (warp >> 2) & 1;     // query tile and column half
         const int row = 32 * (warp & 3) + lane;               // TMEM lane
