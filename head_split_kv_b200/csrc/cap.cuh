@@ -9,14 +9,13 @@
 // tanh in two forms:
 //   * tanh_sfu: 1 - 2 / (1 + e^2y), two SFU operations, any y.  Absolute
 //     error a few 1e-7 (of 1), so a capped score is within cap * 1e-6.
-//   * poly_fma2: y * P(y^2) on the FMA pipe for |y| <= 1, where most scores of
-//     a trained model lie (|s| <= cap); P has five coefficients, fitted here
-//     to the smallest largest relative error on [-1, 1], 7.0e-6: at a cap
-//     of 50 at most 2.7e-4 of a weight, far below the 2^-8 of its rounding to
-//     bf16.
-//     The tensor-core kernels use it for a warp's part of a tile when every
-//     |y| there is at most 1, since their SFU share is already as large as
-//     the MMA's time.
+//   * poly_fma2: y * P(y^2) on the FMA pipe for |y| <= 0.7, where nearly all
+//     scores of a trained model lie (|s| <= 0.7 cap); P has four coefficients,
+//     fitted here to the smallest largest relative error there, 6.8e-6: at a
+//     cap of 50 at most 2.1e-4 of a weight, far below the 2^-8 of its rounding
+//     to bf16.  The tensor-core kernels use it for a warp's part of a tile when
+//     every |y| there is in range: their SFU share (the exponentials) is
+//     already as large as the MMAs' time.
 #pragma once
 
 #include "common.cuh"
@@ -43,27 +42,27 @@ __device__ __forceinline__ float tanh_sfu(float y) {
     return fmaf(-2.f, sfu_rcp(1.f + e), 1.f);
 }
 
-constexpr float kTanhRange = 1.f;   // of |y|
-constexpr float kTanh0 = 0.999993085861206f, kTanh1 = -0.3329806625843048f, kTanh2 = 0.13036811351776123f,
-                kTanh3 = -0.04481755197048187f, kTanh4 = 0.00903642363846302f;
+constexpr float kTanhRange = 0.7f;   // of |y|
+constexpr float kTanh0 = 0.9999933242797852f, kTanh1 = -0.33289048075675964f, kTanh2 = 0.12864212691783905f,
+                kTanh3 = -0.037290528416633606f;
 
-// f * tanh(k x) of a pair of dot products with |k x| <= 1: the polynomial's
-// coefficients times f and the powers of k, so that it takes x itself.
+// f * tanh(k x) of a pair of dot products with |k x| in range: the
+// polynomial's coefficients times f and the powers of k, so that it takes x
+// itself; u is x^2.
 struct TanhPoly {
-    float a0, a1, a2, a3, a4;
+    float a0, a1, a2, a3;
 };
 __device__ __forceinline__ TanhPoly tanh_poly(float k, float f = 1.f) {
-    const float k2 = k * k, s0 = f * k, s1 = s0 * k2, s2 = s1 * k2, s3 = s2 * k2;
-    return {kTanh0 * s0, kTanh1 * s1, kTanh2 * s2, kTanh3 * s3, kTanh4 * (s3 * k2)};
+    const float k2 = k * k, s0 = f * k, s1 = s0 * k2, s2 = s1 * k2;
+    return {kTanh0 * s0, kTanh1 * s1, kTanh2 * s2, kTanh3 * (s2 * k2)};
 }
-__device__ __forceinline__ float2 poly_fma2(float2 x, const TanhPoly& c) {
-    const float2 u = fmul2(x, x);
-    float2 p = ffma2(u, make_float2(c.a4, c.a4), make_float2(c.a3, c.a3));
-    p = ffma2(p, u, make_float2(c.a2, c.a2));
+__device__ __forceinline__ float2 poly_fma2(float2 x, float2 u, const TanhPoly& c) {
+    float2 p = ffma2(u, make_float2(c.a3, c.a3), make_float2(c.a2, c.a2));
     p = ffma2(p, u, make_float2(c.a1, c.a1));
     p = ffma2(p, u, make_float2(c.a0, c.a0));
     return fmul2(p, x);
 }
+__device__ __forceinline__ float2 poly_fma2(float2 x, const TanhPoly& c) { return poly_fma2(x, fmul2(x, x), c); }
 
 // The largest |x|, in four chains.
 template <int W>

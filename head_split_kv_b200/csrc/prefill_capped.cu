@@ -12,19 +12,23 @@
 // splits of a key range merge by addition.  (Larger caps, and caches of 8- or
 // 4-bit codes, whose fp16 p needs the maximum, take prefill_tc.cu.)
 //
-// Work, schedule of key tiles and masks: prefill_sched.cuh, as prefill_tc.cu:
-// a CTA owns two 128-row query tiles that share every 128-key tile;
-// TMEM S0 | S1 | O0 | O1, 128 columns each; the MMA thread's order is
-//   QK0(0) QK1(0) | PV0(0) QK0(1) PV1(0) QK1(1) | ...
-// Roles (576 threads): warps 0-15 the exponentials (warp w: query tile w / 8,
-// lanes 32 (w % 4) .., columns 64 ((w / 4) % 2) ..), warp 16 TMA, warp 17 MMA.
-// Each takes 32 columns at a time from TMEM: tanh on the FMA pipe when the
-// warp's |k x| are all within its polynomial's range (cap.cuh), one
-// exponential pair in kFmaExpEvery on the FMA pipe too, the others on the SFU;
-// p packed as bf16 goes over the columns it came from.  The row sum adds
-// the rounded p, so that an output is a convex combination of V rows.
-// Bound: SFU, FMA pipe and tensor pipe alike, about 1,000 cycles each per
-// 128 x 128 tile.
+// Work and masks as in prefill_tc.cu (prefill_sched.cuh), but a CTA owns one
+// 128-row query tile: S then has three buffers in TMEM (S0 | S1 | S2 | O, 128
+// columns each), the tensor core runs up to three Q K^T ahead, and a warp's
+// exponentials wait for no MMA.  (With two query tiles to a CTA and one S
+// each, a warp spent 1,850 of 4,650 cycles of a tile pair waiting for P V and
+// the next Q K^T; the price, K and V read once per 128 queries instead of
+// 256, is L2 traffic, 6 TB/s.)
+// Roles (576 threads): warps 0-15 the exponentials, in two groups of eight
+// that take alternate key tiles (warp w of a group: lanes 32 (w % 4) .., columns
+// 64 (w / 4) ..), warp 16 TMA (K and V three tiles deep), warp 17 MMA, in
+// the order PV(j) QK(j + 3).
+// Each warp takes 32 columns at a time from TMEM: tanh on the FMA pipe, the
+// exponential on the SFU, p packed as bf16 over the columns it came from.  The
+// polynomial's range (cap.cuh) is checked after the fact by a vote over the
+// largest x^2; a part outside takes its scores from TMEM again and tanh on the
+// SFU.  The row sum adds the rounded p, so that an output is a convex
+// combination of V rows.
 #include <cuda.h>
 
 #include "cap.cuh"
@@ -38,52 +42,68 @@ namespace {
 
 constexpr int kExpWarps = 16, kTmaWarp = 16, kMmaWarp = 17, kThreads = 576;
 constexpr int kRegThreads = 640;                   // five warps to a sub-partition: 96 registers
-constexpr int kFmaExpEvery = 4;
+constexpr int kStages = 3;                         // K and V tiles in shared memory, S tiles in TMEM
 constexpr uint32_t kTmemCols = 512;
-__device__ __forceinline__ constexpr uint32_t col_s(int i) { return 128u * (uint32_t)i; }
-__device__ __forceinline__ constexpr uint32_t col_o(int i) { return 256u + 128u * (uint32_t)i; }
-constexpr uint32_t kQBytes = BM * HD * 2;          // 32 KB per query tile (two 16 KB halves of d)
-constexpr uint32_t kTileBytes = BN * HD * 2;       // 32 KB per K or V tile (two 16 KB halves of d)
+constexpr uint32_t kColO = 384;
+constexpr uint32_t kTileBytes = BN * HD * 2;       // 32 KB per Q, K or V tile (two 16 KB halves of d)
 constexpr uint32_t kHalfBytes = kTileBytes / 2;
 constexpr uint32_t kOffQ = 0;
-constexpr uint32_t kOffK = kOffQ + 2 * kQBytes;
-constexpr uint32_t kOffV = kOffK + 2 * kTileBytes;
-constexpr uint32_t kOffSum = kOffV + 2 * kTileBytes;   // [2][2][128] row sums of the column halves
+constexpr uint32_t kOffK = kOffQ + kTileBytes;
+constexpr uint32_t kOffV = kOffK + kStages * kTileBytes;
+constexpr uint32_t kOffSum = kOffV + kStages * kTileBytes;   // [4][128] partial row sums
 constexpr uint32_t kOffBar = kOffSum + 4 * BM * 4;
-constexpr uint32_t kOffHolder = kOffBar + 16 * 8;
+constexpr uint32_t kOffHolder = kOffBar + 20 * 8;
 constexpr uint32_t kSmemBytes = kOffHolder + 16;
-static_assert(kSmemBytes + 1024 <= 232448, "one CTA per SM");
+static_assert(kSmemBytes <= 232448, "one CTA per SM");
 
-// 2^x for a pair, |x| <= 90, on the FMA pipe: as exp2_fma2 of prefill_tc.cu
-// (range reduction to [-0.5, 0.5], a cubic fitted to 7.5e-5), without its
-// clamp: the exponent cannot leave the normal range.
-__device__ __forceinline__ float2 exp2_fma_bounded2(float2 x) {
-    constexpr float kShift = 12582912.f;  // 1.5 * 2^23
-    constexpr float c0 = 0.9999280571937561f, c1 = 0.6932610273361206f, c2 = 0.24261116981506348f,
-                    c3 = 0.055171627551317215f;
-    const float2 t = fadd2(x, make_float2(kShift, kShift));
-    const float2 n = fadd2(t, make_float2(-kShift, -kShift));
-    const float2 f = ffma2(n, make_float2(-1.f, -1.f), x);
-    float2 q = ffma2(make_float2(c3, c3), f, make_float2(c2, c2));
-    q = ffma2(q, f, make_float2(c1, c1));
-    q = ffma2(q, f, make_float2(c0, c0));
-    return make_float2(__uint_as_float(__float_as_uint(q.x) + (__float_as_uint(t.x) << 23)),
-                       __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(t.y) << 23)));
+// The key tiles of query tile mt (chunk rows 128 mt ..), as make_sched lists
+// them for a pair; tile_at and visible_columns take the result.
+__device__ __forceinline__ Sched make_sched_single(const TcArgs& p, bool retrieval, int c0, int mt) {
+    const LayerArgs& a = p.a;
+    Sched s;
+    s.retrieval = retrieval;
+    s.chunk = !retrieval && a.stream_chunk;
+    s.c0 = c0;
+    s.m = mt;
+    const int hi = min(mt, (p.C + BN - 1) / BN - 1);      // the diagonal's tile
+    s.n_prior = retrieval ? (c0 + BN - 1) / BN : 0;
+    s.n_ring = !retrieval && min(c0, a.W) > 0 ? 1 : 0;
+    s.lo = 0;
+    s.sink_tile = 0;
+    if (!retrieval && !s.chunk) {
+        s.lo = max(0, BM * mt - a.recent + 1) / BN;       // first key of the band
+        s.sink_tile = (c0 < a.sink && s.lo > 0) ? 1 : 0;  // the chunk's own sink tokens (sink <= 128)
+    }
+    s.n = s.n_prior + s.n_ring + s.sink_tile + (hi - s.lo + 1);
+    s.n0 = s.n;
+    return s;
+}
+__device__ __forceinline__ bool single_needs_mask(const Sched& s, const Tile& t) {
+    if ((!s.retrieval && !s.chunk) || t.src == SRC_RING) return true;
+    if (t.src == SRC_CACHE) return t.row < 0;
+    return t.row + BN - 1 > BM * s.m;
 }
 
 // 32 columns of a row: dot products x -> p, packed as bf16 in pk; returns the
-// sum of the rounded p.  POLY: every |k x| is within the polynomial's range.
-// One loop from the dot product to the packed p, so that the FMA, SFU and ALU
-// work of neighbouring pairs interleaves.
+// sum of the rounded p.  POLY: tanh by its polynomial, `big` raised to the
+// largest x^2; else on the SFU.  One loop from the dot product to the packed
+// p, so that the FMA, SFU and ALU work of neighbouring pairs interleaves.
 template <bool MASKED, bool POLY>
 __device__ __forceinline__ float exp_loop(const float (&x)[32], uint32_t (&pk)[16], const CapArgs& cap, const TanhPoly& tp,
-                                          uint32_t vis) {
+                                          uint32_t vis, float& big) {
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    float b[2] = {0.f, 0.f};
 #pragma unroll
     for (int c2 = 0; c2 < 16; ++c2) {
         float2 v = make_float2(x[2 * c2], x[2 * c2 + 1]);
-        v = POLY ? poly_fma2(v, tp) : make_float2(cap.c2 * tanh_sfu(v.x * cap.k), cap.c2 * tanh_sfu(v.y * cap.k));
-        float2 e = c2 % kFmaExpEvery == kFmaExpEvery - 1 ? exp2_fma_bounded2(v) : make_float2(sfu_exp2(v.x), sfu_exp2(v.y));
+        if constexpr (POLY) {
+            const float2 u = fmul2(v, v);
+            b[c2 & 1] = fmax3(b[c2 & 1], u.x, u.y);
+            v = poly_fma2(v, u, tp);
+        } else {
+            v = make_float2(cap.c2 * tanh_sfu(v.x * cap.k), cap.c2 * tanh_sfu(v.y * cap.k));
+        }
+        float2 e = make_float2(sfu_exp2(v.x), sfu_exp2(v.y));
         if constexpr (MASKED) {
             e.x = (vis >> (2 * c2)) & 1u ? e.x : 0.f;
             e.y = (vis >> (2 * c2 + 1)) & 1u ? e.y : 0.f;
@@ -92,17 +112,22 @@ __device__ __forceinline__ float exp_loop(const float (&x)[32], uint32_t (&pk)[1
         pk[c2] = *reinterpret_cast<uint32_t*>(&h);
         sum[c2 & 1] = fadd2(sum[c2 & 1], make_float2(bf16_lo(pk[c2]), bf16_hi(pk[c2])));
     }
+    big = fmaxf(b[0], b[1]);
     return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
 // 32 columns of a row: dot products at s_addr -> p over the first 16 of them.
 template <bool MASKED>
-__device__ __forceinline__ float exp_columns(uint32_t s_addr, const CapArgs& cap, const TanhPoly& tp, uint32_t vis) {
-    float x[32];
+__device__ __forceinline__ float exp_columns(uint32_t s_addr, const CapArgs& cap, const TanhPoly& tp, float x2_max,
+                                             uint32_t vis) {
+    float x[32], big;
     tmem_ld32(s_addr, x);
     uint32_t pk[16];
-    const float l = __all_sync(0xffffffffu, largest(x) * cap.k <= kTanhRange) ? exp_loop<MASKED, true>(x, pk, cap, tp, vis)
-                                                                             : exp_loop<MASKED, false>(x, pk, cap, tp, vis);
+    float l = exp_loop<MASKED, true>(x, pk, cap, tp, vis, big);
+    if (!__all_sync(0xffffffffu, big <= x2_max)) {
+        tmem_ld32(s_addr, x);
+        l = exp_loop<MASKED, false>(x, pk, cap, tp, vis, big);
+    }
     tmem_st16(s_addr, pk);
     return l;
 }
@@ -124,35 +149,37 @@ __global__ void __launch_bounds__(kRegThreads, 1)
     }
     const uint32_t sQ = smem_u32(smem + kOffQ), sK = smem_u32(smem + kOffK), sV = smem_u32(smem + kOffV);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
-    uint64_t* q_full = bars + 0;
-    uint64_t* k_full = bars + 1;    // [2]
-    uint64_t* k_empty = bars + 3;   // [2]
-    uint64_t* v_full = bars + 5;    // [2]
-    uint64_t* v_empty = bars + 7;   // [2]
-    uint64_t* s_full = bars + 9;    // [2]: per query tile
-    uint64_t* p_full = bars + 11;   // [2]: per query tile
-    uint64_t* o_done = bars + 13;   // [2]: per query tile, once
+    uint64_t* k_full = bars + 0;    // [kStages]
+    uint64_t* k_empty = bars + 3;   // [kStages]
+    uint64_t* v_full = bars + 6;    // [kStages]
+    uint64_t* v_empty = bars + 9;   // [kStages]
+    uint64_t* s_full = bars + 12;   // [kStages]
+    uint64_t* p_full = bars + 15;   // [kStages]
+    uint64_t* q_full = bars + 18;
+    uint64_t* o_done = bars + 19;
     uint32_t* holder = reinterpret_cast<uint32_t*>(smem + kOffHolder);
 
-    // the work item: as prefill_tc.cu, (sequence, KV head) outermost, then the
-    // split, then the query-tile pair (heaviest first) and the query head
-    const bool retrieval = (int)blockIdx.x < p.n_ret_ctas;
-    int unit = 0, split = 0, m, g, hs, b;
+    // the work item, ordered as in prefill_tc.cu: (sequence, KV head)
+    // outermost, then the split, then the query tile (heaviest first) and
+    // the query head
+    const bool retrieval = (int)blockIdx.x < 2 * p.n_ret_ctas;
+    const int n_mt = 2 * p.n_mpairs;                  // the last may lie past the chunk
+    int unit = 0, split = 0, mt, g, hs, b;
     if (retrieval) {
-        const int per_group = p.n_mpairs * a.G;
+        const int per_group = n_mt * a.G;
         const int r = (int)blockIdx.x;
         const int inner = r % per_group;
         split = (r / per_group) % p.ns;
         const int bh = r / (per_group * p.ns);
         g = inner % a.G;
-        m = p.n_mpairs - 1 - inner / a.G;
+        mt = n_mt - 1 - inner / a.G;
         hs = bh % a.R;
         b = bh / a.R;
-        unit = (bh * p.n_mpairs + m) * a.G + g;
+        unit = (bh * p.n_mpairs + mt / 2) * a.G + g;  // of the pair: records and tickets are laid out by pairs
     } else {
-        int idx = (int)blockIdx.x - p.n_ret_ctas;
+        int idx = (int)blockIdx.x - 2 * p.n_ret_ctas;
         const int per_m = a.B * a.S * a.G;
-        m = p.n_mpairs - 1 - idx / per_m;
+        mt = n_mt - 1 - idx / per_m;
         idx %= per_m;
         g = idx % a.G;
         hs = (idx / a.G) % a.S;
@@ -163,10 +190,11 @@ __global__ void __launch_bounds__(kRegThreads, 1)
     int c0 = p.seq_len ? p.seq_len[b] : 0;            // no lengths: whole sequences, no cache
     if (c0 < 0) c0 = 0;
     if (retrieval && c0 > a.capacity) {
-        if (tid == 0 && m == p.n_mpairs - 1 && p.status) atomicOr(p.status, DUO_DEV_BAD_LENGTH);
+        if (tid == 0 && mt == 0 && p.status) atomicOr(p.status, DUO_DEV_BAD_LENGTH);
         c0 = a.capacity;
     }
-    const Sched sc = make_sched(p, retrieval, c0, m);
+    if (BM * mt >= p.C) return;
+    const Sched sc = make_sched_single(p, retrieval, c0, mt);
     int ns_use = 1, j0 = 0, j1 = sc.n;
     if (retrieval && p.ns > 1) {
         ns_use = min(p.ns, max(1, sc.n / kMinSplitTiles));
@@ -174,21 +202,20 @@ __global__ void __launch_bounds__(kRegThreads, 1)
         j0 = split * sc.n / ns_use;
         j1 = (split + 1) * sc.n / ns_use;
     }
-    const int nl = j1 - j0;                           // tiles of this CTA for Q1
-    const int nl0 = max(0, min(j1, sc.n0) - j0);      // ... and for Q0
+    const int nl = j1 - j0;                           // tiles of this CTA, at least one
 
     if (warp == kMmaWarp) tmem_alloc(holder, kTmemCols);
     if (tid == 0) {
-        mbar_init(q_full, 1);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kStages; ++i) {
             mbar_init(&k_full[i], 1);
             mbar_init(&k_empty[i], 1);
             mbar_init(&v_full[i], 1);
             mbar_init(&v_empty[i], 1);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], kExpWarps / 2);
-            mbar_init(&o_done[i], 1);
         }
+        mbar_init(q_full, 1);
+        mbar_init(o_done, 1);
         fence_barrier_init();
     }
     tc_fence_before();
@@ -198,19 +225,17 @@ __global__ void __launch_bounds__(kRegThreads, 1)
 
     if (warp == kTmaWarp) {
         if (lane == 0) {
-            mbar_arrive_expect_tx(q_full, 2 * kQBytes);
-            for (int qi = 0; qi < 2; ++qi)
-                for (int half = 0; half < 2; ++half)
-                    tma_load_4d(sQ + qi * kQBytes + half * (kQBytes / 2), &tmQ, 64 * half, q_idx, BM * (2 * m + qi), b,
-                                q_full);
+            mbar_arrive_expect_tx(q_full, kTileBytes);
+            for (int half = 0; half < 2; ++half)
+                tma_load_4d(sQ + half * kHalfBytes, &tmQ, 64 * half, q_idx, BM * mt, b, q_full);
             const int cache_z = b * a.R + slot, ring_z = b * a.S + (slot - a.R);
             bool ok = true;
             for (int j = 0; j < nl && ok; ++j) {
                 const Tile t = tile_at(sc, j0 + j);
-                const int st = j & 1;
+                const int st = j % kStages, use = j / kStages;
                 for (int kv = 0; kv < 2 && ok; ++kv) {
                     uint64_t* full = kv ? &v_full[st] : &k_full[st];
-                    if (j >= 2) ok = mbar_wait(kv ? &v_empty[st] : &k_empty[st], ((j >> 1) - 1) & 1, p.status);
+                    if (use > 0) ok = mbar_wait(kv ? &v_empty[st] : &k_empty[st], (use - 1) & 1, p.status);
                     if (!ok) break;
                     mbar_arrive_expect_tx(full, kTileBytes);
                     const uint32_t dst = (kv ? sV : sK) + st * kTileBytes;
@@ -234,164 +259,140 @@ __global__ void __launch_bounds__(kRegThreads, 1)
         constexpr uint32_t idesc_qk = idesc_bf16(BM, BN, 0, 0);
         constexpr uint32_t idesc_pv = idesc_bf16(BM, HD, 0, 1);
         const uint32_t q_lo = sw128_lo(sQ, 16), k_lo = sw128_lo(sK, 16), v_lo = sw128_lo(sV, kHalfBytes);
-        auto issue_qk = [&](int qi, int j) {
-            const uint32_t q = q_lo + qi * (kQBytes >> 4), k = k_lo + (j & 1) * (kTileBytes >> 4);
+        bool ok = mbar_wait(q_full, 0, p.status);
+        auto issue_qk = [&](int j) {                  // after its K tile: S(j) and the stage's release
+            const int st = j % kStages;
+            ok = ok && mbar_wait(&k_full[st], (j / kStages) & 1, p.status);
+            if (!ok) return;
+            tc_fence_after();
+            const uint32_t k = k_lo + st * (kTileBytes >> 4);
 #pragma unroll
             for (int kk = 0; kk < HD / 16; ++kk) {
                 const uint32_t o = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
-                tc_mma_lead(lead, tmem + col_s(qi), q + o, k + o, idesc_qk, kk > 0 ? 1u : 0u);
+                tc_mma_lead(lead, tmem + 128 * st, q_lo + o, k + o, idesc_qk, kk > 0 ? 1u : 0u);
             }
-            tc_commit_lead(lead, &s_full[qi]);
+            tc_commit_lead(lead, &s_full[st]);
+            tc_commit_lead(lead, &k_empty[st]);
         };
-        // P from TMEM: 16 packed columns at the start of every 32 of S
-        auto issue_pv = [&](int qi, int j) {
-            const uint32_t v = v_lo + (j & 1) * (kTileBytes >> 4);
-#pragma unroll
-            for (int kk = 0; kk < BN / 16; ++kk)
-                tc_mma_ta_lead(lead, tmem + col_o(qi), tmem + col_s(qi) + 32 * (kk >> 1) + 8 * (kk & 1),
-                               v + kk * (2048 >> 4), idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
-        };
-        bool ok = mbar_wait(q_full, 0, p.status) && mbar_wait(&k_full[0], 0, p.status);
-        if (ok) {
-            tc_fence_after();
-            if (nl0 > 0) issue_qk(0, 0);
-            issue_qk(1, 0);
-            tc_commit_lead(lead, &k_empty[0]);
-        }
+        for (int j = 0; j < min(nl, kStages); ++j) issue_qk(j);
         for (int j = 0; j < nl && ok; ++j) {
-            const bool next = j + 1 < nl;
-            if (next) ok = mbar_wait(&k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, p.status);
-            ok = ok && mbar_wait(&v_full[j & 1], (j >> 1) & 1, p.status);
-            if (j < nl0) {
-                ok = ok && mbar_wait(&p_full[0], j & 1, p.status);
-                if (!ok) break;
-                tc_fence_after();
-                issue_pv(0, j);
-                if (j == nl0 - 1) tc_commit_lead(lead, &o_done[0]);
-                if (j + 1 < nl0) issue_qk(0, j + 1);
-            }
-            ok = ok && mbar_wait(&p_full[1], j & 1, p.status);
+            const int st = j % kStages, ph = (j / kStages) & 1;
+            ok = mbar_wait(&v_full[st], ph, p.status) && mbar_wait(&p_full[st], ph, p.status);
             if (!ok) break;
             tc_fence_after();
-            issue_pv(1, j);
-            tc_commit_lead(lead, &v_empty[j & 1]);
-            if (!next) tc_commit_lead(lead, &o_done[1]);
-            if (next) {
-                issue_qk(1, j + 1);
-                tc_commit_lead(lead, &k_empty[(j + 1) & 1]);
-            }
+            // P from TMEM: 16 packed columns at the start of every 32 of S
+            const uint32_t v = v_lo + st * (kTileBytes >> 4);
+#pragma unroll
+            for (int kk = 0; kk < BN / 16; ++kk)
+                tc_mma_ta_lead(lead, tmem + kColO, tmem + 128 * st + 32 * (kk >> 1) + 8 * (kk & 1), v + kk * (2048 >> 4),
+                               idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
+            tc_commit_lead(lead, &v_empty[st]);
+            if (j == nl - 1) tc_commit_lead(lead, o_done);
+            if (j + kStages < nl) issue_qk(j + kStages);   // over P(j), behind PV(j)
         }
         __syncwarp();
     } else if (warp < kExpWarps) {
-        const int qi = warp >> 3, half = (warp >> 2) & 1;     // query tile and column half
+        const int group = warp >> 3, half = (warp >> 2) & 1;  // key tiles j % 2 == group; column half
         const int row = 32 * (warp & 3) + lane;               // TMEM lane
-        const int crow = BM * (2 * m + qi) + row;             // chunk row
-        const int n_me = qi ? nl : nl0;
+        const int crow = BM * mt + row;                       // chunk row
         const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const TanhPoly tp = tanh_poly(a.cap.k, a.cap.c2);
+        const float x2_max = (kTanhRange / a.cap.k) * (kTanhRange / a.cap.k);
         float l_sum = 0.f;
         bool ok = true;
-        for (int j = 0; j < n_me; ++j) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&s_full[qi], j & 1, p.status));
+        for (int j = group; j < nl; j += 2) {
+            const int st = j % kStages;
+            ok = __all_sync(0xffffffffu, mbar_wait(&s_full[st], (j / kStages) & 1, p.status));
             if (!ok) break;
             tc_fence_after();
             const Tile t = tile_at(sc, j0 + j);
-            const uint32_t s_addr = lane_base + col_s(qi) + 64 * half;
-            if (needs_mask(sc, t, qi)) {
+            const uint32_t s_addr = lane_base + 128 * st + 64 * half;
+            if (single_needs_mask(sc, t)) {
                 uint32_t vis[4] = {0u, 0u, 0u, 0u};           // the tile's keys this row sees, a bit per column
                 visible_columns(a, sc, t, c0 + crow, vis);
-                l_sum += exp_columns<true>(s_addr, a.cap, tp, half ? vis[2] : vis[0]);
-                l_sum += exp_columns<true>(s_addr + 32, a.cap, tp, half ? vis[3] : vis[1]);
+                l_sum += exp_columns<true>(s_addr, a.cap, tp, x2_max, half ? vis[2] : vis[0]);
+                l_sum += exp_columns<true>(s_addr + 32, a.cap, tp, x2_max, half ? vis[3] : vis[1]);
             } else {
-                l_sum += exp_columns<false>(s_addr, a.cap, tp, 0u);
-                l_sum += exp_columns<false>(s_addr + 32, a.cap, tp, 0u);
+                l_sum += exp_columns<false>(s_addr, a.cap, tp, x2_max, 0u);
+                l_sum += exp_columns<false>(s_addr + 32, a.cap, tp, x2_max, 0u);
             }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[qi]);
+            if (lane == 0) mbar_arrive(&p_full[st]);
         }
-        // the row's sum over both column halves
-        float* sums = reinterpret_cast<float*>(smem + kOffSum) + qi * 2 * BM;
-        sums[half * BM + row] = l_sum;
-        asm volatile("bar.sync %0, 256;" ::"r"(1 + qi) : "memory");
-        const float l_row = sums[row] + sums[BM + row];
-        // this thread's output: 64 columns of its row
-        const size_t off = (((size_t)b * p.C + crow) * a.Hq + q_idx) * HD + 64 * half;
+        // the row's sum over both groups and column halves; each thread then
+        // stores 32 columns of its row
+        float* sums = reinterpret_cast<float*>(smem + kOffSum);
+        const int quarter = warp >> 2;
+        sums[quarter * BM + row] = l_sum;
+        asm volatile("bar.sync 1, 512;" ::: "memory");
+        const float l_row = (sums[row] + sums[BM + row]) + (sums[2 * BM + row] + sums[3 * BM + row]);
+        const size_t off = (((size_t)b * p.C + crow) * a.Hq + q_idx) * HD + 32 * quarter;
         const bool out_ok = bounds_ok(b < a.B && q_idx >= 0 && q_idx < a.Hq, p.status);
         const bool live = crow < p.C && out_ok;
-        uint4 pre[8];   // EPI_MIX_KEEP: the streaming attention of these columns, loaded before the wait below
+        uint4 pre[4];   // EPI_MIX_KEEP: the streaming attention of these columns, loaded before the wait below
         if constexpr (EPI == EPI_MIX_KEEP) {
             const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.epi.streaming) + off);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) pre[i] = live ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+            for (int i = 0; i < 4; ++i) pre[i] = live ? src[i] : make_uint4(0u, 0u, 0u, 0u);
         }
-        if (ok && n_me >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&o_done[qi], 0, p.status));
-        const bool have = ok && n_me >= 1;                    // warp-uniform
-        if (have) tc_fence_after();
-        const uint32_t o_addr = lane_base + col_o(qi) + 64 * half;
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(o_done, 0, p.status));
+        float o[32];
+        if (ok) {
+            tc_fence_after();
+            tmem_ld32(lane_base + kColO + 32 * quarter, o);
+        }
         __nv_bfloat16* op = static_cast<__nv_bfloat16*>(p.out) + off;
         if (!out_ok) {
             // debug build: the check failed, nothing is written
         } else if (EPI != EPI_STORE || ns_use == 1) {
-            if (have) {
+            if (ok) {
                 const float inv = l_row > 0.f ? 1.f / l_row : 0.f;
                 const float al = EPI == EPI_MIX_KEEP ? p.epi.alpha[kv_idx] : 0.f;
-                if (EPI != EPI_STORE && half == 0 && live)
+                if (EPI != EPI_STORE && quarter == 0 && live)
                     p.epi.lse[((size_t)b * a.Hq + q_idx) * p.C + crow] = log2f(l_row);
 #pragma unroll
-                for (int ch = 0; ch < 2; ++ch) {
-                    float o[32];
-                    tmem_ld32(o_addr + 32 * ch, o);
+                for (int q4 = 0; q4 < 4; ++q4) {
+                    float v8[8];
 #pragma unroll
-                    for (int q4 = 0; q4 < 4; ++q4) {
-                        float v8[8];
+                    for (int e = 0; e < 8; ++e) v8[e] = o[8 * q4 + e] * inv;
+                    if constexpr (EPI == EPI_MIX_KEEP) {
+                        const uint32_t w[4] = {pre[q4].x, pre[q4].y, pre[q4].z, pre[q4].w};
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) v8[e] = o[8 * q4 + e] * inv;
-                        if constexpr (EPI == EPI_MIX_KEEP) {
-                            const uint4 u = pre[4 * ch + q4];
-                            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                v8[2 * e] = al * v8[2 * e] + (1.f - al) * bf16_lo(w[e]);
-                                v8[2 * e + 1] = al * v8[2 * e + 1] + (1.f - al) * bf16_hi(w[e]);
-                            }
+                        for (int e = 0; e < 4; ++e) {
+                            v8[2 * e] = al * v8[2 * e] + (1.f - al) * bf16_lo(w[e]);
+                            v8[2 * e + 1] = al * v8[2 * e + 1] + (1.f - al) * bf16_hi(w[e]);
                         }
-                        if (live) store_row<__nv_bfloat16, 8>(op + 32 * ch + 8 * q4, v8);
                     }
+                    if (live) store_row<__nv_bfloat16, 8>(op + 8 * q4, v8);
                 }
             }
         } else if (bounds_ok(unit < p.n_units && split < p.ns, p.status)) {
             // this split's record of the query tile (the maximum is 0 for every
-            // row that has keys), then a ticket per unit; the CTA that arrives
-            // last merges (no CTA ever waits)
+            // row), then a ticket per query tile (half a word of the pair's);
+            // the CTA that arrives last merges (no CTA ever waits)
+            const int qi = mt & 1;
             float* rec = p.part + (((size_t)unit * p.ns + split) * 2 + qi) * kPartFloats;
-            if (half == 0) {
-                rec[row] = have ? 0.f : -INFINITY;
-                rec[BM + row] = have ? l_row : 0.f;
+            if (quarter == 0) {
+                rec[row] = ok ? 0.f : -INFINITY;
+                rec[BM + row] = ok ? l_row : 0.f;
             }
 #pragma unroll
-            for (int ch = 0; ch < 2; ++ch) {
-                float o[32];
-                if (have) {
-                    tmem_ld32(o_addr + 32 * ch, o);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = 0.f;
-                }
-#pragma unroll
-                for (int g4 = 0; g4 < 8; ++g4)
-                    reinterpret_cast<float4*>(rec + 2 * BM)[(16 * half + 8 * ch + g4) * BM + row] =
-                        make_float4(o[4 * g4], o[4 * g4 + 1], o[4 * g4 + 2], o[4 * g4 + 3]);
-            }
+            for (int g4 = 0; g4 < 8; ++g4)
+                reinterpret_cast<float4*>(rec + 2 * BM)[(8 * quarter + g4) * BM + row] =
+                    ok ? make_float4(o[4 * g4], o[4 * g4 + 1], o[4 * g4 + 2], o[4 * g4 + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
             __threadfence();
-            asm volatile("bar.sync 3, 512;" ::: "memory");
-            if (tid == 0) holder[1] = (atomicAdd(&p.ticket[unit], 1u) == (unsigned)ns_use - 1) ? 1u : 0u;
-            asm volatile("bar.sync 3, 512;" ::: "memory");
-            if (holder[1] && half == 0) {
+            asm volatile("bar.sync 1, 512;" ::: "memory");
+            if (tid == 0) {
+                const uint32_t seen = atomicAdd(&p.ticket[unit], 1u << (16 * qi)) >> (16 * qi);
+                holder[1] = (seen & 0xffffu) == (uint32_t)ns_use - 1 ? 1u : 0u;
+            }
+            asm volatile("bar.sync 1, 512;" ::: "memory");
+            if (holder[1] && quarter == 0) {
                 __threadfence();
                 merge_split_records(p.part + (size_t)unit * p.ns * 2 * kPartFloats + (size_t)qi * kPartFloats, ns_use, row,
-                                    crow < p.C, op, 4 + qi);
+                                    crow < p.C, op, 2);
             }
         }
     }
@@ -405,6 +406,8 @@ __global__ void __launch_bounds__(kRegThreads, 1)
 
 template <int EPI>
 cudaError_t launch_variant(const TcMaps& m, const TcArgs& p, unsigned grid, cudaStream_t s) {
+    if (grid > 0x3fffffffu) return cudaErrorInvalidConfiguration;
+    grid *= 2;   // a CTA per query tile, not per pair
     static std::atomic<unsigned long long> configured{0};
     const cudaError_t e = smem_limit_once(prefill_capped_kernel<EPI>, (int)kSmemBytes, configured);
     if (e != cudaSuccess) return e;
