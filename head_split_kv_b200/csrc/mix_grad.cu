@@ -412,52 +412,56 @@ __global__ void __launch_bounds__(kRegThreads, 1)
         }
     } else if (warp == kMmaWarp) {
         {
-            // the whole warp, one lane issuing
-            const uint32_t lead = lane == 0 ? 1u : 0u;
+            // the whole warp waits, one lane issues (every call of the
+            // lambdas below is under elect_one)
             constexpr uint32_t idesc_kk = idesc_bf16(BM, BM, 0, 0);
             constexpr uint32_t idesc_mn = idesc_bf16(BM, HD, 0, 1);
-            const uint32_t x_lo = sw128_lo(sX, 16), y_lo = sw128_lo(sY, 16), y_mn = sw128_lo(sY, kHalfBytes);
             // D = X_w Y_w(j)^T over d
             auto issue_xy = [&](uint32_t col, int w, int j) {
-                const uint32_t x = x_lo + w * (kTileBytes >> 4), y = y_lo + ((j & 1) * 2 + w) * (kTileBytes >> 4);
+                const uint64_t x = sw128_desc(sX + w * kTileBytes, 16, 1024);
+                const uint64_t y = sw128_desc(sY + ((j & 1) * 2 + w) * kTileBytes, 16, 1024);
 #pragma unroll
                 for (int kk = 0; kk < HD / 16; ++kk) {
                     const uint32_t o = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
-                    tc_mma_lead(lead, tmem + col, x + o, y + o, idesc_kk, kk > 0 ? 1u : 0u);
+                    tc_mma(tmem + col, x + o, y + o, idesc_kk, kk > 0 ? 1u : 0u);
                 }
             };
             // ACC += A (bf16 over the columns it came from) Y_w(j), over the inner rows
             auto issue_acc = [&](uint32_t col, uint32_t a_col, int w, int j) {
-                const uint32_t y = y_mn + ((j & 1) * 2 + w) * (kTileBytes >> 4);
+                const uint64_t y = sw128_desc(sY + ((j & 1) * 2 + w) * kTileBytes, kHalfBytes, 1024);
 #pragma unroll
                 for (int kk = 0; kk < BM / 16; ++kk)
-                    tc_mma_ta_lead(lead, tmem + col, tmem + a_col + kCols * (kk >> 1) + 8 * (kk & 1), y + kk * (2048 >> 4),
-                                   idesc_mn, (j > 0 || kk > 0) ? 1u : 0u);
+                    tc_mma_ta(tmem + col, tmem + a_col + kCols * (kk >> 1) + 8 * (kk & 1), y + kk * (2048 >> 4), idesc_mn,
+                              (j > 0 || kk > 0) ? 1u : 0u);
             };
             auto wait_tile = [&](int j) { return mbar_wait(&y_full[j & 1], (j >> 1) & 1, p.status); };
             auto issue_s = [&](int j) {
                 issue_xy(s_col<MODE>(j), 0, j);
-                tc_commit_lead(lead, &s_full[j & 1]);
+                tc_commit(&s_full[j & 1]);
             };
             auto issue_d = [&](int j) {
                 issue_xy(d_col<MODE>(j), 1, j);
-                tc_commit_lead(lead, &d_full[j & 1]);
+                tc_commit(&d_full[j & 1]);
             };
             bool ok = mbar_wait(x_full, 0, p.status) && wait_tile(0);
             if (ok) {
                 tc_fence_after();
-                issue_s(0);
-                issue_d(0);
-                if (kStats) tc_commit_lead(lead, &y_empty[0]);
+                if (elect_one()) {
+                    issue_s(0);
+                    issue_d(0);
+                    if (kStats) tc_commit(&y_empty[0]);
+                }
             }
             if (!kKeys && n_in > 1 && ok) {
                 ok = wait_tile(1);
                 if (ok) {
                     tc_fence_after();
-                    issue_s(1);
-                    if (kStats) {
-                        issue_d(1);
-                        tc_commit_lead(lead, &y_empty[1]);
+                    if (elect_one()) {
+                        issue_s(1);
+                        if (kStats) {
+                            issue_d(1);
+                            tc_commit(&y_empty[1]);
+                        }
                     }
                 }
             }
@@ -470,9 +474,11 @@ __global__ void __launch_bounds__(kRegThreads, 1)
                         ok = wait_tile(j + 2);
                         if (!ok) break;
                         tc_fence_after();
-                        issue_s(j + 2);
-                        issue_d(j + 2);
-                        tc_commit_lead(lead, &y_empty[j & 1]);
+                        if (elect_one()) {
+                            issue_s(j + 2);
+                            issue_d(j + 2);
+                            tc_commit(&y_empty[j & 1]);
+                        }
                     }
                 } else {
                     const bool next = j + 1 < n_in;
@@ -481,25 +487,29 @@ __global__ void __launch_bounds__(kRegThreads, 1)
                         ok = ok && mbar_wait(&w_ready[j & 1], ph, p.status);
                         if (!ok) break;
                         tc_fence_after();
-                        issue_acc(kColA1, kColS, 1, j);
-                        if (next) issue_s(j + 1);
+                        if (elect_one()) {
+                            issue_acc(kColA1, kColS, 1, j);
+                            if (next) issue_s(j + 1);
+                        }
                     }
                     ok = mbar_wait(&g_ready[j & 1], ph, p.status);
                     if (!ok) break;
                     tc_fence_after();
-                    issue_acc(kColA2, kColP, 0, j);
-                    tc_commit_lead(lead, &y_empty[j & 1]);
-                    if (next) issue_d(j + 1);
+                    if (elect_one()) {
+                        issue_acc(kColA2, kColP, 0, j);
+                        tc_commit(&y_empty[j & 1]);
+                        if (next) issue_d(j + 1);
+                    }
                     if (!kKeys && j + 2 < n_in) {
                         // one S ahead: its slot was read before dS(j) was written
                         ok = mbar_wait(&w_ready[j & 1], ph, p.status) && wait_tile(j + 2);
                         if (!ok) break;
                         tc_fence_after();
-                        issue_s(j + 2);
+                        if (elect_one()) issue_s(j + 2);
                     }
                 }
             }
-            if (ok) tc_commit_lead(lead, done);
+            if (ok && elect_one()) tc_commit(done);
         }
         __syncwarp();
     } else if (warp < kElemWarps) {

@@ -254,25 +254,25 @@ __global__ void __launch_bounds__(kRegThreads, 1)
             }
         }
     } else if (warp == kMmaWarp) {
-        // the whole warp, one lane issuing
-        const uint32_t lead = lane == 0 ? 1u : 0u;
+        // the whole warp waits, one lane issues
         constexpr uint32_t idesc_qk = idesc_bf16(BM, BN, 0, 0);
         constexpr uint32_t idesc_pv = idesc_bf16(BM, HD, 0, 1);
-        const uint32_t q_lo = sw128_lo(sQ, 16), k_lo = sw128_lo(sK, 16), v_lo = sw128_lo(sV, kHalfBytes);
         bool ok = mbar_wait(q_full, 0, p.status);
         auto issue_qk = [&](int j) {                  // after its K tile: S(j) and the stage's release
             const int st = j % kStages;
             ok = ok && mbar_wait(&k_full[st], (j / kStages) & 1, p.status);
             if (!ok) return;
             tc_fence_after();
-            const uint32_t k = k_lo + st * (kTileBytes >> 4);
+            if (elect_one()) {
+                const uint64_t qd = sw128_desc(sQ, 16, 1024), kd = sw128_desc(sK + st * kTileBytes, 16, 1024);
 #pragma unroll
-            for (int kk = 0; kk < HD / 16; ++kk) {
-                const uint32_t o = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
-                tc_mma_lead(lead, tmem + 128 * st, q_lo + o, k + o, idesc_qk, kk > 0 ? 1u : 0u);
+                for (int kk = 0; kk < HD / 16; ++kk) {
+                    const uint32_t o = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
+                    tc_mma(tmem + 128 * st, qd + o, kd + o, idesc_qk, kk > 0 ? 1u : 0u);
+                }
+                tc_commit(&s_full[st]);
+                tc_commit(&k_empty[st]);
             }
-            tc_commit_lead(lead, &s_full[st]);
-            tc_commit_lead(lead, &k_empty[st]);
         };
         for (int j = 0; j < min(nl, kStages); ++j) issue_qk(j);
         for (int j = 0; j < nl && ok; ++j) {
@@ -280,14 +280,16 @@ __global__ void __launch_bounds__(kRegThreads, 1)
             ok = mbar_wait(&v_full[st], ph, p.status) && mbar_wait(&p_full[st], ph, p.status);
             if (!ok) break;
             tc_fence_after();
-            // P from TMEM: 16 packed columns at the start of every 32 of S
-            const uint32_t v = v_lo + st * (kTileBytes >> 4);
+            if (elect_one()) {
+                // P from TMEM: 16 packed columns at the start of every 32 of S
+                const uint64_t vd = sw128_desc(sV + st * kTileBytes, kHalfBytes, 1024);
 #pragma unroll
-            for (int kk = 0; kk < BN / 16; ++kk)
-                tc_mma_ta_lead(lead, tmem + kColO, tmem + 128 * st + 32 * (kk >> 1) + 8 * (kk & 1), v + kk * (2048 >> 4),
-                               idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
-            tc_commit_lead(lead, &v_empty[st]);
-            if (j == nl - 1) tc_commit_lead(lead, o_done);
+                for (int kk = 0; kk < BN / 16; ++kk)
+                    tc_mma_ta(tmem + kColO, tmem + 128 * st + 32 * (kk >> 1) + 8 * (kk & 1), vd + kk * (2048 >> 4), idesc_pv,
+                              (j > 0 || kk > 0) ? 1u : 0u);
+                tc_commit(&v_empty[st]);
+                if (j == nl - 1) tc_commit(o_done);
+            }
             if (j + kStages < nl) issue_qk(j + kStages);   // over P(j), behind PV(j)
         }
         __syncwarp();
