@@ -19,10 +19,11 @@
 // each, a warp spent 1,850 of 4,650 cycles of a tile pair waiting for P V and
 // the next Q K^T; the price, K and V read once per 128 queries instead of
 // 256, is L2 traffic, 6 TB/s.)
-// Roles (576 threads): warps 0-15 the exponentials, in two groups of eight
+// Roles (608 threads): warps 0-15 the exponentials, in two groups of eight
 // that take alternate key tiles (warp w of a group: lanes 32 (w % 4) .., columns
-// 64 (w / 4) ..), warp 16 TMA (K and V three tiles deep), warp 17 MMA, in
-// the order PV(j) QK(j + 3).
+// 64 (w / 4) ..), warp 16 TMA (K and V three tiles deep), warps 17 and 18 the
+// MMAs of Q K^T and of P V: one issuing warp's waits and instructions took
+// 1,850 cycles a tile, two run side by side.
 // Each warp takes 32 columns at a time from TMEM: tanh on the FMA pipe, the
 // exponential on the SFU, p packed as bf16 over the columns it came from.  The
 // polynomial's range (cap.cuh) is checked after the fact by a vote over the
@@ -40,7 +41,7 @@
 namespace duo {
 namespace {
 
-constexpr int kExpWarps = 16, kTmaWarp = 16, kMmaWarp = 17, kThreads = 576;
+constexpr int kExpWarps = 16, kTmaWarp = 16, kQkWarp = 17, kPvWarp = 18, kThreads = 608;
 constexpr int kRegThreads = 640;                   // five warps to a sub-partition: 96 registers
 constexpr int kStages = 3;                         // K and V tiles in shared memory, S tiles in TMEM
 constexpr uint32_t kTmemCols = 512;
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(kRegThreads, 1)
     }
     const int nl = j1 - j0;                           // tiles of this CTA, at least one
 
-    if (warp == kMmaWarp) tmem_alloc(holder, kTmemCols);
+    if (warp == kQkWarp) tmem_alloc(holder, kTmemCols);
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&k_full[i], 1);
@@ -253,15 +254,16 @@ __global__ void __launch_bounds__(kRegThreads, 1)
                 }
             }
         }
-    } else if (warp == kMmaWarp) {
-        // the whole warp waits, one lane issues
+    } else if (warp == kQkWarp) {
+        // S(j) = Q K(j)^T; the whole warp waits, one lane issues
         constexpr uint32_t idesc_qk = idesc_bf16(BM, BN, 0, 0);
-        constexpr uint32_t idesc_pv = idesc_bf16(BM, HD, 0, 1);
         bool ok = mbar_wait(q_full, 0, p.status);
-        auto issue_qk = [&](int j) {                  // after its K tile: S(j) and the stage's release
-            const int st = j % kStages;
-            ok = ok && mbar_wait(&k_full[st], (j / kStages) & 1, p.status);
-            if (!ok) return;
+        for (int j = 0; j < nl && ok; ++j) {
+            const int st = j % kStages, use = j / kStages;
+            // the slot holds P(j - kStages) until its P V is done
+            if (use > 0) ok = mbar_wait(&v_empty[st], (use - 1) & 1, p.status);
+            ok = ok && mbar_wait(&k_full[st], use & 1, p.status);
+            if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
                 const uint64_t qd = sw128_desc(sQ, 16, 1024), kd = sw128_desc(sK + st * kTileBytes, 16, 1024);
@@ -273,15 +275,18 @@ __global__ void __launch_bounds__(kRegThreads, 1)
                 tc_commit(&s_full[st]);
                 tc_commit(&k_empty[st]);
             }
-        };
-        for (int j = 0; j < min(nl, kStages); ++j) issue_qk(j);
+        }
+        __syncwarp();
+    } else if (warp == kPvWarp) {
+        // O += P(j) V(j), P from TMEM: 16 packed columns at the start of every 32 of S
+        constexpr uint32_t idesc_pv = idesc_bf16(BM, HD, 0, 1);
+        bool ok = true;
         for (int j = 0; j < nl && ok; ++j) {
             const int st = j % kStages, ph = (j / kStages) & 1;
             ok = mbar_wait(&v_full[st], ph, p.status) && mbar_wait(&p_full[st], ph, p.status);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-                // P from TMEM: 16 packed columns at the start of every 32 of S
                 const uint64_t vd = sw128_desc(sV + st * kTileBytes, kHalfBytes, 1024);
 #pragma unroll
                 for (int kk = 0; kk < BN / 16; ++kk)
@@ -290,7 +295,6 @@ __global__ void __launch_bounds__(kRegThreads, 1)
                 tc_commit(&v_empty[st]);
                 if (j == nl - 1) tc_commit(o_done);
             }
-            if (j + kStages < nl) issue_qk(j + kStages);   // over P(j), behind PV(j)
         }
         __syncwarp();
     } else if (warp < kExpWarps) {
@@ -400,7 +404,7 @@ __global__ void __launch_bounds__(kRegThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == kMmaWarp) {
+    if (warp == kQkWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
