@@ -29,6 +29,12 @@ __device__ __forceinline__ float sfu_exp2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// the same, kept in its place among other such statements
+__device__ __forceinline__ float sfu_exp2_ordered(float x) {
+    float y;
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ float sfu_rcp(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -66,7 +72,7 @@ __device__ __forceinline__ float2 poly_fma2(float2 x, const TanhPoly& c) { retur
 
 // The largest |x|, in four chains.
 template <int W>
-__device__ __forceinline__ float largest(const float (&x)[W]) {
+__device__ __forceinline__ float largest(const float* x) {
     static_assert(W % 8 == 0, "pairs for four chains");
     float m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll

@@ -42,16 +42,16 @@
 // S and dP are computed in both (7 products instead of 5).
 //   outer tiles X0, X1 = K, V (or Q, dout), resident in shared memory;
 //   inner tiles Y0, Y1 = Q, dout (or K, V), TMA into a 2-stage ring.
-//   S = X0 Y0^T, dP = X1 Y1^T (lane = outer row), then W and dS rounded to
-//   bf16 over the columns of S and dP they came from, and
+//   S = X0 Y0^T, dP = X1 Y1^T (lane = outer row), then W and dS, rounded to
+//   bf16, share the columns of dP, and
 //   ACC1 += W Y1 (dV), ACC2 += dS Y0 (dK or dQ) with A read from TMEM.
 // TMEM: S | dP | ACC1 | ACC2, 128 columns each; without ACC1 (statistics, dQ) a
 // second S takes its place, and for the statistics a second dP that of ACC2.
-// Keys outer, the MMA thread's order is
-//   ACC1(j) S(j+1) | ACC2(j) dP(j+1) | ...
-// so the element-wise warps turn dP(j) into dS(j) while the tensor core runs
-// ACC1(j) and S(j+1), and S(j+1) into W(j+1) while it runs ACC2(j) and
-// dP(j+1); with two S it is always one S ahead.
+// S is free as soon as the element-wise warps have loaded it, so S(j + 1) is
+// there when they have finished tile j, and
+//   ACC1(j) ACC2(j) dP(j + 1)
+// run while they turn S(j + 1) into weights.  (With W over S's columns, S(j + 1)
+// had to wait for ACC1(j), and the warps for it: dK and dV 355 -> @@ us.)
 // Roles (576 threads): warps 0-15 element-wise (warp w: lanes 32 (w % 4) ..,
 // columns 32 (w / 4) ..), warp 16 TMA, warp 17 MMA.  Sixteen warps at 96
 // registers (an SM sub-partition holds five warps) against eight at 168: the
@@ -73,6 +73,7 @@ namespace {
 constexpr int BM = 128;            // rows of an outer or inner tile
 constexpr int HD = 128;
 constexpr int kElemWarps = 16, kCols = 32;          // columns of an element-wise warp
+constexpr int kChunk = 16;                          // of them taken from TMEM at a time
 constexpr int kTmaWarp = 16, kMmaWarp = 17, kGradThreads = 576;
 constexpr int kRegThreads = 640;                   // five warps to a sub-partition: 96 registers
 constexpr uint32_t kTmemCols = 512;
@@ -155,24 +156,23 @@ __device__ __forceinline__ float2 tanh2(float2 x, const CapArgs& cap, const Tanh
     return POLY ? poly_fma2(x, tp) : make_float2(tanh_sfu(x.x * cap.k), tanh_sfu(x.y * cap.k));
 }
 
-// A warp's 32 columns: x[] dot products -> W, or with a cap -W times its slope
-// (t^2 - 1 is one instruction; the sign goes into the last multiply); W packed
-// as bf16 to TMEM on the way when COLS (keys outer).  MASKED: some column is
-// not seen, or is seen by both attentions.  One loop from the dot product to
-// the packed W, so that the FMA, SFU and ALU work of neighbouring pairs
-// interleaves (in separate loops the pipes took turns: their shares of the
-// time added up to 96 %).
+// A warp's 32 columns: x[] dot products -> W, or with a cap -W times
+// its slope (t^2 - 1 is one instruction; the sign goes into the last multiply);
+// pk[] = W packed as bf16 when COLS (keys outer).  MASKED: some
+// column is not seen, or is seen by both attentions.  One loop from the dot
+// product to the packed W, so that the FMA, SFU and ALU work of neighbouring
+// pairs interleaves (in separate loops the pipes took turns: their shares of
+// the time added up to 96 %).
 template <bool CAP, bool COLS, bool MASKED, bool POLY>
-__device__ __forceinline__ void weights_loop(float (&x)[kCols], const LayerArgs& a, float sl, const RowStats& r,
-                                             const Seen& seen, uint32_t sign, uint32_t w_addr) {
-    uint32_t pk[kCols / 2];
-    const TanhPoly tp = tanh_poly(a.cap.k);
+__device__ __forceinline__ void weights_loop(float* x, const LayerArgs& a, float sl, const TanhPoly& tp, const RowStats& r,
+                                             const Seen& seen, int col0, uint32_t* pk) {
 #pragma unroll
-    for (int c4 = 0; c4 < kCols / 4; ++c4) {
-        float4 l4 = stat4<COLS>(r, 0, c4);
+    for (int c4 = 0; c4 < kChunk / 4; ++c4) {
+        const int q4 = col0 / 4 + c4;
+        float4 l4 = stat4<COLS>(r, 0, q4);
         if constexpr (MASKED) {
-            l4 = choose4(seen.lam, 4 * c4, stat4<COLS>(r, 2, c4), l4);
-            l4 = choose4(seen.causal, 4 * c4, l4, make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY));
+            l4 = choose4(seen.lam, 4 * q4, stat4<COLS>(r, 2, q4), l4);
+            l4 = choose4(seen.causal, 4 * q4, l4, make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY));
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -188,51 +188,72 @@ __device__ __forceinline__ void weights_loop(float (&x)[kCols], const LayerArgs&
                 v = ffma2(v, make_float2(sl, sl), nl);
             }
             v = make_float2(sfu_exp2(v.x), sfu_exp2(v.y));
-            if constexpr (COLS) pk[c / 2] = pack_bf16(v.x, v.y) ^ sign;
+            if constexpr (COLS) pk[c / 2] = pack_bf16(v.x, v.y);
             if constexpr (CAP) v = fmul2(v, slope);
             x[c] = v.x;
             x[c + 1] = v.y;
         }
     }
-    if constexpr (COLS) tmem_st16(w_addr, pk);
 }
 template <bool CAP, bool COLS, bool MASKED>
-__device__ __forceinline__ void weights(float (&x)[kCols], const LayerArgs& a, float sl, const RowStats& r,
-                                        const Seen& seen, uint32_t sign, uint32_t w_addr) {
-    if (!CAP || __all_sync(0xffffffffu, largest(x) * a.cap.k <= kTanhRange))
-        weights_loop<CAP, COLS, MASKED, true>(x, a, sl, r, seen, sign, w_addr);
-    else
-        weights_loop<CAP, COLS, MASKED, false>(x, a, sl, r, seen, sign, w_addr);
+__device__ __forceinline__ void weights(float (&x)[kCols], uint32_t (&pk)[kCols / 2], const LayerArgs& a, float sl,
+                                        const TanhPoly& tp, const RowStats& r, const Seen& seen) {
+#pragma unroll
+    for (int ch = 0; ch < kCols / kChunk; ++ch) {
+        float* y = x + kChunk * ch;
+        if (!CAP || __all_sync(0xffffffffu, largest<kChunk>(y) * a.cap.k <= kTanhRange))
+            weights_loop<CAP, COLS, MASKED, true>(y, a, sl, tp, r, seen, kChunk * ch, pk + kChunk / 2 * ch);
+        else
+            weights_loop<CAP, COLS, MASKED, false>(y, a, sl, tp, r, seen, kChunk * ch, pk + kChunk / 2 * ch);
+    }
 }
 
-// x[] as weights left it, TMEM dP -> dS (with a cap: -dS) packed as bf16 over
-// dP's columns.
+// x[] and pk[] as weights left them, TMEM dP -> of every 16 columns of dP's the
+// first 8 hold W (COLS) and the last 8 dS (with a cap: -dS), packed as bf16.
 template <bool COLS, bool MASKED>
-__device__ __forceinline__ void score_grads(const float (&x)[kCols], const RowStats& r, const Seen& seen,
-                                            uint32_t sign, uint32_t d_addr) {
-    float d[kCols];
-    tmem_ld32(d_addr, d);
-    uint32_t pk[kCols / 2];
+__device__ __forceinline__ void score_grads(const float (&x)[kCols], const uint32_t (&pk)[kCols / 2], const RowStats& r,
+                                            const Seen& seen, uint32_t d_addr) {
 #pragma unroll
-    for (int c4 = 0; c4 < kCols / 4; ++c4) {
-        float4 q = stat4<COLS>(r, 1, c4);
-        if constexpr (MASKED) q = choose4(seen.lam, 4 * c4, stat4<COLS>(r, 3, c4), q);
-        const int c = 4 * c4;
-        const float2 u = fmul2(make_float2(x[c], x[c + 1]), fadd2(make_float2(d[c], d[c + 1]), make_float2(q.x, q.y)));
-        const float2 v = fmul2(make_float2(x[c + 2], x[c + 3]), fadd2(make_float2(d[c + 2], d[c + 3]), make_float2(q.z, q.w)));
-        pk[2 * c4] = pack_bf16(u.x, u.y) ^ sign;
-        pk[2 * c4 + 1] = pack_bf16(v.x, v.y) ^ sign;
+    for (int ch = 0; ch < kCols / kChunk; ++ch) {
+        float d[kChunk];
+        tmem_ld16(d_addr + kChunk * ch, d);
+        uint32_t o[kChunk];
+#pragma unroll
+        for (int c4 = 0; c4 < kChunk / 4; ++c4) {
+            const int q4 = kChunk / 4 * ch + c4;
+            float4 q = stat4<COLS>(r, 1, q4);
+            if constexpr (MASKED) q = choose4(seen.lam, 4 * q4, stat4<COLS>(r, 3, q4), q);
+            const float* w = x + 4 * q4;
+            const int c = 4 * c4;
+            const float2 u = fmul2(make_float2(w[0], w[1]), fadd2(make_float2(d[c], d[c + 1]), make_float2(q.x, q.y)));
+            const float2 v = fmul2(make_float2(w[2], w[3]), fadd2(make_float2(d[c + 2], d[c + 3]), make_float2(q.z, q.w)));
+            o[kChunk / 2 + 2 * c4] = pack_bf16(u.x, u.y);
+            o[kChunk / 2 + 2 * c4 + 1] = pack_bf16(v.x, v.y);
+            if constexpr (COLS) {
+                o[2 * c4] = pk[2 * q4];
+                o[2 * c4 + 1] = pk[2 * q4 + 1];
+            }
+        }
+        if constexpr (COLS) {
+            tmem_st16(d_addr + kChunk * ch, o);
+        } else {
+            uint32_t g[kChunk / 2];
+#pragma unroll
+            for (int c = 0; c < kChunk / 2; ++c) g[c] = o[kChunk / 2 + c];
+            tmem_st8(d_addr + kChunk * ch + kChunk / 2, g);
+        }
     }
-    tmem_st16(d_addr, pk);
 }
 
 // A tile with keys that both attentions see, for a gate outside [0, 1]: the
 // shares a P_c and (1 - a) P_s differ in sign and are formed one by one (the
-// statistics hold lse_s - log2 |1 - a| and D_s), 16 columns at a time.  Signs
-// as in weights.
+// statistics hold lse_s - log2 |1 - a| and D_s), 16 columns at a time.  For a
+// negative a everything a CTA accumulates is negated, so that |a| P_c is W in
+// the other tiles; here its share is positive and the other one negative,
+// whichever of the two signs is the odd one.
 template <bool CAP, bool COLS>
-__device__ __forceinline__ void signed_shares(const LayerArgs& a, float sl, const RowStats& r, Seen seen, bool neg_c,
-                                              bool neg_s, uint32_t s_addr, uint32_t d_addr) {
+__device__ __forceinline__ void signed_shares(const LayerArgs& a, float sl, const RowStats& r, Seen seen,
+                                              uint32_t s_addr, uint32_t d_addr) {
 #pragma unroll 1
     for (int ch = 0; ch < kCols / 16; ++ch) {
         float x[16], d[16];
@@ -252,12 +273,10 @@ __device__ __forceinline__ void signed_shares(const LayerArgs& a, float sl, cons
             } else {
                 s = x[c] * sl;
             }
-            float wc = (seen.causal >> c) & 1u ? sfu_exp2(s + lc) : 0.f;
-            float ws = (seen.lam >> c) & 1u ? sfu_exp2(s + ls) : 0.f;
-            wc = neg_c ? -wc : wc;
-            ws = neg_s ? -ws : ws;
-            x[c] = wc + ws;
-            d[c] = slope * fmaf(x[c], d[c], fmaf(wc, qc, ws * qs));
+            const float wc = (seen.causal >> c) & 1u ? sfu_exp2(s + lc) : 0.f;
+            const float ws = (seen.lam >> c) & 1u ? sfu_exp2(s + ls) : 0.f;
+            x[c] = wc - ws;
+            d[c] = slope * fmaf(x[c], d[c], fmaf(wc, qc, -ws * qs));
         }
         seen.causal >>= 16;
         seen.lam >>= 16;
@@ -266,8 +285,8 @@ __device__ __forceinline__ void signed_shares(const LayerArgs& a, float sl, cons
             pw[c] = pack_bf16(x[2 * c], x[2 * c + 1]);
             pg[c] = pack_bf16(d[2 * c], d[2 * c + 1]);
         }
-        if constexpr (COLS) tmem_st8(s_addr + 8 * ch, pw);
-        tmem_st8(d_addr + 8 * ch, pg);
+        if constexpr (COLS) tmem_st8(d_addr + 16 * ch, pw);
+        tmem_st8(d_addr + 16 * ch + 8, pg);
     }
 }
 
@@ -313,7 +332,7 @@ __device__ __forceinline__ void add_sums(RowSums& sum, const LayerArgs& a, float
                                          const Seen& seen, uint32_t s_addr, uint32_t d_addr) {
     float x[kCols];
     tmem_ld32(s_addr, x);
-    if (!CAP || __all_sync(0xffffffffu, largest(x) * a.cap.k <= kTanhRange))
+    if (!CAP || __all_sync(0xffffffffu, largest<kCols>(x) * a.cap.k <= kTanhRange))
         sums_loop<CAP, MASKED, true>(sum, x, a, sl, nlse_c, nlse_s, seen, d_addr);
     else
         sums_loop<CAP, MASKED, false>(sum, x, a, sl, nlse_c, nlse_s, seen, d_addr);
@@ -344,8 +363,8 @@ __global__ void __launch_bounds__(kRegThreads, 1)
     uint64_t* y_empty = bars + 3;   // [2]
     uint64_t* s_full = bars + 5;    // [2], by the tile's parity, as the next three
     uint64_t* d_full = bars + 7;
-    uint64_t* w_ready = bars + 9;   // W written (keys outer), S read (statistics: dP too)
-    uint64_t* g_ready = bars + 11;  // dS written
+    uint64_t* w_ready = bars + 9;   // S read (statistics: dP too)
+    uint64_t* g_ready = bars + 11;  // W and dS written
     uint64_t* done = bars + 13;
     uint32_t* holder = reinterpret_cast<uint32_t*>(smem + kOffHolder);
 
@@ -426,12 +445,12 @@ __global__ void __launch_bounds__(kRegThreads, 1)
                     tc_mma(tmem + col, x + o, y + o, idesc_kk, kk > 0 ? 1u : 0u);
                 }
             };
-            // ACC += A (bf16 over the columns it came from) Y_w(j), over the inner rows
+            // ACC += A (W or dS, 8 of every 16 columns of dP's) Y_w(j), over the inner rows
             auto issue_acc = [&](uint32_t col, uint32_t a_col, int w, int j) {
                 const uint64_t y = sw128_desc(sY + ((j & 1) * 2 + w) * kTileBytes, kHalfBytes, 1024);
 #pragma unroll
                 for (int kk = 0; kk < BM / 16; ++kk)
-                    tc_mma_ta(tmem + col, tmem + a_col + kCols * (kk >> 1) + 8 * (kk & 1), y + kk * (2048 >> 4), idesc_mn,
+                    tc_mma_ta(tmem + col, tmem + a_col + kChunk * kk, y + kk * (2048 >> 4), idesc_mn,
                               (j > 0 || kk > 0) ? 1u : 0u);
             };
             auto wait_tile = [&](int j) { return mbar_wait(&y_full[j & 1], (j >> 1) & 1, p.status); };
@@ -482,21 +501,19 @@ __global__ void __launch_bounds__(kRegThreads, 1)
                     }
                 } else {
                     const bool next = j + 1 < n_in;
-                    if constexpr (kKeys) {
-                        if (next) ok = wait_tile(j + 1);
-                        ok = ok && mbar_wait(&w_ready[j & 1], ph, p.status);
+                    if (kKeys && next) {
+                        // S(j) is in registers: its columns take S(j + 1)
+                        ok = wait_tile(j + 1) && mbar_wait(&w_ready[j & 1], ph, p.status);
                         if (!ok) break;
                         tc_fence_after();
-                        if (elect_one()) {
-                            issue_acc(kColA1, kColS, 1, j);
-                            if (next) issue_s(j + 1);
-                        }
+                        if (elect_one()) issue_s(j + 1);
                     }
                     ok = mbar_wait(&g_ready[j & 1], ph, p.status);
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
-                        issue_acc(kColA2, kColP, 0, j);
+                        if (kKeys) issue_acc(kColA1, kColP, 1, j);
+                        issue_acc(kColA2, kColP + kChunk / 2, 0, j);
                         tc_commit(&y_empty[j & 1]);
                         if (next) issue_d(j + 1);
                     }
@@ -520,7 +537,7 @@ __global__ void __launch_bounds__(kRegThreads, 1)
         const float sl = a.scale * kLog2e;
         const float al = p.alpha[kv];
         const bool neg_c = al < 0.f, neg_s = 1.f - al < 0.f;
-        const uint32_t sign = neg_c ? 0x80008000u : 0u;        // of a packed pair of W or dS, where only a P_c counts
+        const TanhPoly tp = tanh_poly(a.cap.k);
         const int orow = BM * ot + row;                       // key (keys outer) or query
         RowStats rs{0.f, 0.f, 0.f, 0.f, nullptr};
         RowSums sum{0.f, 0.f, 0.f, 0.f};
@@ -566,28 +583,27 @@ __global__ void __launch_bounds__(kRegThreads, 1)
                 continue;
             } else if (plain || !(neg_c || neg_s)) {
                 float x[kCols];
+                uint32_t pk[kCols / 2];
                 tmem_ld32(s_addr, x);
-                if (plain)
-                    weights<CAP, kKeys, false>(x, a, sl, rs, seen, sign, s_addr);
-                else
-                    weights<CAP, kKeys, true>(x, a, sl, rs, seen, 0u, s_addr);
-                if constexpr (kKeys) tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&w_ready[j & 1]);
+                if (plain)
+                    weights<CAP, kKeys, false>(x, pk, a, sl, tp, rs, seen);
+                else
+                    weights<CAP, kKeys, true>(x, pk, a, sl, tp, rs, seen);
                 ok = __all_sync(0xffffffffu, mbar_wait(&d_full[j & 1], ph, p.status));
                 if (!ok) break;
                 tc_fence_after();
                 if (plain)
-                    score_grads<kKeys, false>(x, rs, seen, sign, d_addr);
+                    score_grads<kKeys, false>(x, pk, rs, seen, d_addr);
                 else
-                    score_grads<kKeys, true>(x, rs, seen, 0u, d_addr);
+                    score_grads<kKeys, true>(x, pk, rs, seen, d_addr);
             } else {
                 ok = __all_sync(0xffffffffu, mbar_wait(&d_full[j & 1], ph, p.status));
                 if (!ok) break;
                 tc_fence_after();
-                signed_shares<CAP, kKeys>(a, sl, rs, seen, neg_c, neg_s, s_addr, d_addr);
-                tmem_wait_st();
+                signed_shares<CAP, kKeys>(a, sl, rs, seen, s_addr, d_addr);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&w_ready[j & 1]);
@@ -650,7 +666,8 @@ __global__ void __launch_bounds__(kRegThreads, 1)
 #pragma unroll
             for (int t = 0; t < (kKeys ? 2 : 1); ++t) {
                 __nv_bfloat16* o = static_cast<__nv_bfloat16*>(t ? p.d1 : p.d0) + off;
-                const float f = t ? 1.f : CAP ? -a.scale : a.scale;   // dS held back the softmax scale
+                // dS held back the softmax scale; a negative gate's sums are negated
+                const float f = (t ? 1.f : CAP ? -a.scale : a.scale) * (neg_c ? -1.f : 1.f);
                 float v[kCols];
                 tmem_ld32(lane_addr + (t ? kColA1 : kColA2) + kCols * wg, v);
 #pragma unroll

@@ -79,10 +79,11 @@ __device__ __forceinline__ Sched make_sched_single(const TcArgs& p, bool retriev
     s.n0 = s.n;
     return s;
 }
-__device__ __forceinline__ bool single_needs_mask(const Sched& s, const Tile& t) {
-    if ((!s.retrieval && !s.chunk) || t.src == SRC_RING) return true;
-    if (t.src == SRC_CACHE) return t.row < 0;
-    return t.row + BN - 1 > BM * s.m;
+// Tiles first .. last - 1 of the list need no mask: all but the tile that
+// starts before position 0, the ring and the diagonal's (Lambda mode: none).
+__device__ __forceinline__ void unmasked_tiles(const Sched& s, int& first, int& last) {
+    first = s.retrieval ? (s.c0 % BN != 0 ? 1 : 0) : s.n_ring;
+    last = s.retrieval || s.chunk ? s.n - 1 : 0;
 }
 
 // 32 columns of a row: dot products x -> p, packed as bf16 in pk; returns the
@@ -92,14 +93,14 @@ __device__ __forceinline__ bool single_needs_mask(const Sched& s, const Tile& t)
 template <bool MASKED, bool POLY>
 __device__ __forceinline__ float exp_loop(const float (&x)[32], uint32_t (&pk)[16], const CapArgs& cap, const TanhPoly& tp,
                                           uint32_t vis, float& big) {
-    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-    float b[2] = {0.f, 0.f};
+    float2 sum = make_float2(0.f, 0.f);
+    big = 0.f;
 #pragma unroll
     for (int c2 = 0; c2 < 16; ++c2) {
         float2 v = make_float2(x[2 * c2], x[2 * c2 + 1]);
         if constexpr (POLY) {
             const float2 u = fmul2(v, v);
-            b[c2 & 1] = fmax3(b[c2 & 1], u.x, u.y);
+            big = fmax3(big, u.x, u.y);
             v = poly_fma2(v, u, tp);
         } else {
             v = make_float2(cap.c2 * tanh_sfu(v.x * cap.k), cap.c2 * tanh_sfu(v.y * cap.k));
@@ -111,25 +112,30 @@ __device__ __forceinline__ float exp_loop(const float (&x)[32], uint32_t (&pk)[1
         }
         __nv_bfloat162 h = __floats2bfloat162_rn(e.x, e.y);
         pk[c2] = *reinterpret_cast<uint32_t*>(&h);
-        sum[c2 & 1] = fadd2(sum[c2 & 1], make_float2(bf16_lo(pk[c2]), bf16_hi(pk[c2])));
+        sum = fadd2(sum, make_float2(bf16_lo(pk[c2]), bf16_hi(pk[c2])));
     }
-    big = fmaxf(b[0], b[1]);
-    return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+    return sum.x + sum.y;
 }
 
-// 32 columns of a row: dot products at s_addr -> p over the first 16 of them.
+// 64 columns of a row: dot products at s_addr -> p over the first half of every 32.
 template <bool MASKED>
 __device__ __forceinline__ float exp_columns(uint32_t s_addr, const CapArgs& cap, const TanhPoly& tp, float x2_max,
-                                             uint32_t vis) {
-    float x[32], big;
-    tmem_ld32(s_addr, x);
-    uint32_t pk[16];
-    float l = exp_loop<MASKED, true>(x, pk, cap, tp, vis, big);
-    if (!__all_sync(0xffffffffu, big <= x2_max)) {
-        tmem_ld32(s_addr, x);
-        l = exp_loop<MASKED, false>(x, pk, cap, tp, vis, big);
+                                             uint64_t vis) {
+    float l = 0.f;
+#pragma unroll 1
+    for (int ch = 0; ch < 64 / 32; ++ch) {
+        float x[32], big;
+        tmem_ld32(s_addr + 32 * ch, x);
+        uint32_t pk[16];
+        float t = exp_loop<MASKED, true>(x, pk, cap, tp, (uint32_t)vis, big);
+        if (!__all_sync(0xffffffffu, big <= x2_max)) {
+            tmem_ld32(s_addr + 32 * ch, x);
+            t = exp_loop<MASKED, false>(x, pk, cap, tp, (uint32_t)vis, big);
+        }
+        l += t;
+        vis >>= 32;
+        tmem_st16(s_addr + 32 * (ch / (32 / 32)) + 16 * (ch % (32 / 32)), pk);
     }
-    tmem_st16(s_addr, pk);
     return l;
 }
 
@@ -306,21 +312,21 @@ __global__ void __launch_bounds__(kRegThreads, 1)
         const float x2_max = (kTanhRange / a.cap.k) * (kTanhRange / a.cap.k);
         float l_sum = 0.f;
         bool ok = true;
+        int plain_first, plain_last;
+        unmasked_tiles(sc, plain_first, plain_last);
         for (int j = group; j < nl; j += 2) {
             const int st = j % kStages;
             ok = __all_sync(0xffffffffu, mbar_wait(&s_full[st], (j / kStages) & 1, p.status));
             if (!ok) break;
             tc_fence_after();
-            const Tile t = tile_at(sc, j0 + j);
             const uint32_t s_addr = lane_base + 128 * st + 64 * half;
-            if (single_needs_mask(sc, t)) {
-                uint32_t vis[4] = {0u, 0u, 0u, 0u};           // the tile's keys this row sees, a bit per column
-                visible_columns(a, sc, t, c0 + crow, vis);
-                l_sum += exp_columns<true>(s_addr, a.cap, tp, x2_max, half ? vis[2] : vis[0]);
-                l_sum += exp_columns<true>(s_addr + 32, a.cap, tp, x2_max, half ? vis[3] : vis[1]);
-            } else {
+            if (j0 + j >= plain_first && j0 + j < plain_last) {
                 l_sum += exp_columns<false>(s_addr, a.cap, tp, x2_max, 0u);
-                l_sum += exp_columns<false>(s_addr + 32, a.cap, tp, x2_max, 0u);
+            } else {
+                uint32_t vis[4] = {0u, 0u, 0u, 0u};           // the tile's keys this row sees, a bit per column
+                visible_columns(a, sc, tile_at(sc, j0 + j), c0 + crow, vis);
+                const uint64_t v64 = half ? ((uint64_t)vis[3] << 32 | vis[2]) : ((uint64_t)vis[1] << 32 | vis[0]);
+                l_sum += exp_columns<true>(s_addr, a.cap, tp, x2_max, v64);
             }
             tmem_wait_st();
             tc_fence_before();
