@@ -54,18 +54,24 @@ constexpr float kTanh0 = 0.9999933242797852f, kTanh1 = -0.33289048075675964f, kT
 
 // f * tanh(k x) of a pair of dot products with |k x| in range: the
 // polynomial's coefficients times f and the powers of k, so that it takes x
-// itself; u is x^2.
+// itself; u is x^2.  A kernel parameter: every constant is a pair of equal
+// halves, as the packed instructions take them, read from the parameter bank
+// instead of held in registers.
 struct TanhPoly {
-    float a0, a1, a2, a3;
+    float2 a0, a1, a2, a3;
+    float2 c2, minus1;   // c2 = cap log2(e); -1
+    float x2_max;        // the largest x^2 in range
 };
-__device__ __forceinline__ TanhPoly tanh_poly(float k, float f = 1.f) {
-    const float k2 = k * k, s0 = f * k, s1 = s0 * k2, s2 = s1 * k2;
-    return {kTanh0 * s0, kTanh1 * s1, kTanh2 * s2, kTanh3 * (s2 * k2)};
+inline TanhPoly tanh_poly(const CapArgs& cap, float f) {
+    const float k = cap.k, k2 = k * k, s0 = f * k, s1 = s0 * k2, s2 = s1 * k2;
+    auto two = [](float x) { return make_float2(x, x); };
+    return {two(kTanh0 * s0), two(kTanh1 * s1), two(kTanh2 * s2), two(kTanh3 * (s2 * k2)),
+            two(cap.c2),      two(-1.f),        cap.on ? (kTanhRange / k) * (kTanhRange / k) : 0.f};
 }
 __device__ __forceinline__ float2 poly_fma2(float2 x, float2 u, const TanhPoly& c) {
-    float2 p = ffma2(u, make_float2(c.a3, c.a3), make_float2(c.a2, c.a2));
-    p = ffma2(p, u, make_float2(c.a1, c.a1));
-    p = ffma2(p, u, make_float2(c.a0, c.a0));
+    float2 p = ffma2(u, c.a3, c.a2);
+    p = ffma2(p, u, c.a1);
+    p = ffma2(p, u, c.a0);
     return fmul2(p, x);
 }
 __device__ __forceinline__ float2 poly_fma2(float2 x, const TanhPoly& c) { return poly_fma2(x, fmul2(x, x), c); }

@@ -100,6 +100,7 @@ struct GradArgs {
     float* part;           // [Hkv][B][n_tiles][G], the shares of dalpha
     float* dalpha;
     int32_t* status;
+    TanhPoly poly;         // tanh(k x)
 };
 
 // What a launch computes: the rows' statistics, dK and dV (keys outer), or dQ.
@@ -182,8 +183,8 @@ __device__ __forceinline__ void weights_loop(float* x, const LayerArgs& a, float
             float2 slope;
             if constexpr (CAP) {
                 v = tanh2<POLY>(v, a.cap, tp);
-                slope = ffma2(v, v, make_float2(-1.f, -1.f));
-                v = ffma2(v, make_float2(a.cap.c2, a.cap.c2), nl);
+                slope = ffma2(v, v, tp.minus1);
+                v = ffma2(v, tp.c2, nl);
             } else {
                 v = ffma2(v, make_float2(sl, sl), nl);
             }
@@ -295,10 +296,9 @@ struct RowSums {
     float lc, dc, ls, ds;
 };
 template <bool CAP, bool MASKED, bool POLY>
-__device__ __forceinline__ void sums_loop(RowSums& sum, const float (&x)[kCols], const LayerArgs& a, float sl, float nlse_c,
-                                          float nlse_s, const Seen& seen, uint32_t d_addr) {
+__device__ __forceinline__ void sums_loop(RowSums& sum, const float (&x)[kCols], const LayerArgs& a, float sl, const TanhPoly& tp,
+                                          float nlse_c, float nlse_s, const Seen& seen, uint32_t d_addr) {
     const float f = CAP ? a.cap.c2 : sl;
-    const TanhPoly tp = tanh_poly(a.cap.k);
     float2 lc = make_float2(0.f, 0.f), dc = lc;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -328,14 +328,14 @@ __device__ __forceinline__ void sums_loop(RowSums& sum, const float (&x)[kCols],
     sum.dc += dc.x + dc.y;
 }
 template <bool CAP, bool MASKED>
-__device__ __forceinline__ void add_sums(RowSums& sum, const LayerArgs& a, float sl, float nlse_c, float nlse_s,
+__device__ __forceinline__ void add_sums(RowSums& sum, const LayerArgs& a, float sl, const TanhPoly& tp, float nlse_c, float nlse_s,
                                          const Seen& seen, uint32_t s_addr, uint32_t d_addr) {
     float x[kCols];
     tmem_ld32(s_addr, x);
     if (!CAP || __all_sync(0xffffffffu, largest<kCols>(x) * a.cap.k <= kTanhRange))
-        sums_loop<CAP, MASKED, true>(sum, x, a, sl, nlse_c, nlse_s, seen, d_addr);
+        sums_loop<CAP, MASKED, true>(sum, x, a, sl, tp, nlse_c, nlse_s, seen, d_addr);
     else
-        sums_loop<CAP, MASKED, false>(sum, x, a, sl, nlse_c, nlse_s, seen, d_addr);
+        sums_loop<CAP, MASKED, false>(sum, x, a, sl, tp, nlse_c, nlse_s, seen, d_addr);
 }
 
 // TMEM columns of S(j) and dP(j).
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kRegThreads, 1)
         const float sl = a.scale * kLog2e;
         const float al = p.alpha[kv];
         const bool neg_c = al < 0.f, neg_s = 1.f - al < 0.f;
-        const TanhPoly tp = tanh_poly(a.cap.k);
+        const TanhPoly& tp = p.poly;
         const int orow = BM * ot + row;                       // key (keys outer) or query
         RowStats rs{0.f, 0.f, 0.f, 0.f, nullptr};
         RowSums sum{0.f, 0.f, 0.f, 0.f};
@@ -551,8 +551,10 @@ __global__ void __launch_bounds__(kRegThreads, 1)
             rs = {st[0], st[p.n_pad], st[2 * (size_t)p.n_pad], st[3 * (size_t)p.n_pad], nullptr};
         }
         bool ok = true;
+        int it = inner_tile(0) - 1;                           // inner_tile(j), step by step
         for (int j = 0; j < n_in; ++j) {
-            const int it = inner_tile(j), ph = (j >> 1) & 1;
+            it = it + 1 < p.n_tiles || !kKeys ? it + 1 : ot;
+            const int ph = (j >> 1) & 1;
             const uint32_t s_addr = lane_addr + s_col<MODE>(j) + kCols * wg, d_addr = lane_addr + d_col<MODE>(j) + kCols * wg;
             if constexpr (kKeys) {
                 rs.cols = reinterpret_cast<const float*>(smem + kOffStat + (j & 1) * kStatBytes) + kCols * wg;
@@ -574,9 +576,9 @@ __global__ void __launch_bounds__(kRegThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 if (plain)
-                    add_sums<CAP, false>(sum, a, sl, rs.lse_c, rs.lse_l, seen, s_addr, d_addr);
+                    add_sums<CAP, false>(sum, a, sl, tp, rs.lse_c, rs.lse_l, seen, s_addr, d_addr);
                 else
-                    add_sums<CAP, true>(sum, a, sl, rs.lse_c, rs.lse_l, seen, s_addr, d_addr);
+                    add_sums<CAP, true>(sum, a, sl, tp, rs.lse_c, rs.lse_l, seen, s_addr, d_addr);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&w_ready[j & 1]);
@@ -729,7 +731,7 @@ cudaError_t launch_mix_grad_tc(const LayerArgs& a, const MixGradArgs& g, int N, 
         const uint32_t bx[4] = {64, 1, BM, 1};
         if (!encode_tmap_bf16(&m[i], base[i], 4, d, st, bx)) return cudaErrorInvalidValue;
     }
-    GradArgs p{a, N, pl.n_tiles, pl.n_pad, g.stats, g.lse, g.alpha, nullptr, nullptr, g.part, g.dalpha, g.status};
+    GradArgs p{a, N, pl.n_tiles, pl.n_pad, g.stats, g.lse, g.alpha, nullptr, nullptr, g.part, g.dalpha, g.status, tanh_poly(a.cap, 1.f)};
     cudaError_t e = a.cap.on ? launch_grad<STATS, true>(m, p, s) : launch_grad<STATS, false>(m, p, s);
     if (e != cudaSuccess) return e;
     p.d0 = g.dk;

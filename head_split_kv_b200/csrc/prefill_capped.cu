@@ -119,8 +119,7 @@ __device__ __forceinline__ float exp_loop(const float (&x)[32], uint32_t (&pk)[1
 
 // 64 columns of a row: dot products at s_addr -> p over the first half of every 32.
 template <bool MASKED>
-__device__ __forceinline__ float exp_columns(uint32_t s_addr, const CapArgs& cap, const TanhPoly& tp, float x2_max,
-                                             uint64_t vis) {
+__device__ __forceinline__ float exp_columns(uint32_t s_addr, const CapArgs& cap, const TanhPoly& tp, uint64_t vis) {
     float l = 0.f;
 #pragma unroll 1
     for (int ch = 0; ch < 64 / 32; ++ch) {
@@ -128,7 +127,7 @@ __device__ __forceinline__ float exp_columns(uint32_t s_addr, const CapArgs& cap
         tmem_ld32(s_addr + 32 * ch, x);
         uint32_t pk[16];
         float t = exp_loop<MASKED, true>(x, pk, cap, tp, (uint32_t)vis, big);
-        if (!__all_sync(0xffffffffu, big <= x2_max)) {
+        if (!__all_sync(0xffffffffu, big <= tp.x2_max)) {
             tmem_ld32(s_addr + 32 * ch, x);
             t = exp_loop<MASKED, false>(x, pk, cap, tp, (uint32_t)vis, big);
         }
@@ -308,8 +307,6 @@ __global__ void __launch_bounds__(kRegThreads, 1)
         const int row = 32 * (warp & 3) + lane;               // TMEM lane
         const int crow = BM * mt + row;                       // chunk row
         const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        const TanhPoly tp = tanh_poly(a.cap.k, a.cap.c2);
-        const float x2_max = (kTanhRange / a.cap.k) * (kTanhRange / a.cap.k);
         float l_sum = 0.f;
         bool ok = true;
         int plain_first, plain_last;
@@ -321,12 +318,12 @@ __global__ void __launch_bounds__(kRegThreads, 1)
             tc_fence_after();
             const uint32_t s_addr = lane_base + 128 * st + 64 * half;
             if (j0 + j >= plain_first && j0 + j < plain_last) {
-                l_sum += exp_columns<false>(s_addr, a.cap, tp, x2_max, 0u);
+                l_sum += exp_columns<false>(s_addr, a.cap, p.poly, 0u);
             } else {
                 uint32_t vis[4] = {0u, 0u, 0u, 0u};           // the tile's keys this row sees, a bit per column
                 visible_columns(a, sc, tile_at(sc, j0 + j), c0 + crow, vis);
                 const uint64_t v64 = half ? ((uint64_t)vis[3] << 32 | vis[2]) : ((uint64_t)vis[1] << 32 | vis[0]);
-                l_sum += exp_columns<true>(s_addr, a.cap, tp, x2_max, v64);
+                l_sum += exp_columns<true>(s_addr, a.cap, p.poly, v64);
             }
             tmem_wait_st();
             tc_fence_before();

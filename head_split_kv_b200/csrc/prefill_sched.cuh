@@ -5,6 +5,7 @@
 
 #include <cuda.h>
 
+#include "cap.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "tcgen05.cuh"
@@ -36,6 +37,7 @@ struct TcArgs {
     float* part;           // [n_units][ns][2][kPartFloats] partial records (ns > 1)
     uint32_t* ticket;      // [n_units] arrivals; the last split merges them
     EpiArgs epi;           // gated-mix epilogues (EPI_MIX, EPI_DOT)
+    TanhPoly poly;         // capped scores: c2 tanh(k x)
     const int32_t* seq_len;
     int32_t* status;
     void* out;

@@ -146,7 +146,7 @@ __device__ __forceinline__ float2 exp2_fma2(float2 x) {
 // domain already, before the mask: on the FMA pipe when every |k * s| of the
 // warp's part of the tile is at most 1 (a vote), else on the SFU.
 template <bool CAP>
-__device__ __forceinline__ float softmax_tile(uint32_t s_addr, float sl, const CapArgs& cap, bool masked,
+__device__ __forceinline__ float softmax_tile(uint32_t s_addr, float sl, const CapArgs& cap, const TanhPoly& tp, bool masked,
                                               const uint32_t (&vis)[4], float& m_ref, float& l_sum, bool& need,
                                               const float* qsc) {
     float s[128];
@@ -179,10 +179,9 @@ __device__ __forceinline__ float softmax_tile(uint32_t s_addr, float sl, const C
         for (int i = 0; i < 4; ++i)
             big = fmax3(big, fmaxf(hi[i], s[124 + i]), -fminf(lo[i], s[124 + i]));
         if (__all_sync(0xffffffffu, big * cap.k <= kTanhRange)) {
-            const TanhPoly cp = tanh_poly(cap.k, cap.c2);
 #pragma unroll
             for (int c = 0; c < 128; c += 2) {
-                const float2 t = poly_fma2(make_float2(s[c], s[c + 1]), cp);
+                const float2 t = poly_fma2(make_float2(s[c], s[c + 1]), tp);
                 s[c] = t.x;
                 s[c + 1] = t.y;
             }
@@ -507,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float* qsc = QS && t.src == SRC_CACHE
                                    ? reinterpret_cast<const float*>(smem + kOffScale + (j & 3) * kScaleTileBytes)
                                    : nullptr;
-            const float corr = softmax_tile<CAP>(lane_base + col_s(qi), sl, a.cap, masked, vis, m_ref, l_sum, need,
+            const float corr = softmax_tile<CAP>(lane_base + col_s(qi), sl, a.cap, p.poly, masked, vis, m_ref, l_sum, need,
                                                  qsc);
             // O_qi holds every PV up to tile j - 1 (the commit behind s_full
             // covered them); rescale it before PV_qi(j) is issued
@@ -754,6 +753,7 @@ cudaError_t launch_prefill_tc(const LayerArgs& a, const CacheArgs& c, const void
     p.seq_len = c.seq_len;
     p.status = c.status;
     p.out = out;
+    p.poly = tanh_poly(a.cap, a.cap.c2);
     p.epi = epi ? *epi : EpiArgs{};
     const long grid = (long)p.n_ret_ctas + (long)a.B * a.S * a.G * p.n_mpairs;
     if (grid == 0) return cudaSuccess;
