@@ -782,10 +782,14 @@ duo_status duo_gated_mix_train(const duo_layer_desc* desc, const float* alpha, f
     if (sv.tc) {
         duo::CacheArgs none{};
         none.status = status;
-        duo::EpiArgs keep;
-        keep.mode = duo::EPI_KEEP;
-        keep.lse = lse + (size_t)a.B * a.Hq * N;
-        e = duo::launch_prefill_tc(as, none, q, k, v, N, streaming, nullptr, 0, (cudaStream_t)stream, &keep);
+        e = cudaSuccess;
+        if (!duo::cap_bounds_scores(as)) {
+            // the streaming attention first, to be mixed in by the causal launch
+            duo::EpiArgs keep;
+            keep.mode = duo::EPI_KEEP;
+            keep.lse = lse + (size_t)a.B * a.Hq * N;
+            e = duo::launch_prefill_tc(as, none, q, k, v, N, streaming, nullptr, 0, (cudaStream_t)stream, &keep);
+        }
         duo::EpiArgs mix;
         mix.mode = duo::EPI_MIX_KEEP;
         mix.alpha = alpha;

@@ -120,6 +120,10 @@ struct EpiArgs {
     const void* streaming = nullptr;   // EPI_MIX_KEEP: [B][C][Hq][d]
     float* lse = nullptr;              // EPI_KEEP, EPI_MIX_KEEP: [B][Hq][C], log2 of the sum of 2^score
 };
+// Are the layer's scores capped low enough that their exponentials need no
+// running maximum (prefill_capped.cu)?  Then EPI_MIX_KEEP computes both
+// attentions by itself, lse holding both planes.
+inline bool cap_bounds_scores(const LayerArgs& a) { return a.cap.on && a.cap.c2 <= 87.f; }
 // qscale non-NULL: the full cache holds 8- or 4-bit codes (as bf16 values)
 // and qscale [B][R][capacity][4] fp32 the (k scale, v scale, -, -) of each
 // row, applied to the scores and to p.

@@ -30,6 +30,12 @@
 // largest x^2; a part outside takes its scores from TMEM again and tanh on the
 // SFU.  The row sum adds the rounded p, so that an output is a convex
 // combination of V rows.
+// The gated mix (MIX) computes both attentions at once: p is the same under
+// both masks, so a tile with sink or recent keys writes p twice, once for the
+// causal mask and once for the Lambda mask, side by side in the columns of its
+// scores, and P V runs once into each of two accumulators (S0 | S1 | Os | Oc;
+// two S tiles in flight).  A separate pass over the Lambda tiles took 70 us of
+// 253 for 4,096 tokens and 32 heads.
 #include <cuda.h>
 
 #include "cap.cuh"
@@ -43,9 +49,11 @@ namespace {
 
 constexpr int kExpWarps = 16, kTmaWarp = 16, kQkWarp = 17, kPvWarp = 18, kThreads = 608;
 constexpr int kRegThreads = 640;                   // five warps to a sub-partition: 96 registers
-constexpr int kStages = 3;                         // K and V tiles in shared memory, S tiles in TMEM
+constexpr int kStages = 3;                         // K and V tiles in shared memory
+template <bool MIX>
+__device__ __forceinline__ constexpr int s_slots() { return MIX ? 2 : 3; }   // S tiles in TMEM
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColO = 384;
+constexpr uint32_t kColO = 384, kColOs = 256;      // Os: the Lambda attention (MIX)
 constexpr uint32_t kTileBytes = BN * HD * 2;       // 32 KB per Q, K or V tile (two 16 KB halves of d)
 constexpr uint32_t kHalfBytes = kTileBytes / 2;
 constexpr uint32_t kOffQ = 0;
@@ -53,7 +61,7 @@ constexpr uint32_t kOffK = kOffQ + kTileBytes;
 constexpr uint32_t kOffV = kOffK + kStages * kTileBytes;
 constexpr uint32_t kOffSum = kOffV + kStages * kTileBytes;   // [4][128] partial row sums
 constexpr uint32_t kOffBar = kOffSum + 4 * BM * 4;
-constexpr uint32_t kOffHolder = kOffBar + 20 * 8;
+constexpr uint32_t kOffHolder = kOffBar + 24 * 8;
 constexpr uint32_t kSmemBytes = kOffHolder + 16;
 static_assert(kSmemBytes <= 232448, "one CTA per SM");
 
@@ -90,10 +98,12 @@ __device__ __forceinline__ void unmasked_tiles(const Sched& s, int& first, int& 
 // sum of the rounded p.  POLY: tanh by its polynomial, `big` raised to the
 // largest x^2; else on the SFU.  One loop from the dot product to the packed
 // p, so that the FMA, SFU and ALU work of neighbouring pairs interleaves.
-template <bool MASKED, bool POLY>
-__device__ __forceinline__ float exp_loop(const float (&x)[32], uint32_t (&pk)[16], const CapArgs& cap, const TanhPoly& tp,
-                                          uint32_t vis, float& big) {
-    float2 sum = make_float2(0.f, 0.f);
+// LAM: the sum in .y and the packed pairs in pk[16 ..] are those of the columns
+// in `lam` (a subset of vis).
+template <bool MASKED, bool LAM, bool POLY>
+__device__ __forceinline__ float2 exp_loop(const float (&x)[32], uint32_t (&pk)[LAM ? 32 : 16], const CapArgs& cap,
+                                           const TanhPoly& tp, uint32_t vis, uint32_t lam, float& big) {
+    float2 sum = make_float2(0.f, 0.f), sum_l = sum;
     big = 0.f;
 #pragma unroll
     for (int c2 = 0; c2 < 16; ++c2) {
@@ -113,33 +123,53 @@ __device__ __forceinline__ float exp_loop(const float (&x)[32], uint32_t (&pk)[1
         __nv_bfloat162 h = __floats2bfloat162_rn(e.x, e.y);
         pk[c2] = *reinterpret_cast<uint32_t*>(&h);
         sum = fadd2(sum, make_float2(bf16_lo(pk[c2]), bf16_hi(pk[c2])));
+        if constexpr (LAM) {
+            pk[16 + c2] = ((lam >> (2 * c2)) & 1u ? pk[c2] & 0xffffu : 0u) |
+                          ((lam >> (2 * c2 + 1)) & 1u ? pk[c2] & 0xffff0000u : 0u);
+            sum_l = fadd2(sum_l, make_float2(bf16_lo(pk[16 + c2]), bf16_hi(pk[16 + c2])));
+        }
     }
-    return sum.x + sum.y;
+    return make_float2(sum.x + sum.y, sum_l.x + sum_l.y);
 }
 
-// 64 columns of a row: dot products at s_addr -> p over the first half of every 32.
-template <bool MASKED>
-__device__ __forceinline__ float exp_columns(uint32_t s_addr, const CapArgs& cap, const TanhPoly& tp, uint64_t vis) {
-    float l = 0.f;
+// 64 columns of a row: dot products at s_addr -> p over the first half of every
+// 32, and (LAM) p under the Lambda mask over the second half; the row's sums
+// are added to l.
+template <bool MASKED, bool LAM>
+__device__ __forceinline__ void exp_columns(float2& l, uint32_t s_addr, const CapArgs& cap, const TanhPoly& tp,
+                                            uint64_t vis, uint64_t lam) {
 #pragma unroll 1
-    for (int ch = 0; ch < 64 / 32; ++ch) {
+    for (int ch = 0; ch < 2; ++ch) {
         float x[32], big;
         tmem_ld32(s_addr + 32 * ch, x);
-        uint32_t pk[16];
-        float t = exp_loop<MASKED, true>(x, pk, cap, tp, (uint32_t)vis, big);
+        uint32_t pk[LAM ? 32 : 16];
+        float2 t = exp_loop<MASKED, LAM, true>(x, pk, cap, tp, (uint32_t)vis, (uint32_t)lam, big);
         if (!__all_sync(0xffffffffu, big <= tp.x2_max)) {
             tmem_ld32(s_addr + 32 * ch, x);
-            t = exp_loop<MASKED, false>(x, pk, cap, tp, (uint32_t)vis, big);
+            t = exp_loop<MASKED, LAM, false>(x, pk, cap, tp, (uint32_t)vis, (uint32_t)lam, big);
         }
-        l += t;
+        l = fadd2(l, t);
         vis >>= 32;
-        tmem_st16(s_addr + 32 * (ch / (32 / 32)) + 16 * (ch % (32 / 32)), pk);
+        lam >>= 32;
+        if constexpr (LAM)
+            tmem_st32(s_addr + 32 * ch, pk);
+        else
+            tmem_st16(s_addr + 32 * ch, pk);
     }
-    return l;
 }
 
-// EPI: EPI_STORE (store, or key-range split records), EPI_KEEP, EPI_MIX_KEEP
-// (internal.h).
+// MIX (whole sequences, no cache: tile j holds keys 128 j ..): does query tile
+// mt see keys of tile j in the Lambda attention?
+__device__ __forceinline__ bool lambda_tile(const LayerArgs& a, int mt, int j) {
+    return j * BN < a.sink || (mt - j) * BM - (BN - 1) < a.recent;
+}
+
+__device__ __forceinline__ uint64_t half_bits(const uint32_t (&v)[4], int half) {
+    return half ? ((uint64_t)v[3] << 32 | v[2]) : ((uint64_t)v[1] << 32 | v[0]);
+}
+
+// EPI: EPI_STORE (store, or key-range split records) or EPI_MIX_KEEP (both
+// attentions, mixed; every KV head in the retrieval block).
 template <int EPI>
 __global__ void __launch_bounds__(kRegThreads, 1)
     prefill_capped_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmKc,
@@ -147,6 +177,8 @@ __global__ void __launch_bounds__(kRegThreads, 1)
                           const __grid_constant__ CUtensorMap tmVx, const __grid_constant__ CUtensorMap tmKr,
                           const __grid_constant__ CUtensorMap tmVr, const TcArgs p) {
     extern __shared__ __align__(1024) uint8_t smem[];
+    constexpr bool MIX = EPI == EPI_MIX_KEEP;
+    constexpr int kSlots = s_slots<MIX>();
     const LayerArgs& a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if ((smem_u32(smem) & 1023u) != 0) {   // the swizzled layouts need 1024-byte alignment
@@ -159,10 +191,11 @@ __global__ void __launch_bounds__(kRegThreads, 1)
     uint64_t* k_empty = bars + 3;   // [kStages]
     uint64_t* v_full = bars + 6;    // [kStages]
     uint64_t* v_empty = bars + 9;   // [kStages]
-    uint64_t* s_full = bars + 12;   // [kStages]
-    uint64_t* p_full = bars + 15;   // [kStages]
-    uint64_t* q_full = bars + 18;
-    uint64_t* o_done = bars + 19;
+    uint64_t* s_full = bars + 12;   // [kSlots], as the next two
+    uint64_t* p_full = bars + 15;
+    uint64_t* s_free = bars + 18;
+    uint64_t* q_full = bars + 21;
+    uint64_t* o_done = bars + 22;
     uint32_t* holder = reinterpret_cast<uint32_t*>(smem + kOffHolder);
 
     // the work item, ordered as in prefill_tc.cu: (sequence, KV head)
@@ -217,8 +250,11 @@ __global__ void __launch_bounds__(kRegThreads, 1)
             mbar_init(&k_empty[i], 1);
             mbar_init(&v_full[i], 1);
             mbar_init(&v_empty[i], 1);
+        }
+        for (int i = 0; i < kSlots; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], kExpWarps / 2);
+            mbar_init(&s_free[i], 1);
         }
         mbar_init(q_full, 1);
         mbar_init(o_done, 1);
@@ -264,10 +300,10 @@ __global__ void __launch_bounds__(kRegThreads, 1)
         constexpr uint32_t idesc_qk = idesc_bf16(BM, BN, 0, 0);
         bool ok = mbar_wait(q_full, 0, p.status);
         for (int j = 0; j < nl && ok; ++j) {
-            const int st = j % kStages, use = j / kStages;
-            // the slot holds P(j - kStages) until its P V is done
-            if (use > 0) ok = mbar_wait(&v_empty[st], (use - 1) & 1, p.status);
-            ok = ok && mbar_wait(&k_full[st], use & 1, p.status);
+            const int st = j % kStages, sl = j % kSlots, use = j / kSlots;
+            // the slot holds P(j - kSlots) until its P V is done
+            if (use > 0) ok = mbar_wait(&s_free[sl], (use - 1) & 1, p.status);
+            ok = ok && mbar_wait(&k_full[st], (j / kStages) & 1, p.status);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
@@ -275,9 +311,9 @@ __global__ void __launch_bounds__(kRegThreads, 1)
 #pragma unroll
                 for (int kk = 0; kk < HD / 16; ++kk) {
                     const uint32_t o = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
-                    tc_mma(tmem + 128 * st, qd + o, kd + o, idesc_qk, kk > 0 ? 1u : 0u);
+                    tc_mma(tmem + 128 * sl, qd + o, kd + o, idesc_qk, kk > 0 ? 1u : 0u);
                 }
-                tc_commit(&s_full[st]);
+                tc_commit(&s_full[sl]);
                 tc_commit(&k_empty[st]);
             }
         }
@@ -285,21 +321,30 @@ __global__ void __launch_bounds__(kRegThreads, 1)
     } else if (warp == kPvWarp) {
         // O += P(j) V(j), P from TMEM: 16 packed columns at the start of every 32 of S
         constexpr uint32_t idesc_pv = idesc_bf16(BM, HD, 0, 1);
-        bool ok = true;
+        bool ok = true, first_lam = true;
         for (int j = 0; j < nl && ok; ++j) {
-            const int st = j % kStages, ph = (j / kStages) & 1;
-            ok = mbar_wait(&v_full[st], ph, p.status) && mbar_wait(&p_full[st], ph, p.status);
+            const int st = j % kStages, sl = j % kSlots;
+            ok = mbar_wait(&v_full[st], (j / kStages) & 1, p.status) && mbar_wait(&p_full[sl], (j / kSlots) & 1, p.status);
             if (!ok) break;
             tc_fence_after();
+            const bool lam = MIX && lambda_tile(a, mt, j);
             if (elect_one()) {
                 const uint64_t vd = sw128_desc(sV + st * kTileBytes, kHalfBytes, 1024);
 #pragma unroll
                 for (int kk = 0; kk < BN / 16; ++kk)
-                    tc_mma_ta(tmem + kColO, tmem + 128 * st + 32 * (kk >> 1) + 8 * (kk & 1), vd + kk * (2048 >> 4), idesc_pv,
+                    tc_mma_ta(tmem + kColO, tmem + 128 * sl + 32 * (kk >> 1) + 8 * (kk & 1), vd + kk * (2048 >> 4), idesc_pv,
                               (j > 0 || kk > 0) ? 1u : 0u);
+                if (lam) {
+#pragma unroll
+                    for (int kk = 0; kk < BN / 16; ++kk)
+                        tc_mma_ta(tmem + kColOs, tmem + 128 * sl + 32 * (kk >> 1) + 16 + 8 * (kk & 1), vd + kk * (2048 >> 4),
+                                  idesc_pv, (!first_lam || kk > 0) ? 1u : 0u);
+                }
                 tc_commit(&v_empty[st]);
+                tc_commit(&s_free[sl]);
                 if (j == nl - 1) tc_commit(o_done);
             }
+            if (lam) first_lam = false;
         }
         __syncwarp();
     } else if (warp < kExpWarps) {
@@ -307,45 +352,54 @@ __global__ void __launch_bounds__(kRegThreads, 1)
         const int row = 32 * (warp & 3) + lane;               // TMEM lane
         const int crow = BM * mt + row;                       // chunk row
         const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        float l_sum = 0.f;
+        float2 l = make_float2(0.f, 0.f);                     // row sums: causal (or the head's mask), Lambda (MIX)
         bool ok = true;
         int plain_first, plain_last;
         unmasked_tiles(sc, plain_first, plain_last);
+        Sched lam_sc = sc;                                    // the same tiles under the Lambda mask
+        lam_sc.retrieval = false;
         for (int j = group; j < nl; j += 2) {
-            const int st = j % kStages;
-            ok = __all_sync(0xffffffffu, mbar_wait(&s_full[st], (j / kStages) & 1, p.status));
+            const int sl = j % kSlots;
+            ok = __all_sync(0xffffffffu, mbar_wait(&s_full[sl], (j / kSlots) & 1, p.status));
             if (!ok) break;
             tc_fence_after();
-            const uint32_t s_addr = lane_base + 128 * st + 64 * half;
-            if (j0 + j >= plain_first && j0 + j < plain_last) {
-                l_sum += exp_columns<false>(s_addr, a.cap, p.poly, 0u);
-            } else {
+            const uint32_t s_addr = lane_base + 128 * sl + 64 * half;
+            if (MIX && lambda_tile(a, mt, j)) {
+                const Tile t = tile_at(sc, j);
+                uint32_t vis[4] = {0u, 0u, 0u, 0u}, lam[4] = {0u, 0u, 0u, 0u};
+                visible_columns(a, sc, t, crow, vis);
+                visible_columns(a, lam_sc, t, crow, lam);
+                exp_columns<true, true>(l, s_addr, a.cap, p.poly, half_bits(vis, half), half_bits(lam, half));
+            } else if (j0 + j >= plain_first && j0 + j < plain_last) {
+                exp_columns<false, false>(l, s_addr, a.cap, p.poly, 0u, 0u);
+            } else if (!MIX) {
                 uint32_t vis[4] = {0u, 0u, 0u, 0u};           // the tile's keys this row sees, a bit per column
                 visible_columns(a, sc, tile_at(sc, j0 + j), c0 + crow, vis);
-                const uint64_t v64 = half ? ((uint64_t)vis[3] << 32 | vis[2]) : ((uint64_t)vis[1] << 32 | vis[0]);
-                l_sum += exp_columns<true>(s_addr, a.cap, p.poly, v64);
+                exp_columns<true, false>(l, s_addr, a.cap, p.poly, half_bits(vis, half), 0u);
             }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[st]);
+            if (lane == 0) mbar_arrive(&p_full[sl]);
         }
         // the row's sum over both groups and column halves; each thread then
         // stores 32 columns of its row
         float* sums = reinterpret_cast<float*>(smem + kOffSum);
         const int quarter = warp >> 2;
-        sums[quarter * BM + row] = l_sum;
-        asm volatile("bar.sync 1, 512;" ::: "memory");
-        const float l_row = (sums[row] + sums[BM + row]) + (sums[2 * BM + row] + sums[3 * BM + row]);
+        auto row_total = [&](float part) {
+            sums[quarter * BM + row] = part;
+            asm volatile("bar.sync 1, 512;" ::: "memory");
+            return (sums[row] + sums[BM + row]) + (sums[2 * BM + row] + sums[3 * BM + row]);
+        };
+        const float l_row = row_total(l.x);
+        float l_lam = 0.f;
+        if constexpr (MIX) {
+            asm volatile("bar.sync 1, 512;" ::: "memory");    // everyone has read the first totals
+            l_lam = row_total(l.y);
+        }
         const size_t off = (((size_t)b * p.C + crow) * a.Hq + q_idx) * HD + 32 * quarter;
         const bool out_ok = bounds_ok(b < a.B && q_idx >= 0 && q_idx < a.Hq, p.status);
         const bool live = crow < p.C && out_ok;
-        uint4 pre[4];   // EPI_MIX_KEEP: the streaming attention of these columns, loaded before the wait below
-        if constexpr (EPI == EPI_MIX_KEEP) {
-            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.epi.streaming) + off);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) pre[i] = live ? src[i] : make_uint4(0u, 0u, 0u, 0u);
-        }
         ok = __all_sync(0xffffffffu, ok && mbar_wait(o_done, 0, p.status));
         float o[32];
         if (ok) {
@@ -355,25 +409,31 @@ __global__ void __launch_bounds__(kRegThreads, 1)
         __nv_bfloat16* op = static_cast<__nv_bfloat16*>(p.out) + off;
         if (!out_ok) {
             // debug build: the check failed, nothing is written
-        } else if (EPI != EPI_STORE || ns_use == 1) {
+        } else if (MIX || ns_use == 1) {
             if (ok) {
                 const float inv = l_row > 0.f ? 1.f / l_row : 0.f;
-                const float al = EPI == EPI_MIX_KEEP ? p.epi.alpha[kv_idx] : 0.f;
-                if (EPI != EPI_STORE && quarter == 0 && live)
-                    p.epi.lse[((size_t)b * a.Hq + q_idx) * p.C + crow] = log2f(l_row);
+                if constexpr (MIX) {
+                    // both attentions into the mix, and both log-sums kept
+                    const float al = p.epi.alpha[kv_idx];
+                    const float fc = al * inv, fs = l_lam > 0.f ? (1.f - al) / l_lam : 0.f;
+                    if (quarter == 0 && live) {
+                        const size_t r = ((size_t)b * a.Hq + q_idx) * p.C + crow;
+                        p.epi.lse[r] = log2f(l_row);
+                        p.epi.lse[(size_t)a.B * a.Hq * p.C + r] = log2f(l_lam);
+                    }
+                    float os[32];
+                    tmem_ld32(lane_base + kColOs + 32 * quarter, os);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = fmaf(fs, os[e], fc * o[e]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] *= inv;
+                }
 #pragma unroll
                 for (int q4 = 0; q4 < 4; ++q4) {
                     float v8[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v8[e] = o[8 * q4 + e] * inv;
-                    if constexpr (EPI == EPI_MIX_KEEP) {
-                        const uint32_t w[4] = {pre[q4].x, pre[q4].y, pre[q4].z, pre[q4].w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            v8[2 * e] = al * v8[2 * e] + (1.f - al) * bf16_lo(w[e]);
-                            v8[2 * e + 1] = al * v8[2 * e + 1] + (1.f - al) * bf16_hi(w[e]);
-                        }
-                    }
+                    for (int e = 0; e < 8; ++e) v8[e] = o[8 * q4 + e];
                     if (live) store_row<__nv_bfloat16, 8>(op + 8 * q4, v8);
                 }
             }
@@ -427,11 +487,8 @@ cudaError_t launch_variant(const TcMaps& m, const TcArgs& p, unsigned grid, cuda
 }  // namespace
 
 cudaError_t launch_prefill_capped(const TcMaps& m, const TcArgs& p, int mode, unsigned grid, cudaStream_t s) {
-    switch (mode) {
-        case EPI_STORE: return launch_variant<EPI_STORE>(m, p, grid, s);
-        case EPI_KEEP: return launch_variant<EPI_KEEP>(m, p, grid, s);
-        case EPI_MIX_KEEP: return launch_variant<EPI_MIX_KEEP>(m, p, grid, s);
-    }
+    if (mode == EPI_STORE) return launch_variant<EPI_STORE>(m, p, grid, s);
+    if (mode == EPI_MIX_KEEP) return launch_variant<EPI_MIX_KEEP>(m, p, grid, s);
     return cudaErrorInvalidValue;
 }
 

@@ -186,9 +186,8 @@ struct TcMaps {
     CUtensorMap q, kc, vc, kx, vx, kr, vr, sc;
 };
 
-// prefill_capped.cu takes capped scores whose exponentials need no maximum:
-// c2 = cap log2(e) at most this.
-constexpr float kBoundedC2 = 87.f;
+// prefill_capped.cu: EPI_STORE, and EPI_MIX_KEEP with both attentions in the
+// one launch (epi.streaming is not read).
 cudaError_t launch_prefill_capped(const TcMaps& m, const TcArgs& p, int mode, unsigned grid, cudaStream_t s);
 
 // ------------------------------------------------------------------ split merge

@@ -769,7 +769,7 @@ cudaError_t launch_prefill_tc(const LayerArgs& a, const CacheArgs& c, const void
     }
     const unsigned g = (unsigned)grid;
     const TcMaps mp{mQ, mKc, mVc, mKx, mVx, mKr, mVr, mS};
-    if (a.cap.on && !qs && a.cap.c2 <= kBoundedC2) return launch_prefill_capped(mp, p, mode, g, s);
+    if (cap_bounds_scores(a) && !qs) return launch_prefill_capped(mp, p, mode, g, s);
     if (a.cap.on) {
         switch (mode) {
             case EPI_STORE: return qs ? launch_variant<EPI_STORE, true, true>(mp, p, g, s)

@@ -47,6 +47,7 @@ CASES = [   # hq, hkv, d, dtype, B, N, cap, gain, sink, recent, alpha
     (8, 1, 128, "bf16", 1, 384, 5.0, 10.0, 16, 64, None),             # scores far past the cap
     (2, 2, 128, "bf16", 1, 300, 20.0, 3.0, 0, 1, [1.5, -0.75]),       # gates outside [0, 1], the smallest window
     (4, 2, 128, "bf16", 1, 1, 30.0, 3.0, 16, 64, None),
+    (4, 2, 128, "bf16", 1, 300, 200.0, 3.0, 16, 64, None),            # a cap too high for exponentials without a maximum
     (4, 2, 128, "bf16", 3, 129, 30.0, 3.0, 100, 28, None),
     (4, 4, 128, "bf16", 1, 200, 30.0, 3.0, 130, 200, None),           # a window the tensor-core kernels do not take
     (8, 4, 64, "bf16", 2, 130, 30.0, 3.0, 16, 64, None),
