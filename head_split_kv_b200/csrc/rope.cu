@@ -12,9 +12,14 @@
 // to half a turn are fp64; the sine and cosine of the reduced angle are fp32,
 // with the part of the reduced angle below its fp32 value added to first
 // order.  A token's pairs are the same for all of its heads: a CTA takes one
-// token and a range of head rows and evaluates each pair's angle once, into
-// shared memory.  Each thread first loads the row pieces it will rotate, so
-// that the reads of HBM run under the trigonometry.
+// token's head rows (or a range of them) and evaluates each pair's angle once,
+// into shared memory.  Each thread first loads the row pieces it will rotate --
+// their addresses need no length -- so that the reads of HBM run under the
+// trigonometry and the look-up of the lengths and pages.  A thread has the same
+// place in all of its rows, so it takes its cosines and sines from shared
+// memory once.  (Measured on the 4,096-token chunk, 18 us: a grid of resident
+// CTAs that walks the tokens, loading one ahead, took 23 us at 80 registers,
+// two or four tokens to a CTA the same as one.)
 //
 // A head row is cut into units of two 16-byte pieces.  Where the pairs are
 // (i, i + rot/2) a unit takes the two pieces whose elements pair up, so both
@@ -33,7 +38,7 @@ namespace duo {
 namespace {
 
 constexpr int kRopeThreads = 256;   // most threads of a CTA
-constexpr int kAhead = 2;           // units a thread loads before the angles are ready
+constexpr int kAhead = 2;           // rows a thread loads before it stores the first
 constexpr int kMaxPairs = 64;       // head_dim / 2
 
 struct RopeKernelArgs {
@@ -48,13 +53,13 @@ struct RopeKernelArgs {
     int rows_per_cta;
 };
 
-// cos and sin (times factor) of the token's pairs, by the CTA's first threads.
-__device__ __forceinline__ void token_angles(const RopeArgs& r, int b, int t, int T, int B, int p_cache,
-                                             float2* cs) {
+// cos and sin (times factor) of the pairs of token (b, t), by the CTA's threads.
+__device__ __forceinline__ void token_angles(const RopeArgs& r, const int32_t* seq_len, int b, int t, int T, int B,
+                                             float* cos_t, float* sin_t) {
     const int n_pairs = r.rot_dim >> 1;
     for (int i = threadIdx.x; i < n_pairs; i += blockDim.x) {
         const int axis = (i >= r.section_end[0]) + (i >= r.section_end[1]);
-        const int p = r.pos ? r.pos[((size_t)axis * B + b) * T + t] : p_cache;
+        const int p = r.pos ? r.pos[((size_t)axis * B + b) * T + t] : (seq_len ? seq_len[b] : 0) + t;
         constexpr double kInvTwoPi = 0.15915494309189533577;
         const double turns = (double)p * ((double)r.inv_freq[i] * kInvTwoPi);
         const double half = 2.0 * (turns - rint(turns));           // half turns in [-1, 1]
@@ -64,121 +69,118 @@ __device__ __forceinline__ void token_angles(const RopeArgs& r, int b, int t, in
         sincospif(hi, &s, &c);
         const float c2 = fmaf(-s, lo, c);
         const float s2 = fmaf(c, lo, s);
-        cs[i] = make_float2(c2 * r.factor, (r.inverse ? -s2 : s2) * r.factor);
+        cos_t[i] = c2 * r.factor;
+        sin_t[i] = (r.inverse ? -s2 : s2) * r.factor;
     }
 }
 
-__device__ __forceinline__ void rotate(float& a, float& b, float2 cs) {
+__device__ __forceinline__ void rotate(float& a, float& b, float c, float s) {
     const float x = a, y = b;
-    a = fmaf(x, cs.x, -y * cs.y);
-    b = fmaf(y, cs.x, x * cs.y);
+    a = fmaf(x, c, -y * s);
+    b = fmaf(y, c, x * s);
 }
 
-// One 16-byte piece as fp32 values and back (rounded once).
+// One 16-byte piece as fp32 pairs and back (rounded once).
 template <typename T>
 struct Piece;
 template <>
 struct Piece<__nv_bfloat16> {
     static constexpr int N = 8;
-    __device__ static __forceinline__ void unpack(const uint4& w, float (&o)[8]) {
-        o[0] = bf16_lo(w.x); o[1] = bf16_hi(w.x); o[2] = bf16_lo(w.y); o[3] = bf16_hi(w.y);
-        o[4] = bf16_lo(w.z); o[5] = bf16_hi(w.z); o[6] = bf16_lo(w.w); o[7] = bf16_hi(w.w);
+    __device__ static __forceinline__ void unpack(const uint4& w, float2 (&o)[4]) {
+        o[0] = make_float2(bf16_lo(w.x), bf16_hi(w.x));
+        o[1] = make_float2(bf16_lo(w.y), bf16_hi(w.y));
+        o[2] = make_float2(bf16_lo(w.z), bf16_hi(w.z));
+        o[3] = make_float2(bf16_lo(w.w), bf16_hi(w.w));
     }
-    __device__ static __forceinline__ uint4 pack(const float (&v)[8]) {
+    __device__ static __forceinline__ uint4 pack(const float2 (&v)[4]) {
+        const float f[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
         uint4 w;
-        store_row<__nv_bfloat16, 8>(reinterpret_cast<__nv_bfloat16*>(&w), v);
+        store_row<__nv_bfloat16, 8>(reinterpret_cast<__nv_bfloat16*>(&w), f);
         return w;
     }
 };
 template <>
 struct Piece<float> {
     static constexpr int N = 4;
-    __device__ static __forceinline__ void unpack(const uint4& w, float (&o)[4]) {
-        o[0] = __uint_as_float(w.x); o[1] = __uint_as_float(w.y); o[2] = __uint_as_float(w.z); o[3] = __uint_as_float(w.w);
+    __device__ static __forceinline__ void unpack(const uint4& w, float2 (&o)[2]) {
+        o[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+        o[1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
     }
-    __device__ static __forceinline__ uint4 pack(const float (&v)[4]) {
-        return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    __device__ static __forceinline__ uint4 pack(const float2 (&v)[2]) {
+        return make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
     }
 };
 
 // The two pieces of unit u of a row.
-struct UnitAt {
-    int p0, p1;      // piece indices
-    int pair0;       // first pair index of piece 0's elements when they pair with piece 1's; else -1
-};
 template <typename T>
-__device__ __forceinline__ UnitAt unit_at(const RopeArgs& r, bool turned, int u) {
-    const int np = (r.rot_dim >> 1) / Piece<T>::N;   // pieces of half a rotation (halves layout)
-    if (turned && r.layout == DUO_ROPE_HALVES) {
-        if (u < np) return {u, u + np, u * Piece<T>::N};
-        return {2 * u, 2 * u + 1, -1};               // 2 np + 2 (u - np)
-    }
-    return {2 * u, 2 * u + 1, -1};
+__device__ __forceinline__ void unit_pieces(const RopeArgs& r, bool turned, int u, int& p0, int& p1) {
+    const int np = (r.rot_dim >> 1) / Piece<T>::N;    // pieces of half a rotation (halves layout)
+    const bool split = turned && r.layout == DUO_ROPE_HALVES && u < np;
+    p0 = split ? u : 2 * u;                           // from 2 np on, pieces in order
+    p1 = split ? u + np : 2 * u + 1;
 }
 
+// Unit u of a row turned by its N pairs' cosines and sines (halves: pair i is
+// element i of both pieces; neighbours: piece 0 holds the first N / 2 pairs).
 template <typename T>
-__device__ __forceinline__ void turn_unit(const RopeArgs& r, const UnitAt& at, const float2* cs, uint4& w0, uint4& w1) {
+__device__ __forceinline__ void turn_unit(const RopeArgs& r, const float2 (&c)[Piece<T>::N / 2],
+                                          const float2 (&s)[Piece<T>::N / 2], uint4& w0, uint4& w1) {
     constexpr int N = Piece<T>::N;
+    float2 a[N / 2], b[N / 2];
+    Piece<T>::unpack(w0, a);
+    Piece<T>::unpack(w1, b);
     if (r.layout == DUO_ROPE_HALVES) {
-        if (at.pair0 < 0) return;
-        float a[N], b[N];
-        Piece<T>::unpack(w0, a);
-        Piece<T>::unpack(w1, b);
 #pragma unroll
-        for (int i = 0; i < N; ++i) rotate(a[i], b[i], cs[at.pair0 + i]);
-        w0 = Piece<T>::pack(a);
-        w1 = Piece<T>::pack(b);
+        for (int i = 0; i < N / 2; ++i) {
+            const float2 x = a[i], y = b[i];
+            const float2 ys = fmul2(y, s[i]);
+            a[i] = ffma2(x, c[i], make_float2(-ys.x, -ys.y));
+            b[i] = ffma2(y, c[i], fmul2(x, s[i]));
+        }
     } else {
-        const int n_pairs = r.rot_dim >> 1;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint4& w = h ? w1 : w0;
-            const int pr = (h ? at.p1 : at.p0) * (N / 2);
-            if (pr >= n_pairs) continue;
-            float x[N];
-            Piece<T>::unpack(w, x);
-#pragma unroll
-            for (int i = 0; i < N / 2; ++i)
-                if (pr + i < n_pairs) rotate(x[2 * i], x[2 * i + 1], cs[pr + i]);
-            w = Piece<T>::pack(x);
+        for (int i = 0; i < N / 4; ++i) {
+            rotate(a[2 * i].x, a[2 * i].y, c[i].x, s[i].x);
+            rotate(a[2 * i + 1].x, a[2 * i + 1].y, c[i].y, s[i].y);
+            rotate(b[2 * i].x, b[2 * i].y, c[N / 4 + i].x, s[N / 4 + i].x);
+            rotate(b[2 * i + 1].x, b[2 * i + 1].y, c[N / 4 + i].y, s[N / 4 + i].y);
         }
     }
+    w0 = Piece<T>::pack(a);
+    w1 = Piece<T>::pack(b);
 }
 
-// Where a head row goes: NULL when it is not stored.
-struct RowTarget {
-    const void* src;
-    void* dst;
-    bool turned;
-};
-
-// Head row `row` of token (b, t): rows 0 .. n_q - 1 are q's, then k's, then
-// v's.  For an append the cache row of k and v follows from the position
-// p = L + t; status bits are set by the thread that asks with `report`.
+// Head row `row` of token bt: rows 0 .. n_q - 1 are q's, then k's, then v's.
+// Where it comes from (NULL: an append of later tokens evicts it) ...
 template <typename T, bool APPEND>
-__device__ __forceinline__ RowTarget row_target(const LayerArgs& a, const CacheArgs& c, const RopeKernelArgs& x,
-                                                int b, int t, int row, int L, bool report) {
-    const size_t bt = (size_t)b * x.T + t;
-    const int D = a.D;
-    if (row < x.n_q) {
-        const size_t o = (bt * x.n_q + row) * D;
-        return {static_cast<const T*>(x.q) + o, static_cast<T*>(x.q_out) + o, true};
-    }
+__device__ __forceinline__ const T* row_src(const LayerArgs& a, const RopeKernelArgs& x, size_t bt, int t, int row,
+                                            bool& turned) {
+    turned = row < x.n_q + x.n_k;
+    if (row < x.n_q) return static_cast<const T*>(x.q) + (bt * x.n_q + row) * a.D;
+    const int kv = row - x.n_q >= x.n_k, h = row - x.n_q - (kv ? x.n_k : 0);
+    if (APPEND && a.slot_of[h] >= a.R && t >= a.sink && t < x.T - a.recent) return nullptr;
+    return static_cast<const T*>(kv ? x.v : x.k) + (bt * x.n_k + h) * a.D;
+}
+
+// ... and where it goes (NULL: not stored).  For an append the cache row of k
+// and v follows from the position p = L + t; status bits are set, and the ring
+// position is written, by the thread that asks with `report`.
+template <typename T, bool APPEND>
+__device__ __forceinline__ T* row_dst(const LayerArgs& a, const CacheArgs& c, const RopeKernelArgs& x, size_t bt, int b,
+                                      int t, int row, int L, bool report) {
+    if (row < x.n_q) return static_cast<T*>(x.q_out) + (bt * x.n_q + row) * a.D;
     const int kv = row - x.n_q >= x.n_k;              // 0: K, 1: V
     const int h = row - x.n_q - (kv ? x.n_k : 0);
     if constexpr (!APPEND) {
-        const size_t o = (bt * x.n_k + h) * D;
-        return {static_cast<const T*>(x.k) + o, static_cast<T*>(x.k_out) + o, true};
+        return static_cast<T*>(x.k_out) + (bt * x.n_k + h) * a.D;
     } else {
-        RowTarget none{nullptr, nullptr, false};
-        const T* src = static_cast<const T*>(kv ? x.v : x.k) + (bt * a.Hkv + h) * D;
         const int slot = a.slot_of[h];
-        if (!bounds_ok(slot >= 0 && slot < a.R + a.S, c.status)) return none;
+        if (!bounds_ok(slot >= 0 && slot < a.R + a.S, c.status)) return nullptr;
         const int p = L + t;
         if (slot < a.R) {
             if (p < 0 || p >= a.capacity) {
                 if (report) atomicOr(c.status, DUO_DEV_FULL_CACHE_OVERFLOW);
-                return none;
+                return nullptr;
             }
             size_t dst_row;
             if (a.page_size == 0) {
@@ -187,22 +189,21 @@ __device__ __forceinline__ RowTarget row_target(const LayerArgs& a, const CacheA
                 const int pg = c.page_table[(size_t)b * a.max_pages + p / a.page_size];
                 if (pg < 0 || pg >= a.n_pages) {
                     if (report) atomicOr(c.status, DUO_DEV_BAD_PAGE);
-                    return none;
+                    return nullptr;
                 }
                 dst_row = ((size_t)pg * a.R + slot) * a.page_size + p % a.page_size;
             }
-            return {src, static_cast<T*>(kv ? c.v_full : c.k_full) + dst_row * D, !kv};
+            return static_cast<T*>(kv ? c.v_full : c.k_full) + dst_row * a.D;
         }
         if (p < 0) {
             if (report) atomicOr(c.status, DUO_DEV_BAD_LENGTH);
-            return none;
+            return nullptr;
         }
-        if (p >= a.sink && t < x.T - a.recent) return none;   // does not survive this append
+        if (p >= a.sink && t < x.T - a.recent) return nullptr;   // does not survive this append
         const int rs = ring_slot(p, a.sink, a.recent);
-        if (!bounds_ok(rs >= 0 && rs < a.W, c.status)) return none;
+        if (!bounds_ok(rs >= 0 && rs < a.W, c.status)) return nullptr;
         if (report && !kv && slot == a.R) c.ring_pos[(size_t)b * a.W + rs] = p;
-        const size_t dst_row = ((size_t)b * a.S + (slot - a.R)) * a.W + rs;
-        return {src, static_cast<T*>(kv ? c.v_ring : c.k_ring) + dst_row * D, !kv};
+        return static_cast<T*>(kv ? c.v_ring : c.k_ring) + (((size_t)b * a.S + (slot - a.R)) * a.W + rs) * a.D;
     }
 }
 
@@ -222,65 +223,77 @@ __device__ __forceinline__ void advance_lengths(const LayerArgs& a, const CacheA
     }
 }
 
-// VEC: units of two 16-byte pieces; else one pair (or two elements) a unit.
-template <typename T, bool APPEND, bool VEC>
+// VEC: units of two 16-byte pieces, thread (unit, row) walking the rows; else
+// one pair (or two elements) a unit.
+template <typename T, int D, bool APPEND, bool VEC>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const LayerArgs a, const CacheArgs c,
                                                             const RopeKernelArgs x) {
-    __shared__ float2 cs[kMaxPairs];
-    const int bt = blockIdx.x;
-    const int b = bt / x.T, t = bt - b * x.T;
-    const int n_rows = x.n_q + x.n_k + x.n_v;
+    __shared__ __align__(16) float cos_t[kMaxPairs], sin_t[kMaxPairs];
+    const int bt = blockIdx.x, b = bt / x.T, t = bt - b * x.T;
     const int row0 = blockIdx.y * x.rows_per_cta;
-    const int rows = min(x.rows_per_cta, n_rows - row0);
-    const int L = c.seq_len ? c.seq_len[b] : 0;
+    const int row1 = min(row0 + x.rows_per_cta, x.n_q + x.n_k + x.n_v);
+    const int half = x.r.rot_dim >> 1;
     if constexpr (VEC) {
-        const int upr = a.D / (2 * Piece<T>::N);       // units per row
-        const int units = rows * upr;
-        for (int u0 = threadIdx.x; u0 - (int)threadIdx.x < units; u0 += kAhead * blockDim.x) {
-            RowTarget tg[kAhead];
-            UnitAt at[kAhead];
+        constexpr int N = Piece<T>::N, kUnits = D / (2 * N);   // units of a row
+        const int k = threadIdx.x % kUnits, step = blockDim.x / kUnits;
+        // does this thread turn anything?  (pairs past the rotation: by 1, 0)
+        const bool turns = k * N < (x.r.layout == DUO_ROPE_HALVES ? half : (half + N - 1) / N * N);
+        float2 cc[N / 2], ss[N / 2];
+        int L = 0;
+        bool ready = false;
+        // every thread of the CTA makes the first pass, for its barrier
+        for (int r = row0 + (int)threadIdx.x / kUnits; r < row1 || !ready; r += kAhead * step) {
+            const T* src[kAhead];
+            bool turned[kAhead];
+            int p0[kAhead], p1[kAhead];
             uint4 w[kAhead][2];
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
-                const int u = u0 + i * blockDim.x;
-                tg[i] = {nullptr, nullptr, false};
-                if (u < units) {
-                    const int row = u / upr, k = u - row * upr;
-                    tg[i] = row_target<T, APPEND>(a, c, x, b, t, row0 + row, L, k == 0);
-                    at[i] = unit_at<T>(x.r, tg[i].turned, k);
-                    if (tg[i].src) {
-                        w[i][0] = static_cast<const uint4*>(tg[i].src)[at[i].p0];
-                        w[i][1] = static_cast<const uint4*>(tg[i].src)[at[i].p1];
-                    }
-                }
+                const int row = r + i * step;
+                src[i] = row < row1 ? row_src<T, APPEND>(a, x, bt, t, row, turned[i]) : nullptr;
+                if (!src[i]) continue;
+                unit_pieces<T>(x.r, turned[i], k, p0[i], p1[i]);
+                w[i][0] = reinterpret_cast<const uint4*>(src[i])[p0[i]];
+                w[i][1] = reinterpret_cast<const uint4*>(src[i])[p1[i]];
             }
-            if (u0 == (int)threadIdx.x) {              // the first pass: the angles, under those loads
-                token_angles(x.r, b, t, x.T, a.B, L + t, cs);
+            if (!ready) {                              // the angles, under those loads
+                ready = true;
+                if (APPEND) L = c.seq_len[b];
+                token_angles(x.r, c.seq_len, b, t, x.T, a.B, cos_t, sin_t);
                 __syncthreads();
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) {
+                    const int pr = k * N + 2 * i;
+                    cc[i] = make_float2(pr < half ? cos_t[pr] : 1.f, pr + 1 < half ? cos_t[pr + 1] : 1.f);
+                    ss[i] = make_float2(pr < half ? sin_t[pr] : 0.f, pr + 1 < half ? sin_t[pr + 1] : 0.f);
+                }
             }
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
-                if (!tg[i].src) continue;
-                if (tg[i].turned) turn_unit<T>(x.r, at[i], cs, w[i][0], w[i][1]);
-                static_cast<uint4*>(tg[i].dst)[at[i].p0] = w[i][0];
-                static_cast<uint4*>(tg[i].dst)[at[i].p1] = w[i][1];
+                if (!src[i]) continue;
+                T* dst = row_dst<T, APPEND>(a, c, x, bt, b, t, r + i * step, L, k == 0);
+                if (!dst) continue;
+                if (turned[i] && turns) turn_unit<T>(x.r, cc, ss, w[i][0], w[i][1]);
+                reinterpret_cast<uint4*>(dst)[p0[i]] = w[i][0];
+                reinterpret_cast<uint4*>(dst)[p1[i]] = w[i][1];
             }
         }
     } else {
-        token_angles(x.r, b, t, x.T, a.B, L + t, cs);
+        const int L = APPEND ? c.seq_len[b] : 0;
+        token_angles(x.r, c.seq_len, b, t, x.T, a.B, cos_t, sin_t);
         __syncthreads();
-        const int upr = a.D / 2, half = x.r.rot_dim >> 1;
-        for (int u = threadIdx.x; u < rows * upr; u += blockDim.x) {
-            const int row = u / upr, k = u - row * upr;
-            const RowTarget tg = row_target<T, APPEND>(a, c, x, b, t, row0 + row, L, k == 0);
-            if (!tg.src) continue;
-            const bool turn = tg.turned && k < half;
-            const int e0 = turn ? k : 2 * k, e1 = turn ? k + half : 2 * k + 1;   // halves layout
-            const T* s = static_cast<const T*>(tg.src);
-            float v0 = Elem<T>::to_f32(s[e0]), v1 = Elem<T>::to_f32(s[e1]);
-            if (turn) rotate(v0, v1, cs[k]);
-            static_cast<T*>(tg.dst)[e0] = Elem<T>::from_f32(v0);
-            static_cast<T*>(tg.dst)[e1] = Elem<T>::from_f32(v1);
+        for (int u = threadIdx.x; u < (row1 - row0) * (D / 2); u += blockDim.x) {
+            const int row = row0 + u / (D / 2), k = u % (D / 2);
+            bool turned;
+            const T* src = row_src<T, APPEND>(a, x, bt, t, row, turned);
+            T* dst = src ? row_dst<T, APPEND>(a, c, x, bt, b, t, row, L, k == 0) : nullptr;
+            if (!dst) continue;
+            const bool is_pair = turned && k < half;
+            const int e0 = is_pair ? k : 2 * k, e1 = is_pair ? k + half : 2 * k + 1;   // halves layout
+            float v0 = Elem<T>::to_f32(src[e0]), v1 = Elem<T>::to_f32(src[e1]);
+            if (is_pair) rotate(v0, v1, cos_t[k], sin_t[k]);
+            dst[e0] = Elem<T>::from_f32(v0);
+            dst[e1] = Elem<T>::from_f32(v1);
         }
     }
     if constexpr (APPEND) advance_lengths(a, c, x.T);
@@ -294,7 +307,7 @@ template <int BITS>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_q_kernel(const LayerArgs a, const CacheArgs c,
                                                                      const RopeKernelArgs x) {
     using T = __nv_bfloat16;
-    __shared__ float2 cs[kMaxPairs];
+    __shared__ float cos_t[kMaxPairs], sin_t[kMaxPairs];
     const int bt = blockIdx.x;
     const int b = bt / x.T, t = bt - b * x.T;
     const int n_rows = x.n_q + x.n_k + x.n_v;
@@ -302,7 +315,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_q_kernel(const Layer
     const int rows = min(x.rows_per_cta, n_rows - row0);
     const int L = c.seq_len[b];
     const int lane = threadIdx.x & 31;
-    token_angles(x.r, b, t, x.T, a.B, L + t, cs);
+    token_angles(x.r, c.seq_len, b, t, x.T, a.B, cos_t, sin_t);
     __syncthreads();
     const int half = x.r.rot_dim >> 1;
     for (int row = threadIdx.x >> 5; row < rows; row += blockDim.x >> 5) {
@@ -326,9 +339,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_q_kernel(const Layer
                     continue;
                 }
             } else {
-                const RowTarget tg = row_target<T, true>(a, c, x, b, t, rr, L, lane == 0);
-                if (!tg.dst) continue;
-                dst = static_cast<T*>(tg.dst);
+                dst = row_dst<T, true>(a, c, x, bt, b, t, rr, L, lane == 0);
+                if (!dst) continue;
             }
         }
         const uint2 w = reinterpret_cast<const uint2*>(src)[lane];
@@ -337,7 +349,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_q_kernel(const Layer
             if (x.r.layout == DUO_ROPE_PAIRS) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                    if (2 * lane + i < half) rotate(e[2 * i], e[2 * i + 1], cs[2 * lane + i]);
+                    if (2 * lane + i < half) rotate(e[2 * i], e[2 * i + 1], cos_t[2 * lane + i], sin_t[2 * lane + i]);
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -346,7 +358,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_q_kernel(const Layer
                         const int k = f < half ? f : f - half;
                         float lo = f < half ? e[i] : __bfloat162float(src[k]);
                         float hi = f < half ? __bfloat162float(src[k + half]) : e[i];
-                        rotate(lo, hi, cs[k]);
+                        rotate(lo, hi, cos_t[k], sin_t[k]);
                         e[i] = f < half ? lo : hi;
                     }
                 }
@@ -373,39 +385,36 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_q_kernel(const Layer
     advance_lengths(a, c, x.T);
 }
 
-// Head rows a CTA takes: as many as its threads hold in kAhead units each,
-// fewer when the tokens alone do not fill the SMs (a decode step).
-int rows_per_cta(int tokens, int n_rows, int units_per_row, int* threads) {
-    int rows = kAhead * kRopeThreads / units_per_row;
-    if (rows > n_rows) rows = n_rows;
-    const int fill = 2 * sm_count();
-    while (rows > 8 && (long)tokens * ((n_rows + rows - 1) / rows) < fill) rows = (rows + 1) / 2;
-    // even shares
-    const int parts = (n_rows + rows - 1) / rows;
-    rows = (n_rows + parts - 1) / parts;
-    int th = (rows * units_per_row + kAhead - 1) / kAhead;
-    th = (th + 31) / 32 * 32;
-    if (th < 64) th = 64;
-    if (th > kRopeThreads) th = kRopeThreads;
-    *threads = th;
-    return rows;
-}
-
-template <typename T, bool APPEND>
+template <typename T, int D, bool APPEND>
 cudaError_t launch_t(const LayerArgs& a, const CacheArgs& c, RopeKernelArgs x, cudaStream_t s) {
     const int n_rows = x.n_q + x.n_k + x.n_v;
     const long tokens = (long)a.B * x.T;
     if (tokens > 0x7fffffffL) return cudaErrorInvalidConfiguration;
-    constexpr int N = Piece<T>::N;
+    constexpr int N = Piece<T>::N, kUnits = D / (2 * N);
     const bool vec = x.r.layout == DUO_ROPE_PAIRS || (x.r.rot_dim / 2) % N == 0;
-    int threads;
-    x.rows_per_cta = rows_per_cta((int)tokens, n_rows, a.D / (2 * N), &threads);
-    const dim3 grid((unsigned)tokens, (unsigned)((n_rows + x.rows_per_cta - 1) / x.rows_per_cta));
+    // a CTA's rows: as many as its threads hold in kAhead units each, fewer
+    // when the tokens alone do not fill the SMs (a decode step)
+    const int room = kAhead * kRopeThreads / kUnits;
+    int rows = room < n_rows ? room : n_rows;
+    while (rows > 8 && tokens * ((n_rows + rows - 1) / rows) < 2L * sm_count()) rows = (rows + 1) / 2;
+    const int parts = (n_rows + rows - 1) / rows;
+    x.rows_per_cta = (n_rows + parts - 1) / parts;    // even shares
+    int threads = (x.rows_per_cta * kUnits + kAhead - 1) / kAhead;
+    threads = (threads + 31) / 32 * 32;               // whole units of a row: kUnits divides 32
+    if (threads < 64) threads = 64;
+    const dim3 grid((unsigned)tokens, (unsigned)parts);
     if (vec)
-        rope_kernel<T, APPEND, true><<<grid, threads, 0, s>>>(a, c, x);
+        rope_kernel<T, D, APPEND, true><<<grid, threads, 0, s>>>(a, c, x);
     else
-        rope_kernel<T, APPEND, false><<<grid, threads, 0, s>>>(a, c, x);
+        rope_kernel<T, D, APPEND, false><<<grid, threads, 0, s>>>(a, c, x);
     return cudaGetLastError();
+}
+
+template <bool APPEND>
+cudaError_t launch(const LayerArgs& a, const CacheArgs& c, const RopeKernelArgs& x, cudaStream_t s) {
+    if (a.dtype == DUO_BF16)
+        return a.D == 128 ? launch_t<__nv_bfloat16, 128, APPEND>(a, c, x, s) : launch_t<__nv_bfloat16, 64, APPEND>(a, c, x, s);
+    return a.D == 128 ? launch_t<float, 128, APPEND>(a, c, x, s) : launch_t<float, 64, APPEND>(a, c, x, s);
 }
 
 }  // namespace
@@ -414,8 +423,7 @@ cudaError_t launch_rope(const LayerArgs& a, const int32_t* seq_len, const RopeAr
                         void* q_out, void* k_out, int T, cudaStream_t s) {
     CacheArgs c{};
     c.seq_len = const_cast<int32_t*>(seq_len);
-    RopeKernelArgs x{r, q, k, nullptr, q_out, k_out, T, q ? a.Hq : 0, k ? a.Hkv : 0, 0, 0};
-    return a.dtype == DUO_BF16 ? launch_t<__nv_bfloat16, false>(a, c, x, s) : launch_t<float, false>(a, c, x, s);
+    return launch<false>(a, c, RopeKernelArgs{r, q, k, nullptr, q_out, k_out, T, q ? a.Hq : 0, k ? a.Hkv : 0, 0, 0}, s);
 }
 
 cudaError_t launch_append_rope(const LayerArgs& a, const CacheArgs& c, const RopeArgs& r, const void* q,
@@ -425,8 +433,10 @@ cudaError_t launch_append_rope(const LayerArgs& a, const CacheArgs& c, const Rop
         const int n_rows = x.n_q + 2 * a.Hkv;
         const long tokens = (long)a.B * T;
         if (tokens > 0x7fffffffL) return cudaErrorInvalidConfiguration;
-        int threads;
-        x.rows_per_cta = rows_per_cta((int)tokens, n_rows, 8, &threads);
+        // one warp a row, a token's rows spread over CTAs until the SMs are filled
+        x.rows_per_cta = n_rows;
+        while (x.rows_per_cta > 8 && tokens * ((n_rows + x.rows_per_cta - 1) / x.rows_per_cta) < 2L * sm_count())
+            x.rows_per_cta = (x.rows_per_cta + 1) / 2;
         const dim3 grid((unsigned)tokens, (unsigned)((n_rows + x.rows_per_cta - 1) / x.rows_per_cta));
         if (a.kv_bits == 8)
             rope_append_q_kernel<8><<<grid, kRopeThreads, 0, s>>>(a, c, x);
@@ -434,7 +444,7 @@ cudaError_t launch_append_rope(const LayerArgs& a, const CacheArgs& c, const Rop
             rope_append_q_kernel<4><<<grid, kRopeThreads, 0, s>>>(a, c, x);
         return cudaGetLastError();
     }
-    return a.dtype == DUO_BF16 ? launch_t<__nv_bfloat16, true>(a, c, x, s) : launch_t<float, true>(a, c, x, s);
+    return launch<true>(a, c, x, s);
 }
 
 }  // namespace duo

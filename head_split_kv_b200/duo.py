@@ -148,10 +148,21 @@ def _ptr(x) -> int:
     return int(x.data_ptr())
 
 
+_raw_stream = None
+
+
 def _stream(s) -> int:
     if s is None:
-        import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        # torch's current stream, as the raw handle: building the Stream object
+        # costs 3 us of host time, as much as a whole call of this binding
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
+            if not hasattr(torch._C, "_cuda_getCurrentRawStream"):
+                return int(torch.cuda.current_stream().cuda_stream)
+            torch.cuda.init()
+            _raw_stream = (torch._C._cuda_getCurrentRawStream, torch.cuda.current_device)
+        return _raw_stream[0](_raw_stream[1]())
     if isinstance(s, int):
         return s
     return int(s.cuda_stream)
