@@ -3,13 +3,17 @@
 // capped pre-fill, and the gated mix's training forward and backward passes.
 // All arithmetic is fp32 (CUDA's exp2f and tanhf).
 //
-// 256 threads as 16 x 16; every product is a register tile of 4 x 4 scores
-// (or 4 rows x D / 16 columns) per thread, operands in shared memory as fp32
-// rows padded by four floats, so that 16 threads reading 16 rows use all
-// banks.  A thread's rows are 4 ty .. 4 ty + 3, the same for scores and
-// accumulators, so a row's softmax state stays in the 16 threads of one
-// half-warp (shuffles, no shared memory); its score columns are tx + 16 j.
-// Probabilities pass between the products through shared memory, transposed.
+// 256 threads as 16 x 16; every product is a register tile of RI x 4 scores
+// (or RI rows x D / 16 columns) per thread, RI = 4 (tiles of 64 outer rows) or
+// 2 (32 outer rows: twice the CTAs, for grids that would leave SMs idle).
+// Operands lie in shared memory as fp32 rows padded by four floats, so that 16
+// threads reading 16 rows use all banks.  A thread's rows are RI ty .., the
+// same for scores and accumulators, so a row's softmax state stays in the 16
+// threads of one half-warp (shuffles, no shared memory); its score columns are
+// tx + 16 j.  Probabilities pass between the products through shared memory,
+// transposed.  The next tile's rows are loaded into registers while the
+// current one is computed (rows of 512 bytes, fp32 with d 128, would take too
+// many and are not).
 // Bound by the fp32 FMA pipe and, for short sequences, by latency.
 #include "cap.cuh"
 #include "common.cuh"
@@ -19,68 +23,86 @@
 namespace duo {
 namespace {
 
-constexpr int TT = 64;              // rows of a tile
+constexpr int TT = 64;              // rows of an inner tile
 constexpr int kTiledThreads = 256;
-constexpr int PS = TT + 4;          // row stride of the transposed probabilities
 
 template <int D>
 __host__ __device__ constexpr int row_stride() { return D + 4; }
 template <int D>
-__host__ __device__ constexpr size_t tile_floats() { return (size_t)TT * row_stride<D>(); }
+__host__ __device__ constexpr size_t tile_floats(int rows) { return (size_t)rows * row_stride<D>(); }
+template <int RI>
+__host__ __device__ constexpr int p_stride() { return 16 * RI + 4; }   // of the transposed probabilities
 
-// 64 rows of D elements into shared memory as fp32; rows where src(r) is NULL are zero.
-template <typename T, int D, typename F>
-__device__ __forceinline__ void load_tile(float* dst, F src) {
-    constexpr int N = 16 / (int)sizeof(T), PPR = D / N;   // elements of a 16-byte piece, pieces per row
+// ROWS rows of D elements on their way from global memory to shared memory as
+// fp32: fetch (rows where src(r) is NULL are zero), then store.
+template <typename T, int D, int ROWS>
+struct Rows {
+    static constexpr int N = 16 / (int)sizeof(T), PPR = D / N;   // elements of a 16-byte piece, pieces per row
+    static constexpr int kPer = ROWS * PPR / kTiledThreads;
+    uint4 w[kPer];
+    template <typename F>
+    __device__ __forceinline__ void fetch(F src) {
 #pragma unroll
-    for (int k = 0; k < TT * PPR / kTiledThreads; ++k) {
-        const int i = threadIdx.x + k * kTiledThreads, r = i / PPR, c = i % PPR * N;
-        const T* p = src(r);
-        float v[N];
-        if (p) load_row_f32<T, N>(p + c, v);
-        else
-#pragma unroll
-            for (int e = 0; e < N; ++e) v[e] = 0.f;
-#pragma unroll
-        for (int e = 0; e < N; e += 4)
-            *reinterpret_cast<float4*>(dst + r * row_stride<D>() + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        for (int k = 0; k < kPer; ++k) {
+            const int i = threadIdx.x + k * kTiledThreads;
+            const T* p = src(i / PPR);
+            w[k] = p ? reinterpret_cast<const uint4*>(p)[i % PPR] : make_uint4(0u, 0u, 0u, 0u);
+        }
     }
-}
-
-// s[i][j] = X row (4 ty + i) . Y row (tx + 16 j)
-template <int D>
-__device__ __forceinline__ void tile_dot(const float* x, const float* y, int tx, int ty, float (&s)[4][4]) {
+    __device__ __forceinline__ void store(float* dst) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+        for (int k = 0; k < kPer; ++k) {
+            const int i = threadIdx.x + k * kTiledThreads, r = i / PPR, c = i % PPR * N;
+            float v[N];
+            load_row_f32<T, N>(reinterpret_cast<const T*>(&w[k]), v);
+#pragma unroll
+            for (int e = 0; e < N; e += 4)
+                *reinterpret_cast<float4*>(dst + r * row_stride<D>() + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        }
+    }
+};
+template <typename T, int D>
+__host__ __device__ constexpr bool prefetches() { return D * sizeof(T) < 512; }
+
+// s[i][j] = X row (RI ty + i) . Y row (tx + 16 j)
+template <int D, int RI>
+__device__ __forceinline__ void tile_dot(const float* x, const float* y, int tx, int ty, float (&s)[RI][4]) {
+#pragma unroll
+    for (int i = 0; i < RI; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
 #pragma unroll 4
     for (int e = 0; e < D; e += 4) {
-        float4 a[4], b[4];
+        float4 a[RI], b[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(x + (4 * ty + i) * row_stride<D>() + e);
+        for (int i = 0; i < RI; ++i) a[i] = *reinterpret_cast<const float4*>(x + (RI * ty + i) * row_stride<D>() + e);
 #pragma unroll
         for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(y + (tx + 16 * j) * row_stride<D>() + e);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < RI; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 s[i][j] = fmaf(a[i].x, b[j].x, fmaf(a[i].y, b[j].y, fmaf(a[i].z, b[j].z, fmaf(a[i].w, b[j].w, s[i][j]))));
     }
 }
 
-// acc[i][:] += sum over the tile's 64 inner rows k of pt[k][4 ty + i] * y[k][columns 4 tx + 64 j ..]
-template <int D>
-__device__ __forceinline__ void tile_acc(const float* pt, const float* y, int tx, int ty, float (&acc)[4][D / 16]) {
+// acc[i][:] += sum over the tile's 64 inner rows k of pt[k][RI ty + i] * y[k][columns 4 tx + 64 j ..]
+template <int D, int RI>
+__device__ __forceinline__ void tile_acc(const float* pt, const float* y, int tx, int ty, float (&acc)[RI][D / 16]) {
 #pragma unroll 4
     for (int k = 0; k < TT; ++k) {
-        const float4 p = *reinterpret_cast<const float4*>(pt + k * PS + 4 * ty);
+        float pr[RI];
+#pragma unroll
+        for (int i = 0; i < RI; i += 2) {
+            const float2 p = *reinterpret_cast<const float2*>(pt + k * p_stride<RI>() + RI * ty + i);
+            pr[i] = p.x;
+            pr[i + 1] = p.y;
+        }
 #pragma unroll
         for (int j = 0; j < D / 64; ++j) {
             const float4 v = *reinterpret_cast<const float4*>(y + k * row_stride<D>() + 4 * tx + 64 * j);
-            const float pr[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < RI; ++i) {
                 acc[i][4 * j] = fmaf(pr[i], v.x, acc[i][4 * j]);
                 acc[i][4 * j + 1] = fmaf(pr[i], v.y, acc[i][4 * j + 1]);
                 acc[i][4 * j + 2] = fmaf(pr[i], v.z, acc[i][4 * j + 2]);
@@ -90,11 +112,14 @@ __device__ __forceinline__ void tile_acc(const float* pt, const float* y, int tx
     }
 }
 
-// pt[tx + 16 j][4 ty .. + 3] = p[..][j]
-__device__ __forceinline__ void put_transposed(float* pt, const float (&p)[4][4], int tx, int ty) {
+// pt[tx + 16 j][RI ty ..] = p[..][j]
+template <int RI>
+__device__ __forceinline__ void put_transposed(float* pt, const float (&p)[RI][4], int tx, int ty) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<float4*>(pt + (tx + 16 * j) * PS + 4 * ty) = make_float4(p[0][j], p[1][j], p[2][j], p[3][j]);
+#pragma unroll
+        for (int i = 0; i < RI; i += 2)
+            *reinterpret_cast<float2*>(pt + (tx + 16 * j) * p_stride<RI>() + RI * ty + i) = make_float2(p[i][j], p[i + 1][j]);
 }
 
 // Over the 16 threads that hold a row's columns.
@@ -111,10 +136,10 @@ __device__ __forceinline__ float row_sum(float v) {
 
 // One online-softmax step of a row group: x (log2-domain scores, -inf where
 // unseen) becomes p; m, l and acc are brought to the new maximum.
-template <int W>
-__device__ __forceinline__ void softmax_step(float (&x)[4][4], float (&m)[4], float (&l)[4], float (&acc)[4][W]) {
+template <int RI, int W>
+__device__ __forceinline__ void softmax_step(float (&x)[RI][4], float (&m)[RI], float (&l)[RI], float (&acc)[RI][W]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RI; ++i) {
         const float mn = fmaxf(m[i], row_max(fmaxf(fmaxf(x[i][0], x[i][1]), fmaxf(x[i][2], x[i][3]))));
         const float corr = exp2f(m[i] - mn);
         float sum = 0.f;
@@ -144,26 +169,28 @@ struct TiledArgs {
     float* lse;            // mix: [2][B][Hq][N]
 };
 
-template <int D, bool MIX>
+template <int D, bool MIX, int RI>
 constexpr size_t forward_smem() {
-    return (3 * tile_floats<D>() + (MIX ? 2 : 1) * (size_t)TT * PS) * sizeof(float) + TT * sizeof(int);
+    return (tile_floats<D>(16 * RI) + 2 * tile_floats<D>(TT) + (MIX ? 2 : 1) * (size_t)TT * p_stride<RI>()) * sizeof(float) +
+           TT * sizeof(int);
 }
 
-template <typename T, int D, bool MIX, bool CAP>
+template <typename T, int D, bool MIX, bool CAP, int RI>
 __global__ void __launch_bounds__(kTiledThreads) tiled_forward_kernel(const LayerArgs a, const CacheArgs c,
                                                                       const TiledArgs s) {
     extern __shared__ __align__(16) float sm[];
+    constexpr int OT = 16 * RI, PS = p_stride<RI>();   // query rows of the CTA
     float* sQ = sm;
-    float* sK = sQ + tile_floats<D>();
-    float* sV = sK + tile_floats<D>();
-    float* sP = sV + tile_floats<D>();
+    float* sK = sQ + tile_floats<D>(OT);
+    float* sV = sK + tile_floats<D>(TT);
+    float* sP = sV + tile_floats<D>(TT);
     float* sP2 = sP + TT * PS;                        // mix only
     int* sPos = reinterpret_cast<int*>(sP + (MIX ? 2 : 1) * TT * PS);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int b = blockIdx.z, slot = blockIdx.y / a.G, g = blockIdx.y % a.G;
     const int q_idx = a.q_head0[slot] + g, kv_idx = a.kv_head[slot];
     if (!bounds_ok(b < a.B && q_idx >= 0 && q_idx < a.Hq && kv_idx >= 0 && kv_idx < a.Hkv, c.status)) return;
-    const int r0 = (gridDim.x - 1 - blockIdx.x) * TT;  // the longest rows first
+    const int r0 = (gridDim.x - 1 - blockIdx.x) * OT;  // the longest rows first
     const int N = s.N;
     const bool retrieval = MIX || slot < a.R;
     int c0 = 0;
@@ -174,13 +201,17 @@ __global__ void __launch_bounds__(kTiledThreads) tiled_forward_kernel(const Laye
             c0 = c0 < 0 ? 0 : a.capacity;
         }
     }
-    load_tile<T, D>(sQ, [&](int r) {
-        return r0 + r < N ? static_cast<const T*>(s.q) + (((size_t)b * N + r0 + r) * a.Hq + q_idx) * D : nullptr;
-    });
+    {
+        Rows<T, D, OT> q;
+        q.fetch([&](int r) -> const T* {
+            return r0 + r < N ? static_cast<const T*>(s.q) + (((size_t)b * N + r0 + r) * a.Hq + q_idx) * D : nullptr;
+        });
+        q.store(sQ);
+    }
     constexpr int W = D / 16;
-    float o[4][W], o2[MIX ? 4 : 1][W], m[4], l[4], m2[4], l2[4];
+    float o[RI][W], o2[MIX ? RI : 1][W], m[RI], l[RI], m2[RI], l2[RI];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RI; ++i) {
         m[i] = m2[i] = kNegBig;
         l[i] = l2[i] = 0.f;
 #pragma unroll
@@ -188,12 +219,12 @@ __global__ void __launch_bounds__(kTiledThreads) tiled_forward_kernel(const Laye
     }
     if constexpr (MIX) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < RI; ++i)
 #pragma unroll
             for (int e = 0; e < W; ++e) o2[i][e] = 0.f;
     }
     const float sl = a.scale * kLog2e;
-    const int last = min(N, r0 + TT);                 // chunk rows some query of this tile sees
+    const int last = min(N, r0 + OT);                 // chunk rows some query of this tile sees
     // key segments: 0 = prior keys from the caches, 1 and 2 = chunk rows
     int begin[3] = {0, 0, 0}, end[3] = {0, last, 0};
     if constexpr (!MIX) {
@@ -204,70 +235,96 @@ __global__ void __launch_bounds__(kTiledThreads) tiled_forward_kernel(const Laye
             end[2] = last;
         }
     }
-    for (int seg = 0; seg < 3; ++seg) {
-        for (int k0 = begin[seg]; k0 < end[seg]; k0 += TT) {
-            const int nk = min(TT, end[seg] - k0);
-            __syncthreads();
-            auto row = [&](int r, const void* full, const void* ring, const void* chunk) -> const T* {
-                if (r >= nk) return nullptr;
-                const int kr = k0 + r;
-                if (MIX || seg > 0) return static_cast<const T*>(chunk) + (((size_t)b * N + kr) * a.Hkv + kv_idx) * D;
-                if (retrieval) return static_cast<const T*>(full) + (((size_t)b * a.R + slot) * a.capacity + kr) * D;
-                const int pos = c.ring_pos[(size_t)b * a.W + kr];
-                if (pos < 0 || pos >= c0) return nullptr;
-                return static_cast<const T*>(ring) + (((size_t)b * a.S + (slot - a.R)) * a.W + kr) * D;
-            };
-            load_tile<T, D>(sK, [&](int r) { return row(r, c.k_full, c.k_ring, s.k); });
-            load_tile<T, D>(sV, [&](int r) { return row(r, c.v_full, c.v_ring, s.v); });
-            if (threadIdx.x < TT) {
-                const int r = threadIdx.x;
-                int pos = -1;
-                if (r < nk) {
-                    pos = MIX || seg > 0 ? c0 + k0 + r : retrieval ? k0 + r : c.ring_pos[(size_t)b * a.W + k0 + r];
-                    if (!MIX && seg == 0 && pos >= c0) pos = -1;   // only tokens before the chunk come from the caches
-                }
-                sPos[r] = pos;
+    // the tiles in their order: the first, and the one after (seg, k0)
+    int seg = -1, k0 = 0;
+    auto step = [&](int& sg, int& k) {
+        if (sg >= 0 && k + TT < end[sg]) {
+            k += TT;
+            return true;
+        }
+        while (++sg < 3)
+            if (begin[sg] < end[sg]) {
+                k = begin[sg];
+                return true;
             }
-            __syncthreads();
-            float x[4][4], x2[4][4];
-            tile_dot<D>(sQ, sK, tx, ty, x);
-            // the tile's keys are before the band of every row: no Lambda state (mix)
-            const bool lam_tile = MIX && (k0 < a.sink || r0 - (k0 + TT - 1) < a.recent);
+        return false;
+    };
+    Rows<T, D, TT> nk_, nv_;
+    auto fetch = [&](int sg, int k) {
+        const int n = min(TT, end[sg] - k);
+        auto row = [&](int r, const void* full, const void* ring, const void* chunk) -> const T* {
+            if (r >= n) return nullptr;
+            const int kr = k + r;
+            if (MIX || sg > 0) return static_cast<const T*>(chunk) + (((size_t)b * N + kr) * a.Hkv + kv_idx) * D;
+            if (retrieval) return static_cast<const T*>(full) + (((size_t)b * a.R + slot) * a.capacity + kr) * D;
+            const int pos = c.ring_pos[(size_t)b * a.W + kr];
+            if (pos < 0 || pos >= c0) return nullptr;
+            return static_cast<const T*>(ring) + (((size_t)b * a.S + (slot - a.R)) * a.W + kr) * D;
+        };
+        nk_.fetch([&](int r) { return row(r, c.k_full, c.k_ring, s.k); });
+        nv_.fetch([&](int r) { return row(r, c.v_full, c.v_ring, s.v); });
+    };
+    bool more = step(seg, k0);
+    if (prefetches<T, D>() && more) fetch(seg, k0);
+    while (more) {
+        const int nk = min(TT, end[seg] - k0);
+        __syncthreads();
+        if (!prefetches<T, D>()) fetch(seg, k0);
+        nk_.store(sK);
+        nv_.store(sV);
+        if (threadIdx.x < TT) {
+            const int r = threadIdx.x;
+            int pos = -1;
+            if (r < nk) {
+                pos = MIX || seg > 0 ? c0 + k0 + r : retrieval ? k0 + r : c.ring_pos[(size_t)b * a.W + k0 + r];
+                if (!MIX && seg == 0 && pos >= c0) pos = -1;   // only tokens before the chunk come from the caches
+            }
+            sPos[r] = pos;
+        }
+        __syncthreads();
+        int seg1 = seg, k1 = k0;
+        more = step(seg1, k1);
+        if (prefetches<T, D>() && more) fetch(seg1, k1);
+        float x[RI][4], x2[RI][4];
+        tile_dot<D, RI>(sQ, sK, tx, ty, x);
+        // the tile's keys are before the band of every row: no Lambda state (mix)
+        const bool lam_tile = MIX && (k0 < a.sink || r0 - (k0 + TT - 1) < a.recent);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int pos = sPos[tx + 16 * j];
+        for (int j = 0; j < 4; ++j) {
+            const int pos = sPos[tx + 16 * j];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int P = c0 + r0 + 4 * ty + i;
-                    const bool causal = pos >= 0 && pos <= P;
-                    const bool lam = causal && (pos < a.sink || (!MIX && a.stream_chunk ? pos >= c0 - a.recent
-                                                                                       : P - pos < a.recent));
-                    const float sc = score_log2<CAP, true>(x[i][j], sl, a.cap);
-                    x[i][j] = (MIX || retrieval ? causal : lam) ? sc : -INFINITY;
-                    x2[i][j] = lam ? sc : -INFINITY;
-                }
-            }
-            softmax_step<W>(x, m, l, o);
-            put_transposed(sP, x, tx, ty);
-            if constexpr (MIX) {
-                if (lam_tile) {
-                    softmax_step<W>(x2, m2, l2, o2);
-                    put_transposed(sP2, x2, tx, ty);
-                }
-            }
-            __syncthreads();
-            tile_acc<D>(sP, sV, tx, ty, o);
-            if constexpr (MIX) {
-                if (lam_tile) tile_acc<D>(sP2, sV, tx, ty, o2);
+            for (int i = 0; i < RI; ++i) {
+                const int P = c0 + r0 + RI * ty + i;
+                const bool causal = pos >= 0 && pos <= P;
+                const bool lam = causal && (pos < a.sink || (!MIX && a.stream_chunk ? pos >= c0 - a.recent
+                                                                                   : P - pos < a.recent));
+                const float sc = score_log2<CAP, true>(x[i][j], sl, a.cap);
+                x[i][j] = (MIX || retrieval ? causal : lam) ? sc : -INFINITY;
+                x2[i][j] = lam ? sc : -INFINITY;
             }
         }
+        softmax_step<RI, W>(x, m, l, o);
+        put_transposed<RI>(sP, x, tx, ty);
+        if constexpr (MIX) {
+            if (lam_tile) {
+                softmax_step<RI, W>(x2, m2, l2, o2);
+                put_transposed<RI>(sP2, x2, tx, ty);
+            }
+        }
+        __syncthreads();
+        tile_acc<D, RI>(sP, sV, tx, ty, o);
+        if constexpr (MIX) {
+            if (lam_tile) tile_acc<D, RI>(sP2, sV, tx, ty, o2);
+        }
+        seg = seg1;
+        k0 = k1;
     }
     const float al = MIX ? s.alpha[kv_idx] : 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RI; ++i) {
         const float ls = row_sum(l[i]), inv = ls > 0.f ? 1.f / ls : 0.f;
         const float ls2 = MIX ? row_sum(l2[i]) : 0.f, inv2 = ls2 > 0.f ? 1.f / ls2 : 0.f;
-        const int r = r0 + 4 * ty + i;
+        const int r = r0 + RI * ty + i;
         if (r >= N) continue;
         const size_t off = (((size_t)b * N + r) * a.Hq + q_idx) * D + 4 * tx;
         if (MIX && tx == 0) {
@@ -387,52 +444,54 @@ struct TiledGradArgs {
     int N, n_pad;
 };
 
-template <int D, bool KEYS>
+template <int D, bool KEYS, int RI>
 constexpr size_t grad_smem() {
-    return (4 * tile_floats<D>() + (KEYS ? 2 : 1) * (size_t)TT * PS + 4 * TT) * sizeof(float);
+    return (2 * tile_floats<D>(16 * RI) + 2 * tile_floats<D>(TT) + (KEYS ? 2 : 1) * (size_t)TT * p_stride<RI>() + 4 * TT) *
+           sizeof(float);
 }
 
-template <typename T, int D, bool KEYS, bool CAP>
+template <typename T, int D, bool KEYS, bool CAP, int RI>
 __global__ void __launch_bounds__(kTiledThreads) tiled_grad_kernel(const LayerArgs a, const TiledGradArgs p) {
     extern __shared__ __align__(16) float sm[];
+    constexpr int OT = 16 * RI, PS = p_stride<RI>();   // outer rows of the CTA
     float* sX0 = sm;
-    float* sX1 = sX0 + tile_floats<D>();
-    float* sY0 = sX1 + tile_floats<D>();
-    float* sY1 = sY0 + tile_floats<D>();
-    float* sStat = sY1 + tile_floats<D>();            // [4][TT] of the tile's queries
+    float* sX1 = sX0 + tile_floats<D>(OT);
+    float* sY0 = sX1 + tile_floats<D>(OT);
+    float* sY1 = sY0 + tile_floats<D>(TT);
+    float* sStat = sY1 + tile_floats<D>(TT);          // [4][TT] of the tile's queries
     float* sG = sStat + 4 * TT;                       // dS, transposed
     float* sW = sG + TT * PS;                         // W, transposed (keys outer)
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int b = blockIdx.z, head = blockIdx.y, N = p.N;
     const int heads = KEYS ? a.Hkv : a.Hq, kv = KEYS ? head : head / a.G;
-    const int nt = (N + TT - 1) / TT;
-    const int ot = KEYS ? blockIdx.x : nt - 1 - blockIdx.x;   // the longest first
-    auto rows = [&](const void* base, int H, int h, int tile) {
+    const int ot = KEYS ? blockIdx.x : gridDim.x - 1 - blockIdx.x;   // the longest first
+    const int o0 = ot * OT, n_it = (N + TT - 1) / TT;                // first outer row; inner tiles of the sequence
+    auto rows = [&](const void* base, int H, int h, int first) {
         return [=](int r) -> const T* {
-            const int i = tile * TT + r;
+            const int i = first + r;
             return i < N ? static_cast<const T*>(base) + (((size_t)b * N + i) * H + h) * D : nullptr;
         };
     };
-    auto load_stats = [&](int qh, int tile) {
-        if (threadIdx.x < TT) {
+    auto load_stats = [&](int qh, int first, int n) {
+        if (threadIdx.x < n) {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 sStat[r * TT + threadIdx.x] =
-                    p.stats[(((size_t)b * a.Hq + qh) * 4 + r) * p.n_pad + tile * TT + threadIdx.x];
+                    p.stats[(((size_t)b * a.Hq + qh) * 4 + r) * p.n_pad + first + threadIdx.x];
         }
     };
-    if constexpr (KEYS) {
-        load_tile<T, D>(sX0, rows(p.k, a.Hkv, kv, ot));
-        load_tile<T, D>(sX1, rows(p.v, a.Hkv, kv, ot));
-    } else {
-        load_tile<T, D>(sX0, rows(p.q, a.Hq, head, ot));
-        load_tile<T, D>(sX1, rows(p.dout, a.Hq, head, ot));
-        load_stats(head, ot);
+    {
+        Rows<T, D, OT> x0, x1;
+        x0.fetch(KEYS ? rows(p.k, a.Hkv, kv, o0) : rows(p.q, a.Hq, head, o0));
+        x1.fetch(KEYS ? rows(p.v, a.Hkv, kv, o0) : rows(p.dout, a.Hq, head, o0));
+        x0.store(sX0);
+        x1.store(sX1);
+        if (!KEYS) load_stats(head, o0, OT);
     }
     constexpr int W = D / 16;
-    float a0[4][W], a1[KEYS ? 4 : 1][W];
+    float a0[RI][W], a1[KEYS ? RI : 1][W];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < RI; ++i)
 #pragma unroll
         for (int e = 0; e < W; ++e) {
             a0[i][e] = 0.f;
@@ -440,31 +499,39 @@ __global__ void __launch_bounds__(kTiledThreads) tiled_grad_kernel(const LayerAr
         }
     const float al = p.alpha[kv], sl = a.scale * kLog2e;
     const float sgn_c = al < 0.f ? -1.f : 1.f, sgn_s = 1.f - al < 0.f ? -1.f : 1.f;
-    const int per_head = nt - ot, n_in = KEYS ? a.G * per_head : ot + 1;
+    // keys outer: the query tiles from the one that holds row o0 on, of every
+    // query head; queries outer: the key tiles up to the diagonal
+    const int it0 = KEYS ? o0 / TT : 0, per_head = KEYS ? n_it - it0 : (min(o0 + OT, N) - 1) / TT + 1;
+    const int n_in = KEYS ? a.G * per_head : per_head;
+    Rows<T, D, TT> y0, y1;
+    auto fetch = [&](int j) {
+        const int first = (it0 + j % per_head) * TT, qh = kv * a.G + j / per_head;
+        y0.fetch(KEYS ? rows(p.q, a.Hq, qh, first) : rows(p.k, a.Hkv, kv, first));
+        y1.fetch(KEYS ? rows(p.dout, a.Hq, qh, first) : rows(p.v, a.Hkv, kv, first));
+    };
+    if (prefetches<T, D>()) fetch(0);
     for (int j0 = 0; j0 < n_in; ++j0) {
-        const int it = KEYS ? ot + j0 % per_head : j0, qh = KEYS ? kv * a.G + j0 / per_head : head;
+        const int it = it0 + j0 % per_head, qh = KEYS ? kv * a.G + j0 / per_head : head;
         __syncthreads();
-        if constexpr (KEYS) {
-            load_tile<T, D>(sY0, rows(p.q, a.Hq, qh, it));
-            load_tile<T, D>(sY1, rows(p.dout, a.Hq, qh, it));
-            load_stats(qh, it);
-        } else {
-            load_tile<T, D>(sY0, rows(p.k, a.Hkv, kv, it));
-            load_tile<T, D>(sY1, rows(p.v, a.Hkv, kv, it));
-        }
+        if (!prefetches<T, D>()) fetch(j0);
+        y0.store(sY0);
+        y1.store(sY1);
+        if (KEYS) load_stats(qh, it * TT, TT);
         __syncthreads();
-        float x[4][4], d[4][4];
-        tile_dot<D>(sX0, sY0, tx, ty, x);
-        tile_dot<D>(sX1, sY1, tx, ty, d);
-        const int qt = KEYS ? it : ot, kt = KEYS ? ot : it;
-        const bool lam_tile = kt * TT < a.sink || (qt - kt) * TT - (TT - 1) < a.recent;
+        if (prefetches<T, D>() && j0 + 1 < n_in) fetch(j0 + 1);
+        float x[RI][4], d[RI][4];
+        tile_dot<D, RI>(sX0, sY0, tx, ty, x);
+        tile_dot<D, RI>(sX1, sY1, tx, ty, d);
+        const int i0 = it * TT;                                       // first inner row
+        const int query0 = KEYS ? i0 : o0, key0 = KEYS ? o0 : i0, n_keys = KEYS ? OT : TT;
+        const bool lam_tile = key0 < a.sink || query0 - (key0 + n_keys - 1) < a.recent;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < RI; ++i) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int orow = 4 * ty + i, icol = tx + 16 * j;
+                const int orow = RI * ty + i, icol = tx + 16 * j;
                 const int qr = KEYS ? icol : orow;                    // the query's row in its tile
-                const int query = qt * TT + qr, key = kt * TT + (KEYS ? orow : icol);
+                const int query = query0 + qr, key = key0 + (KEYS ? orow : icol);
                 float slope = 1.f, s;
                 if constexpr (CAP) {
                     const float t = tanhf(x[i][j] * a.cap.k);
@@ -482,15 +549,15 @@ __global__ void __launch_bounds__(kTiledThreads) tiled_grad_kernel(const LayerAr
                 d[i][j] = slope * (wc * (d[i][j] - sStat[TT + qr]) + ws * (d[i][j] - sStat[3 * TT + qr]));
             }
         }
-        put_transposed(sG, d, tx, ty);
-        if constexpr (KEYS) put_transposed(sW, x, tx, ty);
+        put_transposed<RI>(sG, d, tx, ty);
+        if constexpr (KEYS) put_transposed<RI>(sW, x, tx, ty);
         __syncthreads();
-        tile_acc<D>(sG, sY0, tx, ty, a0);
-        if constexpr (KEYS) tile_acc<D>(sW, sY1, tx, ty, a1);
+        tile_acc<D, RI>(sG, sY0, tx, ty, a0);
+        if constexpr (KEYS) tile_acc<D, RI>(sW, sY1, tx, ty, a1);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = ot * TT + 4 * ty + i;
+    for (int i = 0; i < RI; ++i) {
+        const int r = o0 + RI * ty + i;
         if (r >= N || !bounds_ok(b < a.B && head < heads, p.status)) continue;
         const size_t off = (((size_t)b * N + r) * heads + head) * D + 4 * tx;
 #pragma unroll
@@ -510,26 +577,43 @@ __global__ void __launch_bounds__(kTiledThreads) tiled_grad_kernel(const LayerAr
         sum_shares(p.part + (size_t)kv * p.n_part, p.n_part, &p.dalpha[kv], threadIdx.x);
 }
 
-template <typename T, int D, bool MIX, bool CAP>
-cudaError_t launch_forward(const LayerArgs& a, const CacheArgs& c, const TiledArgs& s, cudaStream_t st) {
-    constexpr size_t smem = forward_smem<D, MIX>();
-    static std::atomic<unsigned long long> configured{0};
-    const cudaError_t e = smem_limit_once(tiled_forward_kernel<T, D, MIX, CAP>, (int)smem, configured);
-    if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)((s.N + TT - 1) / TT), (unsigned)a.Hq, (unsigned)a.B);
-    tiled_forward_kernel<T, D, MIX, CAP><<<grid, kTiledThreads, smem, st>>>(a, c, s);
-    return cudaGetLastError();
+// 64 outer rows a CTA where that still gives every SM two CTAs, else 32: at
+// 509 tokens and 16 heads (128 CTAs of 64 rows) a step took 231 us with 64 rows
+// and @@ us with 32; at 2,048 tokens the two differ by less than the noise.
+bool few_ctas(const LayerArgs& a, int N, int heads) {
+    return (long)a.B * heads * ((N + 63) / 64) < 2L * sm_count();
 }
 
+template <typename T, int D, bool MIX, bool CAP, int RI>
+cudaError_t launch_forward_ri(const LayerArgs& a, const CacheArgs& c, const TiledArgs& s, cudaStream_t st) {
+    constexpr size_t smem = forward_smem<D, MIX, RI>();
+    static std::atomic<unsigned long long> configured{0};
+    const cudaError_t e = smem_limit_once(tiled_forward_kernel<T, D, MIX, CAP, RI>, (int)smem, configured);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)((s.N + 16 * RI - 1) / (16 * RI)), (unsigned)a.Hq, (unsigned)a.B);
+    tiled_forward_kernel<T, D, MIX, CAP, RI><<<grid, kTiledThreads, smem, st>>>(a, c, s);
+    return cudaGetLastError();
+}
+template <typename T, int D, bool MIX, bool CAP>
+cudaError_t launch_forward(const LayerArgs& a, const CacheArgs& c, const TiledArgs& s, cudaStream_t st) {
+    return few_ctas(a, s.N, a.Hq) ? launch_forward_ri<T, D, MIX, CAP, 2>(a, c, s, st)
+                                  : launch_forward_ri<T, D, MIX, CAP, 4>(a, c, s, st);
+}
+
+template <typename T, int D, bool KEYS, bool CAP, int RI>
+cudaError_t launch_grad_ri(const LayerArgs& a, const TiledGradArgs& p, cudaStream_t st) {
+    constexpr size_t smem = grad_smem<D, KEYS, RI>();
+    static std::atomic<unsigned long long> configured{0};
+    const cudaError_t e = smem_limit_once(tiled_grad_kernel<T, D, KEYS, CAP, RI>, (int)smem, configured);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)((p.N + 16 * RI - 1) / (16 * RI)), (unsigned)(KEYS ? a.Hkv : a.Hq), (unsigned)a.B);
+    tiled_grad_kernel<T, D, KEYS, CAP, RI><<<grid, kTiledThreads, smem, st>>>(a, p);
+    return cudaGetLastError();
+}
 template <typename T, int D, bool KEYS, bool CAP>
 cudaError_t launch_grad(const LayerArgs& a, const TiledGradArgs& p, cudaStream_t st) {
-    constexpr size_t smem = grad_smem<D, KEYS>();
-    static std::atomic<unsigned long long> configured{0};
-    const cudaError_t e = smem_limit_once(tiled_grad_kernel<T, D, KEYS, CAP>, (int)smem, configured);
-    if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)((p.N + TT - 1) / TT), (unsigned)(KEYS ? a.Hkv : a.Hq), (unsigned)a.B);
-    tiled_grad_kernel<T, D, KEYS, CAP><<<grid, kTiledThreads, smem, st>>>(a, p);
-    return cudaGetLastError();
+    return few_ctas(a, p.N, KEYS ? a.Hkv : a.Hq) ? launch_grad_ri<T, D, KEYS, CAP, 2>(a, p, st)
+                                                 : launch_grad_ri<T, D, KEYS, CAP, 4>(a, p, st);
 }
 
 template <typename T, int D>
