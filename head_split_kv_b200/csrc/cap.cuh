@@ -7,8 +7,9 @@
 // capped largest dot product.
 //
 // tanh in two forms:
-//   * tanh_sfu: 1 - 2 / (1 + e^2y), two SFU operations, any y.  Absolute
-//     error a few 1e-7 (of 1), so a capped score is within cap * 1e-6.
+//   * tanh_sfu: 1 - 2 / (1 + e^2y), two SFU operations, absolute error a few
+//     1e-7; below |y| = 1/16, where that would be much of a small y (a large
+//     cap scales it back up), y - y^3 / 3.  Relative error up to 6e-6, any y.
 //   * poly_fma2: y * P(y^2) on the FMA pipe for |y| <= 0.7, where nearly all
 //     scores of a trained model lie (|s| <= 0.7 cap); P has four coefficients,
 //     fitted here to the smallest largest relative error there, 6.8e-6: at a
@@ -29,12 +30,6 @@ __device__ __forceinline__ float sfu_exp2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// the same, kept in its place among other such statements
-__device__ __forceinline__ float sfu_exp2_ordered(float x) {
-    float y;
-    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ float sfu_rcp(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -45,7 +40,8 @@ __device__ __forceinline__ float tanh_sfu(float y) {
     // e^2y overflows to inf for large y (1 / inf = 0: tanh = 1) and underflows
     // to 0 for small y (tanh = -1)
     const float e = sfu_exp2(y * (2.f * kLog2e));
-    return fmaf(-2.f, sfu_rcp(1.f + e), 1.f);
+    const float t = fmaf(-2.f, sfu_rcp(1.f + e), 1.f);
+    return fabsf(y) < 0.0625f ? fmaf(y * y * y, -1.f / 3.f, y) : t;
 }
 
 constexpr float kTanhRange = 0.7f;   // of |y|

@@ -51,7 +51,7 @@
 // there when they have finished tile j, and
 //   ACC1(j) ACC2(j) dP(j + 1)
 // run while they turn S(j + 1) into weights.  (With W over S's columns, S(j + 1)
-// had to wait for ACC1(j), and the warps for it: dK and dV 355 -> @@ us.)
+// had to wait for ACC1(j), and the warps for it: dK and dV 355 -> 323 us.)
 // Roles (576 threads): warps 0-15 element-wise (warp w: lanes 32 (w % 4) ..,
 // columns 32 (w / 4) ..), warp 16 TMA, warp 17 MMA.  Sixteen warps at 96
 // registers (an SM sub-partition holds five warps) against eight at 168: the

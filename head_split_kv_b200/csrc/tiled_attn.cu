@@ -187,10 +187,15 @@ __global__ void __launch_bounds__(kTiledThreads) tiled_forward_kernel(const Laye
     float* sP2 = sP + TT * PS;                        // mix only
     int* sPos = reinterpret_cast<int*>(sP + (MIX ? 2 : 1) * TT * PS);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int b = blockIdx.z, slot = blockIdx.y / a.G, g = blockIdx.y % a.G;
+    const int tiles = (s.N + OT - 1) / OT, heads = a.B * a.Hq;
+    // MIX: tile t of every head before the next shorter one (a step of 509 tokens
+    // 233 -> 211 us); a pre-fill chunk's tiles are about as long as one another,
+    // and a head's tiles side by side keep its keys in L2 (105 us; 119 the other way)
+    const int t = MIX ? blockIdx.x / heads : blockIdx.x % tiles, bh = MIX ? blockIdx.x % heads : blockIdx.x / tiles;
+    const int b = bh / a.Hq, hq = bh % a.Hq, slot = hq / a.G, g = hq % a.G;
     const int q_idx = a.q_head0[slot] + g, kv_idx = a.kv_head[slot];
     if (!bounds_ok(b < a.B && q_idx >= 0 && q_idx < a.Hq && kv_idx >= 0 && kv_idx < a.Hkv, c.status)) return;
-    const int r0 = (gridDim.x - 1 - blockIdx.x) * OT;  // the longest rows first
+    const int r0 = (tiles - 1 - t) * OT;               // the longest rows first
     const int N = s.N;
     const bool retrieval = MIX || slot < a.R;
     int c0 = 0;
@@ -462,9 +467,10 @@ __global__ void __launch_bounds__(kTiledThreads) tiled_grad_kernel(const LayerAr
     float* sG = sStat + 4 * TT;                       // dS, transposed
     float* sW = sG + TT * PS;                         // W, transposed (keys outer)
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int b = blockIdx.z, head = blockIdx.y, N = p.N;
-    const int heads = KEYS ? a.Hkv : a.Hq, kv = KEYS ? head : head / a.G;
-    const int ot = KEYS ? blockIdx.x : gridDim.x - 1 - blockIdx.x;   // the longest first
+    const int heads = KEYS ? a.Hkv : a.Hq, N = p.N, tiles = (N + OT - 1) / OT;
+    const int t = blockIdx.x / (a.B * heads), bh = blockIdx.x % (a.B * heads), b = bh / heads, head = bh % heads;
+    const int kv = KEYS ? head : head / a.G;
+    const int ot = KEYS ? t : tiles - 1 - t;                         // the longest of every head first
     const int o0 = ot * OT, n_it = (N + TT - 1) / TT;                // first outer row; inner tiles of the sequence
     auto rows = [&](const void* base, int H, int h, int first) {
         return [=](int r) -> const T* {
@@ -579,7 +585,7 @@ __global__ void __launch_bounds__(kTiledThreads) tiled_grad_kernel(const LayerAr
 
 // 64 outer rows a CTA where that still gives every SM two CTAs, else 32: at
 // 509 tokens and 16 heads (128 CTAs of 64 rows) a step took 231 us with 64 rows
-// and @@ us with 32; at 2,048 tokens the two differ by less than the noise.
+// and 209 us with 32; at 2,048 tokens the two differ by less than the noise.
 bool few_ctas(const LayerArgs& a, int N, int heads) {
     return (long)a.B * heads * ((N + 63) / 64) < 2L * sm_count();
 }
@@ -590,8 +596,9 @@ cudaError_t launch_forward_ri(const LayerArgs& a, const CacheArgs& c, const Tile
     static std::atomic<unsigned long long> configured{0};
     const cudaError_t e = smem_limit_once(tiled_forward_kernel<T, D, MIX, CAP, RI>, (int)smem, configured);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)((s.N + 16 * RI - 1) / (16 * RI)), (unsigned)a.Hq, (unsigned)a.B);
-    tiled_forward_kernel<T, D, MIX, CAP, RI><<<grid, kTiledThreads, smem, st>>>(a, c, s);
+    const long ctas = (long)a.B * a.Hq * ((s.N + 16L * RI - 1) / (16 * RI));
+    if (ctas > 0x7fffffffL) return cudaErrorInvalidConfiguration;
+    tiled_forward_kernel<T, D, MIX, CAP, RI><<<(unsigned)ctas, kTiledThreads, smem, st>>>(a, c, s);
     return cudaGetLastError();
 }
 template <typename T, int D, bool MIX, bool CAP>
@@ -606,8 +613,9 @@ cudaError_t launch_grad_ri(const LayerArgs& a, const TiledGradArgs& p, cudaStrea
     static std::atomic<unsigned long long> configured{0};
     const cudaError_t e = smem_limit_once(tiled_grad_kernel<T, D, KEYS, CAP, RI>, (int)smem, configured);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)((p.N + 16 * RI - 1) / (16 * RI)), (unsigned)(KEYS ? a.Hkv : a.Hq), (unsigned)a.B);
-    tiled_grad_kernel<T, D, KEYS, CAP, RI><<<grid, kTiledThreads, smem, st>>>(a, p);
+    const long ctas = (long)a.B * (KEYS ? a.Hkv : a.Hq) * ((p.N + 16L * RI - 1) / (16 * RI));
+    if (ctas > 0x7fffffffL) return cudaErrorInvalidConfiguration;
+    tiled_grad_kernel<T, D, KEYS, CAP, RI><<<(unsigned)ctas, kTiledThreads, smem, st>>>(a, p);
     return cudaGetLastError();
 }
 template <typename T, int D, bool KEYS, bool CAP>

@@ -469,11 +469,10 @@ duo_status duo_append_kv_rope(const duo_layer_desc* desc, const duo_kv_state* st
  * before the mask and the softmax.  cap = 0: not capped (the plain call).
  * Everything else -- tensors, caches of every kind, workspaces (those of the
  * plain calls), status bits, refusals -- is as for the plain calls.
- * The capped score is within cap * 1e-6 of the formula in decode and, on the
- * tensor-core pre-fill, within 8e-6 of its own size (7e-6 of it from the
- * polynomial that stands for tanh where |s| <= cap).
+ * A bf16 layer's capped score is within 8e-6 of its own size of the formula (an
+ * fp32 layer's: fp32 rounding).
  * Errors: as the plain calls, and DUO_ERR_INVALID_ARG for a cap that is
- * negative, not finite, or below scale / 1e4.
+ * negative, not finite, below scale / 1e4 or above 2e38.
  */
 duo_status duo_decode_attn_capped(const duo_layer_desc* desc, const duo_kv_state* st, float cap, const void* q,
                                   void* out, void* workspace, size_t ws_bytes, duo_stream_t stream);

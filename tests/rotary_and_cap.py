@@ -70,20 +70,20 @@ def attend_tolerance(q, k, v, cap, scale, dtype):
 
     Weights, bf16: each is rounded to 8 bits (half a step, 2^-8 of the value at most
     of its binade's lower end) and computed from a score that is off by at most
-    (d + 16) fp32 half-steps of its terms plus the cap's own 1e-6 * cap and
+    (d + 16) fp32 half-steps of its terms plus the cap's own
     8e-6 of the score; the exponential on the FMA pipe adds 7.5e-5.
-    Weights, fp32: the score's error and four half-steps of cap; the sums over
+    Weights, fp32: the score's error and four half-steps of the score; the sums over
     m keys add their error, (8 + sqrt(m)) half-steps of a convex combination."""
     if not len(k):
         return 0.0
     vmax, m, d = float(np.abs(v).max()), len(k), q.shape[1]
     terms = float((np.abs(q) @ np.abs(k).T * scale).max())
     score = (d + 16) * HALF["fp32"] * terms
+    s = min(terms, cap) if cap else terms
     if dtype == "bf16":
-        s = min(terms, cap) if cap else terms
-        w = 2.0 ** -8 + score + 1e-6 * cap + 8e-6 * s + 7.5e-5
+        w = 2.0 ** -8 + score + 8e-6 * s + 7.5e-5
         return (2 * w + 2.0 ** -8) * vmax
-    w = score + 4 * cap * HALF["fp32"] + 4 * HALF["fp32"]
+    w = score + 4 * s * HALF["fp32"] + 4 * HALF["fp32"]
     return (2 * w + 2 * (8 + math.sqrt(m)) * HALF["fp32"]) * vmax
 
 
@@ -123,7 +123,7 @@ def mix_ref(q, k, v, do, alpha, cap, sink, recent, dtype):
             s = capped(raw, cap)
             slope = 1.0 - np.tanh(raw / cap) ** 2 if cap else np.ones_like(raw)
             terms = np.abs(qq) @ np.abs(kk).T * scale
-            es = (d + 16) * h32 * terms + ((8e-6 * np.abs(s) + 1e-6 * cap) if bf else 4 * cap * h32)
+            es = (d + 16) * h32 * terms + (8e-6 if bf else 4 * h32) * np.abs(s)
             e = 2 * es.max(1, initial=0.0, where=causal)[:, None] + (1e-4 if bf else 16 * h32)   # weight and log-sum
             dp = oo @ vv.T
             dp_size = np.abs(oo) @ np.abs(vv).T

@@ -43,6 +43,9 @@ DECODES = [   # hq, hkv, d, dtype, retrieval, quant, paged, lengths, gain, cap
     (8, 4, 128, "bf16", [0, 2], "int8", False, [513, 1], 3.0, 30.0),
     (8, 8, 128, "bf16", [0, 2], "int4", False, [300, 64], 30.0, 10.0),
     (32, 4, 128, "bf16", [3], "int4", False, [1000], 3.0, 50.0),
+    (16, 4, 128, "bf16", [1, 2], "none", True, [513, 2], 3.0, 1e6),       # so far below that tanh's own
+    (8, 4, 128, "bf16", [0, 2], "int8", False, [300, 9], 3.0, 1e38),      # absolute error would show
+    (8, 4, 64, "fp32", [1, 2], "none", False, [200, 17], 10.0, 1e30),
 ]
 
 
@@ -134,6 +137,9 @@ PREFILLS = [   # hq, hkv, d, dtype, retrieval, quant, mode, B, chunks, gain, cap
     (8, 4, 64, "bf16", [1], "none", "lambda", 2, [33, 90], 3.0, 30.0),
     (8, 4, 64, "fp32", [1, 2], "none", "chunk", 1, [33, 1, 90], 10.0, 7.0),
     (4, 4, 128, "fp32", [0, 1, 2, 3], "none", "lambda", 1, [100, 31], 3.0, 30.0),
+    (8, 4, 128, "bf16", [0, 3], "none", "lambda", 1, [130, 200], 3.0, 1e6),
+    (8, 4, 128, "bf16", [0, 3], "int8", "lambda", 1, [130, 200], 3.0, 1e38),
+    (8, 4, 64, "fp32", [1, 2], "none", "chunk", 1, [33, 90], 10.0, 1e30),
 ]
 
 
