@@ -48,7 +48,10 @@
 // nothing and adds sign * <dout row, attention row> over the CTA's rows into
 // dalpha[kv] (the gate gradient, one launch per sign).  Both load the row
 // they combine with before waiting for the last MMAs, so its latency hides
-// behind them.
+// behind them.  The training forward's variants, EPI_KEEP and EPI_MIX_KEEP,
+// also store each row's log-sum; they serve it without a cap or with a cap too
+// large for prefill_capped.cu.  CAP: scores capped by a tanh (cap.cuh) before
+// the mask, for those caps and for 8- and 4-bit caches.
 #include <cuda.h>
 
 #include "cap.cuh"

@@ -641,7 +641,7 @@ cudaError_t launch_grads(const LayerArgs& a, TiledGradArgs p, const StatArgs& x,
 
 cudaError_t launch_tiled_prefill(const LayerArgs& a, const CacheArgs& c, const void* q, const void* k, const void* v,
                                  int C, void* out, cudaStream_t st) {
-    if (a.B > 65535 || !a.cap.on) return cudaErrorInvalidConfiguration;
+    if (!a.cap.on) return cudaErrorInvalidConfiguration;
     const TiledArgs s{q, k, v, C, out, nullptr, nullptr, nullptr, nullptr};
     if (a.dtype == DUO_BF16) {
         if (a.D == 128) return launch_forward<__nv_bfloat16, 128, false, true>(a, c, s, st);
@@ -653,7 +653,6 @@ cudaError_t launch_tiled_prefill(const LayerArgs& a, const CacheArgs& c, const v
 
 cudaError_t launch_tiled_mix(const LayerArgs& a, const float* alpha, const void* q, const void* k, const void* v, int N,
                              void* out, float* causal, float* streaming, float* lse, int32_t* status, cudaStream_t st) {
-    if (a.B > 65535) return cudaErrorInvalidConfiguration;
     const TiledArgs s{q, k, v, N, out, alpha, causal, streaming, lse};
     CacheArgs c{};
     c.status = status;

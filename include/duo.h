@@ -469,6 +469,9 @@ duo_status duo_append_kv_rope(const duo_layer_desc* desc, const duo_kv_state* st
  * before the mask and the softmax.  cap = 0: not capped (the plain call).
  * Everything else -- tensors, caches of every kind, workspaces (those of the
  * plain calls), status bits, refusals -- is as for the plain calls.
+ * In a pre-fill a masked key's value meets a weight of 0 in the matrix product,
+ * as in the plain call: v_chunk, and once seq_len > 0 every ring slot, must be
+ * finite (zero-fill the ring before its first use).
  * A bf16 layer's capped score is within 8e-6 of its own size of the formula (an
  * fp32 layer's: fp32 rounding).
  * Errors: as the plain calls, and DUO_ERR_INVALID_ARG for a cap that is
@@ -594,6 +597,8 @@ duo_status duo_gated_mix_grad_alpha(const duo_layer_desc* desc, const void* q, c
  * (the weights and their gradients rounded to bf16 as MMA operands, sums in
  * fp32); the rest on the CUDA cores in fp32.
  * N == 0: nothing is done but that dalpha is zeroed.
+ * q, k, v and dout must be finite: masked entries are weights of 0 in matrix
+ * products.
  * status: as for duo_gated_mix.
  * Errors: DUO_ERR_INVALID_ARG, DUO_ERR_SHAPE, DUO_ERR_CAPACITY (saved,
  * workspace), DUO_ERR_UNSUPPORTED, DUO_ERR_CUDA.

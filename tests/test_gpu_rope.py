@@ -80,6 +80,25 @@ def test_rope_matches_the_formula(duo, case, inverse):
     assert np.array_equal(bits(q2), bits(qo)) and np.array_equal(bits(k2), bits(ko))
 
 
+@pytest.mark.parametrize("layout,rot", [("pairs", 6), ("pairs", 20), ("halves", 6), ("halves", 64)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_channels_past_the_rotation_are_kept(duo, layout, rot, dtype):
+    """Infinities, NaN and -0 behind rot_dim come out as they went in, and reach no other channel."""
+    t = torch()
+    sh = S.LayerShape(4, 2, 128, dtype)
+    (q, k, _), inv, _, rope = _setup(duo, sh, 1, 5, rot, [rot // 2], layout, 1.0, 2)
+    for x in (q, k):
+        x[..., rot::4], x[..., rot + 1::4], x[..., rot + 2::4] = float("inf"), -0.0, float("nan")
+    desc = duo.desc_init(1, 4, 2, 128, duo.BF16 if dtype == "bf16" else duo.FP32, [0, 1], 2)
+    qo, ko = t.zeros_like(q), t.zeros_like(k)
+    duo.rope_qk(desc, rope, q, k, qo, ko, 5, seq_len=t.tensor([70], dtype=t.int32, device="cuda"))
+    for x, y in ((q, qo), (k, ko)):
+        x, y = f64(x), f64(y)
+        assert np.array_equal(y[..., rot:], x[..., rot:], equal_nan=True)
+        assert np.all(np.signbit(y[..., rot + 1::4]))
+        assert np.all(np.isfinite(y[..., :rot]))
+
+
 def test_rope_gradient_is_the_transpose(duo):
     """<rope(x), g> = <x, rope_inverse(g)>, and a difference quotient of a loss
     agrees with the gradient (the map is linear, so up to rounding)."""
