@@ -3,9 +3,9 @@
 // capped pre-fill, and the gated mix's training forward and backward passes.
 // All arithmetic is fp32 (CUDA's exp2f and tanhf).
 //
-// 256 threads as 16 x 16; every product is a register tile of RI x 4 scores
-// (or RI rows x D / 16 columns) per thread, RI = 4 (tiles of 64 outer rows) or
-// 2 (32 outer rows: twice the CTAs, for grids that would leave SMs idle).
+// Threads as 16 x 16 or 8 x 16; every product is a register tile of RI x 4
+// scores (or RI rows x D / 16 columns) per thread, in tiles of 64 outer rows
+// or 32 (twice the CTAs, for grids that would leave SMs idle).
 // Operands lie in shared memory as fp32 rows padded by four floats, so that 16
 // threads reading 16 rows use all banks.  A thread's rows are RI ty .., the
 // same for scores and accumulators, so a row's softmax state stays in the 16
@@ -14,7 +14,14 @@
 // transposed.  The next tile's rows are loaded into registers while the
 // current one is computed (rows of 512 bytes, fp32 with d 128, would take too
 // many and are not).
-// Bound by the fp32 FMA pipe and, for short sequences, by latency.
+// Bound by shared-memory reads (a 32 x 64 x 64 product took 2,800 cycles for
+// 1,024 of FMAs, with 6 16-byte reads to 32 FMAs a thread) and, for short
+// sequences, by the longest CTA.  The training kernels at d 64 take 8 x 16
+// threads, which read less (8 to 64) and leave room for three CTAs to an SM: a
+// step of 509 tokens 211 -> 197 us, one of 2,048 and 32 + 8 heads 2.99 -> 2.70
+// ms.  A pre-fill of few CTAs has an SM to each,
+// and 128 threads hide less of the latency there (107 us with 256, 131 with
+// 128).
 #include "cap.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -24,27 +31,29 @@ namespace duo {
 namespace {
 
 constexpr int TT = 64;              // rows of an inner tile
-constexpr int kTiledThreads = 256;
+// Threads of a CTA: 16 x 16, and 8 x 16 for the training kernels at d 64.
+template <int D, bool TRAIN>
+__host__ __device__ constexpr int tiled_threads() { return D == 64 && TRAIN ? 128 : 256; }
 
 template <int D>
 __host__ __device__ constexpr int row_stride() { return D + 4; }
 template <int D>
 __host__ __device__ constexpr size_t tile_floats(int rows) { return (size_t)rows * row_stride<D>(); }
-template <int RI>
-__host__ __device__ constexpr int p_stride() { return 16 * RI + 4; }   // of the transposed probabilities
+template <int OT>
+__host__ __device__ constexpr int p_stride() { return OT + 4; }   // of the transposed probabilities
 
 // ROWS rows of D elements on their way from global memory to shared memory as
 // fp32: fetch (rows where src(r) is NULL are zero), then store.
-template <typename T, int D, int ROWS>
+template <typename T, int D, int ROWS, int TH>
 struct Rows {
     static constexpr int N = 16 / (int)sizeof(T), PPR = D / N;   // elements of a 16-byte piece, pieces per row
-    static constexpr int kPer = ROWS * PPR / kTiledThreads;
+    static constexpr int kPer = ROWS * PPR / TH;
     uint4 w[kPer];
     template <typename F>
     __device__ __forceinline__ void fetch(F src) {
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-            const int i = threadIdx.x + k * kTiledThreads;
+            const int i = threadIdx.x + k * TH;
             const T* p = src(i / PPR);
             w[k] = p ? reinterpret_cast<const uint4*>(p)[i % PPR] : make_uint4(0u, 0u, 0u, 0u);
         }
@@ -52,7 +61,7 @@ struct Rows {
     __device__ __forceinline__ void store(float* dst) const {
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-            const int i = threadIdx.x + k * kTiledThreads, r = i / PPR, c = i % PPR * N;
+            const int i = threadIdx.x + k * TH, r = i / PPR, c = i % PPR * N;
             float v[N];
             load_row_f32<T, N>(reinterpret_cast<const T*>(&w[k]), v);
 #pragma unroll
@@ -87,16 +96,19 @@ __device__ __forceinline__ void tile_dot(const float* x, const float* y, int tx,
 }
 
 // acc[i][:] += sum over the tile's 64 inner rows k of pt[k][RI ty + i] * y[k][columns 4 tx + 64 j ..]
-template <int D, int RI>
+template <int D, int RI, int PS>
 __device__ __forceinline__ void tile_acc(const float* pt, const float* y, int tx, int ty, float (&acc)[RI][D / 16]) {
 #pragma unroll 4
     for (int k = 0; k < TT; ++k) {
-        float pr[RI];
+        __align__(16) float pr[RI];
+        if constexpr (RI % 4 == 0) {
 #pragma unroll
-        for (int i = 0; i < RI; i += 2) {
-            const float2 p = *reinterpret_cast<const float2*>(pt + k * p_stride<RI>() + RI * ty + i);
-            pr[i] = p.x;
-            pr[i + 1] = p.y;
+            for (int i = 0; i < RI; i += 4)
+                *reinterpret_cast<float4*>(pr + i) = *reinterpret_cast<const float4*>(pt + k * PS + RI * ty + i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < RI; i += 2)
+                *reinterpret_cast<float2*>(pr + i) = *reinterpret_cast<const float2*>(pt + k * PS + RI * ty + i);
         }
 #pragma unroll
         for (int j = 0; j < D / 64; ++j) {
@@ -113,13 +125,13 @@ __device__ __forceinline__ void tile_acc(const float* pt, const float* y, int tx
 }
 
 // pt[tx + 16 j][RI ty ..] = p[..][j]
-template <int RI>
+template <int RI, int PS>
 __device__ __forceinline__ void put_transposed(float* pt, const float (&p)[RI][4], int tx, int ty) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int i = 0; i < RI; i += 2)
-            *reinterpret_cast<float2*>(pt + (tx + 16 * j) * p_stride<RI>() + RI * ty + i) = make_float2(p[i][j], p[i + 1][j]);
+            *reinterpret_cast<float2*>(pt + (tx + 16 * j) * PS + RI * ty + i) = make_float2(p[i][j], p[i + 1][j]);
 }
 
 // Over the 16 threads that hold a row's columns.
@@ -169,17 +181,17 @@ struct TiledArgs {
     float* lse;            // mix: [2][B][Hq][N]
 };
 
-template <int D, bool MIX, int RI>
+template <int D, bool MIX, int OT>
 constexpr size_t forward_smem() {
-    return (tile_floats<D>(16 * RI) + 2 * tile_floats<D>(TT) + (MIX ? 2 : 1) * (size_t)TT * p_stride<RI>()) * sizeof(float) +
+    return (tile_floats<D>(OT) + 2 * tile_floats<D>(TT) + (MIX ? 2 : 1) * (size_t)TT * p_stride<OT>()) * sizeof(float) +
            TT * sizeof(int);
 }
 
-template <typename T, int D, bool MIX, bool CAP, int RI>
-__global__ void __launch_bounds__(kTiledThreads) tiled_forward_kernel(const LayerArgs a, const CacheArgs c,
+template <typename T, int D, bool MIX, bool CAP, int OT>
+__global__ void __launch_bounds__(tiled_threads<D, MIX>()) tiled_forward_kernel(const LayerArgs a, const CacheArgs c,
                                                                       const TiledArgs s) {
     extern __shared__ __align__(16) float sm[];
-    constexpr int OT = 16 * RI, PS = p_stride<RI>();   // query rows of the CTA
+    constexpr int TH = tiled_threads<D, MIX>(), RI = 16 * OT / TH, PS = p_stride<OT>();   // OT query rows a CTA
     float* sQ = sm;
     float* sK = sQ + tile_floats<D>(OT);
     float* sV = sK + tile_floats<D>(TT);
@@ -207,7 +219,7 @@ __global__ void __launch_bounds__(kTiledThreads) tiled_forward_kernel(const Laye
         }
     }
     {
-        Rows<T, D, OT> q;
+        Rows<T, D, OT, TH> q;
         q.fetch([&](int r) -> const T* {
             return r0 + r < N ? static_cast<const T*>(s.q) + (((size_t)b * N + r0 + r) * a.Hq + q_idx) * D : nullptr;
         });
@@ -254,7 +266,7 @@ __global__ void __launch_bounds__(kTiledThreads) tiled_forward_kernel(const Laye
             }
         return false;
     };
-    Rows<T, D, TT> nk_, nv_;
+    Rows<T, D, TT, TH> nk_, nv_;
     auto fetch = [&](int sg, int k) {
         const int n = min(TT, end[sg] - k);
         auto row = [&](int r, const void* full, const void* ring, const void* chunk) -> const T* {
@@ -309,17 +321,17 @@ __global__ void __launch_bounds__(kTiledThreads) tiled_forward_kernel(const Laye
             }
         }
         softmax_step<RI, W>(x, m, l, o);
-        put_transposed<RI>(sP, x, tx, ty);
+        put_transposed<RI, PS>(sP, x, tx, ty);
         if constexpr (MIX) {
             if (lam_tile) {
                 softmax_step<RI, W>(x2, m2, l2, o2);
-                put_transposed<RI>(sP2, x2, tx, ty);
+                put_transposed<RI, PS>(sP2, x2, tx, ty);
             }
         }
         __syncthreads();
-        tile_acc<D, RI>(sP, sV, tx, ty, o);
+        tile_acc<D, RI, PS>(sP, sV, tx, ty, o);
         if constexpr (MIX) {
-            if (lam_tile) tile_acc<D, RI>(sP2, sV, tx, ty, o2);
+            if (lam_tile) tile_acc<D, RI, PS>(sP2, sV, tx, ty, o2);
         }
         seg = seg1;
         k0 = k1;
@@ -449,16 +461,16 @@ struct TiledGradArgs {
     int N, n_pad;
 };
 
-template <int D, bool KEYS, int RI>
+template <int D, bool KEYS, int OT>
 constexpr size_t grad_smem() {
-    return (2 * tile_floats<D>(16 * RI) + 2 * tile_floats<D>(TT) + (KEYS ? 2 : 1) * (size_t)TT * p_stride<RI>() + 4 * TT) *
+    return (2 * tile_floats<D>(OT) + 2 * tile_floats<D>(TT) + (KEYS ? 2 : 1) * (size_t)TT * p_stride<OT>() + 4 * TT) *
            sizeof(float);
 }
 
-template <typename T, int D, bool KEYS, bool CAP, int RI>
-__global__ void __launch_bounds__(kTiledThreads) tiled_grad_kernel(const LayerArgs a, const TiledGradArgs p) {
+template <typename T, int D, bool KEYS, bool CAP, int OT>
+__global__ void __launch_bounds__(tiled_threads<D, true>()) tiled_grad_kernel(const LayerArgs a, const TiledGradArgs p) {
     extern __shared__ __align__(16) float sm[];
-    constexpr int OT = 16 * RI, PS = p_stride<RI>();   // outer rows of the CTA
+    constexpr int TH = tiled_threads<D, true>(), RI = 16 * OT / TH, PS = p_stride<OT>();   // OT outer rows a CTA
     float* sX0 = sm;
     float* sX1 = sX0 + tile_floats<D>(OT);
     float* sY0 = sX1 + tile_floats<D>(OT);
@@ -487,7 +499,7 @@ __global__ void __launch_bounds__(kTiledThreads) tiled_grad_kernel(const LayerAr
         }
     };
     {
-        Rows<T, D, OT> x0, x1;
+        Rows<T, D, OT, TH> x0, x1;
         x0.fetch(KEYS ? rows(p.k, a.Hkv, kv, o0) : rows(p.q, a.Hq, head, o0));
         x1.fetch(KEYS ? rows(p.v, a.Hkv, kv, o0) : rows(p.dout, a.Hq, head, o0));
         x0.store(sX0);
@@ -509,7 +521,7 @@ __global__ void __launch_bounds__(kTiledThreads) tiled_grad_kernel(const LayerAr
     // query head; queries outer: the key tiles up to the diagonal
     const int it0 = KEYS ? o0 / TT : 0, per_head = KEYS ? n_it - it0 : (min(o0 + OT, N) - 1) / TT + 1;
     const int n_in = KEYS ? a.G * per_head : per_head;
-    Rows<T, D, TT> y0, y1;
+    Rows<T, D, TT, TH> y0, y1;
     auto fetch = [&](int j) {
         const int first = (it0 + j % per_head) * TT, qh = kv * a.G + j / per_head;
         y0.fetch(KEYS ? rows(p.q, a.Hq, qh, first) : rows(p.k, a.Hkv, kv, first));
@@ -555,11 +567,11 @@ __global__ void __launch_bounds__(kTiledThreads) tiled_grad_kernel(const LayerAr
                 d[i][j] = slope * (wc * (d[i][j] - sStat[TT + qr]) + ws * (d[i][j] - sStat[3 * TT + qr]));
             }
         }
-        put_transposed<RI>(sG, d, tx, ty);
-        if constexpr (KEYS) put_transposed<RI>(sW, x, tx, ty);
+        put_transposed<RI, PS>(sG, d, tx, ty);
+        if constexpr (KEYS) put_transposed<RI, PS>(sW, x, tx, ty);
         __syncthreads();
-        tile_acc<D, RI>(sG, sY0, tx, ty, a0);
-        if constexpr (KEYS) tile_acc<D, RI>(sW, sY1, tx, ty, a1);
+        tile_acc<D, RI, PS>(sG, sY0, tx, ty, a0);
+        if constexpr (KEYS) tile_acc<D, RI, PS>(sW, sY1, tx, ty, a1);
     }
 #pragma unroll
     for (int i = 0; i < RI; ++i) {
@@ -585,43 +597,43 @@ __global__ void __launch_bounds__(kTiledThreads) tiled_grad_kernel(const LayerAr
 
 // 64 outer rows a CTA where that still gives every SM two CTAs, else 32: at
 // 509 tokens and 16 heads (128 CTAs of 64 rows) a step took 231 us with 64 rows
-// and 209 us with 32; at 2,048 tokens the two differ by less than the noise.
+// and 209 us with 32 (both with 16 x 16 threads); at 2,048 tokens the two differ by less than the noise.
 bool few_ctas(const LayerArgs& a, int N, int heads) {
     return (long)a.B * heads * ((N + 63) / 64) < 2L * sm_count();
 }
 
-template <typename T, int D, bool MIX, bool CAP, int RI>
-cudaError_t launch_forward_ri(const LayerArgs& a, const CacheArgs& c, const TiledArgs& s, cudaStream_t st) {
-    constexpr size_t smem = forward_smem<D, MIX, RI>();
+template <typename T, int D, bool MIX, bool CAP, int OT>
+cudaError_t launch_forward_rows(const LayerArgs& a, const CacheArgs& c, const TiledArgs& s, cudaStream_t st) {
+    constexpr size_t smem = forward_smem<D, MIX, OT>();
     static std::atomic<unsigned long long> configured{0};
-    const cudaError_t e = smem_limit_once(tiled_forward_kernel<T, D, MIX, CAP, RI>, (int)smem, configured);
+    const cudaError_t e = smem_limit_once(tiled_forward_kernel<T, D, MIX, CAP, OT>, (int)smem, configured);
     if (e != cudaSuccess) return e;
-    const long ctas = (long)a.B * a.Hq * ((s.N + 16L * RI - 1) / (16 * RI));
+    const long ctas = (long)a.B * a.Hq * ((s.N + OT - 1L) / OT);
     if (ctas > 0x7fffffffL) return cudaErrorInvalidConfiguration;
-    tiled_forward_kernel<T, D, MIX, CAP, RI><<<(unsigned)ctas, kTiledThreads, smem, st>>>(a, c, s);
+    tiled_forward_kernel<T, D, MIX, CAP, OT><<<(unsigned)ctas, tiled_threads<D, MIX>(), smem, st>>>(a, c, s);
     return cudaGetLastError();
 }
 template <typename T, int D, bool MIX, bool CAP>
 cudaError_t launch_forward(const LayerArgs& a, const CacheArgs& c, const TiledArgs& s, cudaStream_t st) {
-    return few_ctas(a, s.N, a.Hq) ? launch_forward_ri<T, D, MIX, CAP, 2>(a, c, s, st)
-                                  : launch_forward_ri<T, D, MIX, CAP, 4>(a, c, s, st);
+    return few_ctas(a, s.N, a.Hq) ? launch_forward_rows<T, D, MIX, CAP, 32>(a, c, s, st)
+                                  : launch_forward_rows<T, D, MIX, CAP, 64>(a, c, s, st);
 }
 
-template <typename T, int D, bool KEYS, bool CAP, int RI>
-cudaError_t launch_grad_ri(const LayerArgs& a, const TiledGradArgs& p, cudaStream_t st) {
-    constexpr size_t smem = grad_smem<D, KEYS, RI>();
+template <typename T, int D, bool KEYS, bool CAP, int OT>
+cudaError_t launch_grad_rows(const LayerArgs& a, const TiledGradArgs& p, cudaStream_t st) {
+    constexpr size_t smem = grad_smem<D, KEYS, OT>();
     static std::atomic<unsigned long long> configured{0};
-    const cudaError_t e = smem_limit_once(tiled_grad_kernel<T, D, KEYS, CAP, RI>, (int)smem, configured);
+    const cudaError_t e = smem_limit_once(tiled_grad_kernel<T, D, KEYS, CAP, OT>, (int)smem, configured);
     if (e != cudaSuccess) return e;
-    const long ctas = (long)a.B * (KEYS ? a.Hkv : a.Hq) * ((p.N + 16L * RI - 1) / (16 * RI));
+    const long ctas = (long)a.B * (KEYS ? a.Hkv : a.Hq) * ((p.N + OT - 1L) / OT);
     if (ctas > 0x7fffffffL) return cudaErrorInvalidConfiguration;
-    tiled_grad_kernel<T, D, KEYS, CAP, RI><<<(unsigned)ctas, kTiledThreads, smem, st>>>(a, p);
+    tiled_grad_kernel<T, D, KEYS, CAP, OT><<<(unsigned)ctas, tiled_threads<D, true>(), smem, st>>>(a, p);
     return cudaGetLastError();
 }
 template <typename T, int D, bool KEYS, bool CAP>
 cudaError_t launch_grad(const LayerArgs& a, const TiledGradArgs& p, cudaStream_t st) {
-    return few_ctas(a, p.N, KEYS ? a.Hkv : a.Hq) ? launch_grad_ri<T, D, KEYS, CAP, 2>(a, p, st)
-                                                 : launch_grad_ri<T, D, KEYS, CAP, 4>(a, p, st);
+    return few_ctas(a, p.N, KEYS ? a.Hkv : a.Hq) ? launch_grad_rows<T, D, KEYS, CAP, 32>(a, p, st)
+                                                 : launch_grad_rows<T, D, KEYS, CAP, 64>(a, p, st);
 }
 
 template <typename T, int D>
