@@ -19,9 +19,10 @@
 // sequences, by the longest CTA.  The training kernels at d 64 take 8 x 16
 // threads, which read less (8 to 64) and leave room for three CTAs to an SM: a
 // step of 509 tokens 211 -> 197 us, one of 2,048 and 32 + 8 heads 2.99 -> 2.70
-// ms.  A pre-fill of few CTAs has an SM to each,
-// and 128 threads hide less of the latency there (107 us with 256, 131 with
-// 128).
+// ms.  A pre-fill of few CTAs has an SM to each, where one such group hides too
+// little latency: two groups take alternate key tiles, each with its own
+// running softmax, and merge at the end (2 x 333 rows behind 900 tokens:
+// 106 us with 16 x 16 threads on one tile, 131 with 8 x 16, 91 with two groups).
 #include "cap.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -31,9 +32,12 @@ namespace duo {
 namespace {
 
 constexpr int TT = 64;              // rows of an inner tile
-// Threads of a CTA: 16 x 16, and 8 x 16 for the training kernels at d 64.
-template <int D, bool TRAIN>
-__host__ __device__ constexpr int tiled_threads() { return D == 64 && TRAIN ? 128 : 256; }
+// Threads that share an inner tile: 16 x 16; 8 x 16 for the training kernels
+// at d 64, and for pre-fills of few CTAs (32 rows), which have two such groups.
+template <int D, bool TRAIN, int OT>
+__host__ __device__ constexpr int tiled_threads() { return D == 64 && (TRAIN || OT == 32) ? 128 : 256; }
+template <int D, bool TRAIN, int OT>
+__host__ __device__ constexpr int tiled_groups() { return D == 64 && !TRAIN && OT == 32 ? 2 : 1; }
 
 template <int D>
 __host__ __device__ constexpr int row_stride() { return D + 4; }
@@ -50,18 +54,18 @@ struct Rows {
     static constexpr int kPer = ROWS * PPR / TH;
     uint4 w[kPer];
     template <typename F>
-    __device__ __forceinline__ void fetch(F src) {
+    __device__ __forceinline__ void fetch(int tid, F src) {
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-            const int i = threadIdx.x + k * TH;
+            const int i = tid + k * TH;
             const T* p = src(i / PPR);
             w[k] = p ? reinterpret_cast<const uint4*>(p)[i % PPR] : make_uint4(0u, 0u, 0u, 0u);
         }
     }
-    __device__ __forceinline__ void store(float* dst) const {
+    __device__ __forceinline__ void store(int tid, float* dst) const {
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-            const int i = threadIdx.x + k * TH, r = i / PPR, c = i % PPR * N;
+            const int i = tid + k * TH, r = i / PPR, c = i % PPR * N;
             float v[N];
             load_row_f32<T, N>(reinterpret_cast<const T*>(&w[k]), v);
 #pragma unroll
@@ -181,28 +185,40 @@ struct TiledArgs {
     float* lse;            // mix: [2][B][Hq][N]
 };
 
+// What a group has to itself: K, V, P (two of them for the mix), positions.
+template <int D, bool MIX, int OT>
+__host__ __device__ constexpr size_t group_floats() {
+    return 2 * tile_floats<D>(TT) + (MIX ? 2 : 1) * (size_t)TT * p_stride<OT>() + TT;
+}
 template <int D, bool MIX, int OT>
 constexpr size_t forward_smem() {
-    return (tile_floats<D>(OT) + 2 * tile_floats<D>(TT) + (MIX ? 2 : 1) * (size_t)TT * p_stride<OT>()) * sizeof(float) +
-           TT * sizeof(int);
+    return tile_floats<D>(OT) * sizeof(float) + tiled_groups<D, MIX, OT>() * group_floats<D, MIX, OT>() * sizeof(float);
 }
 
 template <typename T, int D, bool MIX, bool CAP, int OT>
-__global__ void __launch_bounds__(tiled_threads<D, MIX>()) tiled_forward_kernel(const LayerArgs a, const CacheArgs c,
-                                                                      const TiledArgs s) {
+__global__ void __launch_bounds__(tiled_threads<D, MIX, OT>() * tiled_groups<D, MIX, OT>())
+    tiled_forward_kernel(const LayerArgs a, const CacheArgs c, const TiledArgs s) {
     extern __shared__ __align__(16) float sm[];
-    constexpr int TH = tiled_threads<D, MIX>(), RI = 16 * OT / TH, PS = p_stride<OT>();   // OT query rows a CTA
+    constexpr int TH = tiled_threads<D, MIX, OT>(), GROUPS = tiled_groups<D, MIX, OT>();
+    constexpr int RI = 16 * OT / TH, PS = p_stride<OT>();   // OT query rows a CTA
+    const int tid = threadIdx.x % TH, group = threadIdx.x / TH;
+    auto group_sync = [&] {
+        if constexpr (GROUPS == 1)
+            __syncthreads();
+        else
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(TH) : "memory");
+    };
     float* sQ = sm;
-    float* sK = sQ + tile_floats<D>(OT);
+    float* sK = sQ + tile_floats<D>(OT) + group * group_floats<D, MIX, OT>();
     float* sV = sK + tile_floats<D>(TT);
     float* sP = sV + tile_floats<D>(TT);
     float* sP2 = sP + TT * PS;                        // mix only
     int* sPos = reinterpret_cast<int*>(sP + (MIX ? 2 : 1) * TT * PS);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int tx = tid & 15, ty = tid >> 4;
     const int tiles = (s.N + OT - 1) / OT, heads = a.B * a.Hq;
     // MIX: tile t of every head before the next shorter one (a step of 509 tokens
     // 233 -> 211 us); a pre-fill chunk's tiles are about as long as one another,
-    // and a head's tiles side by side keep its keys in L2 (105 us; 119 the other way)
+    // and a head's tiles side by side keep its keys in L2 (106 us; 119 the other way)
     const int t = MIX ? blockIdx.x / heads : blockIdx.x % tiles, bh = MIX ? blockIdx.x % heads : blockIdx.x / tiles;
     const int b = bh / a.Hq, hq = bh % a.Hq, slot = hq / a.G, g = hq % a.G;
     const int q_idx = a.q_head0[slot] + g, kv_idx = a.kv_head[slot];
@@ -218,13 +234,14 @@ __global__ void __launch_bounds__(tiled_threads<D, MIX>()) tiled_forward_kernel(
             c0 = c0 < 0 ? 0 : a.capacity;
         }
     }
-    {
+    if (group == 0) {
         Rows<T, D, OT, TH> q;
-        q.fetch([&](int r) -> const T* {
+        q.fetch(tid, [&](int r) -> const T* {
             return r0 + r < N ? static_cast<const T*>(s.q) + (((size_t)b * N + r0 + r) * a.Hq + q_idx) * D : nullptr;
         });
-        q.store(sQ);
+        q.store(tid, sQ);
     }
+    if constexpr (GROUPS > 1) __syncthreads();
     constexpr int W = D / 16;
     float o[RI][W], o2[MIX ? RI : 1][W], m[RI], l[RI], m2[RI], l2[RI];
 #pragma unroll
@@ -278,19 +295,26 @@ __global__ void __launch_bounds__(tiled_threads<D, MIX>()) tiled_forward_kernel(
             if (pos < 0 || pos >= c0) return nullptr;
             return static_cast<const T*>(ring) + (((size_t)b * a.S + (slot - a.R)) * a.W + kr) * D;
         };
-        nk_.fetch([&](int r) { return row(r, c.k_full, c.k_ring, s.k); });
-        nv_.fetch([&](int r) { return row(r, c.v_full, c.v_ring, s.v); });
+        nk_.fetch(tid, [&](int r) { return row(r, c.k_full, c.k_ring, s.k); });
+        nv_.fetch(tid, [&](int r) { return row(r, c.v_full, c.v_ring, s.v); });
+    };
+    // a group's tiles: every one, or every second
+    auto step_group = [&](int& sg, int& k) {
+        bool there = step(sg, k);
+        if (GROUPS > 1 && there) there = step(sg, k);
+        return there;
     };
     bool more = step(seg, k0);
+    if (group == 1 && more) more = step(seg, k0);
     if (prefetches<T, D>() && more) fetch(seg, k0);
     while (more) {
         const int nk = min(TT, end[seg] - k0);
-        __syncthreads();
+        group_sync();
         if (!prefetches<T, D>()) fetch(seg, k0);
-        nk_.store(sK);
-        nv_.store(sV);
-        if (threadIdx.x < TT) {
-            const int r = threadIdx.x;
+        nk_.store(tid, sK);
+        nv_.store(tid, sV);
+        if (tid < TT) {
+            const int r = tid;
             int pos = -1;
             if (r < nk) {
                 pos = MIX || seg > 0 ? c0 + k0 + r : retrieval ? k0 + r : c.ring_pos[(size_t)b * a.W + k0 + r];
@@ -298,9 +322,9 @@ __global__ void __launch_bounds__(tiled_threads<D, MIX>()) tiled_forward_kernel(
             }
             sPos[r] = pos;
         }
-        __syncthreads();
+        group_sync();
         int seg1 = seg, k1 = k0;
-        more = step(seg1, k1);
+        more = step_group(seg1, k1);
         if (prefetches<T, D>() && more) fetch(seg1, k1);
         float x[RI][4], x2[RI][4];
         tile_dot<D, RI>(sQ, sK, tx, ty, x);
@@ -328,13 +352,37 @@ __global__ void __launch_bounds__(tiled_threads<D, MIX>()) tiled_forward_kernel(
                 put_transposed<RI, PS>(sP2, x2, tx, ty);
             }
         }
-        __syncthreads();
+        group_sync();
         tile_acc<D, RI, PS>(sP, sV, tx, ty, o);
         if constexpr (MIX) {
             if (lam_tile) tile_acc<D, RI, PS>(sP2, sV, tx, ty, o2);
         }
         seg = seg1;
         k0 = k1;
+    }
+    if constexpr (GROUPS > 1) {
+        // the second group's (m, l, o) through its K tile, merged by the first
+        static_assert(RI * (W + 2) * TH <= tile_floats<D>(TT), "a K tile holds a group's state");
+        float* rec = sQ + tile_floats<D>(OT) + group_floats<D, MIX, OT>() + tid;
+        if (group == 1) {
+#pragma unroll
+            for (int i = 0; i < RI; ++i) {
+                rec[(i * (W + 2)) * TH] = m[i];
+                rec[(i * (W + 2) + 1) * TH] = l[i];
+#pragma unroll
+                for (int e = 0; e < W; ++e) rec[(i * (W + 2) + 2 + e) * TH] = o[i][e];
+            }
+        }
+        __syncthreads();
+        if (group == 1) return;
+#pragma unroll
+        for (int i = 0; i < RI; ++i) {
+            const float m1 = rec[(i * (W + 2)) * TH], mn = fmaxf(m[i], m1);
+            const float w0 = exp2f(m[i] - mn), w1 = exp2f(m1 - mn);
+            l[i] = l[i] * w0 + rec[(i * (W + 2) + 1) * TH] * w1;
+#pragma unroll
+            for (int e = 0; e < W; ++e) o[i][e] = o[i][e] * w0 + rec[(i * (W + 2) + 2 + e) * TH] * w1;
+        }
     }
     const float al = MIX ? s.alpha[kv_idx] : 0.f;
 #pragma unroll
@@ -468,9 +516,9 @@ constexpr size_t grad_smem() {
 }
 
 template <typename T, int D, bool KEYS, bool CAP, int OT>
-__global__ void __launch_bounds__(tiled_threads<D, true>()) tiled_grad_kernel(const LayerArgs a, const TiledGradArgs p) {
+__global__ void __launch_bounds__(tiled_threads<D, true, OT>()) tiled_grad_kernel(const LayerArgs a, const TiledGradArgs p) {
     extern __shared__ __align__(16) float sm[];
-    constexpr int TH = tiled_threads<D, true>(), RI = 16 * OT / TH, PS = p_stride<OT>();   // OT outer rows a CTA
+    constexpr int TH = tiled_threads<D, true, OT>(), RI = 16 * OT / TH, PS = p_stride<OT>();   // OT outer rows a CTA
     float* sX0 = sm;
     float* sX1 = sX0 + tile_floats<D>(OT);
     float* sY0 = sX1 + tile_floats<D>(OT);
@@ -500,10 +548,10 @@ __global__ void __launch_bounds__(tiled_threads<D, true>()) tiled_grad_kernel(co
     };
     {
         Rows<T, D, OT, TH> x0, x1;
-        x0.fetch(KEYS ? rows(p.k, a.Hkv, kv, o0) : rows(p.q, a.Hq, head, o0));
-        x1.fetch(KEYS ? rows(p.v, a.Hkv, kv, o0) : rows(p.dout, a.Hq, head, o0));
-        x0.store(sX0);
-        x1.store(sX1);
+        x0.fetch(threadIdx.x, KEYS ? rows(p.k, a.Hkv, kv, o0) : rows(p.q, a.Hq, head, o0));
+        x1.fetch(threadIdx.x, KEYS ? rows(p.v, a.Hkv, kv, o0) : rows(p.dout, a.Hq, head, o0));
+        x0.store(threadIdx.x, sX0);
+        x1.store(threadIdx.x, sX1);
         if (!KEYS) load_stats(head, o0, OT);
     }
     constexpr int W = D / 16;
@@ -524,16 +572,16 @@ __global__ void __launch_bounds__(tiled_threads<D, true>()) tiled_grad_kernel(co
     Rows<T, D, TT, TH> y0, y1;
     auto fetch = [&](int j) {
         const int first = (it0 + j % per_head) * TT, qh = kv * a.G + j / per_head;
-        y0.fetch(KEYS ? rows(p.q, a.Hq, qh, first) : rows(p.k, a.Hkv, kv, first));
-        y1.fetch(KEYS ? rows(p.dout, a.Hq, qh, first) : rows(p.v, a.Hkv, kv, first));
+        y0.fetch(threadIdx.x, KEYS ? rows(p.q, a.Hq, qh, first) : rows(p.k, a.Hkv, kv, first));
+        y1.fetch(threadIdx.x, KEYS ? rows(p.dout, a.Hq, qh, first) : rows(p.v, a.Hkv, kv, first));
     };
     if (prefetches<T, D>()) fetch(0);
     for (int j0 = 0; j0 < n_in; ++j0) {
         const int it = it0 + j0 % per_head, qh = KEYS ? kv * a.G + j0 / per_head : head;
         __syncthreads();
         if (!prefetches<T, D>()) fetch(j0);
-        y0.store(sY0);
-        y1.store(sY1);
+        y0.store(threadIdx.x, sY0);
+        y1.store(threadIdx.x, sY1);
         if (KEYS) load_stats(qh, it * TT, TT);
         __syncthreads();
         if (prefetches<T, D>() && j0 + 1 < n_in) fetch(j0 + 1);
@@ -610,7 +658,7 @@ cudaError_t launch_forward_rows(const LayerArgs& a, const CacheArgs& c, const Ti
     if (e != cudaSuccess) return e;
     const long ctas = (long)a.B * a.Hq * ((s.N + OT - 1L) / OT);
     if (ctas > 0x7fffffffL) return cudaErrorInvalidConfiguration;
-    tiled_forward_kernel<T, D, MIX, CAP, OT><<<(unsigned)ctas, tiled_threads<D, MIX>(), smem, st>>>(a, c, s);
+    tiled_forward_kernel<T, D, MIX, CAP, OT><<<(unsigned)ctas, tiled_threads<D, MIX, OT>() * tiled_groups<D, MIX, OT>(), smem, st>>>(a, c, s);
     return cudaGetLastError();
 }
 template <typename T, int D, bool MIX, bool CAP>
@@ -627,7 +675,7 @@ cudaError_t launch_grad_rows(const LayerArgs& a, const TiledGradArgs& p, cudaStr
     if (e != cudaSuccess) return e;
     const long ctas = (long)a.B * (KEYS ? a.Hkv : a.Hq) * ((p.N + OT - 1L) / OT);
     if (ctas > 0x7fffffffL) return cudaErrorInvalidConfiguration;
-    tiled_grad_kernel<T, D, KEYS, CAP, OT><<<(unsigned)ctas, tiled_threads<D, true>(), smem, st>>>(a, p);
+    tiled_grad_kernel<T, D, KEYS, CAP, OT><<<(unsigned)ctas, tiled_threads<D, true, OT>(), smem, st>>>(a, p);
     return cudaGetLastError();
 }
 template <typename T, int D, bool KEYS, bool CAP>
