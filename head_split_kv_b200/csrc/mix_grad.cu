@@ -36,10 +36,13 @@
 // mix_grad_kernel, twice: with keys outer (dK, dV: a CTA owns 128 keys of one
 // KV head and walks the 128-query tiles at or below the diagonal of every
 // query head of the group) and with queries outer (dQ: 128 queries of one
-// query head, walking the key tiles up to the diagonal).  So no partial sum
-// leaves a CTA: no atomics, results do not depend on the order CTAs run in,
-// and the heads of a group are summed in the accumulator.  The price is that
-// S and dP are computed in both (7 products instead of 5).
+// query head, walking the key tiles up to the diagonal).  Where the first key
+// tile alone would outlast an SM's share, the two CTAs of a cluster halve a
+// tile's queries and each adds the other's part of one accumulator through
+// shared memory (share_key_tiles).  So no partial sum goes through global
+// memory: no atomics, results do not depend on the order CTAs run in, and the
+// heads of a group are summed in the accumulator.  The price is that S and dP
+// are computed in both (7 products instead of 5).
 //   outer tiles X0, X1 = K, V (or Q, dout), resident in shared memory;
 //   inner tiles Y0, Y1 = Q, dout (or K, V), TMA into a 2-stage ring.
 //   S = X0 Y0^T, dP = X1 Y1^T (lane = outer row), then W and dS, rounded to
@@ -103,12 +106,31 @@ struct GradArgs {
     TanhPoly poly;         // tanh(k x)
 };
 
-// What a launch computes: the rows' statistics, dK and dV (keys outer), or dQ.
-enum { STATS = 0, KEYS = 1, QUERIES = 2 };
+// What a launch computes: the rows' statistics, dK and dV (keys outer; with
+// pairs of CTAs that share a key tile), or dQ.
+enum { STATS = 0, KEYS = 1, QUERIES = 2, KEY_PAIRS = 3 };
+__host__ __device__ constexpr bool keys_outer(int mode) { return mode == KEYS || mode == KEY_PAIRS; }
 
 __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
     __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
     return *reinterpret_cast<uint32_t*>(&h);
+}
+
+// Every thread of the cluster's CTAs, what they wrote to shared memory visible after it.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile(
+        "barrier.cluster.arrive.release.aligned;\n\t"
+        "barrier.cluster.wait.acquire.aligned;" ::
+            : "memory");
+}
+// The address of this CTA's shared-memory location in CTA `rank` of the cluster, and a store there.
+__device__ __forceinline__ uint32_t peer_smem(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void st_peer(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 // Bits lo .. hi (inclusive, clipped to 0 .. 31).
@@ -340,7 +362,7 @@ __device__ __forceinline__ void add_sums(RowSums& sum, const LayerArgs& a, float
 
 // TMEM columns of S(j) and dP(j).
 template <int MODE>
-__device__ __forceinline__ uint32_t s_col(int j) { return MODE != KEYS && (j & 1) ? kColA1 : kColS; }
+__device__ __forceinline__ uint32_t s_col(int j) { return !keys_outer(MODE) && (j & 1) ? kColA1 : kColS; }
 template <int MODE>
 __device__ __forceinline__ uint32_t d_col(int j) { return MODE == STATS && (j & 1) ? kColA2 : kColP; }
 
@@ -349,7 +371,7 @@ __global__ void __launch_bounds__(kRegThreads, 1)
     mix_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDo,
                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const GradArgs p) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    constexpr bool kKeys = MODE == KEYS, kStats = MODE == STATS;
+    constexpr bool kKeys = keys_outer(MODE), kStats = MODE == STATS, kPairs = MODE == KEY_PAIRS;
     const LayerArgs& a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if ((smem_u32(smem) & 1023u) != 0) {   // the swizzled layouts need 1024-byte alignment
@@ -371,15 +393,19 @@ __global__ void __launch_bounds__(kRegThreads, 1)
     // Work item, the longest first.  Keys outer: key tile ot of KV head `head`,
     // whose inner tiles are (query head of the group, query tile >= ot);
     // queries outer: query tile ot of query head `head`, key tiles 0 .. ot.
+    // Pairs: a cluster of two CTAs takes an item, half of its inner tiles each.
     const int heads = kKeys ? a.Hkv : a.Hq;
-    const int ord = blockIdx.x / (a.B * heads), rest = blockIdx.x % (a.B * heads);
+    const int item = kPairs ? blockIdx.x >> 1 : blockIdx.x, part = kPairs ? blockIdx.x & 1 : 0;
+    const int ord = item / (a.B * heads), rest = item % (a.B * heads);
     const int head = rest % heads, b = rest / heads;
     const int ot = kKeys ? ord : p.n_tiles - 1 - ord;
     const int kv = kKeys ? head : head / a.G;
     const int per_head = p.n_tiles - ot;                   // keys outer: query tiles per query head
-    const int n_in = kKeys ? a.G * per_head : ot + 1;
-    auto inner_tile = [&](int j) { return kKeys ? ot + j % per_head : j; };
-    auto inner_qhead = [&](int j) { return kKeys ? kv * a.G + j / per_head : head; };
+    const int n_all = kKeys ? a.G * per_head : ot + 1;
+    const int j_first = part * ((n_all + 1) / 2);          // this CTA's: j_first .. j_first + n_in - 1, none if n_all is 1
+    const int n_in = !kPairs ? n_all : part ? n_all / 2 : (n_all + 1) / 2;
+    auto inner_tile = [&](int j) { return kKeys ? ot + (j_first + j) % per_head : j; };
+    auto inner_qhead = [&](int j) { return kKeys ? kv * a.G + (j_first + j) / per_head : head; };
 
     if (warp == kMmaWarp) tmem_alloc(holder, kTmemCols);
     if (tid == 0) {
@@ -401,8 +427,9 @@ __global__ void __launch_bounds__(kRegThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *holder;
 
+    bool ok = n_in > 0;   // element-wise warps: the accumulators are complete
     if (warp == kTmaWarp) {
-        if (lane == 0) {
+        if (lane == 0 && n_in > 0) {
             const CUtensorMap* mx0 = kKeys ? &tmK : &tmQ;
             const CUtensorMap* mx1 = kKeys ? &tmV : &tmDo;
             const CUtensorMap* my0 = kKeys ? &tmQ : &tmK;
@@ -462,7 +489,7 @@ __global__ void __launch_bounds__(kRegThreads, 1)
                 issue_xy(d_col<MODE>(j), 1, j);
                 tc_commit(&d_full[j & 1]);
             };
-            bool ok = mbar_wait(x_full, 0, p.status) && wait_tile(0);
+            ok = ok && mbar_wait(x_full, 0, p.status) && wait_tile(0);
             if (ok) {
                 tc_fence_after();
                 if (elect_one()) {
@@ -550,7 +577,6 @@ __global__ void __launch_bounds__(kRegThreads, 1)
             const float* st = p.stats + ((size_t)b * a.Hq + head) * 4 * p.n_pad + orow;
             rs = {st[0], st[p.n_pad], st[2 * (size_t)p.n_pad], st[3 * (size_t)p.n_pad], nullptr};
         }
-        bool ok = true;
         int it = inner_tile(0) - 1;                           // inner_tile(j), step by step
         for (int j = 0; j < n_in; ++j) {
             it = it + 1 < p.n_tiles || !kKeys ? it + 1 : ot;
@@ -661,17 +687,58 @@ __global__ void __launch_bounds__(kRegThreads, 1)
                     p.part[(((size_t)kv * a.B + b) * p.n_tiles + ot) * a.G + head % a.G] =
                         (share[0] + share[1]) + (share[2] + share[3]);
             }
-        } else if (ok) {
-            tc_fence_after();
-            const size_t off = (((size_t)b * p.N + orow) * heads + head) * HD + kCols * wg;
-            const bool live = orow < p.N && bounds_ok(b < a.B && head < heads, p.status);
+        }
+        // one warp per KV head adds up the shares of dalpha, in their order
+        if (kKeys && ot == 0 && b == 0 && part == 0 && warp == 0) {
+            const int n = a.B * p.n_tiles * a.G;
+            sum_shares(p.part + (size_t)kv * n, n, &p.dalpha[kv], lane);
+        }
+    }
+    if constexpr (!kStats) {
+        // Pairs: each CTA hands one accumulator to the other, over the tiles that are
+        // done with (64 KB, [column][row]), and stores the sum of the other
+        // accumulator: the first dK, the second dV.
+        const int wg = warp >> 2, row = 32 * (warp & 3) + lane;
+        const bool elem = warp < kElemWarps;
+        const uint32_t acc = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kCols * wg;
+        const uint32_t slot = (uint32_t)((kCols * wg * BM + row) * 4);
+        auto take = [&](uint32_t col, float (&v)[kCols]) {
+            if (ok) {
+                tc_fence_after();
+                tmem_ld32(acc + col, v);
+            } else {
 #pragma unroll
-            for (int t = 0; t < (kKeys ? 2 : 1); ++t) {
+                for (int i = 0; i < kCols; ++i) v[i] = 0.f;
+            }
+        };
+        float v[kCols];
+        if constexpr (kPairs) {
+            __syncwarp();
+            cluster_sync();
+            if (elem) {
+                take(part ? kColA2 : kColA1, v);
+                const uint32_t to = peer_smem(sY, part ^ 1) + slot;
+#pragma unroll
+                for (int i = 0; i < kCols; ++i) st_peer(to + i * BM * 4, v[i]);
+            }
+            __syncwarp();
+            cluster_sync();
+        }
+        if (elem) {
+            const int orow = BM * ot + row;
+            const bool live = orow < p.N && (kPairs || ok) && bounds_ok(b < a.B && head < heads, p.status);
+            const size_t off = (((size_t)b * p.N + orow) * heads + head) * HD + kCols * wg;
+            const float sign = p.alpha[kv] < 0.f ? -1.f : 1.f;   // a negative gate's sums are negated
+#pragma unroll
+            for (int t = kPairs ? part : 0; t < (kPairs ? part + 1 : kKeys ? 2 : 1); ++t) {
+                take(t ? kColA1 : kColA2, v);
+                if constexpr (kPairs) {
+                    const float* peer = reinterpret_cast<const float*>(smem + kOffY + slot);
+#pragma unroll
+                    for (int i = 0; i < kCols; ++i) v[i] += peer[i * BM];
+                }
                 __nv_bfloat16* o = static_cast<__nv_bfloat16*>(t ? p.d1 : p.d0) + off;
-                // dS held back the softmax scale; a negative gate's sums are negated
-                const float f = (t ? 1.f : CAP ? -a.scale : a.scale) * (neg_c ? -1.f : 1.f);
-                float v[kCols];
-                tmem_ld32(lane_addr + (t ? kColA1 : kColA2) + kCols * wg, v);
+                const float f = (t ? 1.f : CAP ? -a.scale : a.scale) * sign;   // dS held back the softmax scale
 #pragma unroll
                 for (int e = 0; e < kCols / 8; ++e) {
                     float v8[8];
@@ -680,11 +747,6 @@ __global__ void __launch_bounds__(kRegThreads, 1)
                     if (live) store_row<__nv_bfloat16, 8>(o + 8 * e, v8);
                 }
             }
-        }
-        // one warp per KV head adds up the shares of dalpha, in their order
-        if (kKeys && ot == 0 && b == 0 && warp == 0) {
-            const int n = a.B * p.n_tiles * a.G;
-            sum_shares(p.part + (size_t)kv * n, n, &p.dalpha[kv], lane);
         }
     }
     tc_fence_before();
@@ -700,10 +762,31 @@ cudaError_t launch_grad(const CUtensorMap (&m)[4], const GradArgs& p, cudaStream
     static std::atomic<unsigned long long> configured{0};
     const cudaError_t e = smem_limit_once(mix_grad_kernel<MODE, CAP>, (int)kGradSmem, configured);
     if (e != cudaSuccess) return e;
-    const long grid = (long)p.a.B * (MODE == KEYS ? p.a.Hkv : p.a.Hq) * p.n_tiles;
+    const long grid = (long)p.a.B * (keys_outer(MODE) ? p.a.Hkv : p.a.Hq) * p.n_tiles * (MODE == KEY_PAIRS ? 2 : 1);
     if (grid > 0x7fffffffL) return cudaErrorInvalidConfiguration;
-    mix_grad_kernel<MODE, CAP><<<(unsigned)grid, kGradThreads, kGradSmem, s>>>(m[0], m[1], m[2], m[3], p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kGradThreads);
+    cfg.dynamicSmemBytes = kGradSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute cluster{};
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = MODE == KEY_PAIRS ? 2 : 1;
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    cfg.attrs = &cluster;
+    cfg.numAttrs = MODE == KEY_PAIRS ? 1 : 0;
+    const cudaError_t launched = cudaLaunchKernelEx(&cfg, mix_grad_kernel<MODE, CAP>, m[0], m[1], m[2], m[3], p);
+    return launched != cudaSuccess ? launched : cudaGetLastError();
+}
+
+// Two CTAs to a key tile where the first, seen by every query of its group,
+// would take one CTA longer than an SM's share of all tiles: a whole step of
+// 4,096 tokens and 32 + 8 heads 900 -> 876 us, of 1,000 tokens 169 -> 136; with
+// 32 + 32 heads at 4,096, below the rule, pairs lose (923 -> 1,004: the pair's
+// exchange and its second load of K and V).
+bool share_key_tiles(const LayerArgs& a, int n_tiles) {
+    const long all = (long)a.B * a.Hkv * n_tiles * (n_tiles + 1) / 2;   // in tiles of one query head, as the next
+    return (long)n_tiles * sm_count() > all;
 }
 
 }  // namespace
@@ -736,7 +819,10 @@ cudaError_t launch_mix_grad_tc(const LayerArgs& a, const MixGradArgs& g, int N, 
     if (e != cudaSuccess) return e;
     p.d0 = g.dk;
     p.d1 = g.dv;
-    e = a.cap.on ? launch_grad<KEYS, true>(m, p, s) : launch_grad<KEYS, false>(m, p, s);
+    if (share_key_tiles(a, pl.n_tiles))
+        e = a.cap.on ? launch_grad<KEY_PAIRS, true>(m, p, s) : launch_grad<KEY_PAIRS, false>(m, p, s);
+    else
+        e = a.cap.on ? launch_grad<KEYS, true>(m, p, s) : launch_grad<KEYS, false>(m, p, s);
     if (e != cudaSuccess) return e;
     p.d0 = g.dq;
     p.d1 = nullptr;

@@ -49,6 +49,8 @@ CASES = [   # hq, hkv, d, dtype, B, N, cap, gain, sink, recent, alpha
     (4, 2, 128, "bf16", 1, 1, 30.0, 3.0, 16, 64, None),
     (4, 2, 128, "bf16", 1, 300, 200.0, 3.0, 16, 64, None),            # a cap too high for exponentials without a maximum
     (4, 2, 128, "bf16", 3, 129, 30.0, 3.0, 100, 28, None),
+    (32, 32, 128, "bf16", 5, 129, 30.0, 3.0, 16, 64, None),           # enough key tiles for a CTA each
+    (64, 32, 128, "bf16", 4, 190, 0.0, 1.0, 16, 64, None),
     (4, 4, 128, "bf16", 1, 200, 30.0, 3.0, 130, 200, None),           # a window the tensor-core kernels do not take
     (8, 4, 64, "bf16", 2, 130, 30.0, 3.0, 16, 64, None),
     (8, 4, 64, "fp32", 2, 201, 20.0, 3.0, 16, 64, [0.0, 1.0, -0.5, 2.0]),
