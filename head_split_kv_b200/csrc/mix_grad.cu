@@ -42,7 +42,7 @@
 // shared memory (share_key_tiles).  So no partial sum goes through global
 // memory: no atomics, results do not depend on the order CTAs run in, and the
 // heads of a group are summed in the accumulator.  The price is that S and dP
-// are computed in both (7 products instead of 5).
+// are computed in every launch (9 products instead of 5).
 //   outer tiles X0, X1 = K, V (or Q, dout), resident in shared memory;
 //   inner tiles Y0, Y1 = Q, dout (or K, V), TMA into a 2-stage ring.
 //   S = X0 Y0^T, dP = X1 Y1^T (lane = outer row), then W and dS, rounded to
