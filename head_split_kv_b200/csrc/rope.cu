@@ -24,8 +24,8 @@
 // A head row is cut into units of two 16-byte pieces.  Where the pairs are
 // (i, i + rot/2) a unit takes the two pieces whose elements pair up, so both
 // results come from registers (and in-place calls need no care); where the
-// pairs are neighbours each piece is its own.  Rotations whose half is not a
-// whole number of pieces take one pair a unit (element accesses).
+// pairs are neighbours each piece is its own.  Rotations whose pairs do not
+// fill whole units take one pair a unit (element accesses).
 //
 // Bound: HBM for long chunks (each row read once and written once), launch
 // and load latency for a decode step's rows.
@@ -79,16 +79,6 @@ __device__ __forceinline__ void rotate(float& a, float& b, float c, float s) {
     a = fmaf(x, c, -y * s);
     b = fmaf(y, c, x * s);
 }
-// A pair past the rotation (by 1, 0) keeps its bits: 0 times an infinity would
-// spoil its partner, and -0 would become 0.
-__device__ __forceinline__ void rotate_or_keep(float& a, float& b, float c, float s) {
-    float x = a, y = b;
-    rotate(x, y, c, s);
-    const bool keep = c == 1.f && s == 0.f;
-    a = keep ? a : x;
-    b = keep ? b : y;
-}
-
 // One 16-byte piece as fp32 pairs and back (rounded once).
 template <typename T>
 struct Piece;
@@ -149,10 +139,10 @@ __device__ __forceinline__ void turn_unit(const RopeArgs& r, const float2 (&c)[P
     } else {
 #pragma unroll
         for (int i = 0; i < N / 4; ++i) {
-            rotate_or_keep(a[2 * i].x, a[2 * i].y, c[i].x, s[i].x);
-            rotate_or_keep(a[2 * i + 1].x, a[2 * i + 1].y, c[i].y, s[i].y);
-            rotate_or_keep(b[2 * i].x, b[2 * i].y, c[N / 4 + i].x, s[N / 4 + i].x);
-            rotate_or_keep(b[2 * i + 1].x, b[2 * i + 1].y, c[N / 4 + i].y, s[N / 4 + i].y);
+            rotate(a[2 * i].x, a[2 * i].y, c[i].x, s[i].x);
+            rotate(a[2 * i + 1].x, a[2 * i + 1].y, c[i].y, s[i].y);
+            rotate(b[2 * i].x, b[2 * i].y, c[N / 4 + i].x, s[N / 4 + i].x);
+            rotate(b[2 * i + 1].x, b[2 * i + 1].y, c[N / 4 + i].y, s[N / 4 + i].y);
         }
     }
     w0 = Piece<T>::pack(a);
@@ -245,8 +235,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const LayerArgs a, c
     if constexpr (VEC) {
         constexpr int N = Piece<T>::N, kUnits = D / (2 * N);   // units of a row
         const int k = threadIdx.x % kUnits, step = blockDim.x / kUnits;
-        // does this thread turn anything?  (pairs past the rotation: by 1, 0)
-        const bool turns = k * N < (x.r.layout == DUO_ROPE_HALVES ? half : (half + N - 1) / N * N);
+        const bool turns = k * N < half;               // whole units turn or pass
         float2 cc[N / 2], ss[N / 2];
         int L = 0;
         bool ready = false;
@@ -273,8 +262,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const LayerArgs a, c
 #pragma unroll
                 for (int i = 0; i < N / 2; ++i) {
                     const int pr = k * N + 2 * i;
-                    cc[i] = make_float2(pr < half ? cos_t[pr] : 1.f, pr + 1 < half ? cos_t[pr + 1] : 1.f);
-                    ss[i] = make_float2(pr < half ? sin_t[pr] : 0.f, pr + 1 < half ? sin_t[pr + 1] : 0.f);
+                    cc[i] = turns ? *reinterpret_cast<const float2*>(cos_t + pr) : make_float2(1.f, 1.f);
+                    ss[i] = turns ? *reinterpret_cast<const float2*>(sin_t + pr) : make_float2(0.f, 0.f);
                 }
             }
 #pragma unroll
@@ -298,7 +287,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const LayerArgs a, c
             T* dst = src ? row_dst<T, APPEND>(a, c, x, bt, b, t, row, L, k == 0) : nullptr;
             if (!dst) continue;
             const bool is_pair = turned && k < half;
-            const int e0 = is_pair ? k : 2 * k, e1 = is_pair ? k + half : 2 * k + 1;   // halves layout
+            const bool apart = is_pair && x.r.layout == DUO_ROPE_HALVES;
+            const int e0 = apart ? k : 2 * k, e1 = apart ? k + half : 2 * k + 1;
             float v0 = Elem<T>::to_f32(src[e0]), v1 = Elem<T>::to_f32(src[e1]);
             if (is_pair) rotate(v0, v1, cos_t[k], sin_t[k]);
             dst[e0] = Elem<T>::from_f32(v0);
@@ -400,7 +390,7 @@ cudaError_t launch_t(const LayerArgs& a, const CacheArgs& c, RopeKernelArgs x, c
     const long tokens = (long)a.B * x.T;
     if (tokens > 0x7fffffffL) return cudaErrorInvalidConfiguration;
     constexpr int N = Piece<T>::N, kUnits = D / (2 * N);
-    const bool vec = x.r.layout == DUO_ROPE_PAIRS || (x.r.rot_dim / 2) % N == 0;
+    const bool vec = (x.r.rot_dim / 2) % N == 0;
     // a CTA's rows: as many as its threads hold in kAhead units each, fewer
     // when the tokens alone do not fill the SMs (a decode step)
     const int room = kAhead * kRopeThreads / kUnits;

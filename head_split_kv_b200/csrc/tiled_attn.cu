@@ -19,10 +19,11 @@
 // sequences, by the longest CTA.  The training kernels at d 64 take 8 x 16
 // threads, which read less (8 to 64) and leave room for three CTAs to an SM: a
 // step of 509 tokens 211 -> 197 us, one of 2,048 and 32 + 8 heads 2.99 -> 2.70
-// ms.  A pre-fill of few CTAs has an SM to each, where one such group hides too
-// little latency: two groups take alternate key tiles, each with its own
-// running softmax, and merge at the end (2 x 333 rows behind 900 tokens:
-// 106 us with 16 x 16 threads on one tile, 131 with 8 x 16, 91 with two groups).
+// ms.  In small grids a CTA has much of an SM to itself, where one such group
+// hides too little latency: two groups take alternate inner tiles, each with
+// its own sums (or running softmax), and merge at the end: that step 197 -> 142
+// us; a pre-fill of 2 x 333 rows behind 900 tokens 106 us with 16 x 16 threads
+// on one tile, 131 with 8 x 16, 91 with two groups.
 #include "cap.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -33,11 +34,18 @@ namespace {
 
 constexpr int TT = 64;              // rows of an inner tile
 // Threads that share an inner tile: 16 x 16; 8 x 16 for the training kernels
-// at d 64, and for pre-fills of few CTAs (32 rows), which have two such groups.
+// at d 64, and in CTAs of 32 rows (small grids), which have two such groups.
 template <int D, bool TRAIN, int OT>
 __host__ __device__ constexpr int tiled_threads() { return D == 64 && (TRAIN || OT == 32) ? 128 : 256; }
-template <int D, bool TRAIN, int OT>
-__host__ __device__ constexpr int tiled_groups() { return D == 64 && !TRAIN && OT == 32 ? 2 : 1; }
+template <int D, int OT>
+__host__ __device__ constexpr int tiled_groups() { return D == 64 && OT == 32 ? 2 : 1; }
+template <int GROUPS, int TH>
+__device__ __forceinline__ void group_sync(int group) {
+    if constexpr (GROUPS == 1)
+        __syncthreads();
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(TH) : "memory");
+}
 
 template <int D>
 __host__ __device__ constexpr int row_stride() { return D + 4; }
@@ -192,22 +200,16 @@ __host__ __device__ constexpr size_t group_floats() {
 }
 template <int D, bool MIX, int OT>
 constexpr size_t forward_smem() {
-    return tile_floats<D>(OT) * sizeof(float) + tiled_groups<D, MIX, OT>() * group_floats<D, MIX, OT>() * sizeof(float);
+    return tile_floats<D>(OT) * sizeof(float) + tiled_groups<D, OT>() * group_floats<D, MIX, OT>() * sizeof(float);
 }
 
 template <typename T, int D, bool MIX, bool CAP, int OT>
-__global__ void __launch_bounds__(tiled_threads<D, MIX, OT>() * tiled_groups<D, MIX, OT>())
+__global__ void __launch_bounds__(tiled_threads<D, MIX, OT>() * tiled_groups<D, OT>())
     tiled_forward_kernel(const LayerArgs a, const CacheArgs c, const TiledArgs s) {
     extern __shared__ __align__(16) float sm[];
-    constexpr int TH = tiled_threads<D, MIX, OT>(), GROUPS = tiled_groups<D, MIX, OT>();
+    constexpr int TH = tiled_threads<D, MIX, OT>(), GROUPS = tiled_groups<D, OT>();
     constexpr int RI = 16 * OT / TH, PS = p_stride<OT>();   // OT query rows a CTA
     const int tid = threadIdx.x % TH, group = threadIdx.x / TH;
-    auto group_sync = [&] {
-        if constexpr (GROUPS == 1)
-            __syncthreads();
-        else
-            asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(TH) : "memory");
-    };
     float* sQ = sm;
     float* sK = sQ + tile_floats<D>(OT) + group * group_floats<D, MIX, OT>();
     float* sV = sK + tile_floats<D>(TT);
@@ -309,7 +311,7 @@ __global__ void __launch_bounds__(tiled_threads<D, MIX, OT>() * tiled_groups<D, 
     if (prefetches<T, D>() && more) fetch(seg, k0);
     while (more) {
         const int nk = min(TT, end[seg] - k0);
-        group_sync();
+        group_sync<GROUPS, TH>(group);
         if (!prefetches<T, D>()) fetch(seg, k0);
         nk_.store(tid, sK);
         nv_.store(tid, sV);
@@ -322,7 +324,7 @@ __global__ void __launch_bounds__(tiled_threads<D, MIX, OT>() * tiled_groups<D, 
             }
             sPos[r] = pos;
         }
-        group_sync();
+        group_sync<GROUPS, TH>(group);
         int seg1 = seg, k1 = k0;
         more = step_group(seg1, k1);
         if (prefetches<T, D>() && more) fetch(seg1, k1);
@@ -352,7 +354,7 @@ __global__ void __launch_bounds__(tiled_threads<D, MIX, OT>() * tiled_groups<D, 
                 put_transposed<RI, PS>(sP2, x2, tx, ty);
             }
         }
-        group_sync();
+        group_sync<GROUPS, TH>(group);
         tile_acc<D, RI, PS>(sP, sV, tx, ty, o);
         if constexpr (MIX) {
             if (lam_tile) tile_acc<D, RI, PS>(sP2, sV, tx, ty, o2);
@@ -361,28 +363,39 @@ __global__ void __launch_bounds__(tiled_threads<D, MIX, OT>() * tiled_groups<D, 
         k0 = k1;
     }
     if constexpr (GROUPS > 1) {
-        // the second group's (m, l, o) through its K tile, merged by the first
-        static_assert(RI * (W + 2) * TH <= tile_floats<D>(TT), "a K tile holds a group's state");
+        // the second group's (m, l, o) through its K and V tiles, merged by the first
+        constexpr int kState = RI * (W + 2);
+        static_assert((MIX ? 2 : 1) * kState * TH <= 2 * tile_floats<D>(TT), "the tiles hold a group's state");
         float* rec = sQ + tile_floats<D>(OT) + group_floats<D, MIX, OT>() + tid;
-        if (group == 1) {
+        auto put = [&](float* r, const float (&ms)[RI], const float (&ls)[RI], const float (&acc)[RI][W]) {
 #pragma unroll
             for (int i = 0; i < RI; ++i) {
-                rec[(i * (W + 2)) * TH] = m[i];
-                rec[(i * (W + 2) + 1) * TH] = l[i];
+                r[(i * (W + 2)) * TH] = ms[i];
+                r[(i * (W + 2) + 1) * TH] = ls[i];
 #pragma unroll
-                for (int e = 0; e < W; ++e) rec[(i * (W + 2) + 2 + e) * TH] = o[i][e];
+                for (int e = 0; e < W; ++e) r[(i * (W + 2) + 2 + e) * TH] = acc[i][e];
             }
+        };
+        auto merge = [&](const float* r, float (&ms)[RI], float (&ls)[RI], float (&acc)[RI][W]) {
+#pragma unroll
+            for (int i = 0; i < RI; ++i) {
+                const float m1 = r[(i * (W + 2)) * TH], mn = fmaxf(ms[i], m1);
+                const float w0 = exp2f(ms[i] - mn), w1 = exp2f(m1 - mn);
+                ms[i] = mn;
+                ls[i] = ls[i] * w0 + r[(i * (W + 2) + 1) * TH] * w1;
+#pragma unroll
+                for (int e = 0; e < W; ++e) acc[i][e] = acc[i][e] * w0 + r[(i * (W + 2) + 2 + e) * TH] * w1;
+            }
+        };
+        if (group == 1) {
+            group_sync<GROUPS, TH>(group);
+            put(rec, m, l, o);
+            if constexpr (MIX) put(rec + kState * TH, m2, l2, o2);
         }
         __syncthreads();
         if (group == 1) return;
-#pragma unroll
-        for (int i = 0; i < RI; ++i) {
-            const float m1 = rec[(i * (W + 2)) * TH], mn = fmaxf(m[i], m1);
-            const float w0 = exp2f(m[i] - mn), w1 = exp2f(m1 - mn);
-            l[i] = l[i] * w0 + rec[(i * (W + 2) + 1) * TH] * w1;
-#pragma unroll
-            for (int e = 0; e < W; ++e) o[i][e] = o[i][e] * w0 + rec[(i * (W + 2) + 2 + e) * TH] * w1;
-        }
+        merge(rec, m, l, o);
+        if constexpr (MIX) merge(rec + kState * TH, m2, l2, o2);
     }
     const float al = MIX ? s.alpha[kv_idx] : 0.f;
 #pragma unroll
@@ -509,24 +522,31 @@ struct TiledGradArgs {
     int N, n_pad;
 };
 
+// What a group has to itself: Y0, Y1, the queries' statistics, dS (and W).
+template <int D, bool KEYS, int OT>
+__host__ __device__ constexpr size_t grad_group_floats() {
+    return 2 * tile_floats<D>(TT) + (KEYS ? 2 : 1) * (size_t)TT * p_stride<OT>() + 4 * TT;
+}
 template <int D, bool KEYS, int OT>
 constexpr size_t grad_smem() {
-    return (2 * tile_floats<D>(OT) + 2 * tile_floats<D>(TT) + (KEYS ? 2 : 1) * (size_t)TT * p_stride<OT>() + 4 * TT) *
-           sizeof(float);
+    return (2 * tile_floats<D>(OT) + tiled_groups<D, OT>() * grad_group_floats<D, KEYS, OT>()) * sizeof(float);
 }
 
 template <typename T, int D, bool KEYS, bool CAP, int OT>
-__global__ void __launch_bounds__(tiled_threads<D, true, OT>()) tiled_grad_kernel(const LayerArgs a, const TiledGradArgs p) {
+__global__ void __launch_bounds__(tiled_threads<D, true, OT>() * tiled_groups<D, OT>())
+    tiled_grad_kernel(const LayerArgs a, const TiledGradArgs p) {
     extern __shared__ __align__(16) float sm[];
-    constexpr int TH = tiled_threads<D, true, OT>(), RI = 16 * OT / TH, PS = p_stride<OT>();   // OT outer rows a CTA
+    constexpr int TH = tiled_threads<D, true, OT>(), GROUPS = tiled_groups<D, OT>();
+    constexpr int RI = 16 * OT / TH, PS = p_stride<OT>();   // OT outer rows a CTA
+    const int tid = threadIdx.x % TH, group = threadIdx.x / TH;
     float* sX0 = sm;
     float* sX1 = sX0 + tile_floats<D>(OT);
-    float* sY0 = sX1 + tile_floats<D>(OT);
+    float* sY0 = sX1 + tile_floats<D>(OT) + group * grad_group_floats<D, KEYS, OT>();
     float* sY1 = sY0 + tile_floats<D>(TT);
     float* sStat = sY1 + tile_floats<D>(TT);          // [4][TT] of the tile's queries
     float* sG = sStat + 4 * TT;                       // dS, transposed
     float* sW = sG + TT * PS;                         // W, transposed (keys outer)
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int tx = tid & 15, ty = tid >> 4;
     const int heads = KEYS ? a.Hkv : a.Hq, N = p.N, tiles = (N + OT - 1) / OT;
     const int t = blockIdx.x / (a.B * heads), bh = blockIdx.x % (a.B * heads), b = bh / heads, head = bh % heads;
     const int kv = KEYS ? head : head / a.G;
@@ -539,21 +559,20 @@ __global__ void __launch_bounds__(tiled_threads<D, true, OT>()) tiled_grad_kerne
         };
     };
     auto load_stats = [&](int qh, int first, int n) {
-        if (threadIdx.x < n) {
+        if (tid < n) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                sStat[r * TT + threadIdx.x] =
-                    p.stats[(((size_t)b * a.Hq + qh) * 4 + r) * p.n_pad + first + threadIdx.x];
+            for (int r = 0; r < 4; ++r) sStat[r * TT + tid] = p.stats[(((size_t)b * a.Hq + qh) * 4 + r) * p.n_pad + first + tid];
         }
     };
-    {
+    if (!KEYS) load_stats(head, o0, OT);
+    if (group == 0) {
         Rows<T, D, OT, TH> x0, x1;
-        x0.fetch(threadIdx.x, KEYS ? rows(p.k, a.Hkv, kv, o0) : rows(p.q, a.Hq, head, o0));
-        x1.fetch(threadIdx.x, KEYS ? rows(p.v, a.Hkv, kv, o0) : rows(p.dout, a.Hq, head, o0));
-        x0.store(threadIdx.x, sX0);
-        x1.store(threadIdx.x, sX1);
-        if (!KEYS) load_stats(head, o0, OT);
+        x0.fetch(tid, KEYS ? rows(p.k, a.Hkv, kv, o0) : rows(p.q, a.Hq, head, o0));
+        x1.fetch(tid, KEYS ? rows(p.v, a.Hkv, kv, o0) : rows(p.dout, a.Hq, head, o0));
+        x0.store(tid, sX0);
+        x1.store(tid, sX1);
     }
+    if constexpr (GROUPS > 1) __syncthreads();
     constexpr int W = D / 16;
     float a0[RI][W], a1[KEYS ? RI : 1][W];
 #pragma unroll
@@ -572,19 +591,19 @@ __global__ void __launch_bounds__(tiled_threads<D, true, OT>()) tiled_grad_kerne
     Rows<T, D, TT, TH> y0, y1;
     auto fetch = [&](int j) {
         const int first = (it0 + j % per_head) * TT, qh = kv * a.G + j / per_head;
-        y0.fetch(threadIdx.x, KEYS ? rows(p.q, a.Hq, qh, first) : rows(p.k, a.Hkv, kv, first));
-        y1.fetch(threadIdx.x, KEYS ? rows(p.dout, a.Hq, qh, first) : rows(p.v, a.Hkv, kv, first));
+        y0.fetch(tid, KEYS ? rows(p.q, a.Hq, qh, first) : rows(p.k, a.Hkv, kv, first));
+        y1.fetch(tid, KEYS ? rows(p.dout, a.Hq, qh, first) : rows(p.v, a.Hkv, kv, first));
     };
-    if (prefetches<T, D>()) fetch(0);
-    for (int j0 = 0; j0 < n_in; ++j0) {
+    if (prefetches<T, D>() && group < n_in) fetch(group);
+    for (int j0 = group; j0 < n_in; j0 += GROUPS) {
         const int it = it0 + j0 % per_head, qh = KEYS ? kv * a.G + j0 / per_head : head;
-        __syncthreads();
+        group_sync<GROUPS, TH>(group);
         if (!prefetches<T, D>()) fetch(j0);
-        y0.store(threadIdx.x, sY0);
-        y1.store(threadIdx.x, sY1);
+        y0.store(tid, sY0);
+        y1.store(tid, sY1);
         if (KEYS) load_stats(qh, it * TT, TT);
-        __syncthreads();
-        if (prefetches<T, D>() && j0 + 1 < n_in) fetch(j0 + 1);
+        group_sync<GROUPS, TH>(group);
+        if (prefetches<T, D>() && j0 + GROUPS < n_in) fetch(j0 + GROUPS);
         float x[RI][4], d[RI][4];
         tile_dot<D, RI>(sX0, sY0, tx, ty, x);
         tile_dot<D, RI>(sX1, sY1, tx, ty, d);
@@ -617,14 +636,35 @@ __global__ void __launch_bounds__(tiled_threads<D, true, OT>()) tiled_grad_kerne
         }
         put_transposed<RI, PS>(sG, d, tx, ty);
         if constexpr (KEYS) put_transposed<RI, PS>(sW, x, tx, ty);
-        __syncthreads();
+        group_sync<GROUPS, TH>(group);
         tile_acc<D, RI, PS>(sG, sY0, tx, ty, a0);
         if constexpr (KEYS) tile_acc<D, RI, PS>(sW, sY1, tx, ty, a1);
+    }
+    bool stores = true;
+    if constexpr (GROUPS > 1) {
+        // the second group's sums through its Y0 tile
+        static_assert((KEYS ? 2 : 1) * RI * W * TH <= tile_floats<D>(TT), "a tile holds a group's sums");
+        float* rec = sX1 + tile_floats<D>(OT) + grad_group_floats<D, KEYS, OT>() + tid;
+        stores = group == 0;
+        if (!stores) group_sync<GROUPS, TH>(group);
+#pragma unroll
+        for (int k = 0; k < RI * W; ++k)
+            if (!stores) {
+                rec[k * TH] = a0[k / W][k % W];
+                if constexpr (KEYS) rec[(RI * W + k) * TH] = a1[k / W][k % W];
+            }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < RI * W; ++k)
+            if (stores) {
+                a0[k / W][k % W] += rec[k * TH];
+                if constexpr (KEYS) a1[k / W][k % W] += rec[(RI * W + k) * TH];
+            }
     }
 #pragma unroll
     for (int i = 0; i < RI; ++i) {
         const int r = o0 + RI * ty + i;
-        if (r >= N || !bounds_ok(b < a.B && head < heads, p.status)) continue;
+        if (!stores || r >= N || !bounds_ok(b < a.B && head < heads, p.status)) continue;
         const size_t off = (((size_t)b * N + r) * heads + head) * D + 4 * tx;
 #pragma unroll
         for (int j = 0; j < D / 64; ++j) {
@@ -645,7 +685,8 @@ __global__ void __launch_bounds__(tiled_threads<D, true, OT>()) tiled_grad_kerne
 
 // 64 outer rows a CTA where that still gives every SM two CTAs, else 32: at
 // 509 tokens and 16 heads (128 CTAs of 64 rows) a step took 231 us with 64 rows
-// and 209 us with 32 (both with 16 x 16 threads); at 2,048 tokens the two differ by less than the noise.
+// and 209 with 32, both with one group of 16 x 16 threads; at 2,048 tokens the
+// two differed by less than the noise.
 bool few_ctas(const LayerArgs& a, int N, int heads) {
     return (long)a.B * heads * ((N + 63) / 64) < 2L * sm_count();
 }
@@ -658,7 +699,7 @@ cudaError_t launch_forward_rows(const LayerArgs& a, const CacheArgs& c, const Ti
     if (e != cudaSuccess) return e;
     const long ctas = (long)a.B * a.Hq * ((s.N + OT - 1L) / OT);
     if (ctas > 0x7fffffffL) return cudaErrorInvalidConfiguration;
-    tiled_forward_kernel<T, D, MIX, CAP, OT><<<(unsigned)ctas, tiled_threads<D, MIX, OT>() * tiled_groups<D, MIX, OT>(), smem, st>>>(a, c, s);
+    tiled_forward_kernel<T, D, MIX, CAP, OT><<<(unsigned)ctas, tiled_threads<D, MIX, OT>() * tiled_groups<D, OT>(), smem, st>>>(a, c, s);
     return cudaGetLastError();
 }
 template <typename T, int D, bool MIX, bool CAP>
@@ -675,7 +716,7 @@ cudaError_t launch_grad_rows(const LayerArgs& a, const TiledGradArgs& p, cudaStr
     if (e != cudaSuccess) return e;
     const long ctas = (long)a.B * (KEYS ? a.Hkv : a.Hq) * ((p.N + OT - 1L) / OT);
     if (ctas > 0x7fffffffL) return cudaErrorInvalidConfiguration;
-    tiled_grad_kernel<T, D, KEYS, CAP, OT><<<(unsigned)ctas, tiled_threads<D, true, OT>(), smem, st>>>(a, p);
+    tiled_grad_kernel<T, D, KEYS, CAP, OT><<<(unsigned)ctas, tiled_threads<D, true, OT>() * tiled_groups<D, OT>(), smem, st>>>(a, p);
     return cudaGetLastError();
 }
 template <typename T, int D, bool KEYS, bool CAP>
