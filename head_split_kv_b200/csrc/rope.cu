@@ -17,7 +17,7 @@
 // their addresses need no length -- so that the reads of HBM run under the
 // trigonometry and the look-up of the lengths and pages.  A thread has the same
 // place in all of its rows, so it takes its cosines and sines from shared
-// memory once.  (A 4,096-token prompt of 32 + 8 heads takes 15 us.  When it took
+// memory once.  (A 4,096-token prompt of 32 + 8 heads takes 16 us.  When it took
 // 18, a grid of resident CTAs that walks the tokens, loading one ahead, took 23
 // at 80 registers, and two or four tokens to a CTA the same as one.)
 //
