@@ -568,11 +568,14 @@ __global__ void __launch_bounds__(kRegThreads, 1)
         const int orow = BM * ot + row;                       // key (keys outer) or query
         RowStats rs{0.f, 0.f, 0.f, 0.f, nullptr};
         RowSums sum{0.f, 0.f, 0.f, 0.f};
+        // statistics: both masks show the query the same keys, so the two attentions
+        // are one: the same log-sum and D, and no share of dalpha but 0
+        const bool one_attention = orow < a.sink + a.recent;
         if constexpr (kStats) {
             const bool live = orow < p.N;
             const size_t r = ((size_t)b * a.Hq + head) * p.N + (live ? orow : 0);
             rs.lse_c = live ? -p.lse[r] : -INFINITY;
-            rs.lse_l = live ? -p.lse[(size_t)a.B * a.Hq * p.N + r] : -INFINITY;
+            rs.lse_l = live ? -p.lse[(one_attention ? 0 : (size_t)a.B * a.Hq * p.N) + r] : -INFINITY;
         } else if constexpr (!kKeys) {
             const float* st = p.stats + ((size_t)b * a.Hq + head) * 4 * p.n_pad + orow;
             rs = {st[0], st[p.n_pad], st[2 * (size_t)p.n_pad], st[3 * (size_t)p.n_pad], nullptr};
@@ -658,9 +661,10 @@ __global__ void __launch_bounds__(kRegThreads, 1)
                     const float4 t = quarter[k * BM + row];
                     o = make_float4(o.x + t.x, o.y + t.y, o.z + t.z, o.w + t.w);
                 }
-                const float lc = sum.lc + o.x, ls = sum.ls + o.z;
+                const float lc = sum.lc + o.x, ls = one_attention ? lc : sum.ls + o.z;
                 const bool live = ok && orow < p.N && lc > 0.f && ls > 0.f;
-                const float dc = live ? (sum.dc + o.y) / lc : 0.f, ds = live ? (sum.ds + o.w) / ls : 0.f;
+                const float dc = live ? (sum.dc + o.y) / lc : 0.f;
+                const float ds = !live ? 0.f : one_attention ? dc : (sum.ds + o.w) / ls;
                 const float lse_c = live ? log2f(lc) - rs.lse_c - log2f(fabsf(al)) : INFINITY;       // +inf: a closed gate
                 const float lse_s = live ? log2f(ls) - rs.lse_l - log2f(fabsf(1.f - al)) : INFINITY;
                 float lse_l = lse_s, dl = ds;

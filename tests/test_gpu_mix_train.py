@@ -71,6 +71,14 @@ def test_mix_step_matches_the_formulas(duo, case):
         assert np.array_equal(bits(g), bits(h))
 
 
+@pytest.mark.parametrize("d,dtype", [(128, "bf16"), (64, "fp32")])
+@pytest.mark.parametrize("cap", [0.0, 30.0, 200.0])
+def test_gates_of_sequences_inside_the_window_have_no_gradient(duo, d, dtype, cap):
+    """Up to sink + recent tokens both attentions are the same, bit for bit."""
+    case = _case(duo, 8, 4, d, dtype, 2, 80, cap, 2.0)
+    assert np.all(f64(_step(duo, case[0], cap, *case[1:])[4]) == 0.0)
+
+
 def test_forward_equals_the_plain_mix(duo):
     """Without a cap the training forward computes what duo_gated_mix computes
     (the same kernels and tiles: the same bits)."""
