@@ -5,12 +5,21 @@
 // A capped score lies in [-cap, cap], so the softmax needs no running maximum:
 // with x the dot product, p = 2^(c2 tanh(k x)) lies in [2^-c2, 2^c2], which for
 // caps up to 60 (c2 <= 87) stays inside fp32 -- and bf16, whose exponent is the
-// same -- with room for the sums: 2^87 a key, 2^20 keys, values up to 2^20.  p
-// is then a function of one score alone.  No row statistic stands between
-// the scores and the exponentials, O is never rescaled, the columns of a row
-// may be split over several threads that never talk until the end, and the
-// splits of a key range merge by addition.  (Larger caps, and caches of 8- or
-// 4-bit codes, whose fp16 p needs the maximum, take prefill_tc.cu.)
+// same -- with room for the row sum of 2^40 keys.  p is then a function of one
+// score alone.  No row statistic stands between the scores and the
+// exponentials, O is never rescaled, the columns of a row may be split over
+// several threads that never talk until the end, and the splits of a key range
+// merge by addition.  (Larger caps, and caches of 8- or 4-bit codes, whose fp16
+// p needs the maximum, take prefill_tc.cu.)
+//
+// O = P V is the one sum whose range depends on more than the cap: with scores
+// near +cap, values past 2^40 or so could overflow it, and in a row whose every
+// score lies near -cap small values would fall below fp32's normal range.  So a
+// CTA looks at its finished rows, and where an |O| is past 2^100 (or not
+// finite), or a row sum below 2^-32, it walks its tiles once more
+// (second_pass) with p = 2^(score - log2(2 l)), l the row's own sum, which is
+// always in range: those weights add up to 1/2, whatever the scores.  Scores
+// and values of a model never ask for it; the test costs one barrier at the end.
 //
 // Work and masks as in prefill_tc.cu (prefill_sched.cuh), but a CTA owns one
 // 128-row query tile: S then has three buffers in TMEM (S0 | S1 | S2 | O, 128
@@ -61,8 +70,9 @@ constexpr uint32_t kOffK = kOffQ + kTileBytes;
 constexpr uint32_t kOffV = kOffK + kStages * kTileBytes;
 constexpr uint32_t kOffSum = kOffV + kStages * kTileBytes;   // [4][128] partial row sums
 constexpr uint32_t kOffBar = kOffSum + 4 * BM * 4;
-constexpr uint32_t kOffHolder = kOffBar + 24 * 8;
+constexpr uint32_t kOffHolder = kOffBar + 24 * 8;  // TMEM base, last split, a row asks for a second pass, a wait ran out
 constexpr uint32_t kSmemBytes = kOffHolder + 16;
+constexpr float kMaxO = 0x1p100f, kMinSum = 0x1p-32f;   // of a row's first pass
 static_assert(kSmemBytes <= 232448, "one CTA per SM");
 
 // The key tiles of query tile mt (chunk rows 128 mt ..), as make_sched lists
@@ -168,6 +178,194 @@ __device__ __forceinline__ uint64_t half_bits(const uint32_t (&v)[4], int half) 
     return half ? ((uint64_t)v[3] << 32 | v[2]) : ((uint64_t)v[1] << 32 | v[0]);
 }
 
+// ------------------------------------------------------------------- roles
+//
+// A CTA's tiles in its passes: number jj = base .. base + nl - 1, base a multiple
+// of nl, so that a second pass goes on where the first left the rings and the
+// barriers' phases.
+
+enum {   // barriers
+    kKFull = 0, kKEmpty = 3, kVFull = 6, kVEmpty = 9,   // [kStages]
+    kSFull = 12, kPFull = 15, kSFree = 18,              // [kSlots]
+    kQFull = 21, kODone = 22                            // kODone: once a pass
+};
+struct Cta {
+    Sched sc;
+    int j0, nl;                        // tiles j0 .. j0 + nl - 1 of the schedule
+    int mt, b, kv_idx, cache_z, ring_z;
+    uint32_t sQ, sK, sV, tmem;
+    uint64_t* bars;
+};
+struct KvMaps {
+    const CUtensorMap *kc, *vc, *kx, *vx, *kr, *vr;
+};
+
+// One thread: K and V tiles, three deep.
+__device__ __forceinline__ void load_tiles(const Cta& c, const KvMaps& m, int base, int32_t* status) {
+    bool ok = true;
+    for (int jj = base; jj < base + c.nl && ok; ++jj) {
+        const Tile t = tile_at(c.sc, c.j0 + jj - base);
+        const int st = jj % kStages, use = jj / kStages;
+        for (int kv = 0; kv < 2 && ok; ++kv) {
+            uint64_t* full = c.bars + (kv ? kVFull : kKFull) + st;
+            if (use > 0) ok = mbar_wait(c.bars + (kv ? kVEmpty : kKEmpty) + st, (use - 1) & 1, status);
+            if (!ok) break;
+            mbar_arrive_expect_tx(full, kTileBytes);
+            const uint32_t dst = (kv ? c.sV : c.sK) + st * kTileBytes;
+            for (int half = 0; half < 2; ++half)
+                for (int rh = 0; rh < BN / kBox; ++rh) {
+                    const uint32_t d2 = dst + half * kHalfBytes + rh * kBox * 128;
+                    const int x = 64 * half, row = t.row + kBox * rh;
+                    if (t.src == SRC_CACHE)
+                        tma_load_3d(d2, kv ? m.vc : m.kc, x, row, c.cache_z, full);
+                    else if (t.src == SRC_CHUNK)
+                        tma_load_4d(d2, kv ? m.vx : m.kx, x, c.kv_idx, row, c.b, full);
+                    else
+                        tma_load_3d(d2, kv ? m.vr : m.kr, x, row, c.ring_z, full);
+                }
+        }
+    }
+}
+
+// One warp: S(j) = Q K(j)^T; the whole warp waits, one lane issues.
+template <int kSlots>
+__device__ __forceinline__ void issue_qk(const Cta& c, int base, int32_t* status) {
+    constexpr uint32_t idesc_qk = idesc_bf16(BM, BN, 0, 0);
+    bool ok = mbar_wait(c.bars + kQFull, 0, status);
+    for (int jj = base; jj < base + c.nl && ok; ++jj) {
+        const int st = jj % kStages, sl = jj % kSlots, use = jj / kSlots;
+        // the slot holds P(jj - kSlots) until its P V is done
+        if (use > 0) ok = mbar_wait(c.bars + kSFree + sl, (use - 1) & 1, status);
+        ok = ok && mbar_wait(c.bars + kKFull + st, (jj / kStages) & 1, status);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+            const uint64_t qd = sw128_desc(c.sQ, 16, 1024), kd = sw128_desc(c.sK + st * kTileBytes, 16, 1024);
+#pragma unroll
+            for (int kk = 0; kk < HD / 16; ++kk) {
+                const uint32_t o = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
+                tc_mma(c.tmem + 128 * sl, qd + o, kd + o, idesc_qk, kk > 0 ? 1u : 0u);
+            }
+            tc_commit(c.bars + kSFull + sl);
+            tc_commit(c.bars + kKEmpty + st);
+        }
+    }
+    __syncwarp();
+}
+
+// One warp: O += P(j) V(j), P from TMEM: 16 packed columns at the start of every 32 of S.
+template <bool MIX, int kSlots>
+__device__ __forceinline__ void issue_pv(const Cta& c, const LayerArgs& a, int base, int32_t* status) {
+    constexpr uint32_t idesc_pv = idesc_bf16(BM, HD, 0, 1);
+    bool ok = true, first_lam = true;
+    for (int jj = base; jj < base + c.nl && ok; ++jj) {
+        const int st = jj % kStages, sl = jj % kSlots;
+        ok = mbar_wait(c.bars + kVFull + st, (jj / kStages) & 1, status) &&
+             mbar_wait(c.bars + kPFull + sl, (jj / kSlots) & 1, status);
+        if (!ok) break;
+        tc_fence_after();
+        const bool lam = MIX && lambda_tile(a, c.mt, jj - base);
+        if (elect_one()) {
+            const uint64_t vd = sw128_desc(c.sV + st * kTileBytes, kHalfBytes, 1024);
+#pragma unroll
+            for (int kk = 0; kk < BN / 16; ++kk)
+                tc_mma_ta(c.tmem + kColO, c.tmem + 128 * sl + 32 * (kk >> 1) + 8 * (kk & 1), vd + kk * (2048 >> 4), idesc_pv,
+                          (jj > base || kk > 0) ? 1u : 0u);
+            if (lam) {
+#pragma unroll
+                for (int kk = 0; kk < BN / 16; ++kk)
+                    tc_mma_ta(c.tmem + kColOs, c.tmem + 128 * sl + 32 * (kk >> 1) + 16 + 8 * (kk & 1), vd + kk * (2048 >> 4),
+                              idesc_pv, (!first_lam || kk > 0) ? 1u : 0u);
+            }
+            tc_commit(c.bars + kVEmpty + st);
+            tc_commit(c.bars + kSFree + sl);
+            if (jj == base + c.nl - 1) tc_commit(c.bars + kODone);
+        }
+        if (lam) first_lam = false;
+    }
+    __syncwarp();
+}
+
+// The second pass, by all of the CTA's warps: every row's exponents lowered by
+// its bias (bias_l: of the Lambda attention).  Returns a thread's share of the
+// row's sums and whether every wait ended.  Rare, so kept out of line.
+struct RowShare {
+    float2 l;
+    bool ok;
+};
+template <bool MIX>
+__device__ __noinline__ RowShare second_pass(const Cta& c, const KvMaps& m, const TcArgs& p, float bias, float bias_l) {
+    constexpr int kSlots = s_slots<MIX>();
+    const LayerArgs& a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, base = c.nl;
+    RowShare r{make_float2(0.f, 0.f), true};
+    if (warp == kTmaWarp) {
+        if (lane == 0) load_tiles(c, m, base, p.status);
+        __syncwarp();
+    } else if (warp == kQkWarp) {
+        issue_qk<kSlots>(c, base, p.status);
+    } else if (warp == kPvWarp) {
+        issue_pv<MIX, kSlots>(c, a, base, p.status);
+    } else if (warp < kExpWarps) {
+        const int group = warp >> 3, half = (warp >> 2) & 1;
+        const int P = c.sc.c0 + BM * c.mt + 32 * (warp & 3) + lane;
+        Sched lam_sc = c.sc;
+        lam_sc.retrieval = false;
+        for (int jj = base + ((base ^ group) & 1); jj < base + c.nl; jj += 2) {
+            const int sl = jj % kSlots;
+            r.ok = __all_sync(0xffffffffu, mbar_wait(c.bars + kSFull + sl, (jj / kSlots) & 1, p.status));
+            if (!r.ok) break;
+            tc_fence_after();
+            const Tile t = tile_at(c.sc, c.j0 + jj - base);
+            const bool lam = MIX && lambda_tile(a, c.mt, jj - base);
+            uint32_t vis[4] = {0u, 0u, 0u, 0u}, seen_l[4] = {0u, 0u, 0u, 0u};
+            visible_columns(a, c.sc, t, P, vis);
+            if (lam) visible_columns(a, lam_sc, t, P, seen_l);
+            const uint32_t s_addr = c.tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 128 * sl + 64 * half;
+#pragma unroll 1
+            for (int ch = 0; ch < 2; ++ch) {
+                const uint32_t v = half ? (ch ? vis[3] : vis[2]) : (ch ? vis[1] : vis[0]);
+                const uint32_t w = half ? (ch ? seen_l[3] : seen_l[2]) : (ch ? seen_l[1] : seen_l[0]);
+                float x[32];
+                tmem_ld32(s_addr + 32 * ch, x);
+                uint32_t pk[32];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float e[2], f[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float s = a.cap.c2 * tanh_sfu(x[2 * i + h] * a.cap.k);
+                        e[h] = (v >> (2 * i + h)) & 1u ? sfu_exp2(s - bias) : 0.f;
+                        f[h] = (w >> (2 * i + h)) & 1u ? sfu_exp2(s - bias_l) : 0.f;
+                    }
+                    __nv_bfloat162 pe = __floats2bfloat162_rn(e[0], e[1]), pf = __floats2bfloat162_rn(f[0], f[1]);
+                    pk[i] = *reinterpret_cast<uint32_t*>(&pe);
+                    pk[16 + i] = *reinterpret_cast<uint32_t*>(&pf);
+                    r.l.x += bf16_lo(pk[i]) + bf16_hi(pk[i]);
+                    r.l.y += bf16_lo(pk[16 + i]) + bf16_hi(pk[16 + i]);
+                }
+                tmem_st32(s_addr + 32 * ch, pk);   // the second half is read in Lambda tiles only
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(c.bars + kPFull + sl);
+        }
+    }
+    return r;
+}
+
+// Do 32 columns of a finished row ask for a second pass?
+__device__ __forceinline__ bool out_of_range(uint32_t o_addr, float l) {
+    float o[32], z = 0.f;
+    tmem_ld32(o_addr, o);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) z = fmaf(o[i], 0.f, z);   // NaN where an entry is not finite
+    return !(z == 0.f) || largest<32>(o) > kMaxO || (l > 0.f && l < kMinSum);
+}
+// log2 of twice a row's sum
+__device__ __forceinline__ float row_bias(float l) { return l > 0.f ? log2f(l) + 1.f : 0.f; }
+
 // EPI: EPI_STORE (store, or key-range split records) or EPI_MIX_KEEP (both
 // attentions, mixed; every KV head in the retrieval block).
 template <int EPI>
@@ -175,7 +373,7 @@ __global__ void __launch_bounds__(kRegThreads, 1)
     prefill_capped_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmKc,
                           const __grid_constant__ CUtensorMap tmVc, const __grid_constant__ CUtensorMap tmKx,
                           const __grid_constant__ CUtensorMap tmVx, const __grid_constant__ CUtensorMap tmKr,
-                          const __grid_constant__ CUtensorMap tmVr, const TcArgs p) {
+                          const __grid_constant__ CUtensorMap tmVr, const __grid_constant__ TcArgs p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr bool MIX = EPI == EPI_MIX_KEEP;
     constexpr int kSlots = s_slots<MIX>();
@@ -185,17 +383,7 @@ __global__ void __launch_bounds__(kRegThreads, 1)
         if (tid == 0 && p.status) atomicOr(p.status, DUO_DEV_BAD_LENGTH);
         return;
     }
-    const uint32_t sQ = smem_u32(smem + kOffQ), sK = smem_u32(smem + kOffK), sV = smem_u32(smem + kOffV);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
-    uint64_t* k_full = bars + 0;    // [kStages]
-    uint64_t* k_empty = bars + 3;   // [kStages]
-    uint64_t* v_full = bars + 6;    // [kStages]
-    uint64_t* v_empty = bars + 9;   // [kStages]
-    uint64_t* s_full = bars + 12;   // [kSlots], as the next two
-    uint64_t* p_full = bars + 15;
-    uint64_t* s_free = bars + 18;
-    uint64_t* q_full = bars + 21;
-    uint64_t* o_done = bars + 22;
     uint32_t* holder = reinterpret_cast<uint32_t*>(smem + kOffHolder);
 
     // the work item, ordered as in prefill_tc.cu: (sequence, KV head)
@@ -246,121 +434,74 @@ __global__ void __launch_bounds__(kRegThreads, 1)
     if (warp == kQkWarp) tmem_alloc(holder, kTmemCols);
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&k_full[i], 1);
-            mbar_init(&k_empty[i], 1);
-            mbar_init(&v_full[i], 1);
-            mbar_init(&v_empty[i], 1);
+            mbar_init(bars + kKFull + i, 1);
+            mbar_init(bars + kKEmpty + i, 1);
+            mbar_init(bars + kVFull + i, 1);
+            mbar_init(bars + kVEmpty + i, 1);
         }
         for (int i = 0; i < kSlots; ++i) {
-            mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], kExpWarps / 2);
-            mbar_init(&s_free[i], 1);
+            mbar_init(bars + kSFull + i, 1);
+            mbar_init(bars + kPFull + i, kExpWarps / 2);
+            mbar_init(bars + kSFree + i, 1);
         }
-        mbar_init(q_full, 1);
-        mbar_init(o_done, 1);
+        mbar_init(bars + kQFull, 1);
+        mbar_init(bars + kODone, 1);
+        holder[2] = holder[3] = 0u;
         fence_barrier_init();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *holder;
+    const Cta cta{sc, j0, nl, mt, b, kv_idx, b * a.R + slot, b * a.S + (slot - a.R),
+                  smem_u32(smem + kOffQ), smem_u32(smem + kOffK), smem_u32(smem + kOffV), tmem, bars};
+    const KvMaps maps{&tmKc, &tmVc, &tmKx, &tmVx, &tmKr, &tmVr};
 
+    // exponential warps: group takes the key tiles j % 2 == group, half a column
+    // half; afterwards each thread has 32 columns (quarter) of its row
+    const int group = warp >> 3, half = (warp >> 2) & 1, quarter = warp >> 2;
+    const int row = 32 * (warp & 3) + lane;           // TMEM lane
+    const int crow = BM * mt + row;                   // chunk row
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const bool out_ok = bounds_ok(b < a.B && q_idx >= 0 && q_idx < a.Hq, p.status);
+    const bool live = crow < p.C && out_ok;
+    float l_row = 0.f, l_lam = 0.f;
+    bool ok = true;
+    // the row's sum over both groups and column halves, by every thread of the exponential warps
+    auto row_total = [&](float part) {
+        float* sums = reinterpret_cast<float*>(smem + kOffSum);
+        sums[quarter * BM + row] = part;
+        asm volatile("bar.sync 1, 512;" ::: "memory");
+        return (sums[row] + sums[BM + row]) + (sums[2 * BM + row] + sums[3 * BM + row]);
+    };
+    auto both_totals = [&](float2 l) {
+        l_row = row_total(l.x);
+        if constexpr (MIX) {
+            asm volatile("bar.sync 1, 512;" ::: "memory");    // everyone has read the first totals
+            l_lam = row_total(l.y);
+        }
+    };
     if (warp == kTmaWarp) {
         if (lane == 0) {
-            mbar_arrive_expect_tx(q_full, kTileBytes);
-            for (int half = 0; half < 2; ++half)
-                tma_load_4d(sQ + half * kHalfBytes, &tmQ, 64 * half, q_idx, BM * mt, b, q_full);
-            const int cache_z = b * a.R + slot, ring_z = b * a.S + (slot - a.R);
-            bool ok = true;
-            for (int j = 0; j < nl && ok; ++j) {
-                const Tile t = tile_at(sc, j0 + j);
-                const int st = j % kStages, use = j / kStages;
-                for (int kv = 0; kv < 2 && ok; ++kv) {
-                    uint64_t* full = kv ? &v_full[st] : &k_full[st];
-                    if (use > 0) ok = mbar_wait(kv ? &v_empty[st] : &k_empty[st], (use - 1) & 1, p.status);
-                    if (!ok) break;
-                    mbar_arrive_expect_tx(full, kTileBytes);
-                    const uint32_t dst = (kv ? sV : sK) + st * kTileBytes;
-                    for (int half = 0; half < 2; ++half)
-                        for (int rh = 0; rh < BN / kBox; ++rh) {
-                            const uint32_t d2 = dst + half * kHalfBytes + rh * kBox * 128;
-                            const int x = 64 * half, row = t.row + kBox * rh;
-                            if (t.src == SRC_CACHE)
-                                tma_load_3d(d2, kv ? &tmVc : &tmKc, x, row, cache_z, full);
-                            else if (t.src == SRC_CHUNK)
-                                tma_load_4d(d2, kv ? &tmVx : &tmKx, x, kv_idx, row, b, full);
-                            else
-                                tma_load_3d(d2, kv ? &tmVr : &tmKr, x, row, ring_z, full);
-                        }
-                }
-            }
+            mbar_arrive_expect_tx(bars + kQFull, kTileBytes);
+            for (int half_d = 0; half_d < 2; ++half_d)
+                tma_load_4d(cta.sQ + half_d * kHalfBytes, &tmQ, 64 * half_d, q_idx, BM * mt, b, bars + kQFull);
+            load_tiles(cta, maps, 0, p.status);
         }
+        __syncwarp();
     } else if (warp == kQkWarp) {
-        // S(j) = Q K(j)^T; the whole warp waits, one lane issues
-        constexpr uint32_t idesc_qk = idesc_bf16(BM, BN, 0, 0);
-        bool ok = mbar_wait(q_full, 0, p.status);
-        for (int j = 0; j < nl && ok; ++j) {
-            const int st = j % kStages, sl = j % kSlots, use = j / kSlots;
-            // the slot holds P(j - kSlots) until its P V is done
-            if (use > 0) ok = mbar_wait(&s_free[sl], (use - 1) & 1, p.status);
-            ok = ok && mbar_wait(&k_full[st], (j / kStages) & 1, p.status);
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
-                const uint64_t qd = sw128_desc(sQ, 16, 1024), kd = sw128_desc(sK + st * kTileBytes, 16, 1024);
-#pragma unroll
-                for (int kk = 0; kk < HD / 16; ++kk) {
-                    const uint32_t o = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
-                    tc_mma(tmem + 128 * sl, qd + o, kd + o, idesc_qk, kk > 0 ? 1u : 0u);
-                }
-                tc_commit(&s_full[sl]);
-                tc_commit(&k_empty[st]);
-            }
-        }
-        __syncwarp();
+        issue_qk<kSlots>(cta, 0, p.status);
     } else if (warp == kPvWarp) {
-        // O += P(j) V(j), P from TMEM: 16 packed columns at the start of every 32 of S
-        constexpr uint32_t idesc_pv = idesc_bf16(BM, HD, 0, 1);
-        bool ok = true, first_lam = true;
-        for (int j = 0; j < nl && ok; ++j) {
-            const int st = j % kStages, sl = j % kSlots;
-            ok = mbar_wait(&v_full[st], (j / kStages) & 1, p.status) && mbar_wait(&p_full[sl], (j / kSlots) & 1, p.status);
-            if (!ok) break;
-            tc_fence_after();
-            const bool lam = MIX && lambda_tile(a, mt, j);
-            if (elect_one()) {
-                const uint64_t vd = sw128_desc(sV + st * kTileBytes, kHalfBytes, 1024);
-#pragma unroll
-                for (int kk = 0; kk < BN / 16; ++kk)
-                    tc_mma_ta(tmem + kColO, tmem + 128 * sl + 32 * (kk >> 1) + 8 * (kk & 1), vd + kk * (2048 >> 4), idesc_pv,
-                              (j > 0 || kk > 0) ? 1u : 0u);
-                if (lam) {
-#pragma unroll
-                    for (int kk = 0; kk < BN / 16; ++kk)
-                        tc_mma_ta(tmem + kColOs, tmem + 128 * sl + 32 * (kk >> 1) + 16 + 8 * (kk & 1), vd + kk * (2048 >> 4),
-                                  idesc_pv, (!first_lam || kk > 0) ? 1u : 0u);
-                }
-                tc_commit(&v_empty[st]);
-                tc_commit(&s_free[sl]);
-                if (j == nl - 1) tc_commit(o_done);
-            }
-            if (lam) first_lam = false;
-        }
-        __syncwarp();
+        issue_pv<MIX, kSlots>(cta, a, 0, p.status);
     } else if (warp < kExpWarps) {
-        const int group = warp >> 3, half = (warp >> 2) & 1;  // key tiles j % 2 == group; column half
-        const int row = 32 * (warp & 3) + lane;               // TMEM lane
-        const int crow = BM * mt + row;                       // chunk row
-        const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         float2 l = make_float2(0.f, 0.f);                     // row sums: causal (or the head's mask), Lambda (MIX)
-        bool ok = true;
         int plain_first, plain_last;
         unmasked_tiles(sc, plain_first, plain_last);
         Sched lam_sc = sc;                                    // the same tiles under the Lambda mask
         lam_sc.retrieval = false;
         for (int j = group; j < nl; j += 2) {
             const int sl = j % kSlots;
-            ok = __all_sync(0xffffffffu, mbar_wait(&s_full[sl], (j / kSlots) & 1, p.status));
+            ok = __all_sync(0xffffffffu, mbar_wait(bars + kSFull + sl, (j / kSlots) & 1, p.status));
             if (!ok) break;
             tc_fence_after();
             const uint32_t s_addr = lane_base + 128 * sl + 64 * half;
@@ -380,32 +521,43 @@ __global__ void __launch_bounds__(kRegThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[sl]);
+            if (lane == 0) mbar_arrive(bars + kPFull + sl);
         }
-        // the row's sum over both groups and column halves; each thread then
-        // stores 32 columns of its row
-        float* sums = reinterpret_cast<float*>(smem + kOffSum);
-        const int quarter = warp >> 2;
-        auto row_total = [&](float part) {
-            sums[quarter * BM + row] = part;
-            asm volatile("bar.sync 1, 512;" ::: "memory");
-            return (sums[row] + sums[BM + row]) + (sums[2 * BM + row] + sums[3 * BM + row]);
-        };
-        const float l_row = row_total(l.x);
-        float l_lam = 0.f;
-        if constexpr (MIX) {
-            asm volatile("bar.sync 1, 512;" ::: "memory");    // everyone has read the first totals
-            l_lam = row_total(l.y);
+        both_totals(l);
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(bars + kODone, 0, p.status));
+        if (ok) {
+            tc_fence_after();
+            bool again = out_of_range(lane_base + kColO + 32 * quarter, l_row);
+            if constexpr (MIX) again |= out_of_range(lane_base + kColOs + 32 * quarter, l_lam);
+            if (again && live) holder[2] = 1u;
+        } else {
+            holder[3] = 1u;
         }
-        const size_t off = (((size_t)b * p.C + crow) * a.Hq + q_idx) * HD + 32 * quarter;
-        const bool out_ok = bounds_ok(b < a.B && q_idx >= 0 && q_idx < a.Hq, p.status);
-        const bool live = crow < p.C && out_ok;
-        ok = __all_sync(0xffffffffu, ok && mbar_wait(o_done, 0, p.status));
+    }
+    tc_fence_before();
+    __syncthreads();
+    float bias = 0.f, bias_l = 0.f;                           // log2 by which the row's p were lowered
+    if (holder[2] != 0u && holder[3] == 0u) {
+        tc_fence_after();
+        if (warp < kExpWarps) {
+            bias = row_bias(l_row);
+            bias_l = row_bias(l_lam);
+        }
+        const Cta c2 = cta;                                   // a copy, so that cta itself stays in registers
+        const KvMaps m2 = maps;
+        const RowShare r = second_pass<MIX>(c2, m2, p, bias, bias_l);
+        if (warp < kExpWarps) {
+            both_totals(r.l);
+            ok = __all_sync(0xffffffffu, r.ok && mbar_wait(bars + kODone, 1, p.status));
+        }
+    }
+    if (warp < kExpWarps) {
         float o[32];
         if (ok) {
             tc_fence_after();
             tmem_ld32(lane_base + kColO + 32 * quarter, o);
         }
+        const size_t off = (((size_t)b * p.C + crow) * a.Hq + q_idx) * HD + 32 * quarter;
         __nv_bfloat16* op = static_cast<__nv_bfloat16*>(p.out) + off;
         if (!out_ok) {
             // debug build: the check failed, nothing is written
@@ -418,8 +570,8 @@ __global__ void __launch_bounds__(kRegThreads, 1)
                     const float fc = al * inv, fs = l_lam > 0.f ? (1.f - al) / l_lam : 0.f;
                     if (quarter == 0 && live) {
                         const size_t r = ((size_t)b * a.Hq + q_idx) * p.C + crow;
-                        p.epi.lse[r] = log2f(l_row);
-                        p.epi.lse[(size_t)a.B * a.Hq * p.C + r] = log2f(l_lam);
+                        p.epi.lse[r] = bias + log2f(l_row);
+                        p.epi.lse[(size_t)a.B * a.Hq * p.C + r] = bias_l + log2f(l_lam);
                     }
                     float os[32];
                     tmem_ld32(lane_base + kColOs + 32 * quarter, os);
@@ -438,13 +590,13 @@ __global__ void __launch_bounds__(kRegThreads, 1)
                 }
             }
         } else if (bounds_ok(unit < p.n_units && split < p.ns, p.status)) {
-            // this split's record of the query tile (the maximum is 0 for every
-            // row), then a ticket per query tile (half a word of the pair's);
-            // the CTA that arrives last merges (no CTA ever waits)
+            // this split's record of the query tile (the maximum is the bias, 0
+            // but after a second pass), then a ticket per query tile (half a word
+            // of the pair's); the CTA that arrives last merges (no CTA ever waits)
             const int qi = mt & 1;
             float* rec = p.part + (((size_t)unit * p.ns + split) * 2 + qi) * kPartFloats;
             if (quarter == 0) {
-                rec[row] = ok ? 0.f : -INFINITY;
+                rec[row] = ok ? bias : -INFINITY;
                 rec[BM + row] = ok ? l_row : 0.f;
             }
 #pragma unroll
