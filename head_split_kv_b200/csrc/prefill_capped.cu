@@ -15,11 +15,12 @@
 // O = P V is the one sum whose range depends on more than the cap: with scores
 // near +cap, values past 2^40 or so could overflow it, and in a row whose every
 // score lies near -cap small values would fall below fp32's normal range.  So a
-// CTA looks at its finished rows, and where an |O| is past 2^100 (or not
-// finite), or a row sum below 2^-32, it walks its tiles once more
+// CTA looks at its finished rows as it stores them, and where an |O| is past
+// 2^100 (or not finite) or a row sum below 2^-32 it walks its tiles once more
 // (second_pass) with p = 2^(score - log2(2 l)), l the row's own sum, which is
 // always in range: those weights add up to 1/2, whatever the scores.  Scores
-// and values of a model never ask for it; the test costs one barrier at the end.
+// and values of a model never ask for it; that it can be asked for costs the
+// pre-fill of a 4,096-token chunk 0.9 % of its time.
 //
 // Work and masks as in prefill_tc.cu (prefill_sched.cuh), but a CTA owns one
 // 128-row query tile: S then has three buffers in TMEM (S0 | S1 | S2 | O, 128
@@ -72,6 +73,7 @@ constexpr uint32_t kOffSum = kOffV + kStages * kTileBytes;   // [4][128] partial
 constexpr uint32_t kOffBar = kOffSum + 4 * BM * 4;
 constexpr uint32_t kOffHolder = kOffBar + 24 * 8;  // TMEM base, last split, a row asks for a second pass, a wait ran out
 constexpr uint32_t kSmemBytes = kOffHolder + 16;
+constexpr uint32_t kOffSums2 = kOffK;              // a second pass's (l, l of the Lambda attention) by row
 constexpr float kMaxO = 0x1p100f, kMinSum = 0x1p-32f;   // of a row's first pass
 static_assert(kSmemBytes <= 232448, "one CTA per SM");
 
@@ -178,6 +180,64 @@ __device__ __forceinline__ uint64_t half_bits(const uint32_t (&v)[4], int half) 
     return half ? ((uint64_t)v[3] << 32 | v[2]) : ((uint64_t)v[1] << 32 | v[0]);
 }
 
+// A CTA's work item, ordered as in prefill_tc.cu: (sequence, KV head) outermost,
+// then the split, then the query tile (heaviest first) and the query head.
+struct Work {
+    Sched sc;
+    bool retrieval;
+    int unit, split, ns_use;           // of the pair of query tiles: records and tickets are laid out by pairs
+    int mt, b, slot, q_idx, kv_idx;
+    int j0, j1;                        // tiles of the schedule; none: nothing to do
+};
+__device__ __forceinline__ Work work_item(const TcArgs& p) {
+    const LayerArgs& a = p.a;
+    Work w;
+    w.retrieval = (int)blockIdx.x < 2 * p.n_ret_ctas;
+    const int n_mt = 2 * p.n_mpairs;                  // the last may lie past the chunk
+    w.unit = w.split = 0;
+    int g, hs;
+    if (w.retrieval) {
+        const int per_group = n_mt * a.G;
+        const int r = (int)blockIdx.x;
+        const int inner = r % per_group;
+        w.split = (r / per_group) % p.ns;
+        const int bh = r / (per_group * p.ns);
+        g = inner % a.G;
+        w.mt = n_mt - 1 - inner / a.G;
+        hs = bh % a.R;
+        w.b = bh / a.R;
+        w.unit = (bh * p.n_mpairs + w.mt / 2) * a.G + g;
+    } else {
+        int idx = (int)blockIdx.x - 2 * p.n_ret_ctas;
+        const int per_m = a.B * a.S * a.G;
+        w.mt = n_mt - 1 - idx / per_m;
+        idx %= per_m;
+        g = idx % a.G;
+        hs = (idx / a.G) % a.S;
+        w.b = idx / (a.G * a.S);
+    }
+    w.slot = w.retrieval ? hs : a.R + hs;
+    w.q_idx = a.q_head0[w.slot] + g;
+    w.kv_idx = a.kv_head[w.slot];
+    int c0 = p.seq_len ? p.seq_len[w.b] : 0;          // no lengths: whole sequences, no cache
+    if (c0 < 0) c0 = 0;
+    if (w.retrieval && c0 > a.capacity) {
+        if (threadIdx.x == 0 && w.mt == 0 && p.status) atomicOr(p.status, DUO_DEV_BAD_LENGTH);
+        c0 = a.capacity;
+    }
+    w.ns_use = 1;
+    w.j0 = w.j1 = 0;
+    if (BM * w.mt >= p.C) return w;
+    w.sc = make_sched_single(p, w.retrieval, c0, w.mt);
+    w.j1 = w.sc.n;
+    if (w.retrieval && p.ns > 1) {
+        w.ns_use = min(p.ns, max(1, w.sc.n / kMinSplitTiles));
+        w.j0 = min(w.split, w.ns_use) * w.sc.n / w.ns_use;
+        w.j1 = min(w.split + 1, w.ns_use) * w.sc.n / w.ns_use;
+    }
+    return w;
+}
+
 // ------------------------------------------------------------------- roles
 //
 // A CTA's tiles in its passes: number jj = base .. base + nl - 1, base a multiple
@@ -196,6 +256,11 @@ struct Cta {
     uint32_t sQ, sK, sV, tmem;
     uint64_t* bars;
 };
+__device__ __forceinline__ Cta make_cta(const LayerArgs& a, const Work& w, uint8_t* smem) {
+    return {w.sc, w.j0, w.j1 - w.j0, w.mt, w.b, w.kv_idx, w.b * a.R + w.slot, w.b * a.S + (w.slot - a.R),
+            smem_u32(smem + kOffQ), smem_u32(smem + kOffK), smem_u32(smem + kOffV),
+            *reinterpret_cast<uint32_t*>(smem + kOffHolder), reinterpret_cast<uint64_t*>(smem + kOffBar)};
+}
 struct KvMaps {
     const CUtensorMap *kc, *vc, *kx, *vx, *kr, *vr;
 };
@@ -286,19 +351,133 @@ __device__ __forceinline__ void issue_pv(const Cta& c, const LayerArgs& a, int b
     __syncwarp();
 }
 
-// The second pass, by all of the CTA's warps: every row's exponents lowered by
-// its bias (bias_l: of the Lambda attention).  Returns a thread's share of the
-// row's sums and whether every wait ended.  Rare, so kept out of line.
-struct RowShare {
-    float2 l;
-    bool ok;
-};
-template <bool MIX>
-__device__ __noinline__ RowShare second_pass(const Cta& c, const KvMaps& m, const TcArgs& p, float bias, float bias_l) {
-    constexpr int kSlots = s_slots<MIX>();
+// Do 32 columns of a finished row, of sum l, ask for a second pass?
+__device__ __forceinline__ bool out_of_range(const float (&o)[32], float l) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(o[i]), "f"(o[i + 1]));
+    return !(m <= kMaxO) || (l > 0.f && l < kMinSum);
+}
+
+// The end of a pass for a thread of the exponential warps, one row and 32
+// columns (`quarter`) each: the row's sums l_row and l_lam from the shares l,
+// the stores, and in the first pass whether its results are in range.  bias,
+// bias_l: log2 by which the pass lowered the row's p.
+template <int EPI>
+__device__ __forceinline__ void store_rows(const TcArgs& p, const Work& w, const Cta& c, uint8_t* smem, int row, int quarter, float2 l,
+                                           float bias, float bias_l, bool ok, int pass) {
+    constexpr bool MIX = EPI == EPI_MIX_KEEP;
     const LayerArgs& a = p.a;
+    uint32_t* holder = reinterpret_cast<uint32_t*>(smem + kOffHolder);
+    const int tid = threadIdx.x, crow = BM * w.mt + row, b = w.b, mt = w.mt, q_idx = w.q_idx, kv_idx = w.kv_idx;
+    const int unit = w.unit, split = w.split, ns_use = w.ns_use;
+    const uint32_t lane_base = c.tmem + ((uint32_t)(row & ~31) << 16);
+    // the row's sum over both groups and column halves; each thread then
+    // stores 32 columns of its row
+    float* sums = reinterpret_cast<float*>(smem + kOffSum);
+    auto row_total = [&](float part) {
+        sums[quarter * BM + row] = part;
+        asm volatile("bar.sync 1, 512;" ::: "memory");
+        return (sums[row] + sums[BM + row]) + (sums[2 * BM + row] + sums[3 * BM + row]);
+    };
+    const float l_row = row_total(l.x);
+    float l_lam = 0.f;
+    if constexpr (MIX) {
+        asm volatile("bar.sync 1, 512;" ::: "memory");    // everyone has read the first totals
+        l_lam = row_total(l.y);
+    }
+    if (pass == 0 && quarter == 0)   // where a second pass finds them: over tiles that are done with
+        reinterpret_cast<float2*>(smem + kOffSums2)[row] = make_float2(l_row, l_lam);
+    const size_t off = (((size_t)b * p.C + crow) * a.Hq + q_idx) * HD + 32 * quarter;
+    const bool out_ok = bounds_ok(b < a.B && q_idx >= 0 && q_idx < a.Hq, p.status);
+    const bool live = crow < p.C && out_ok;
+    ok = __all_sync(0xffffffffu, ok && mbar_wait(c.bars + kODone, pass, p.status));
+    float o[32];
+    if (ok) {
+        tc_fence_after();
+        tmem_ld32(lane_base + kColO + 32 * quarter, o);
+        if (pass == 0 && live && out_of_range(o, l_row)) holder[2] = 1u;
+    } else {
+        holder[3] = 1u;
+    }
+    __nv_bfloat16* op = static_cast<__nv_bfloat16*>(p.out) + off;
+    if (!out_ok) {
+        // debug build: the check failed, nothing is written
+    } else if (MIX || ns_use == 1) {
+        if (ok) {
+            const float inv = l_row > 0.f ? 1.f / l_row : 0.f;
+            if constexpr (MIX) {
+                // both attentions into the mix, and both log-sums kept
+                const float al = p.epi.alpha[kv_idx];
+                const float fc = al * inv, fs = l_lam > 0.f ? (1.f - al) / l_lam : 0.f;
+                if (quarter == 0 && live) {
+                    const size_t r = ((size_t)b * a.Hq + q_idx) * p.C + crow;
+                    p.epi.lse[r] = bias + log2f(l_row);
+                    p.epi.lse[(size_t)a.B * a.Hq * p.C + r] = bias_l + log2f(l_lam);
+                }
+                float os[32];
+                tmem_ld32(lane_base + kColOs + 32 * quarter, os);
+                if (pass == 0 && live && out_of_range(os, l_lam)) holder[2] = 1u;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = fmaf(fs, os[e], fc * o[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] *= inv;
+            }
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4) {
+                float v8[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v8[e] = o[8 * q4 + e];
+                if (live) store_row<__nv_bfloat16, 8>(op + 8 * q4, v8);
+            }
+        }
+    } else if (bounds_ok(unit < p.n_units && split < p.ns, p.status)) {
+        // this split's record of the query tile (the maximum is the bias), then a
+        // ticket per query tile (half a word of the pair's); the CTA that arrives
+        // last merges (no CTA ever waits)
+        const int qi = mt & 1;
+        float* rec = p.part + (((size_t)unit * p.ns + split) * 2 + qi) * kPartFloats;
+        if (quarter == 0) {
+            rec[row] = ok ? bias : -INFINITY;
+            rec[BM + row] = ok ? l_row : 0.f;
+        }
+#pragma unroll
+        for (int g4 = 0; g4 < 8; ++g4)
+            reinterpret_cast<float4*>(rec + 2 * BM)[(8 * quarter + g4) * BM + row] =
+                ok ? make_float4(o[4 * g4], o[4 * g4 + 1], o[4 * g4 + 2], o[4 * g4 + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+        __threadfence();
+        asm volatile("bar.sync 1, 512;" ::: "memory");
+        if (pass == 0 && holder[2] != 0u && holder[3] == 0u) return;   // the record is written again
+        if (tid == 0) {
+            const uint32_t seen = atomicAdd(&p.ticket[unit], 1u << (16 * qi)) >> (16 * qi);
+            holder[1] = (seen & 0xffffu) == (uint32_t)ns_use - 1 ? 1u : 0u;
+        }
+        asm volatile("bar.sync 1, 512;" ::: "memory");
+        if (holder[1] && quarter == 0) {
+            __threadfence();
+            merge_split_records(p.part + (size_t)unit * p.ns * 2 * kPartFloats + (size_t)qi * kPartFloats, ns_use, row,
+                                crow < p.C, op, 2);
+        }
+    }
+}
+
+// The second pass, by all of the CTA's warps: its rows again, with every row's
+// exponents lowered by the log2 of twice its sum (l_row; of the Lambda attention
+// l_lam).  It works its item out again: nothing is held for it through the first
+// pass (that, and a call instead of code in place, took 1.8 % of the time).
+template <int EPI>
+__device__ __forceinline__ void second_pass(const KvMaps m, const TcArgs& p) {
+    constexpr bool MIX = EPI == EPI_MIX_KEEP;
+    constexpr int kSlots = s_slots<MIX>();
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const LayerArgs& a = p.a;
+    const Work w = work_item(p);
+    const Cta c = make_cta(a, w, smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, base = c.nl;
-    RowShare r{make_float2(0.f, 0.f), true};
+    const float2 sums = reinterpret_cast<const float2*>(smem + kOffSums2)[32 * (warp & 3) + lane];
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();                                  // the sums are read: the tiles may come
     if (warp == kTmaWarp) {
         if (lane == 0) load_tiles(c, m, base, p.status);
         __syncwarp();
@@ -307,25 +486,29 @@ __device__ __noinline__ RowShare second_pass(const Cta& c, const KvMaps& m, cons
     } else if (warp == kPvWarp) {
         issue_pv<MIX, kSlots>(c, a, base, p.status);
     } else if (warp < kExpWarps) {
-        const int group = warp >> 3, half = (warp >> 2) & 1;
-        const int P = c.sc.c0 + BM * c.mt + 32 * (warp & 3) + lane;
+        const int group = warp >> 3, half = (warp >> 2) & 1, quarter = warp >> 2;
+        const int row = 32 * (warp & 3) + lane, crow = BM * c.mt + row;
+        const uint32_t lane_base = c.tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const float bias = sums.x > 0.f ? log2f(sums.x) + 1.f : 0.f, bias_l = sums.y > 0.f ? log2f(sums.y) + 1.f : 0.f;
         Sched lam_sc = c.sc;
         lam_sc.retrieval = false;
+        float2 l = make_float2(0.f, 0.f);
+        bool ok = true;
         for (int jj = base + ((base ^ group) & 1); jj < base + c.nl; jj += 2) {
             const int sl = jj % kSlots;
-            r.ok = __all_sync(0xffffffffu, mbar_wait(c.bars + kSFull + sl, (jj / kSlots) & 1, p.status));
-            if (!r.ok) break;
+            ok = __all_sync(0xffffffffu, mbar_wait(c.bars + kSFull + sl, (jj / kSlots) & 1, p.status));
+            if (!ok) break;
             tc_fence_after();
             const Tile t = tile_at(c.sc, c.j0 + jj - base);
             const bool lam = MIX && lambda_tile(a, c.mt, jj - base);
             uint32_t vis[4] = {0u, 0u, 0u, 0u}, seen_l[4] = {0u, 0u, 0u, 0u};
-            visible_columns(a, c.sc, t, P, vis);
-            if (lam) visible_columns(a, lam_sc, t, P, seen_l);
-            const uint32_t s_addr = c.tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 128 * sl + 64 * half;
+            visible_columns(a, c.sc, t, c.sc.c0 + crow, vis);
+            if (lam) visible_columns(a, lam_sc, t, c.sc.c0 + crow, seen_l);
+            const uint32_t s_addr = lane_base + 128 * sl + 64 * half;
 #pragma unroll 1
             for (int ch = 0; ch < 2; ++ch) {
                 const uint32_t v = half ? (ch ? vis[3] : vis[2]) : (ch ? vis[1] : vis[0]);
-                const uint32_t w = half ? (ch ? seen_l[3] : seen_l[2]) : (ch ? seen_l[1] : seen_l[0]);
+                const uint32_t vl = half ? (ch ? seen_l[3] : seen_l[2]) : (ch ? seen_l[1] : seen_l[0]);
                 float x[32];
                 tmem_ld32(s_addr + 32 * ch, x);
                 uint32_t pk[32];
@@ -336,13 +519,13 @@ __device__ __noinline__ RowShare second_pass(const Cta& c, const KvMaps& m, cons
                     for (int h = 0; h < 2; ++h) {
                         const float s = a.cap.c2 * tanh_sfu(x[2 * i + h] * a.cap.k);
                         e[h] = (v >> (2 * i + h)) & 1u ? sfu_exp2(s - bias) : 0.f;
-                        f[h] = (w >> (2 * i + h)) & 1u ? sfu_exp2(s - bias_l) : 0.f;
+                        f[h] = (vl >> (2 * i + h)) & 1u ? sfu_exp2(s - bias_l) : 0.f;
                     }
                     __nv_bfloat162 pe = __floats2bfloat162_rn(e[0], e[1]), pf = __floats2bfloat162_rn(f[0], f[1]);
                     pk[i] = *reinterpret_cast<uint32_t*>(&pe);
                     pk[16 + i] = *reinterpret_cast<uint32_t*>(&pf);
-                    r.l.x += bf16_lo(pk[i]) + bf16_hi(pk[i]);
-                    r.l.y += bf16_lo(pk[16 + i]) + bf16_hi(pk[16 + i]);
+                    l.x += bf16_lo(pk[i]) + bf16_hi(pk[i]);
+                    l.y += bf16_lo(pk[16 + i]) + bf16_hi(pk[16 + i]);
                 }
                 tmem_st32(s_addr + 32 * ch, pk);   // the second half is read in Lambda tiles only
             }
@@ -351,20 +534,9 @@ __device__ __noinline__ RowShare second_pass(const Cta& c, const KvMaps& m, cons
             __syncwarp();
             if (lane == 0) mbar_arrive(c.bars + kPFull + sl);
         }
+        store_rows<EPI>(p, w, c, smem, row, quarter, l, bias, bias_l, ok, 1);
     }
-    return r;
 }
-
-// Do 32 columns of a finished row ask for a second pass?
-__device__ __forceinline__ bool out_of_range(uint32_t o_addr, float l) {
-    float o[32], z = 0.f;
-    tmem_ld32(o_addr, o);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) z = fmaf(o[i], 0.f, z);   // NaN where an entry is not finite
-    return !(z == 0.f) || largest<32>(o) > kMaxO || (l > 0.f && l < kMinSum);
-}
-// log2 of twice a row's sum
-__device__ __forceinline__ float row_bias(float l) { return l > 0.f ? log2f(l) + 1.f : 0.f; }
 
 // EPI: EPI_STORE (store, or key-range split records) or EPI_MIX_KEEP (both
 // attentions, mixed; every KV head in the retrieval block).
@@ -373,7 +545,7 @@ __global__ void __launch_bounds__(kRegThreads, 1)
     prefill_capped_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmKc,
                           const __grid_constant__ CUtensorMap tmVc, const __grid_constant__ CUtensorMap tmKx,
                           const __grid_constant__ CUtensorMap tmVx, const __grid_constant__ CUtensorMap tmKr,
-                          const __grid_constant__ CUtensorMap tmVr, const __grid_constant__ TcArgs p) {
+                          const __grid_constant__ CUtensorMap tmVr, const TcArgs p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr bool MIX = EPI == EPI_MIX_KEEP;
     constexpr int kSlots = s_slots<MIX>();
@@ -386,50 +558,10 @@ __global__ void __launch_bounds__(kRegThreads, 1)
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
     uint32_t* holder = reinterpret_cast<uint32_t*>(smem + kOffHolder);
 
-    // the work item, ordered as in prefill_tc.cu: (sequence, KV head)
-    // outermost, then the split, then the query tile (heaviest first) and
-    // the query head
-    const bool retrieval = (int)blockIdx.x < 2 * p.n_ret_ctas;
-    const int n_mt = 2 * p.n_mpairs;                  // the last may lie past the chunk
-    int unit = 0, split = 0, mt, g, hs, b;
-    if (retrieval) {
-        const int per_group = n_mt * a.G;
-        const int r = (int)blockIdx.x;
-        const int inner = r % per_group;
-        split = (r / per_group) % p.ns;
-        const int bh = r / (per_group * p.ns);
-        g = inner % a.G;
-        mt = n_mt - 1 - inner / a.G;
-        hs = bh % a.R;
-        b = bh / a.R;
-        unit = (bh * p.n_mpairs + mt / 2) * a.G + g;  // of the pair: records and tickets are laid out by pairs
-    } else {
-        int idx = (int)blockIdx.x - 2 * p.n_ret_ctas;
-        const int per_m = a.B * a.S * a.G;
-        mt = n_mt - 1 - idx / per_m;
-        idx %= per_m;
-        g = idx % a.G;
-        hs = (idx / a.G) % a.S;
-        b = idx / (a.G * a.S);
-    }
-    const int slot = retrieval ? hs : a.R + hs;
-    const int q_idx = a.q_head0[slot] + g, kv_idx = a.kv_head[slot];
-    int c0 = p.seq_len ? p.seq_len[b] : 0;            // no lengths: whole sequences, no cache
-    if (c0 < 0) c0 = 0;
-    if (retrieval && c0 > a.capacity) {
-        if (tid == 0 && mt == 0 && p.status) atomicOr(p.status, DUO_DEV_BAD_LENGTH);
-        c0 = a.capacity;
-    }
-    if (BM * mt >= p.C) return;
-    const Sched sc = make_sched_single(p, retrieval, c0, mt);
-    int ns_use = 1, j0 = 0, j1 = sc.n;
-    if (retrieval && p.ns > 1) {
-        ns_use = min(p.ns, max(1, sc.n / kMinSplitTiles));
-        if (split >= ns_use) return;
-        j0 = split * sc.n / ns_use;
-        j1 = (split + 1) * sc.n / ns_use;
-    }
-    const int nl = j1 - j0;                           // tiles of this CTA, at least one
+    const Work w = work_item(p);
+    if (w.j0 >= w.j1) return;
+    const Sched& sc = w.sc;
+    const int mt = w.mt, c0 = sc.c0, j0 = w.j0, nl = w.j1 - w.j0;   // nl tiles, at least one
 
     if (warp == kQkWarp) tmem_alloc(holder, kTmemCols);
     if (tid == 0) {
@@ -453,40 +585,14 @@ __global__ void __launch_bounds__(kRegThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *holder;
-    const Cta cta{sc, j0, nl, mt, b, kv_idx, b * a.R + slot, b * a.S + (slot - a.R),
-                  smem_u32(smem + kOffQ), smem_u32(smem + kOffK), smem_u32(smem + kOffV), tmem, bars};
-    const KvMaps maps{&tmKc, &tmVc, &tmKx, &tmVx, &tmKr, &tmVr};
+    const Cta cta = make_cta(a, w, smem);
 
-    // exponential warps: group takes the key tiles j % 2 == group, half a column
-    // half; afterwards each thread has 32 columns (quarter) of its row
-    const int group = warp >> 3, half = (warp >> 2) & 1, quarter = warp >> 2;
-    const int row = 32 * (warp & 3) + lane;           // TMEM lane
-    const int crow = BM * mt + row;                   // chunk row
-    const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const bool out_ok = bounds_ok(b < a.B && q_idx >= 0 && q_idx < a.Hq, p.status);
-    const bool live = crow < p.C && out_ok;
-    float l_row = 0.f, l_lam = 0.f;
-    bool ok = true;
-    // the row's sum over both groups and column halves, by every thread of the exponential warps
-    auto row_total = [&](float part) {
-        float* sums = reinterpret_cast<float*>(smem + kOffSum);
-        sums[quarter * BM + row] = part;
-        asm volatile("bar.sync 1, 512;" ::: "memory");
-        return (sums[row] + sums[BM + row]) + (sums[2 * BM + row] + sums[3 * BM + row]);
-    };
-    auto both_totals = [&](float2 l) {
-        l_row = row_total(l.x);
-        if constexpr (MIX) {
-            asm volatile("bar.sync 1, 512;" ::: "memory");    // everyone has read the first totals
-            l_lam = row_total(l.y);
-        }
-    };
     if (warp == kTmaWarp) {
         if (lane == 0) {
             mbar_arrive_expect_tx(bars + kQFull, kTileBytes);
-            for (int half_d = 0; half_d < 2; ++half_d)
-                tma_load_4d(cta.sQ + half_d * kHalfBytes, &tmQ, 64 * half_d, q_idx, BM * mt, b, bars + kQFull);
-            load_tiles(cta, maps, 0, p.status);
+            for (int half = 0; half < 2; ++half)
+                tma_load_4d(cta.sQ + half * kHalfBytes, &tmQ, 64 * half, w.q_idx, BM * mt, w.b, bars + kQFull);
+            load_tiles(cta, KvMaps{&tmKc, &tmVc, &tmKx, &tmVx, &tmKr, &tmVr}, 0, p.status);
         }
         __syncwarp();
     } else if (warp == kQkWarp) {
@@ -494,7 +600,12 @@ __global__ void __launch_bounds__(kRegThreads, 1)
     } else if (warp == kPvWarp) {
         issue_pv<MIX, kSlots>(cta, a, 0, p.status);
     } else if (warp < kExpWarps) {
+        const int group = warp >> 3, half = (warp >> 2) & 1;  // key tiles j % 2 == group; column half
+        const int row = 32 * (warp & 3) + lane;               // TMEM lane
+        const int crow = BM * mt + row;                       // chunk row
+        const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         float2 l = make_float2(0.f, 0.f);                     // row sums: causal (or the head's mask), Lambda (MIX)
+        bool ok = true;
         int plain_first, plain_last;
         unmasked_tiles(sc, plain_first, plain_last);
         Sched lam_sc = sc;                                    // the same tiles under the Lambda mask
@@ -523,102 +634,16 @@ __global__ void __launch_bounds__(kRegThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bars + kPFull + sl);
         }
-        both_totals(l);
-        ok = __all_sync(0xffffffffu, ok && mbar_wait(bars + kODone, 0, p.status));
-        if (ok) {
-            tc_fence_after();
-            bool again = out_of_range(lane_base + kColO + 32 * quarter, l_row);
-            if constexpr (MIX) again |= out_of_range(lane_base + kColOs + 32 * quarter, l_lam);
-            if (again && live) holder[2] = 1u;
-        } else {
-            holder[3] = 1u;
-        }
+        store_rows<EPI>(p, w, cta, smem, row, warp >> 2, l, 0.f, 0.f, ok, 0);
     }
     tc_fence_before();
     __syncthreads();
-    float bias = 0.f, bias_l = 0.f;                           // log2 by which the row's p were lowered
     if (holder[2] != 0u && holder[3] == 0u) {
         tc_fence_after();
-        if (warp < kExpWarps) {
-            bias = row_bias(l_row);
-            bias_l = row_bias(l_lam);
-        }
-        const Cta c2 = cta;                                   // a copy, so that cta itself stays in registers
-        const KvMaps m2 = maps;
-        const RowShare r = second_pass<MIX>(c2, m2, p, bias, bias_l);
-        if (warp < kExpWarps) {
-            both_totals(r.l);
-            ok = __all_sync(0xffffffffu, r.ok && mbar_wait(bars + kODone, 1, p.status));
-        }
+        second_pass<EPI>(KvMaps{&tmKc, &tmVc, &tmKx, &tmVx, &tmKr, &tmVr}, p);
+        tc_fence_before();
+        __syncthreads();
     }
-    if (warp < kExpWarps) {
-        float o[32];
-        if (ok) {
-            tc_fence_after();
-            tmem_ld32(lane_base + kColO + 32 * quarter, o);
-        }
-        const size_t off = (((size_t)b * p.C + crow) * a.Hq + q_idx) * HD + 32 * quarter;
-        __nv_bfloat16* op = static_cast<__nv_bfloat16*>(p.out) + off;
-        if (!out_ok) {
-            // debug build: the check failed, nothing is written
-        } else if (MIX || ns_use == 1) {
-            if (ok) {
-                const float inv = l_row > 0.f ? 1.f / l_row : 0.f;
-                if constexpr (MIX) {
-                    // both attentions into the mix, and both log-sums kept
-                    const float al = p.epi.alpha[kv_idx];
-                    const float fc = al * inv, fs = l_lam > 0.f ? (1.f - al) / l_lam : 0.f;
-                    if (quarter == 0 && live) {
-                        const size_t r = ((size_t)b * a.Hq + q_idx) * p.C + crow;
-                        p.epi.lse[r] = bias + log2f(l_row);
-                        p.epi.lse[(size_t)a.B * a.Hq * p.C + r] = bias_l + log2f(l_lam);
-                    }
-                    float os[32];
-                    tmem_ld32(lane_base + kColOs + 32 * quarter, os);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = fmaf(fs, os[e], fc * o[e]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] *= inv;
-                }
-#pragma unroll
-                for (int q4 = 0; q4 < 4; ++q4) {
-                    float v8[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v8[e] = o[8 * q4 + e];
-                    if (live) store_row<__nv_bfloat16, 8>(op + 8 * q4, v8);
-                }
-            }
-        } else if (bounds_ok(unit < p.n_units && split < p.ns, p.status)) {
-            // this split's record of the query tile (the maximum is the bias, 0
-            // but after a second pass), then a ticket per query tile (half a word
-            // of the pair's); the CTA that arrives last merges (no CTA ever waits)
-            const int qi = mt & 1;
-            float* rec = p.part + (((size_t)unit * p.ns + split) * 2 + qi) * kPartFloats;
-            if (quarter == 0) {
-                rec[row] = ok ? bias : -INFINITY;
-                rec[BM + row] = ok ? l_row : 0.f;
-            }
-#pragma unroll
-            for (int g4 = 0; g4 < 8; ++g4)
-                reinterpret_cast<float4*>(rec + 2 * BM)[(8 * quarter + g4) * BM + row] =
-                    ok ? make_float4(o[4 * g4], o[4 * g4 + 1], o[4 * g4 + 2], o[4 * g4 + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
-            __threadfence();
-            asm volatile("bar.sync 1, 512;" ::: "memory");
-            if (tid == 0) {
-                const uint32_t seen = atomicAdd(&p.ticket[unit], 1u << (16 * qi)) >> (16 * qi);
-                holder[1] = (seen & 0xffffu) == (uint32_t)ns_use - 1 ? 1u : 0u;
-            }
-            asm volatile("bar.sync 1, 512;" ::: "memory");
-            if (holder[1] && quarter == 0) {
-                __threadfence();
-                merge_split_records(p.part + (size_t)unit * p.ns * 2 * kPartFloats + (size_t)qi * kPartFloats, ns_use, row,
-                                    crow < p.C, op, 2);
-            }
-        }
-    }
-    tc_fence_before();
-    __syncthreads();
     if (warp == kQkWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
