@@ -555,7 +555,7 @@ __global__ void __maxnreg__(decode_max_regs(G))
     if (warp < NW) {
         float q[G][EPL];
         const T* qp = static_cast<const T*>(d.q) + ((size_t)b * a.Hq + a.q_head0[slot]) * D + dl * EPL;
-        const float qs = CAP ? a.cap.k : a.scale * kLog2e;   // capped: the scores become tanh's argument
+        const float qs = a.scale * kLog2e;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             load_row_f32<T, EPL>(qp + (size_t)g * D, q[g]);
@@ -603,7 +603,10 @@ __global__ void __maxnreg__(decode_max_regs(G))
 #pragma unroll
             for (int g = 0; g < G; ++g) {
                 float sv = s[g];
-                if constexpr (CAP) sv = a.cap.c2 * tanhf(sv);
+                if constexpr (CAP) {   // sv is u already
+                    const float y = sv * a.cap.rc2, capped = a.cap.c2 * tanhf(y);
+                    sv = fabsf(y) < 0x1p-12f ? sv : capped;   // below, the cap moves it by less than half a step of fp32
+                }
                 sv = valid ? sv : kNegBig;
                 float mt = sv;
                 if (DUP == 2) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
@@ -1310,8 +1313,7 @@ __device__ __forceinline__ void decode_ring_simt(uint8_t* smem, const LayerArgs&
     const float sl = a.scale * kLog2e;
     for (int i = tid; i < G * D; i += nthr) {
         const int g = i / D, e = i % D;
-        sQ[i] = __bfloat162float(static_cast<const T*>(d.q)[((size_t)b * a.Hq + a.q_head0[slot] + g) * D + e]) *
-                (CAP ? a.cap.k : sl);
+        sQ[i] = __bfloat162float(static_cast<const T*>(d.q)[((size_t)b * a.Hq + a.q_head0[slot] + g) * D + e]) * sl;
     }
     __syncthreads();
     // scores
@@ -1326,7 +1328,7 @@ __device__ __forceinline__ void decode_ring_simt(uint8_t* smem, const LayerArgs&
 #pragma unroll
             for (int e = 0; e < 8; ++e) acc = fmaf(q[piece * 8 + e], kf[e], acc);
         }
-        sS[g * kRingMax + j] = CAP ? a.cap.c2 * tanh_sfu(acc) : acc;
+        sS[g * kRingMax + j] = CAP ? cap_sfu(acc, 1.f, a.cap.rc2, a.cap.c2).s : acc;
     }
     __syncthreads();
     // softmax of each head's scores: p in place, 1 / sum aside

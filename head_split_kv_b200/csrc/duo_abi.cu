@@ -97,7 +97,7 @@ void fill_args(const duo_layer_desc* d, duo::LayerArgs& a) {
     a.kv_bits = d->kv_quant == DUO_KV_INT8 ? 8 : d->kv_quant == DUO_KV_INT4 ? 4 : 0;
     a.page_size = d->page_size;
     a.capacity = a.max_pages = a.n_pages = 0;
-    a.cap = duo::CapArgs{0, 0.f, 0.f};
+    a.cap = duo::CapArgs{0, 0, 0.f, 0.f, 0.f, 0.f};
     a.scale = d->scale > 0.f ? d->scale : 1.0f / std::sqrt(static_cast<float>(d->head_dim));
     for (int i = 0; i < DUO_MAX_KV_HEADS; ++i) {
         a.q_head0[i] = 0;
@@ -202,11 +202,16 @@ duo_status set_cap(duo::LayerArgs& a, float cap) {
     if (!std::isfinite(cap) || cap < 0.f)
         return fail(DUO_ERR_INVALID_ARG, "cap must be finite and >= 0 (0: scores are not capped), got %g", (double)cap);
     if (cap > 0.f) {
+        constexpr double kLog2e = 1.4426950408889634;
         a.cap.on = 1;
-        a.cap.k = a.scale / cap;
-        a.cap.c2 = cap * 1.4426950408889634f;
+        a.cap.sl = (float)(a.scale * kLog2e);
+        a.cap.c2 = (float)(cap * kLog2e);
+        a.cap.rc2 = (float)(1.0 / (cap * kLog2e));
+        a.cap.k = (float)(a.scale / (double)cap);
+        // else y is off by 2^-149 at most, its score by 2^-85
+        a.cap.far = !(a.cap.c2 <= 0x1p64f && a.cap.k >= 0x1p-100f);
         // the kernels raise scale / cap to the 8th power and cap * log2(e) stays fp32
-        if (!(a.cap.k <= 1e4f) || !std::isfinite(a.cap.c2))
+        if (!(a.scale / (double)cap <= 1e4) || !std::isfinite(a.cap.c2))
             return fail(DUO_ERR_INVALID_ARG, "cap %g is out of range (from softmax scale / 1e4 to 2e38)", (double)cap);
     }
     return DUO_OK;

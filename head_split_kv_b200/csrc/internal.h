@@ -29,11 +29,14 @@ inline cudaError_t smem_limit_once(K* kernel, int bytes, std::atomic<unsigned lo
 }
 
 // Capped scores (cap.cuh): the log2-domain score of a dot product x is
-// c2 * tanh(x * k); on is 0 where the layer's scores are not capped.
+// c2 * tanh(x * sl / c2); on is 0 where the layer's scores are not capped.
 struct CapArgs {
     int on;
-    float k;    // softmax scale / cap
-    float c2;   // cap * log2(e)
+    int far;     // the cap is so large that y = x * k may leave fp32 where the score does not
+    float sl;    // softmax scale * log2(e)
+    float c2;    // cap * log2(e)
+    float rc2;   // 1 / c2
+    float k;     // sl / c2
 };
 
 // Flattened, validated view of a layer descriptor plus state, passed by

@@ -109,6 +109,7 @@ struct GradArgs {
 // What a launch computes: the rows' statistics, dK and dV (keys outer; with
 // pairs of CTAs that share a key tile), or dQ.
 enum { STATS = 0, KEYS = 1, QUERIES = 2, KEY_PAIRS = 3 };
+enum { NO_CAP = 0, CAPPED = 1, CAP_FAR = 2 };   // CapArgs::on, ::far
 __host__ __device__ constexpr bool keys_outer(int mode) { return mode == KEYS || mode == KEY_PAIRS; }
 
 __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
@@ -173,10 +174,21 @@ __device__ __forceinline__ float4 choose4(uint32_t bits, int shift, const float4
                        (bits >> (shift + 2)) & 1u ? yes.z : no.z, (bits >> (shift + 3)) & 1u ? yes.w : no.w);
 }
 
-// tanh(k x) of a pair (CAP); POLY: |k x| is within the polynomial's range.
-template <bool POLY>
-__device__ __forceinline__ float2 tanh2(float2 x, const CapArgs& cap, const TanhPoly& tp) {
-    return POLY ? poly_fma2(x, tp) : make_float2(tanh_sfu(x.x * cap.k), tanh_sfu(x.y * cap.k));
+// A pair's scores plus `add`, and t, their tanh (CAP); POLY: the dot products
+// are within the polynomial's range (never under a far cap, whose kernels are
+// instantiations of their own: one for both took 1.5 % more).
+template <int CAP, bool POLY>
+__device__ __forceinline__ float2 capped2(float2 x, const CapArgs& cap, const TanhPoly& tp, float2 add, float2& t) {
+    if constexpr (POLY) {
+        t = poly_fma2(x, tp);
+        return ffma2(t, tp.c2, add);
+    }
+    // the score rounded as the forward pass rounded it: whatever its size, it
+    // does not lie far above the row's log-sum
+    constexpr bool far = CAP == CAP_FAR;
+    const Capped a = cap_sfu<far>(x.x, cap.sl, cap.k, cap.c2), b = cap_sfu<far>(x.y, cap.sl, cap.k, cap.c2);
+    t = make_float2(a.t, b.t);
+    return fadd2(make_float2(a.s, b.s), add);
 }
 
 // A warp's 32 columns: x[] dot products -> W, or with a cap -W times
@@ -186,7 +198,7 @@ __device__ __forceinline__ float2 tanh2(float2 x, const CapArgs& cap, const Tanh
 // product to the packed W, so that the FMA, SFU and ALU work of neighbouring
 // pairs interleaves (in separate loops the pipes took turns: their shares of
 // the time added up to 96 %).
-template <bool CAP, bool COLS, bool MASKED, bool POLY>
+template <int CAP, bool COLS, bool MASKED, bool POLY>
 __device__ __forceinline__ void weights_loop(float* x, const LayerArgs& a, float sl, const TanhPoly& tp, const RowStats& r,
                                              const Seen& seen, int col0, uint32_t* pk) {
 #pragma unroll
@@ -203,28 +215,28 @@ __device__ __forceinline__ void weights_loop(float* x, const LayerArgs& a, float
             float2 v = make_float2(x[c], x[c + 1]);
             const float2 nl = h ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y);
             float2 slope;
-            if constexpr (CAP) {
-                v = tanh2<POLY>(v, a.cap, tp);
-                slope = ffma2(v, v, tp.minus1);
-                v = ffma2(v, tp.c2, nl);
+            if constexpr (CAP != NO_CAP) {
+                float2 t;
+                v = capped2<CAP, POLY>(v, a.cap, tp, nl, t);
+                slope = ffma2(t, t, tp.minus1);
             } else {
                 v = ffma2(v, make_float2(sl, sl), nl);
             }
             v = make_float2(sfu_exp2(v.x), sfu_exp2(v.y));
             if constexpr (COLS) pk[c / 2] = pack_bf16(v.x, v.y);
-            if constexpr (CAP) v = fmul2(v, slope);
+            if constexpr (CAP != NO_CAP) v = fmul2(v, slope);
             x[c] = v.x;
             x[c + 1] = v.y;
         }
     }
 }
-template <bool CAP, bool COLS, bool MASKED>
+template <int CAP, bool COLS, bool MASKED>
 __device__ __forceinline__ void weights(float (&x)[kCols], uint32_t (&pk)[kCols / 2], const LayerArgs& a, float sl,
                                         const TanhPoly& tp, const RowStats& r, const Seen& seen) {
 #pragma unroll
     for (int ch = 0; ch < kCols / kChunk; ++ch) {
         float* y = x + kChunk * ch;
-        if (!CAP || __all_sync(0xffffffffu, largest<kChunk>(y) * a.cap.k <= kTanhRange))
+        if (CAP == NO_CAP || (CAP == CAPPED && __all_sync(0xffffffffu, largest<kChunk>(y) <= tp.x_max)))
             weights_loop<CAP, COLS, MASKED, true>(y, a, sl, tp, r, seen, kChunk * ch, pk + kChunk / 2 * ch);
         else
             weights_loop<CAP, COLS, MASKED, false>(y, a, sl, tp, r, seen, kChunk * ch, pk + kChunk / 2 * ch);
@@ -274,7 +286,7 @@ __device__ __forceinline__ void score_grads(const float (&x)[kCols], const uint3
 // negative a everything a CTA accumulates is negated, so that |a| P_c is W in
 // the other tiles; here its share is positive and the other one negative,
 // whichever of the two signs is the odd one.
-template <bool CAP, bool COLS>
+template <int CAP, bool COLS>
 __device__ __forceinline__ void signed_shares(const LayerArgs& a, float sl, const RowStats& r, Seen seen,
                                               uint32_t s_addr, uint32_t d_addr) {
 #pragma unroll 1
@@ -289,10 +301,10 @@ __device__ __forceinline__ void signed_shares(const LayerArgs& a, float sl, cons
             const float lc = COLS ? st[0] : r.lse_c, qc = COLS ? st[BM] : r.dc;
             const float ls = COLS ? st[2 * BM] : r.lse_l, qs = COLS ? st[3 * BM] : r.dl;
             float slope = 1.f, s;
-            if constexpr (CAP) {
-                const float t = tanh_sfu(x[c] * a.cap.k);
-                slope = fmaf(t, t, -1.f);
-                s = t * a.cap.c2;
+            if constexpr (CAP != NO_CAP) {
+                const Capped cs = cap_sfu<CAP == CAP_FAR>(x[c], sl, a.cap.k, a.cap.c2);
+                slope = fmaf(cs.t, cs.t, -1.f);
+                s = cs.s;
             } else {
                 s = x[c] * sl;
             }
@@ -317,10 +329,10 @@ __device__ __forceinline__ void signed_shares(const LayerArgs& a, float sl, cons
 struct RowSums {
     float lc, dc, ls, ds;
 };
-template <bool CAP, bool MASKED, bool POLY>
+template <int CAP, bool MASKED, bool POLY>
 __device__ __forceinline__ void sums_loop(RowSums& sum, const float (&x)[kCols], const LayerArgs& a, float sl, const TanhPoly& tp,
                                           float nlse_c, float nlse_s, const Seen& seen, uint32_t d_addr) {
-    const float f = CAP ? a.cap.c2 : sl;
+    const float f = CAP == NO_CAP ? sl : POLY ? a.cap.c2 : 1.f;   // t below times f is the score
     float2 lc = make_float2(0.f, 0.f), dc = lc;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -330,7 +342,10 @@ __device__ __forceinline__ void sums_loop(RowSums& sum, const float (&x)[kCols],
         for (int i = 0; i < 16; i += 2) {
             const int c = 16 * h + i;
             float2 t = make_float2(x[c], x[c + 1]);
-            if constexpr (CAP) t = tanh2<POLY>(t, a.cap, tp);
+            if constexpr (CAP != NO_CAP) {
+                constexpr bool far = CAP == CAP_FAR;
+                t = POLY ? poly_fma2(t, tp) : make_float2(score_log2<true, far>(t.x, sl, a.cap), score_log2<true, far>(t.y, sl, a.cap));
+            }
             float2 v = ffma2(t, make_float2(f, f), make_float2(nlse_c, nlse_c));
             if constexpr (MASKED) {
                 // both attentions: the score once more, relative to lse_s
@@ -349,12 +364,12 @@ __device__ __forceinline__ void sums_loop(RowSums& sum, const float (&x)[kCols],
     sum.lc += lc.x + lc.y;
     sum.dc += dc.x + dc.y;
 }
-template <bool CAP, bool MASKED>
+template <int CAP, bool MASKED>
 __device__ __forceinline__ void add_sums(RowSums& sum, const LayerArgs& a, float sl, const TanhPoly& tp, float nlse_c, float nlse_s,
                                          const Seen& seen, uint32_t s_addr, uint32_t d_addr) {
     float x[kCols];
     tmem_ld32(s_addr, x);
-    if (!CAP || __all_sync(0xffffffffu, largest<kCols>(x) * a.cap.k <= kTanhRange))
+    if (CAP == NO_CAP || (CAP == CAPPED && __all_sync(0xffffffffu, largest<kCols>(x) <= tp.x_max)))
         sums_loop<CAP, MASKED, true>(sum, x, a, sl, tp, nlse_c, nlse_s, seen, d_addr);
     else
         sums_loop<CAP, MASKED, false>(sum, x, a, sl, tp, nlse_c, nlse_s, seen, d_addr);
@@ -366,7 +381,7 @@ __device__ __forceinline__ uint32_t s_col(int j) { return !keys_outer(MODE) && (
 template <int MODE>
 __device__ __forceinline__ uint32_t d_col(int j) { return MODE == STATS && (j & 1) ? kColA2 : kColP; }
 
-template <int MODE, bool CAP>
+template <int MODE, int CAP>
 __global__ void __launch_bounds__(kRegThreads, 1)
     mix_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDo,
                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const GradArgs p) {
@@ -742,7 +757,7 @@ __global__ void __launch_bounds__(kRegThreads, 1)
                     for (int i = 0; i < kCols; ++i) v[i] += peer[i * BM];
                 }
                 __nv_bfloat16* o = static_cast<__nv_bfloat16*>(t ? p.d1 : p.d0) + off;
-                const float f = (t ? 1.f : CAP ? -a.scale : a.scale) * sign;   // dS held back the softmax scale
+                const float f = (t ? 1.f : CAP != NO_CAP ? -a.scale : a.scale) * sign;   // dS held back the softmax scale
 #pragma unroll
                 for (int e = 0; e < kCols / 8; ++e) {
                     float v8[8];
@@ -761,8 +776,8 @@ __global__ void __launch_bounds__(kRegThreads, 1)
     }
 }
 
-template <int MODE, bool CAP>
-cudaError_t launch_grad(const CUtensorMap (&m)[4], const GradArgs& p, cudaStream_t s) {
+template <int MODE, int CAP>
+cudaError_t launch_cap(const CUtensorMap (&m)[4], const GradArgs& p, cudaStream_t s) {
     static std::atomic<unsigned long long> configured{0};
     const cudaError_t e = smem_limit_once(mix_grad_kernel<MODE, CAP>, (int)kGradSmem, configured);
     if (e != cudaSuccess) return e;
@@ -781,6 +796,12 @@ cudaError_t launch_grad(const CUtensorMap (&m)[4], const GradArgs& p, cudaStream
     cfg.numAttrs = MODE == KEY_PAIRS ? 1 : 0;
     const cudaError_t launched = cudaLaunchKernelEx(&cfg, mix_grad_kernel<MODE, CAP>, m[0], m[1], m[2], m[3], p);
     return launched != cudaSuccess ? launched : cudaGetLastError();
+}
+
+template <int MODE>
+cudaError_t launch_grad(const CUtensorMap (&m)[4], const GradArgs& p, cudaStream_t s) {
+    const CapArgs& cap = p.a.cap;
+    return !cap.on ? launch_cap<MODE, NO_CAP>(m, p, s) : !cap.far ? launch_cap<MODE, CAPPED>(m, p, s) : launch_cap<MODE, CAP_FAR>(m, p, s);
 }
 
 // Two CTAs to a key tile where the first, seen by every query of its group,
@@ -819,18 +840,15 @@ cudaError_t launch_mix_grad_tc(const LayerArgs& a, const MixGradArgs& g, int N, 
         if (!encode_tmap_bf16(&m[i], base[i], 4, d, st, bx)) return cudaErrorInvalidValue;
     }
     GradArgs p{a, N, pl.n_tiles, pl.n_pad, g.stats, g.lse, g.alpha, nullptr, nullptr, g.part, g.dalpha, g.status, tanh_poly(a.cap, 1.f)};
-    cudaError_t e = a.cap.on ? launch_grad<STATS, true>(m, p, s) : launch_grad<STATS, false>(m, p, s);
+    cudaError_t e = launch_grad<STATS>(m, p, s);
     if (e != cudaSuccess) return e;
     p.d0 = g.dk;
     p.d1 = g.dv;
-    if (share_key_tiles(a, pl.n_tiles))
-        e = a.cap.on ? launch_grad<KEY_PAIRS, true>(m, p, s) : launch_grad<KEY_PAIRS, false>(m, p, s);
-    else
-        e = a.cap.on ? launch_grad<KEYS, true>(m, p, s) : launch_grad<KEYS, false>(m, p, s);
+    e = share_key_tiles(a, pl.n_tiles) ? launch_grad<KEY_PAIRS>(m, p, s) : launch_grad<KEYS>(m, p, s);
     if (e != cudaSuccess) return e;
     p.d0 = g.dq;
     p.d1 = nullptr;
-    return a.cap.on ? launch_grad<QUERIES, true>(m, p, s) : launch_grad<QUERIES, false>(m, p, s);
+    return launch_grad<QUERIES>(m, p, s);
 }
 
 }  // namespace duo

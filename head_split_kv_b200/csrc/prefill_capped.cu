@@ -15,9 +15,9 @@
 // O = P V is the one sum whose range depends on more than the cap: with scores
 // near +cap, values past 2^40 or so could overflow it, and in a row whose every
 // score lies near -cap small values would fall below fp32's normal range.  So a
-// CTA looks at its finished rows as it stores them, and where an |O| is past
-// 2^100 (or not finite) or a row sum below 2^-32 it walks its tiles once more
-// (second_pass) with p = 2^(score - log2(2 l)), l the row's own sum, which is
+// CTA looks at its rows as it stores them, and where a result is not finite (a
+// split's, to be added to others: past 2^100) or a row sum below 2^-32 it walks
+// its tiles once more (second_pass) with p = 2^(score - log2(2 l)), l the row's own sum, which is
 // always in range: those weights add up to 1/2, whatever the scores.  Scores
 // and values of a model never ask for it; that it can be asked for costs the
 // pre-fill of a 4,096-token chunk 0.9 % of its time.
@@ -74,7 +74,7 @@ constexpr uint32_t kOffBar = kOffSum + 4 * BM * 4;
 constexpr uint32_t kOffHolder = kOffBar + 24 * 8;  // TMEM base, last split, a row asks for a second pass, a wait ran out
 constexpr uint32_t kSmemBytes = kOffHolder + 16;
 constexpr uint32_t kOffSums2 = kOffK;              // a second pass's (l, l of the Lambda attention) by row
-constexpr float kMaxO = 0x1p100f, kMinSum = 0x1p-32f;   // of a row's first pass
+constexpr float kMaxO = 0x1p100f, kMinSum = 0x1p-32f;   // of a first pass: a split's |O|, a row's sum
 static_assert(kSmemBytes <= 232448, "one CTA per SM");
 
 // The key tiles of query tile mt (chunk rows 128 mt ..), as make_sched lists
@@ -125,7 +125,7 @@ __device__ __forceinline__ float2 exp_loop(const float (&x)[32], uint32_t (&pk)[
             big = fmax3(big, u.x, u.y);
             v = poly_fma2(v, u, tp);
         } else {
-            v = make_float2(cap.c2 * tanh_sfu(v.x * cap.k), cap.c2 * tanh_sfu(v.y * cap.k));
+            v = make_float2(score_log2<true, false>(v.x, cap.sl, cap), score_log2<true, false>(v.y, cap.sl, cap));
         }
         float2 e = make_float2(sfu_exp2(v.x), sfu_exp2(v.y));
         if constexpr (MASKED) {
@@ -351,12 +351,17 @@ __device__ __forceinline__ void issue_pv(const Cta& c, const LayerArgs& a, int b
     __syncwarp();
 }
 
-// Do 32 columns of a finished row, of sum l, ask for a second pass?
-__device__ __forceinline__ bool out_of_range(const float (&o)[32], float l) {
-    float m = 0.f;
+// Are 32 values all finite and at most `limit` in size?
+__device__ __forceinline__ bool within(const float (&o)[32], float limit) {
+    auto max_nan = [](float a, float b, float c) {
+        float d;
+        asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+        return d;
+    };
+    float m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(o[i]), "f"(o[i + 1]));
-    return !(m <= kMaxO) || (l > 0.f && l < kMinSum);
+    for (int i = 0; i < 32; i += 2) m[(i >> 1) & 3] = max_nan(m[(i >> 1) & 3], o[i], o[i + 1]);
+    return max_nan(max_nan(m[0], m[1], m[2]), m[3], 0.f) <= limit;
 }
 
 // The end of a pass for a thread of the exponential warps, one row and 32
@@ -393,10 +398,15 @@ __device__ __forceinline__ void store_rows(const TcArgs& p, const Work& w, const
     const bool live = crow < p.C && out_ok;
     ok = __all_sync(0xffffffffu, ok && mbar_wait(c.bars + kODone, pass, p.status));
     float o[32];
+    // the first pass: do this row's results, in o, ask for a second one?
+    auto judge = [&](float limit) {
+        if (pass == 0 && live && ok &&
+            (!within(o, limit) || (l_row > 0.f && l_row < kMinSum) || (MIX && l_lam > 0.f && l_lam < kMinSum)))
+            holder[2] = 1u;
+    };
     if (ok) {
         tc_fence_after();
         tmem_ld32(lane_base + kColO + 32 * quarter, o);
-        if (pass == 0 && live && out_of_range(o, l_row)) holder[2] = 1u;
     } else {
         holder[3] = 1u;
     }
@@ -417,7 +427,6 @@ __device__ __forceinline__ void store_rows(const TcArgs& p, const Work& w, const
                 }
                 float os[32];
                 tmem_ld32(lane_base + kColOs + 32 * quarter, os);
-                if (pass == 0 && live && out_of_range(os, l_lam)) holder[2] = 1u;
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] = fmaf(fs, os[e], fc * o[e]);
             } else {
@@ -431,11 +440,13 @@ __device__ __forceinline__ void store_rows(const TcArgs& p, const Work& w, const
                 for (int e = 0; e < 8; ++e) v8[e] = o[8 * q4 + e];
                 if (live) store_row<__nv_bfloat16, 8>(op + 8 * q4, v8);
             }
+            judge(3.4028235e38f);
         }
     } else if (bounds_ok(unit < p.n_units && split < p.ns, p.status)) {
         // this split's record of the query tile (the maximum is the bias), then a
         // ticket per query tile (half a word of the pair's); the CTA that arrives
         // last merges (no CTA ever waits)
+        judge(kMaxO);
         const int qi = mt & 1;
         float* rec = p.part + (((size_t)unit * p.ns + split) * 2 + qi) * kPartFloats;
         if (quarter == 0) {
@@ -517,7 +528,7 @@ __device__ __forceinline__ void second_pass(const KvMaps m, const TcArgs& p) {
                     float e[2], f[2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float s = a.cap.c2 * tanh_sfu(x[2 * i + h] * a.cap.k);
+                        const float s = score_log2<true, false>(x[2 * i + h], a.cap.sl, a.cap);
                         e[h] = (v >> (2 * i + h)) & 1u ? sfu_exp2(s - bias) : 0.f;
                         f[h] = (vl >> (2 * i + h)) & 1u ? sfu_exp2(s - bias_l) : 0.f;
                     }
@@ -638,7 +649,7 @@ __global__ void __launch_bounds__(kRegThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (holder[2] != 0u && holder[3] == 0u) {
+    if (__builtin_expect(holder[2] != 0u && holder[3] == 0u, 0)) {
         tc_fence_after();
         second_pass<EPI>(KvMaps{&tmKc, &tmVc, &tmKx, &tmVx, &tmKr, &tmVr}, p);
         tc_fence_before();

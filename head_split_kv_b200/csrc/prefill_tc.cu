@@ -146,8 +146,9 @@ __device__ __forceinline__ float2 exp2_fma2(float2 x) {
 // of the rounded P.
 //
 // CAP (cap.cuh): the scores become c2 * tanh(k * s) in place, in the log2
-// domain already, before the mask: on the FMA pipe when every |k * s| of the
-// warp's part of the tile is at most 1 (a vote), else on the SFU.
+// domain already, before the mask: on the FMA pipe when every |s| of the
+// warp's part of the tile is in the polynomial's range (a vote), else on the
+// SFU.
 template <bool CAP>
 __device__ __forceinline__ float softmax_tile(uint32_t s_addr, float sl, const CapArgs& cap, const TanhPoly& tp, bool masked,
                                               const uint32_t (&vis)[4], float& m_ref, float& l_sum, bool& need,
@@ -181,16 +182,19 @@ __device__ __forceinline__ float softmax_tile(uint32_t s_addr, float sl, const C
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             big = fmax3(big, fmaxf(hi[i], s[124 + i]), -fminf(lo[i], s[124 + i]));
-        if (__all_sync(0xffffffffu, big * cap.k <= kTanhRange)) {
+        if (__all_sync(0xffffffffu, big <= tp.x_max)) {
 #pragma unroll
             for (int c = 0; c < 128; c += 2) {
                 const float2 t = poly_fma2(make_float2(s[c], s[c + 1]), tp);
                 s[c] = t.x;
                 s[c + 1] = t.y;
             }
+        } else if (!cap.far) {
+#pragma unroll
+            for (int c = 0; c < 128; ++c) s[c] = score_log2<true, false>(s[c], sl, cap);
         } else {
 #pragma unroll
-            for (int c = 0; c < 128; ++c) s[c] = cap.c2 * tanh_sfu(s[c] * cap.k);
+            for (int c = 0; c < 128; ++c) s[c] = score_log2<true, true>(s[c], sl, cap);
         }
     }
     if (masked) {

@@ -24,6 +24,8 @@
 // its own sums (or running softmax), and merge at the end: that step 197 -> 142
 // us; a pre-fill of 2 x 333 rows behind 900 tokens 106 us with 16 x 16 threads
 // on one tile, 131 with 8 x 16, 91 with two groups.
+#include <type_traits>
+
 #include "cap.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -332,20 +334,30 @@ __global__ void __launch_bounds__(tiled_threads<D, MIX, OT>() * tiled_groups<D, 
         tile_dot<D, RI>(sQ, sK, tx, ty, x);
         // the tile's keys are before the band of every row: no Lambda state (mix)
         const bool lam_tile = MIX && (k0 < a.sink || r0 - (k0 + TT - 1) < a.recent);
+        auto scores = [&](auto far) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int pos = sPos[tx + 16 * j];
+            for (int j = 0; j < 4; ++j) {
+                const int pos = sPos[tx + 16 * j];
 #pragma unroll
-            for (int i = 0; i < RI; ++i) {
-                const int P = c0 + r0 + RI * ty + i;
-                const bool causal = pos >= 0 && pos <= P;
-                const bool lam = causal && (pos < a.sink || (!MIX && a.stream_chunk ? pos >= c0 - a.recent
-                                                                                   : P - pos < a.recent));
-                const float sc = score_log2<CAP, true>(x[i][j], sl, a.cap);
-                x[i][j] = (MIX || retrieval ? causal : lam) ? sc : -INFINITY;
-                x2[i][j] = lam ? sc : -INFINITY;
+                for (int i = 0; i < RI; ++i) {
+                    const int P = c0 + r0 + RI * ty + i;
+                    const bool causal = pos >= 0 && pos <= P;
+                    const bool lam = causal && (pos < a.sink || (!MIX && a.stream_chunk ? pos >= c0 - a.recent
+                                                                                       : P - pos < a.recent));
+                    float sc = x[i][j];
+                    if constexpr (CAP)
+                        sc = cap_exact<decltype(far)::value>(sc, sl, a.cap).s;
+                    else
+                        sc *= sl;
+                    x[i][j] = (MIX || retrieval ? causal : lam) ? sc : -INFINITY;
+                    x2[i][j] = lam ? sc : -INFINITY;
+                }
             }
-        }
+        };
+        if (CAP && a.cap.far)
+            scores(std::true_type{});
+        else
+            scores(std::false_type{});
         softmax_step<RI, W>(x, m, l, o);
         put_transposed<RI, PS>(sP, x, tx, ty);
         if constexpr (MIX) {
@@ -610,30 +622,36 @@ __global__ void __launch_bounds__(tiled_threads<D, true, OT>() * tiled_groups<D,
         const int i0 = it * TT;                                       // first inner row
         const int query0 = KEYS ? i0 : o0, key0 = KEYS ? o0 : i0, n_keys = KEYS ? OT : TT;
         const bool lam_tile = key0 < a.sink || query0 - (key0 + n_keys - 1) < a.recent;
+        auto weights_and_grads = [&](auto far) {
 #pragma unroll
-        for (int i = 0; i < RI; ++i) {
+            for (int i = 0; i < RI; ++i) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int orow = RI * ty + i, icol = tx + 16 * j;
-                const int qr = KEYS ? icol : orow;                    // the query's row in its tile
-                const int query = query0 + qr, key = key0 + (KEYS ? orow : icol);
-                float slope = 1.f, s;
-                if constexpr (CAP) {
-                    const float t = tanhf(x[i][j] * a.cap.k);
-                    slope = fmaf(-t, t, 1.f);
-                    s = t * a.cap.c2;
-                } else {
-                    s = x[i][j] * sl;
+                for (int j = 0; j < 4; ++j) {
+                    const int orow = RI * ty + i, icol = tx + 16 * j;
+                    const int qr = KEYS ? icol : orow;                    // the query's row in its tile
+                    const int query = query0 + qr, key = key0 + (KEYS ? orow : icol);
+                    float slope = 1.f, s;
+                    if constexpr (CAP) {
+                        const Capped c = cap_exact<decltype(far)::value>(x[i][j], sl, a.cap);
+                        slope = fmaf(-c.t, c.t, 1.f);
+                        s = c.s;
+                    } else {
+                        s = x[i][j] * sl;
+                    }
+                    const bool causal = key <= query;
+                    const float wc = causal ? sgn_c * exp2f(s - sStat[qr]) : 0.f;
+                    float ws = 0.f;
+                    if (lam_tile && causal && (key < a.sink || query - key < a.recent))
+                        ws = sgn_s * exp2f(s - sStat[2 * TT + qr]);
+                    x[i][j] = wc + ws;
+                    d[i][j] = slope * (wc * (d[i][j] - sStat[TT + qr]) + ws * (d[i][j] - sStat[3 * TT + qr]));
                 }
-                const bool causal = key <= query;
-                const float wc = causal ? sgn_c * exp2f(s - sStat[qr]) : 0.f;
-                float ws = 0.f;
-                if (lam_tile && causal && (key < a.sink || query - key < a.recent))
-                    ws = sgn_s * exp2f(s - sStat[2 * TT + qr]);
-                x[i][j] = wc + ws;
-                d[i][j] = slope * (wc * (d[i][j] - sStat[TT + qr]) + ws * (d[i][j] - sStat[3 * TT + qr]));
             }
-        }
+        };
+        if (CAP && a.cap.far)
+            weights_and_grads(std::true_type{});
+        else
+            weights_and_grads(std::false_type{});
         put_transposed<RI, PS>(sG, d, tx, ty);
         if constexpr (KEYS) put_transposed<RI, PS>(sW, x, tx, ty);
         group_sync<GROUPS, TH>(group);
