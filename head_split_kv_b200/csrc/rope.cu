@@ -150,14 +150,16 @@ __device__ __forceinline__ void turn_unit(const RopeArgs& r, const float2 (&c)[P
 }
 
 // Head row `row` of token bt: rows 0 .. n_q - 1 are q's, then k's, then v's.
-// Where it comes from (NULL: an append of later tokens evicts it) ...
+// Where it comes from (NULL: an append of later tokens evicts it; L is the
+// sequence's length, or 0 while that is on its way: a negative one, which is
+// reported, evicts fewer rows) ...
 template <typename T, bool APPEND>
-__device__ __forceinline__ const T* row_src(const LayerArgs& a, const RopeKernelArgs& x, size_t bt, int t, int row,
+__device__ __forceinline__ const T* row_src(const LayerArgs& a, const RopeKernelArgs& x, size_t bt, int t, int row, int L,
                                             bool& turned) {
     turned = row < x.n_q + x.n_k;
     if (row < x.n_q) return static_cast<const T*>(x.q) + (bt * x.n_q + row) * a.D;
     const int kv = row - x.n_q >= x.n_k, h = row - x.n_q - (kv ? x.n_k : 0);
-    if (APPEND && a.slot_of[h] >= a.R && t >= a.sink && t < x.T - a.recent) return nullptr;
+    if (APPEND && a.slot_of[h] >= a.R && t + min(L, 0) >= a.sink && t < x.T - a.recent) return nullptr;
     return static_cast<const T*>(kv ? x.v : x.k) + (bt * x.n_k + h) * a.D;
 }
 
@@ -222,6 +224,30 @@ __device__ __forceinline__ void advance_lengths(const LayerArgs& a, const CacheA
     }
 }
 
+// Rows row0 .. row1 - 1 of a token, one pair (or two elements) at a time.
+// skipped: only those that a length of 0 would have evicted.
+template <typename T, int D, bool APPEND>
+__device__ __forceinline__ void turn_pairs(const LayerArgs& a, const CacheArgs& c, const RopeKernelArgs& x, size_t bt, int b,
+                                           int t, int row0, int row1, int L, bool skipped, const float* cos_t,
+                                           const float* sin_t) {
+    const int half = x.r.rot_dim >> 1;
+    for (int u = threadIdx.x; u < (row1 - row0) * (D / 2); u += blockDim.x) {
+        const int row = row0 + u / (D / 2), k = u % (D / 2);
+        bool turned;
+        if (skipped && row_src<T, APPEND>(a, x, bt, t, row, 0, turned)) continue;
+        const T* src = row_src<T, APPEND>(a, x, bt, t, row, L, turned);
+        T* dst = src ? row_dst<T, APPEND>(a, c, x, bt, b, t, row, L, k == 0) : nullptr;
+        if (!dst) continue;
+        const bool is_pair = turned && k < half;
+        const bool apart = is_pair && x.r.layout == DUO_ROPE_HALVES;
+        const int e0 = apart ? k : 2 * k, e1 = apart ? k + half : 2 * k + 1;
+        float v0 = Elem<T>::to_f32(src[e0]), v1 = Elem<T>::to_f32(src[e1]);
+        if (is_pair) rotate(v0, v1, cos_t[k], sin_t[k]);
+        dst[e0] = Elem<T>::from_f32(v0);
+        dst[e1] = Elem<T>::from_f32(v1);
+    }
+}
+
 // VEC: units of two 16-byte pieces, thread (unit, row) walking the rows; else
 // one pair (or two elements) a unit.
 template <typename T, int D, bool APPEND, bool VEC>
@@ -248,7 +274,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const LayerArgs a, c
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
                 const int row = r + i * step;
-                src[i] = row < row1 ? row_src<T, APPEND>(a, x, bt, t, row, turned[i]) : nullptr;
+                src[i] = row < row1 ? row_src<T, APPEND>(a, x, bt, t, row, 0, turned[i]) : nullptr;
                 if (!src[i]) continue;
                 unit_pieces<T>(x.r, turned[i], k, p0[i], p1[i]);
                 w[i][0] = reinterpret_cast<const uint4*>(src[i])[p0[i]];
@@ -276,24 +302,12 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const LayerArgs a, c
                 reinterpret_cast<uint4*>(dst)[p1[i]] = w[i][1];
             }
         }
+        if (APPEND && L < 0) turn_pairs<T, D, APPEND>(a, c, x, bt, b, t, row0, row1, L, true, cos_t, sin_t);
     } else {
         const int L = APPEND ? c.seq_len[b] : 0;
         token_angles(x.r, c.seq_len, b, t, x.T, a.B, cos_t, sin_t);
         __syncthreads();
-        for (int u = threadIdx.x; u < (row1 - row0) * (D / 2); u += blockDim.x) {
-            const int row = row0 + u / (D / 2), k = u % (D / 2);
-            bool turned;
-            const T* src = row_src<T, APPEND>(a, x, bt, t, row, turned);
-            T* dst = src ? row_dst<T, APPEND>(a, c, x, bt, b, t, row, L, k == 0) : nullptr;
-            if (!dst) continue;
-            const bool is_pair = turned && k < half;
-            const bool apart = is_pair && x.r.layout == DUO_ROPE_HALVES;
-            const int e0 = apart ? k : 2 * k, e1 = apart ? k + half : 2 * k + 1;
-            float v0 = Elem<T>::to_f32(src[e0]), v1 = Elem<T>::to_f32(src[e1]);
-            if (is_pair) rotate(v0, v1, cos_t[k], sin_t[k]);
-            dst[e0] = Elem<T>::from_f32(v0);
-            dst[e1] = Elem<T>::from_f32(v1);
-        }
+        turn_pairs<T, D, APPEND>(a, c, x, bt, b, t, row0, row1, L, false, cos_t, sin_t);
     }
     if constexpr (APPEND) advance_lengths(a, c, x.T);
 }
