@@ -469,7 +469,7 @@ struct StatArgs {
 template <typename T, int D>
 __global__ void __launch_bounds__(kStatWarps * 32) tiled_stats_kernel(const LayerArgs a, const StatArgs x) {
     constexpr int E = D / 32;      // elements a lane
-    const int chunk = blockIdx.x, kv = blockIdx.y, b = blockIdx.z;
+    const int chunks = x.n_pad / kStatRows, chunk = blockIdx.x % chunks, b = blockIdx.x / chunks, kv = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const float al = x.alpha[kv];
     const float shift_c = -log2f(fabsf(al)), shift_s = -log2f(fabsf(1.f - al));   // +inf for a closed gate
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(kStatWarps * 32) tiled_stats_kernel(const Laye
         float sum = 0.f;
 #pragma unroll
         for (int w = 0; w < kStatWarps; ++w) sum += s_share[w];
-        x.part[((size_t)kv * a.B + b) * gridDim.x + chunk] = sum;
+        x.part[((size_t)kv * a.B + b) * chunks + chunk] = sum;
     }
 }
 
@@ -745,7 +745,9 @@ cudaError_t launch_grad(const LayerArgs& a, const TiledGradArgs& p, cudaStream_t
 
 template <typename T, int D>
 cudaError_t launch_grads(const LayerArgs& a, TiledGradArgs p, const StatArgs& x, void* dq, cudaStream_t st) {
-    const dim3 grid((unsigned)(x.n_pad / kStatRows), (unsigned)a.Hkv, (unsigned)a.B);
+    const long chunks = (long)a.B * (x.n_pad / kStatRows);
+    if (chunks > 0x7fffffffL) return cudaErrorInvalidConfiguration;
+    const dim3 grid((unsigned)chunks, (unsigned)a.Hkv);
     tiled_stats_kernel<T, D><<<grid, kStatWarps * 32, 0, st>>>(a, x);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
@@ -787,7 +789,6 @@ cudaError_t launch_tiled_mix(const LayerArgs& a, const float* alpha, const void*
 }
 
 cudaError_t launch_tiled_mix_grad(const LayerArgs& a, const MixGradArgs& g, int N, cudaStream_t st) {
-    if (a.B > 65535) return cudaErrorInvalidConfiguration;
     const MixGradPlan pl = mix_grad_plan(a, N);
     const StatArgs x{g.dout, g.causal, g.streaming, g.lse, g.alpha, g.stats, g.part, N, pl.n_pad};
     const TiledGradArgs p{g.q, g.dout, g.k, g.v, g.stats, g.alpha, g.dk, g.dv, g.part, a.B * (pl.n_pad / kStatRows),
