@@ -549,12 +549,12 @@ duo_status duo_rope_qk(const duo_layer_desc* desc, const duo_rope* rope, const i
     duo::RopeArgs r;
     if ((s = rope_args(desc, rope, inverse != 0, r)) != DUO_OK) return s;
     if (T < 0) return fail(DUO_ERR_SHAPE, "T must be >= 0 (got %d)", T);
+    if (T == 0) return ok();
     if ((q == nullptr) != (q_out == nullptr) || (k == nullptr) != (k_out == nullptr))
         return fail(DUO_ERR_INVALID_ARG, "duo_rope_qk: q and q_out (k and k_out) are given together");
     if (!q && !k) return fail(DUO_ERR_INVALID_ARG, "duo_rope_qk: neither q nor k is given");
     if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out))
         return fail(DUO_ERR_INVALID_ARG, "duo_rope_qk tensors must be 16-byte aligned");
-    if (T == 0) return ok();
     const size_t row = (size_t)desc->head_dim * (desc->dtype == DUO_BF16 ? 2 : 4);
     const size_t nq = q ? (size_t)desc->batch * T * desc->n_q_heads * row : 0;
     const size_t nk = k ? (size_t)desc->batch * T * desc->n_kv_heads * row : 0;
@@ -766,11 +766,11 @@ duo_status duo_gated_mix_train(const duo_layer_desc* desc, const float* alpha, f
     fill_args(desc, a);
     if ((s = set_cap(a, cap)) != DUO_OK) return s;
     if (N < 0) return fail(DUO_ERR_SHAPE, "N must be >= 0 (got %d)", N);
+    if (N == 0) return ok();
     if (!alpha || !q || !k || !v || !out || !saved || !status)
         return fail(DUO_ERR_INVALID_ARG, "duo_gated_mix_train: NULL argument");
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(saved))
         return fail(DUO_ERR_INVALID_ARG, "duo_gated_mix_train tensors must be 16-byte aligned");
-    if (N == 0) return ok();
     mix_layers(a, as, ac);
     const MixSaved sv = mix_saved(as, ac, N);
     if (saved_bytes < sv.bytes)
@@ -820,15 +820,16 @@ duo_status duo_gated_mix_grad(const duo_layer_desc* desc, const float* alpha, fl
     fill_args(desc, a);
     if ((s = set_cap(a, cap)) != DUO_OK) return s;
     if (N < 0) return fail(DUO_ERR_SHAPE, "N must be >= 0 (got %d)", N);
-    if (!alpha || !q || !k || !v || !saved || !dout || !dq || !dk || !dv || !dalpha || !workspace || !status)
-        return fail(DUO_ERR_INVALID_ARG, "duo_gated_mix_grad: NULL argument");
-    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(saved) || !aligned16(dout) || !aligned16(dq) ||
-        !aligned16(dk) || !aligned16(dv) || !aligned16(workspace))
-        return fail(DUO_ERR_INVALID_ARG, "duo_gated_mix_grad tensors must be 16-byte aligned");
+    if (!dalpha) return fail(DUO_ERR_INVALID_ARG, "duo_gated_mix_grad: NULL argument");
     if (N == 0) {
         const cudaError_t e = cudaMemsetAsync(dalpha, 0, sizeof(float) * desc->n_kv_heads, (cudaStream_t)stream);
         return e == cudaSuccess ? ok() : cuda_fail(e, "duo_gated_mix_grad");
     }
+    if (!alpha || !q || !k || !v || !saved || !dout || !dq || !dk || !dv || !workspace || !status)
+        return fail(DUO_ERR_INVALID_ARG, "duo_gated_mix_grad: NULL argument");
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(saved) || !aligned16(dout) || !aligned16(dq) ||
+        !aligned16(dk) || !aligned16(dv) || !aligned16(workspace))
+        return fail(DUO_ERR_INVALID_ARG, "duo_gated_mix_grad tensors must be 16-byte aligned");
     mix_layers(a, as, ac);
     const MixSaved sv = mix_saved(as, ac, N);
     if (saved_bytes < sv.bytes)

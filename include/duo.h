@@ -437,7 +437,7 @@ duo_status duo_prefill_chunk(const duo_layer_desc* desc, const duo_kv_state* st,
  * state's seq_len before a chunk's pre-fill).
  * inverse != 0: the gradient -- given the gradients of q_out and k_out, those
  * of q and k: the same map by the negative angles.
- * T == 0 is a no-op.
+ * T == 0 is a no-op (the tensors may then be NULL).
  * Errors: DUO_ERR_INVALID_ARG, DUO_ERR_SHAPE, DUO_ERR_CUDA.
  */
 duo_status duo_rope_qk(const duo_layer_desc* desc, const duo_rope* rope, const int32_t* seq_len, const void* q,
@@ -596,7 +596,8 @@ duo_status duo_gated_mix_grad_alpha(const duo_layer_desc* desc, const void* q, c
  * bf16 with d = 128 and sink + recent <= 128 runs on the tcgen05 tensor cores
  * (the weights and their gradients rounded to bf16 as MMA operands, sums in
  * fp32); the rest on the CUDA cores in fp32.
- * N == 0: nothing is done but that dalpha is zeroed.
+ * N == 0: nothing is done but that dalpha is zeroed (the other tensors may then
+ * be NULL).
  * q, k, v and dout must be finite: masked entries are weights of 0 in matrix
  * products.
  * status: as for duo_gated_mix.
