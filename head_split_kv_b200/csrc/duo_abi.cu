@@ -389,6 +389,31 @@ bool overlap(const void* x, size_t nx, const void* y, size_t ny) {
     return a < b + ny && b < a + nx;
 }
 
+// Does an output overlap what the rotation's angles are made of?
+bool hits_angles(const duo_layer_desc* d, const duo_rope* r, const int32_t* seq_len, int32_t T, const void* out, size_t n) {
+    const size_t pos = (size_t)r->n_axes * d->batch * T * sizeof(int32_t);
+    return n > 0 && (overlap(out, n, r->inv_freq, (size_t)r->rot_dim / 2 * sizeof(float)) ||
+                     (r->pos && overlap(out, n, r->pos, pos)) ||
+                     (seq_len && overlap(out, n, seq_len, (size_t)d->batch * sizeof(int32_t))));
+}
+
+// Memory that a call reads or writes.
+struct Range {
+    const void* p;
+    size_t n;
+};
+// The first output that overlaps an input or an earlier output, or -1.
+template <int NI, int NO>
+int overlapping(const Range (&in)[NI], const Range (&out)[NO]) {
+    for (int i = 0; i < NO; ++i) {
+        for (const Range& x : in)
+            if (overlap(out[i].p, out[i].n, x.p, x.n)) return i;
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return i;
+    }
+    return -1;
+}
+
 }  // namespace
 
 // ===========================================================================
@@ -559,7 +584,8 @@ duo_status duo_rope_qk(const duo_layer_desc* desc, const duo_rope* rope, const i
     const size_t nq = q ? (size_t)desc->batch * T * desc->n_q_heads * row : 0;
     const size_t nk = k ? (size_t)desc->batch * T * desc->n_kv_heads * row : 0;
     if ((q != q_out && overlap(q, nq, q_out, nq)) || (k != k_out && overlap(k, nk, k_out, nk)) ||
-        overlap(q_out, nq, k, nk) || overlap(k_out, nk, q, nq) || overlap(q_out, nq, k_out, nk))
+        overlap(q_out, nq, k, nk) || overlap(k_out, nk, q, nq) || overlap(q_out, nq, k_out, nk) ||
+        hits_angles(desc, rope, seq_len, T, q_out, nq) || hits_angles(desc, rope, seq_len, T, k_out, nk))
         return fail(DUO_ERR_INVALID_ARG, "duo_rope_qk: an output overlaps another tensor (it may only be its input itself)");
     duo::LayerArgs a;
     fill_args(desc, a);
@@ -587,7 +613,8 @@ duo_status duo_append_kv_rope(const duo_layer_desc* desc, const duo_kv_state* st
     const size_t row = (size_t)desc->head_dim * (desc->dtype == DUO_BF16 ? 2 : 4);
     const size_t nq = q ? (size_t)desc->batch * T * desc->n_q_heads * row : 0;
     const size_t nk = (size_t)desc->batch * T * desc->n_kv_heads * row;
-    if ((q != q_out && overlap(q, nq, q_out, nq)) || overlap(q_out, nq, k_new, nk) || overlap(q_out, nq, v_new, nk))
+    if ((q != q_out && overlap(q, nq, q_out, nq)) || overlap(q_out, nq, k_new, nk) || overlap(q_out, nq, v_new, nk) ||
+        hits_angles(desc, rope, st->seq_len, T, q_out, nq))
         return fail(DUO_ERR_INVALID_ARG, "duo_append_kv_rope: q_out overlaps another tensor (it may only be q itself)");
     const cudaError_t e = duo::launch_append_rope(a, c, r, q, k_new, v_new, q_out, T, (cudaStream_t)stream);
     return e == cudaSuccess ? ok() : cuda_fail(e, "duo_append_kv_rope");
@@ -777,10 +804,11 @@ duo_status duo_gated_mix_train(const duo_layer_desc* desc, const float* alpha, f
         return fail(DUO_ERR_CAPACITY, "saved holds %zu bytes, duo_gated_mix_train needs %zu", saved_bytes, sv.bytes);
     const size_t es = desc->dtype == DUO_BF16 ? 2 : 4, rows = (size_t)desc->batch * N;
     const size_t nq = rows * desc->n_q_heads * desc->head_dim * es, nkv = rows * desc->n_kv_heads * desc->head_dim * es;
-    for (const void* x : {q, k, v})
-        if (overlap(out, nq, x, x == q ? nq : nkv) || overlap(saved, sv.bytes, x, x == q ? nq : nkv))
-            return fail(DUO_ERR_INVALID_ARG, "duo_gated_mix_train: out or saved overlaps q, k or v");
-    if (overlap(out, nq, saved, sv.bytes)) return fail(DUO_ERR_INVALID_ARG, "duo_gated_mix_train: out overlaps saved");
+    // every output is written while inputs are still being read
+    const Range in[] = {{q, nq}, {k, nkv}, {v, nkv}, {alpha, sizeof(float) * desc->n_kv_heads}},
+                written[] = {{out, nq}, {saved, sv.bytes}, {status, sizeof(int32_t)}};
+    if (overlapping(in, written) >= 0)
+        return fail(DUO_ERR_INVALID_ARG, "duo_gated_mix_train: out, saved or status overlaps an input or one another");
     void* streaming = static_cast<uint8_t*>(saved) + sv.streaming;
     float* lse = static_cast<float*>(saved);
     cudaError_t e;
@@ -839,19 +867,11 @@ duo_status duo_gated_mix_grad(const duo_layer_desc* desc, const float* alpha, fl
         return fail(DUO_ERR_CAPACITY, "workspace holds %zu bytes, duo_gated_mix_grad needs %zu", ws_bytes, plan.bytes);
     const size_t es = desc->dtype == DUO_BF16 ? 2 : 4, rows = (size_t)desc->batch * N;
     const size_t nq = rows * desc->n_q_heads * desc->head_dim * es, nkv = rows * desc->n_kv_heads * desc->head_dim * es;
-    {
-        // every output is written while inputs are still being read
-        const struct { const void* p; size_t n; } in[] = {{q, nq}, {dout, nq}, {k, nkv}, {v, nkv}, {saved, sv.bytes}},
-                                                  out[] = {{dq, nq}, {dk, nkv}, {dv, nkv}, {workspace, plan.bytes}};
-        for (int i = 0; i < 4; ++i) {
-            for (const auto& x : in)
-                if (overlap(out[i].p, out[i].n, x.p, x.n))
-                    return fail(DUO_ERR_INVALID_ARG, "duo_gated_mix_grad: an output or the workspace overlaps an input");
-            for (int j = 0; j < i; ++j)
-                if (overlap(out[i].p, out[i].n, out[j].p, out[j].n))
-                    return fail(DUO_ERR_INVALID_ARG, "duo_gated_mix_grad: two outputs (or the workspace) overlap");
-        }
-    }
+    const size_t ng = sizeof(float) * desc->n_kv_heads;
+    const Range in[] = {{q, nq}, {dout, nq}, {k, nkv}, {v, nkv}, {saved, sv.bytes}, {alpha, ng}},
+                written[] = {{dq, nq}, {dk, nkv}, {dv, nkv}, {dalpha, ng}, {workspace, plan.bytes}, {status, sizeof(int32_t)}};
+    if (overlapping(in, written) >= 0)
+        return fail(DUO_ERR_INVALID_ARG, "duo_gated_mix_grad: an output, the workspace or status overlaps an input or one another");
     const uint8_t* sb = static_cast<const uint8_t*>(saved);
     duo::MixGradArgs g{};
     g.q = q;

@@ -432,9 +432,9 @@ duo_status duo_prefill_chunk(const duo_layer_desc* desc, const duo_kv_state* st,
  * q [B][T][Hq][d], k [B][T][Hkv][d] -> q_out, k_out of the same shapes (the
  * head order does not matter: every head of a token turns alike).  Either of
  * q and k may be NULL, with its output.  An output may be its input itself (in
- * place); other overlaps are refused.  seq_len: device int32 [B] or NULL (0),
- * the position of each sequence's first token where rope->pos is NULL (the
- * state's seq_len before a chunk's pre-fill).
+ * place); other overlaps, with rope's arrays and seq_len too, are refused.
+ * seq_len: device int32 [B] or NULL (0), the position of each sequence's first
+ * token where rope->pos is NULL (the state's seq_len before a chunk's pre-fill).
  * inverse != 0: the gradient -- given the gradients of q_out and k_out, those
  * of q and k: the same map by the negative angles.
  * T == 0 is a no-op (the tensors may then be NULL).
@@ -592,7 +592,8 @@ duo_status duo_gated_mix_grad_alpha(const duo_layer_desc* desc, const void* q, c
  *   workspace: duo_gated_mix_grad_workspace_bytes(desc, N) bytes, 16-byte
  *   aligned, no initialisation; calls that can overlap on the GPU need one each.
  *   No atomics: results do not depend on the order in which CTAs run.
- * Outputs, saved and workspace must not overlap each other or an input.
+ * Outputs, saved, workspace and status must not overlap each other or an input
+ * (dalpha's buffer is not alpha's): refused.
  * bf16 with d = 128 and sink + recent <= 128 runs on the tcgen05 tensor cores
  * (the weights and their gradients rounded to bf16 as MMA operands, sums in
  * fp32); the rest on the CUDA cores in fp32.
