@@ -1,6 +1,7 @@
 // tiled_attn.cu -- attention on the CUDA cores in 64 x 64 tiles, for what the
-// tensor-core kernels do not take (fp32, head_dim 64, wide windows): the
-// capped pre-fill, and the gated mix's training forward and backward passes.
+// tensor-core kernels do not take: the capped pre-fill in fp32 and with
+// head_dim 64, and the gated mix's training forward and backward passes in
+// those and over windows wider than a tile.
 // All arithmetic is fp32 (CUDA's exp2f and tanhf).
 //
 // Threads as 16 x 16 or 8 x 16; every product is a register tile of RI x 4
@@ -764,10 +765,8 @@ cudaError_t launch_tiled_prefill(const LayerArgs& a, const CacheArgs& c, const v
                                  int C, void* out, cudaStream_t st) {
     if (!a.cap.on) return cudaErrorInvalidConfiguration;
     const TiledArgs s{q, k, v, C, out, nullptr, nullptr, nullptr, nullptr};
-    if (a.dtype == DUO_BF16) {
-        if (a.D == 128) return launch_forward<__nv_bfloat16, 128, false, true>(a, c, s, st);
-        return launch_forward<__nv_bfloat16, 64, false, true>(a, c, s, st);
-    }
+    if (a.dtype == DUO_BF16)   // with d 128 a layer the tensor cores take, or one that is refused
+        return a.D == 64 ? launch_forward<__nv_bfloat16, 64, false, true>(a, c, s, st) : cudaErrorInvalidConfiguration;
     if (a.D == 128) return launch_forward<float, 128, false, true>(a, c, s, st);
     return launch_forward<float, 64, false, true>(a, c, s, st);
 }
