@@ -806,7 +806,7 @@ cudaError_t launch_grad(const CUtensorMap (&m)[4], const GradArgs& p, cudaStream
 
 // Two CTAs to a key tile where the first, seen by every query of its group,
 // would take one CTA longer than an SM's share of all tiles: a whole step of
-// 4,096 tokens and 32 + 8 heads 900 -> 876 us, of 1,000 tokens 169 -> 136; with
+// 4,096 tokens and 32 + 8 heads 900 -> 879 us, of 1,000 tokens 169 -> 140; with
 // 32 + 32 heads at 4,096, below the rule, pairs lose (923 -> 1,004: the pair's
 // exchange and its second load of K and V).
 bool share_key_tiles(const LayerArgs& a, int n_tiles) {

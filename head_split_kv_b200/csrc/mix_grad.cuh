@@ -5,8 +5,9 @@
 
 namespace duo {
 
-// The gradient of one gate: its shares (one per 32 rows of a sequence) added
-// in a fixed order by one warp, in fp64.
+// The gradient of one gate: its shares (mix_grad.cu: one per query head and 128
+// rows of a sequence; tiled_attn.cu: one per 32 rows) added in a fixed order by
+// one warp, in fp64.
 __device__ __forceinline__ void sum_shares(const float* part, int n, float* out, int lane) {
     double sum = 0.0;
     for (int i = lane; i < n; i += 32) sum += part[i];

@@ -12,7 +12,7 @@
 
 namespace duo {
 
-constexpr int BM = 128;            // query rows per tile (two tiles per CTA)
+constexpr int BM = 128;            // query rows per tile (prefill_tc.cu: two tiles to a CTA; prefill_capped.cu: one)
 constexpr int BN = 128;            // keys per K/V tile
 constexpr int HD = 128;            // head dim
 constexpr int kBox = 64;           // rows per TMA box (tiles are loaded as 2 x 2 boxes)
@@ -30,7 +30,7 @@ enum { SRC_CACHE = 0, SRC_CHUNK = 1, SRC_RING = 2 };
 struct TcArgs {
     LayerArgs a;
     int C;                 // chunk length
-    int n_mpairs;          // ceil(C / 256)
+    int n_mpairs;          // ceil(C / 256): pairs of query tiles
     int n_units;           // retrieval units B * R * G * n_mpairs
     int ns;                // CTAs per retrieval unit (key-range splits; 1 = none)
     int n_ret_ctas;        // n_units * ns

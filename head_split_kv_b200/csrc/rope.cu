@@ -17,9 +17,10 @@
 // their addresses need no length -- so that the reads of HBM run under the
 // trigonometry and the look-up of the lengths and pages.  A thread has the same
 // place in all of its rows, so it takes its cosines and sines from shared
-// memory once.  (A 4,096-token prompt of 32 + 8 heads takes 16 us.  When it took
-// 18, a grid of resident CTAs that walks the tokens, loading one ahead, took 23
-// at 80 registers, and two or four tokens to a CTA the same as one.)
+// memory once.  (A 4,096-token prompt of 32 + 8 heads takes 20 us, 16 when its
+// rows are still in L2.  When it took 18 there, a grid of resident CTAs that
+// walks the tokens, loading one ahead, took 23 at 80 registers, and two or four
+// tokens to a CTA the same as one.)
 //
 // A head row is cut into units of two 16-byte pieces.  Where the pairs are
 // (i, i + rot/2) a unit takes the two pieces whose elements pair up, so both

@@ -24,7 +24,7 @@
 // hides too little latency: two groups take alternate inner tiles, each with
 // its own sums (or running softmax), and merge at the end: that step 197 -> 142
 // us; a pre-fill of 2 x 333 rows behind 900 tokens 106 us with 16 x 16 threads
-// on one tile, 131 with 8 x 16, 91 with two groups.
+// on one tile, 131 with 8 x 16, 92 with two groups.
 #include <type_traits>
 
 #include "cap.cuh"
