@@ -473,7 +473,8 @@ duo_status duo_append_kv_rope(const duo_layer_desc* desc, const duo_kv_state* st
  * as in the plain call: v_chunk, and once seq_len > 0 every ring slot, must be
  * finite (zero-fill the ring before its first use).
  * A bf16 layer's capped score is within 8e-6 of its own size of the formula (an
- * fp32 layer's: fp32 rounding).
+ * fp32 layer's: fp32 rounding), under any cap and whatever its size.  (Past 2^24
+ * one fp32 score differs from the next by 2 or more.)
  * Errors: as the plain calls, and DUO_ERR_INVALID_ARG for a cap that is
  * negative, not finite, below scale / 1e4 or above 2e38.
  */
@@ -585,7 +586,8 @@ duo_status duo_gated_mix_grad_alpha(const duo_layer_desc* desc, const void* q, c
  * duo_prefill_chunk_capped caps them (0: not capped).
  *   saved: duo_gated_mix_saved_bytes(desc, N) bytes, 16-byte aligned: what
  *   duo_gated_mix_grad needs (both log-sums of every row, and on the CUDA cores
- *   both attentions) with the same desc, alpha, cap, q, k, v and N.
+ *   both attentions) with the same desc, alpha, cap, q, k, v and N; on the
+ *   tensor cores also room for one attention that the forward pass alone uses.
  * Backward: dout [B][N][Hq][d] -> dq [B][N][Hq][d], dk, dv [B][N][Hkv][d] in
  *   the layer's dtype (the heads of a group summed in fp32 and rounded once)
  *   and dalpha [Hkv] fp32; all overwritten.  Gates may have any finite value.
