@@ -16,8 +16,9 @@
 // near +cap, values past 2^40 or so could overflow it, and in a row whose every
 // score lies near -cap small values would fall below fp32's normal range.  So a
 // CTA looks at its rows as it stores them, and where a result is not finite (a
-// split's, to be added to others: past 2^100) or a row sum below 2^-32 it walks
-// its tiles once more (second_pass) with p = 2^(score - log2(2 l)), l the row's own sum, which is
+// split's, to be added to others: past 2^100), or a row sum is below 2^-32 and O
+// below 2^-90 (where products lost to the flush could count), it walks its tiles
+// once more (second_pass) with p = 2^(score - log2(2 l)), l the row's own sum, which is
 // always in range: those weights add up to 1/2, whatever the scores.  Scores
 // and values of a model never ask for it; that it can be asked for costs the
 // pre-fill of a 4,096-token chunk 0.9 % of its time.
@@ -74,7 +75,7 @@ constexpr uint32_t kOffBar = kOffSum + 4 * BM * 4;
 constexpr uint32_t kOffHolder = kOffBar + 24 * 8;  // TMEM base, last split, a row asks for a second pass, a wait ran out
 constexpr uint32_t kSmemBytes = kOffHolder + 16;
 constexpr uint32_t kOffSums2 = kOffK;              // a second pass's (l, l of the Lambda attention) by row
-constexpr float kMaxO = 0x1p100f, kMinSum = 0x1p-32f;   // of a first pass: a split's |O|, a row's sum
+constexpr float kMaxO = 0x1p100f, kMinSum = 0x1p-32f, kMinO = 0x1p-90f;   // of a first pass: a split's |O|; a row's sum with its |O|
 static_assert(kSmemBytes <= 232448, "one CTA per SM");
 
 // The key tiles of query tile mt (chunk rows 128 mt ..), as make_sched lists
@@ -351,8 +352,8 @@ __device__ __forceinline__ void issue_pv(const Cta& c, const LayerArgs& a, int b
     __syncwarp();
 }
 
-// Are 32 values all finite and at most `limit` in size?
-__device__ __forceinline__ bool within(const float (&o)[32], float limit) {
+// The largest size among 32 values; NaN if one is NaN.
+__device__ __forceinline__ float largest_nan(const float (&o)[32]) {
     auto max_nan = [](float a, float b, float c) {
         float d;
         asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -361,7 +362,7 @@ __device__ __forceinline__ bool within(const float (&o)[32], float limit) {
     float m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 32; i += 2) m[(i >> 1) & 3] = max_nan(m[(i >> 1) & 3], o[i], o[i + 1]);
-    return max_nan(max_nan(m[0], m[1], m[2]), m[3], 0.f) <= limit;
+    return max_nan(max_nan(m[0], m[1], m[2]), m[3], 0.f);
 }
 
 // The end of a pass for a thread of the exponential warps, one row and 32
@@ -398,11 +399,13 @@ __device__ __forceinline__ void store_rows(const TcArgs& p, const Work& w, const
     const bool live = crow < p.C && out_ok;
     ok = __all_sync(0xffffffffu, ok && mbar_wait(c.bars + kODone, pass, p.status));
     float o[32];
-    // the first pass: do this row's results, in o, ask for a second one?
-    auto judge = [&](float limit) {
-        if (pass == 0 && live && ok &&
-            (!within(o, limit) || (l_row > 0.f && l_row < kMinSum) || (MIX && l_lam > 0.f && l_lam < kMinSum)))
-            holder[2] = 1u;
+    // the first pass: do this row's results, in o (divided by the sums, or a
+    // split's), ask for a second one?
+    auto judge = [&](float limit, bool divided) {
+        if (pass != 0 || !live || !ok) return;
+        const float m = largest_nan(o);
+        auto lost = [&](float l) { return l > 0.f && l < kMinSum && m * (divided ? l : 1.f) < kMinO; };
+        if (!(m <= limit) || lost(l_row) || (MIX && lost(l_lam))) holder[2] = 1u;
     };
     if (ok) {
         tc_fence_after();
@@ -440,13 +443,13 @@ __device__ __forceinline__ void store_rows(const TcArgs& p, const Work& w, const
                 for (int e = 0; e < 8; ++e) v8[e] = o[8 * q4 + e];
                 if (live) store_row<__nv_bfloat16, 8>(op + 8 * q4, v8);
             }
-            judge(3.4028235e38f);
+            judge(3.4028235e38f, true);
         }
     } else if (bounds_ok(unit < p.n_units && split < p.ns, p.status)) {
         // this split's record of the query tile (the maximum is the bias), then a
         // ticket per query tile (half a word of the pair's); the CTA that arrives
         // last merges (no CTA ever waits)
-        judge(kMaxO);
+        judge(kMaxO, false);
         const int qi = mt & 1;
         float* rec = p.part + (((size_t)unit * p.ns + split) * 2 + qi) * kPartFloats;
         if (quarter == 0) {
