@@ -50,6 +50,7 @@
 //   ACC1 += W Y1 (dV), ACC2 += dS Y0 (dK or dQ) with A read from TMEM.
 // TMEM: S | dP | ACC1 | ACC2, 128 columns each; without ACC1 (statistics, dQ) a
 // second S takes its place, and for the statistics a second dP that of ACC2.
+// (Sequences of one tile add dS's rounding remainder as a third operand; keep_rest.)
 // S is free as soon as the element-wise warps have loaded it, so S(j + 1) is
 // there when they have finished tile j, and
 //   ACC1(j) ACC2(j) dP(j + 1)
@@ -243,16 +244,22 @@ __device__ __forceinline__ void weights(float (&x)[kCols], uint32_t (&pk)[kCols 
     }
 }
 
+// What the rounding of a packed pair took off it, packed as bf16.
+__device__ __forceinline__ uint32_t pack_rest(uint32_t hi, float x, float y) {
+    return pack_bf16(x - bf16_lo(hi), y - bf16_hi(hi));
+}
+
 // x[] and pk[] as weights left them, TMEM dP -> of every 16 columns of dP's the
 // first 8 hold W (COLS) and the last 8 dS (with a cap: -dS), packed as bf16.
-template <bool COLS, bool MASKED>
+// REST: what dS lost in its rounding goes where S was (COLS), or the first 8.
+template <bool COLS, bool MASKED, bool REST>
 __device__ __forceinline__ void score_grads(const float (&x)[kCols], const uint32_t (&pk)[kCols / 2], const RowStats& r,
-                                            const Seen& seen, uint32_t d_addr) {
+                                            const Seen& seen, uint32_t s_addr, uint32_t d_addr) {
 #pragma unroll
     for (int ch = 0; ch < kCols / kChunk; ++ch) {
         float d[kChunk];
         tmem_ld16(d_addr + kChunk * ch, d);
-        uint32_t o[kChunk];
+        uint32_t o[kChunk], rest[kChunk / 2];
 #pragma unroll
         for (int c4 = 0; c4 < kChunk / 4; ++c4) {
             const int q4 = kChunk / 4 * ch + c4;
@@ -264,11 +271,16 @@ __device__ __forceinline__ void score_grads(const float (&x)[kCols], const uint3
             const float2 v = fmul2(make_float2(w[2], w[3]), fadd2(make_float2(d[c + 2], d[c + 3]), make_float2(q.z, q.w)));
             o[kChunk / 2 + 2 * c4] = pack_bf16(u.x, u.y);
             o[kChunk / 2 + 2 * c4 + 1] = pack_bf16(v.x, v.y);
+            if constexpr (REST) {
+                rest[2 * c4] = pack_rest(o[kChunk / 2 + 2 * c4], u.x, u.y);
+                rest[2 * c4 + 1] = pack_rest(o[kChunk / 2 + 2 * c4 + 1], v.x, v.y);
+            }
             if constexpr (COLS) {
                 o[2 * c4] = pk[2 * q4];
                 o[2 * c4 + 1] = pk[2 * q4 + 1];
             }
         }
+        if constexpr (REST) tmem_st8((COLS ? s_addr : d_addr) + kChunk * ch, rest);
         if constexpr (COLS) {
             tmem_st16(d_addr + kChunk * ch, o);
         } else {
@@ -286,7 +298,7 @@ __device__ __forceinline__ void score_grads(const float (&x)[kCols], const uint3
 // negative a everything a CTA accumulates is negated, so that |a| P_c is W in
 // the other tiles; here its share is positive and the other one negative,
 // whichever of the two signs is the odd one.
-template <int CAP, bool COLS>
+template <int CAP, bool COLS, bool REST>
 __device__ __forceinline__ void signed_shares(const LayerArgs& a, float sl, const RowStats& r, Seen seen,
                                               uint32_t s_addr, uint32_t d_addr) {
 #pragma unroll 1
@@ -294,7 +306,7 @@ __device__ __forceinline__ void signed_shares(const LayerArgs& a, float sl, cons
         float x[16], d[16];
         tmem_ld16(s_addr + 16 * ch, x);
         tmem_ld16(d_addr + 16 * ch, d);
-        uint32_t pw[8], pg[8];
+        uint32_t pw[8], pg[8], rest[8];
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
             const float* st = r.cols + 16 * ch + c;
@@ -319,7 +331,9 @@ __device__ __forceinline__ void signed_shares(const LayerArgs& a, float sl, cons
         for (int c = 0; c < 8; ++c) {
             pw[c] = pack_bf16(x[2 * c], x[2 * c + 1]);
             pg[c] = pack_bf16(d[2 * c], d[2 * c + 1]);
+            if constexpr (REST) rest[c] = pack_rest(pg[c], d[2 * c], d[2 * c + 1]);
         }
+        if constexpr (REST) tmem_st8((COLS ? s_addr : d_addr) + 16 * ch, rest);
         if constexpr (COLS) tmem_st8(d_addr + 16 * ch, pw);
         tmem_st8(d_addr + 16 * ch + 8, pg);
     }
@@ -381,7 +395,7 @@ __device__ __forceinline__ uint32_t s_col(int j) { return !keys_outer(MODE) && (
 template <int MODE>
 __device__ __forceinline__ uint32_t d_col(int j) { return MODE == STATS && (j & 1) ? kColA2 : kColP; }
 
-template <int MODE, int CAP>
+template <int MODE, int CAP, bool REST>
 __global__ void __launch_bounds__(kRegThreads, 1)
     mix_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDo,
                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const GradArgs p) {
@@ -487,13 +501,13 @@ __global__ void __launch_bounds__(kRegThreads, 1)
                     tc_mma(tmem + col, x + o, y + o, idesc_kk, kk > 0 ? 1u : 0u);
                 }
             };
-            // ACC += A (W or dS, 8 of every 16 columns of dP's) Y_w(j), over the inner rows
-            auto issue_acc = [&](uint32_t col, uint32_t a_col, int w, int j) {
+            // ACC += A (W, dS or its rest, 8 of every 16 columns of dP's or S's) Y_w(j), over the inner rows
+            auto issue_acc = [&](uint32_t col, uint32_t a_col, int w, int j, bool first = true) {
                 const uint64_t y = sw128_desc(sY + ((j & 1) * 2 + w) * kTileBytes, kHalfBytes, 1024);
 #pragma unroll
                 for (int kk = 0; kk < BM / 16; ++kk)
                     tc_mma_ta(tmem + col, tmem + a_col + kChunk * kk, y + kk * (2048 >> 4), idesc_mn,
-                              (j > 0 || kk > 0) ? 1u : 0u);
+                              (!first || j > 0 || kk > 0) ? 1u : 0u);
             };
             auto wait_tile = [&](int j) { return mbar_wait(&y_full[j & 1], (j >> 1) & 1, p.status); };
             auto issue_s = [&](int j) {
@@ -543,7 +557,7 @@ __global__ void __launch_bounds__(kRegThreads, 1)
                     }
                 } else {
                     const bool next = j + 1 < n_in;
-                    if (kKeys && next) {
+                    if (kKeys && next && !REST) {
                         // S(j) is in registers: its columns take S(j + 1)
                         ok = wait_tile(j + 1) && mbar_wait(&w_ready[j & 1], ph, p.status);
                         if (!ok) break;
@@ -551,12 +565,15 @@ __global__ void __launch_bounds__(kRegThreads, 1)
                         if (elect_one()) issue_s(j + 1);
                     }
                     ok = mbar_wait(&g_ready[j & 1], ph, p.status);
+                    if (REST && kKeys && next) ok = ok && wait_tile(j + 1);
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
                         if (kKeys) issue_acc(kColA1, kColP, 1, j);
                         issue_acc(kColA2, kColP + kChunk / 2, 0, j);
+                        if (REST) issue_acc(kColA2, kKeys ? kColS : kColP, 0, j, false);
                         tc_commit(&y_empty[j & 1]);
+                        if (REST && kKeys && next) issue_s(j + 1);   // S's columns held the rest until here
                         if (next) issue_d(j + 1);
                     }
                     if (!kKeys && j + 2 < n_in) {
@@ -642,14 +659,14 @@ __global__ void __launch_bounds__(kRegThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 if (plain)
-                    score_grads<kKeys, false>(x, pk, rs, seen, d_addr);
+                    score_grads<kKeys, false, REST>(x, pk, rs, seen, s_addr, d_addr);
                 else
-                    score_grads<kKeys, true>(x, pk, rs, seen, d_addr);
+                    score_grads<kKeys, true, REST>(x, pk, rs, seen, s_addr, d_addr);
             } else {
                 ok = __all_sync(0xffffffffu, mbar_wait(&d_full[j & 1], ph, p.status));
                 if (!ok) break;
                 tc_fence_after();
-                signed_shares<CAP, kKeys>(a, sl, rs, seen, s_addr, d_addr);
+                signed_shares<CAP, kKeys, REST>(a, sl, rs, seen, s_addr, d_addr);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&w_ready[j & 1]);
@@ -776,10 +793,10 @@ __global__ void __launch_bounds__(kRegThreads, 1)
     }
 }
 
-template <int MODE, int CAP>
+template <int MODE, int CAP, bool REST>
 cudaError_t launch_cap(const CUtensorMap (&m)[4], const GradArgs& p, cudaStream_t s) {
     static std::atomic<unsigned long long> configured{0};
-    const cudaError_t e = smem_limit_once(mix_grad_kernel<MODE, CAP>, (int)kGradSmem, configured);
+    const cudaError_t e = smem_limit_once(mix_grad_kernel<MODE, CAP, REST>, (int)kGradSmem, configured);
     if (e != cudaSuccess) return e;
     const long grid = (long)p.a.B * (keys_outer(MODE) ? p.a.Hkv : p.a.Hq) * p.n_tiles * (MODE == KEY_PAIRS ? 2 : 1);
     if (grid > 0x7fffffffL) return cudaErrorInvalidConfiguration;
@@ -794,14 +811,16 @@ cudaError_t launch_cap(const CUtensorMap (&m)[4], const GradArgs& p, cudaStream_
     cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
     cfg.attrs = &cluster;
     cfg.numAttrs = MODE == KEY_PAIRS ? 1 : 0;
-    const cudaError_t launched = cudaLaunchKernelEx(&cfg, mix_grad_kernel<MODE, CAP>, m[0], m[1], m[2], m[3], p);
+    const cudaError_t launched = cudaLaunchKernelEx(&cfg, mix_grad_kernel<MODE, CAP, REST>, m[0], m[1], m[2], m[3], p);
     return launched != cudaSuccess ? launched : cudaGetLastError();
 }
 
-template <int MODE>
+template <int MODE, bool REST>
 cudaError_t launch_grad(const CUtensorMap (&m)[4], const GradArgs& p, cudaStream_t s) {
     const CapArgs& cap = p.a.cap;
-    return !cap.on ? launch_cap<MODE, NO_CAP>(m, p, s) : !cap.far ? launch_cap<MODE, CAPPED>(m, p, s) : launch_cap<MODE, CAP_FAR>(m, p, s);
+    return !cap.on    ? launch_cap<MODE, NO_CAP, REST>(m, p, s)
+           : !cap.far ? launch_cap<MODE, CAPPED, REST>(m, p, s)
+                      : launch_cap<MODE, CAP_FAR, REST>(m, p, s);
 }
 
 // Two CTAs to a key tile where the first, seen by every query of its group,
@@ -811,8 +830,17 @@ cudaError_t launch_grad(const CUtensorMap (&m)[4], const GradArgs& p, cudaStream
 // exchange and its second load of K and V).
 bool share_key_tiles(const LayerArgs& a, int n_tiles) {
     const long all = (long)a.B * a.Hkv * n_tiles * (n_tiles + 1) / 2;   // in tiles of one query head, as the next
-    return (long)n_tiles * sm_count() > all;
+    return a.G * n_tiles > 1 && (long)n_tiles * sm_count() > all;       // (one inner tile is not halved)
 }
+
+// dS as two bf16 operands, its value and what the rounding took off, where a
+// sequence is one tile: with few keys a row's gradient is a term or two, whose
+// rounding shows (dq and dk of up to 128 tokens were 1.2 to 1.7 times as far from
+// fp64 as their own rounding, and now are 1.00 times), and the step is mostly
+// launch latency: 43 to 55 us, 2 to 6 more with 4 or 8 query heads to a KV head,
+// none with one.  Over many tiles it would cost a product of nine, and S(j + 1)
+// its place beside dP(j) (the rest of dK's dS waits in S's columns).
+bool keep_rest(int n_tiles) { return n_tiles == 1; }
 
 }  // namespace
 
@@ -840,15 +868,19 @@ cudaError_t launch_mix_grad_tc(const LayerArgs& a, const MixGradArgs& g, int N, 
         if (!encode_tmap_bf16(&m[i], base[i], 4, d, st, bx)) return cudaErrorInvalidValue;
     }
     GradArgs p{a, N, pl.n_tiles, pl.n_pad, g.stats, g.lse, g.alpha, nullptr, nullptr, g.part, g.dalpha, g.status, tanh_poly(a.cap, 1.f)};
-    cudaError_t e = launch_grad<STATS>(m, p, s);
+    cudaError_t e = launch_grad<STATS, false>(m, p, s);
     if (e != cudaSuccess) return e;
     p.d0 = g.dk;
     p.d1 = g.dv;
-    e = share_key_tiles(a, pl.n_tiles) ? launch_grad<KEY_PAIRS>(m, p, s) : launch_grad<KEYS>(m, p, s);
+    const bool rest = keep_rest(pl.n_tiles);
+    if (share_key_tiles(a, pl.n_tiles))
+        e = rest ? launch_grad<KEY_PAIRS, true>(m, p, s) : launch_grad<KEY_PAIRS, false>(m, p, s);
+    else
+        e = rest ? launch_grad<KEYS, true>(m, p, s) : launch_grad<KEYS, false>(m, p, s);
     if (e != cudaSuccess) return e;
     p.d0 = g.dq;
     p.d1 = nullptr;
-    return launch_grad<QUERIES>(m, p, s);
+    return rest ? launch_grad<QUERIES, true>(m, p, s) : launch_grad<QUERIES, false>(m, p, s);
 }
 
 }  // namespace duo

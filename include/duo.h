@@ -597,8 +597,9 @@ duo_status duo_gated_mix_grad_alpha(const duo_layer_desc* desc, const void* q, c
  * Outputs, saved, workspace and status must not overlap each other or an input
  * (dalpha's buffer is not alpha's): refused.
  * bf16 with d = 128 and sink + recent <= 128 runs on the tcgen05 tensor cores
- * (the weights and their gradients rounded to bf16 as MMA operands, sums in
- * fp32); the rest on the CUDA cores in fp32.
+ * (the weights and the scores' gradients rounded to bf16 as MMA operands, the
+ * latter kept as two such operands for N up to 128; sums in fp32); the rest on
+ * the CUDA cores in fp32.
  * N == 0: nothing is done but that dalpha is zeroed (the other tensors may then
  * be NULL).
  * q, k, v and dout must be finite: masked entries are weights of 0 in matrix

@@ -5,7 +5,8 @@ added as such (in quadrature), and only what may be systematic is added up.
 What a kernel rounds, and by how much (half a step of a type: HALF):
   * bf16 MMA operands -- P in the forward pass, W and dS in the backward pass --
     and every bf16 output: independent, at most HALF = 2^-8 of the value, uniform
-    within its step, so of standard deviation at most HALF / sqrt(3);
+    within its step, so of standard deviation at most HALF / sqrt(3); in sequences of
+    up to 128 tokens dS is the sum of two such operands: HALF^2;
   * a score: fp32 sums of d products ((4 + sqrt(d)) half-steps of the terms'
     size) and, under a cap, a tanh within 8e-6 of the score (fp32: 4 half-steps).
     The tanh's error is a function of the score: systematic;
@@ -47,6 +48,7 @@ def mix_bounds(q, k, v, do, alpha, cap, sink, recent, dtype, tc, stored_d=False)
     causal = i[:, None] >= i[None, :]
     lam = causal & ((i[None, :] < sink) | (i[:, None] - i[None, :] < recent))
     r, store = (HALF["bf16"] / math.sqrt(3) if tc else 0.0), HALF[dtype] / math.sqrt(3)
+    r_g = r * HALF["bf16"] if N <= 128 else r
     acc = (8 + math.sqrt(N)) * H32                                       # of an fp32 sum's terms
     res = {"out": np.zeros_like(q), "dq": np.zeros_like(q), "dk": np.zeros_like(k), "dv": np.zeros_like(v), "dalpha": np.zeros(hkv)}
     var, lin = ({n: np.zeros_like(x) for n, x in res.items()} for _ in range(2))
@@ -97,10 +99,10 @@ def mix_bounds(q, k, v, do, alpha, cap, sink, recent, dtype, tc, stored_d=False)
             var["dv"][b, :, j] += r * r * (W * W).T @ (oo * oo)
             lin["dv"][b, :, j] += W_lin.T @ np.abs(oo) + acc * (np.abs(W).T @ np.abs(oo))
             res["dq"][b, :, h] = g @ kk
-            var["dq"][b, :, h] = r * r * (g * g) @ (kk * kk)
+            var["dq"][b, :, h] = r_g * r_g * (g * g) @ (kk * kk)
             lin["dq"][b, :, h] = g_lin @ np.abs(kk) + acc * (np.abs(g) @ np.abs(kk))
             res["dk"][b, :, j] += g.T @ qq
-            var["dk"][b, :, j] += r * r * (g * g).T @ (qq * qq)
+            var["dk"][b, :, j] += r_g * r_g * (g * g).T @ (qq * qq)
             lin["dk"][b, :, j] += g_lin.T @ np.abs(qq) + acc * (np.abs(g).T @ np.abs(qq))
     for n in ("out", "dq", "dk", "dv"):
         var[n] += (store * res[n]) ** 2

@@ -53,6 +53,29 @@ def test_mix_step_within_independent_roundings(duo, case):
         assert excess(n, g, w, bounds[n]) is None, excess(n, g, w, bounds[n])
 
 
+SHORT = [   # sequences of one tile: dS keeps what its rounding takes off, so dq and dk are off by their own rounding alone
+    (1, 1, 2, 0.0, 3.0, 16, 64, [0.5]),
+    (8, 1, 3, 20.0, 3.0, 16, 64, [0.25]),
+    (4, 4, 5, 50.0, 3.0, 0, 1, [0.1, 0.9, 0.5, 0.7]),
+    (8, 2, 17, 0.0, 1.0, 2, 4, [0.3, 0.8]),
+    (8, 2, 64, 30.0, 3.0, 2, 4, [1.5, -0.75]),
+    (8, 4, 100, 0.0, 3.0, 16, 64, [0.0, 1.0, 2.0, -0.5]),
+    (16, 2, 128, 20.0, 3.0, 100, 28, [0.4, 1.25]),
+    (4, 2, 128, 200.0, 3.0, 16, 64, [0.4, 0.6]),
+    (4, 2, 127, 1e20, 3.0, 16, 8, [0.4, -0.6]),
+]
+
+
+@pytest.mark.parametrize("case", SHORT, ids=lambda c: "-".join(str(x) for x in c[:7]))
+def test_short_sequences_within_the_outputs_rounding(duo, case):
+    hq, hkv, N, cap, gain, sink, recent, alpha = case
+    desc, q, k, v, do, al = _case(duo, hq, hkv, 128, "bf16", 3, N, cap, gain, sink, recent, alpha)
+    got = dict(zip(("out", "dq", "dk", "dv", "dalpha"), (f64(x) for x in _step(duo, desc, cap, q, k, v, do, al))))
+    want, bounds = mix_bounds(f64(q), f64(k), f64(v), f64(do), f64(al), cap, sink, recent, "bf16", True)
+    for n, w in want.items():
+        assert excess(n, got[n], w, bounds[n]) is None, excess(n, got[n], w, bounds[n])
+
+
 @pytest.mark.parametrize("d,cap,sink,recent", [(64, 7.0, 4, 8), (64, 0.0, 16, 64), (128, 20.0, 0, 1)])
 def test_gradient_along_its_direction_against_differences(duo, d, cap, sink, recent):
     """fp32: L = <dout, out> moved by +-h along the whole gradient of one input.  The kernel's L against fp64's at the same
